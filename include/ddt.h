@@ -423,6 +423,116 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
                             const int32_t* acc_nodes, const int32_t* acc_len, int32_t* prefix_len,
                             int32_t* src_row, int32_t* dst_pos, int32_t* status, ddt_stream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * ddt_decode_attn_paged -- attention of one new token a request over the paged prefix
+ * cache: the step of a request that has no drafts ([NOTES] "Where the next step is":
+ * attention over paged KV blocks; the plain step itself has no formula there).
+ *
+ * For layer l, request b, query head h (kv head g = h / (Hq/Hkv)):
+ *   o = softmax(scale * q . K^T) V over the prefix rows 0..prefix_len[b]-1 (addressed as
+ *       in ddt_tree_attn_paged) and the new token's own row k_new, v_new.
+ * That is ddt_tree_attn_paged for a tree of the root alone.  The new row is not written to
+ * the cache: ddt_commit_paged with N = A = 1, acc_nodes 0 and acc_len 0 appends it.
+ *   q [L][B][Hq][d], k_new, v_new [L][B][Hkv][d] (in_dtype); k_new and v_new may both be
+ *     NULL: then only the prefix rows are attended to, and o is zero where there are none.
+ *   k_pages, v_pages [L][num_pages][Hkv][page_size][d] (in_dtype), block_table
+ *     [B][max_pages], page_size and capacity as in ddt_tree_attn_paged; rows past the
+ *     prefix are never used, whatever they hold.  Requests may share pages.
+ *   attn_weight [L][B][Hkv][max_pages * page_size] fp32, or NULL.  Row p of the prefix
+ *     (and row prefix_len[b], the new token's once it is appended, if the capacity has it)
+ *     gets the sum over the kv head's query heads of its softmax weights ADDED to its
+ *     entry; the other entries are left as they are.  Start it at zero.
+ *   o [L][B][Hq][d] (out_dtype).
+ *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, max_pages * page_size],
+ *     DDT_ERR_INVALID_ARG if a block-table entry that the prefix needs is outside
+ *     [0, num_pages); the request's output rows are then zero and its sums unchanged.
+ * d in {64, 128, 256}; fp32 and bf16; Hq / Hkv <= 1024; q, k_new, v_new, the pages and o
+ * 16-byte aligned.  The same inputs give the same bits.
+ * workspace: ddt_decode_attn_paged_workspace(...) bytes (want_weight: 1 with attn_weight,
+ * then 4 * L * B * Hq * capacity bytes of it hold scores), 16-byte aligned.
+ * ------------------------------------------------------------------------------- */
+size_t ddt_decode_attn_paged_workspace(int n_layers, int B, int Hq, int Hkv, int d, int page_size,
+                                       int max_pages, ddt_dtype in_dtype, int want_weight);
+ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, int page_size,
+                                 int num_pages, int max_pages, ddt_dtype in_dtype,
+                                 ddt_dtype out_dtype, const void* q, const void* k_new,
+                                 const void* v_new, const void* k_pages, const void* v_pages,
+                                 const int32_t* block_table, const int32_t* prefix_len, float scale,
+                                 void* o, float* attn_weight, int32_t* status, void* workspace,
+                                 size_t ws_bytes, ddt_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * ddt_evict_paged -- eviction from the paged cache by accumulated attention weight (no
+ * counterpart in the pages): bounds a request's cache to `keep` rows.
+ *
+ * For every request with prefix_len[b] > keep, and every layer and kv head on its own,
+ * `keep` of the P = prefix_len[b] cached rows stay: first the rows whose sequence position
+ * is below n_sink or at least seq_len[b] - n_recent, then the others by their attn_weight
+ * entry, largest first (NaN last); ties go to the lower row.  The kept rows at index >=
+ * keep then move, in ascending order, to the evicted rows' indices below keep, in
+ * ascending order: K row, V row, attn_weight entry and row_pos entry.  Attention does not
+ * depend on the order of the rows, so the rows below keep that stay are not moved.
+ *   attn_weight [L][B][Hkv][cap] fp32, cap = max_pages * page_size: as accumulated by
+ *     ddt_decode_attn_paged.  Entries [keep, P) become 0, ready for rows appended there.
+ *   row_pos [L][B][Hkv][cap] int32: sequence positions of the rows < n_placed[b]; a row
+ *     i >= n_placed[b] holds position seq_len[b] - P + i (appended in order since the last
+ *     eviction; n_placed[b] = 0 before the first one, and row_pos need not be set then).
+ *     On return it holds the positions of the keep rows; entries [keep, P) become -1.
+ *   n_placed [B], prefix_len [B]: become keep.  seq_len [B]: tokens of the sequence that
+ *     have been cached, evicted ones included (advance it where prefix_len advances, and
+ *     give it to ddt_build_tree as the base of positions); read only.
+ * Requests with prefix_len[b] <= keep are left as they are (status DDT_OK).  Pages past
+ * ceil(keep / page_size) of a cut request hold nothing any more.
+ *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, cap]; DDT_ERR_INVALID_ARG
+ *     if n_placed[b] is outside [0, prefix_len[b]], if seq_len[b] < prefix_len[b], if a
+ *     block-table entry of the prefix is outside [0, num_pages), or if the request is over
+ *     the budget and one of its pages is used more than once, by itself or by another
+ *     request of the call (an eviction in place would change the other's rows).  Such a
+ *     request is left as it is.
+ * keep >= 1, n_sink + n_recent <= keep; page_size as in ddt_tree_attn_paged; rows of any
+ * d whose bytes are a multiple of 16 (up to 16384); pages 16-byte aligned.
+ * workspace: ddt_evict_paged_workspace(...) bytes, 16-byte aligned.
+ * ------------------------------------------------------------------------------- */
+size_t ddt_evict_paged_workspace(int n_layers, int B, int Hkv, int page_size, int num_pages,
+                                 int max_pages);
+ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, int num_pages,
+                           int max_pages, const int32_t* block_table, ddt_dtype kv_dtype, int keep,
+                           int n_sink, int n_recent, void* k_pages, void* v_pages,
+                           const int32_t* seq_len, float* attn_weight, int32_t* row_pos,
+                           int32_t* prefix_len, int32_t* n_placed, int32_t* status, void* workspace,
+                           size_t ws_bytes, ddt_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * ddt_token_logprobs -- what a serving interface reports about emitted or given tokens
+ * under the target's logits (no counterpart in the pages).
+ *
+ * For entry a of request b, with r = node[b][a] (r = a, and A = N, when node is NULL),
+ * x = target_logits[b][r], and p = softmax(x / temperature):
+ *   logprob[b][a] = log p(token[b][a]);  entropy[b][a] = -sum_v p(v) log p(v), in nats;
+ *   top_token, top_logprob [b][a][0..top_n): the top_n tokens by (x desc, id asc) and
+ *   their log probabilities.
+ * With node = acc_nodes and token = emitted of a walk, these are the emitted tokens'.
+ *   target_logits [B][N][V] (dtype), aligned to its elements; token, node [B][A] int32.
+ *     -inf logits (masked tokens) have probability 0 and log probability -inf.
+ *   node < 0 marks a padding entry: logprob and entropy 0, top_token -1, top_logprob 0,
+ *     status DDT_OK.  token < 0 with a row: no token is given, logprob is 0.
+ *   entropy may be NULL, and top_token and top_logprob where top_n is 0.
+ *   status [B][A]: DDT_ERR_NONFINITE for a row with a NaN or +inf logit or with none above
+ *     -inf (outputs NaN, top_token -1); DDT_ERR_INVALID_ARG for node >= N or token >= V
+ *     (outputs as for padding).
+ * Precision: terms by the hardware base-2 exponential (relative error about 2^-22), summed
+ * in fp32 within 2048 entries and in fp64 across them; logprob and entropy carry an
+ * absolute error of about 1e-6.  The same inputs give the same bits.
+ * temperature > 0 with a finite fp32 reciprocal; 0 <= top_n <= min(32, V); V <= 2^30.
+ * workspace: ddt_token_logprobs_workspace(B, A, V, top_n) bytes, 16-byte aligned.
+ * ------------------------------------------------------------------------------- */
+size_t ddt_token_logprobs_workspace(int B, int A, int V, int top_n);
+ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float temperature,
+                              ddt_dtype dtype, const void* target_logits, const int32_t* node,
+                              const int32_t* token, float* logprob, float* entropy,
+                              int32_t* top_token, float* top_logprob, int32_t* status,
+                              void* workspace, size_t ws_bytes, ddt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -391,4 +391,103 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------- single-token decode
+static bool paging_sizes_ok(int page_size, int num_pages, int max_pages) {
+    return page_rows_ok(page_size) && (long)page_size * max_pages <= (1L << 30) && num_pages >= 1;
+}
+
+// the largest grid and plane counts the kernels index with 32 bits
+static bool decode_sizes_ok(int n_layers, int B, int Hq, int Hkv, int num_pages) {
+    const long most = 0x7fffffffL;
+    return (long)n_layers * B <= most / Hq && (long)n_layers * num_pages <= most / Hkv && Hq / Hkv <= 1024;
+}
+
+size_t ddt_decode_attn_paged_workspace(int n_layers, int B, int Hq, int Hkv, int d, int page_size, int max_pages,
+                                       ddt_dtype in_dtype, int want_weight) {
+    if (n_layers < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 || !dtype_ok(in_dtype) ||
+        !paging_sizes_ok(page_size, 1, max_pages))
+        return 0;
+    return decode_ws_bytes(n_layers, B, Hq, Hkv, d, page_size * max_pages, in_dtype, want_weight != 0);
+}
+
+ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, int page_size, int num_pages,
+                                 int max_pages, ddt_dtype in_dtype, ddt_dtype out_dtype, const void* q,
+                                 const void* k_new, const void* v_new, const void* k_pages, const void* v_pages,
+                                 const int32_t* block_table, const int32_t* prefix_len, float scale, void* o,
+                                 float* attn_weight, int32_t* status, void* workspace, size_t ws_bytes,
+                                 ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1 ||
+        !dtype_ok(in_dtype) || !dtype_ok(out_dtype))
+        return DDT_ERR_INVALID_ARG;
+    if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hq, Hkv, num_pages) ||
+        (d != 64 && d != 128 && d != 256))
+        return DDT_ERR_UNSUPPORTED;
+    if (!q || !k_pages || !v_pages || !block_table || !prefix_len || !o || !status || !workspace || !k_new != !v_new)
+        return DDT_ERR_INVALID_ARG;
+    if (ws_bytes < decode_ws_bytes(n_layers, B, Hq, Hkv, d, page_size * max_pages, in_dtype, attn_weight != nullptr) ||
+        !aligned16(workspace))
+        return DDT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        !aligned16(o))
+        return DDT_ERR_INVALID_ARG;
+    const AttnPaging pg{page_size, num_pages, max_pages, block_table};
+    return from_cuda(launch_decode(n_layers, B, Hq, Hkv, d, pg, in_dtype, out_dtype, q, k_new, v_new, k_pages, v_pages,
+                                   prefix_len, scale, o, attn_weight, status, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------------------ eviction
+size_t ddt_evict_paged_workspace(int n_layers, int B, int Hkv, int page_size, int num_pages, int max_pages) {
+    if (n_layers < 1 || B < 1 || Hkv < 1 || max_pages < 1 || !paging_sizes_ok(page_size, num_pages, max_pages)) return 0;
+    return evict_ws_bytes(n_layers, B, Hkv, AttnPaging{page_size, num_pages, max_pages, nullptr});
+}
+
+ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                           const int32_t* block_table, ddt_dtype kv_dtype, int keep, int n_sink, int n_recent,
+                           void* k_pages, void* v_pages, const int32_t* seq_len, float* attn_weight, int32_t* row_pos,
+                           int32_t* prefix_len, int32_t* n_placed, int32_t* status, void* workspace, size_t ws_bytes,
+                           ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || Hkv < 1 || d < 1 || num_pages < 1 || max_pages < 1 || !dtype_ok(kv_dtype) || keep < 1 ||
+        n_sink < 0 || n_recent < 0 || (long)n_sink + n_recent > keep)
+        return DDT_ERR_INVALID_ARG;
+    const long row_bytes = (long)d * (kv_dtype == DDT_BF16 ? 2 : 4);
+    if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
+        row_bytes % 16 != 0 || row_bytes > 16384)
+        return DDT_ERR_UNSUPPORTED;
+    if (!block_table || !k_pages || !v_pages || !seq_len || !attn_weight || !row_pos || !prefix_len || !n_placed ||
+        !status || !workspace)
+        return DDT_ERR_INVALID_ARG;
+    const AttnPaging pg{page_size, num_pages, max_pages, block_table};
+    if (ws_bytes < evict_ws_bytes(n_layers, B, Hkv, pg) || !aligned16(workspace) || !aligned16(k_pages) ||
+        !aligned16(v_pages))
+        return DDT_ERR_INVALID_ARG;
+    return from_cuda(launch_evict(n_layers, B, Hkv, (int)row_bytes, pg, keep, n_sink, n_recent, k_pages, v_pages, seq_len,
+                                  attn_weight, row_pos, prefix_len, n_placed, status, workspace,
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// --------------------------------------------------------------------- log probabilities
+size_t ddt_token_logprobs_workspace(int B, int A, int V, int top_n) {
+    if (B < 1 || A < 1 || V < 1 || top_n < 0) return 0;
+    return logprobs_ws_bytes(B, A, V, top_n);
+}
+
+ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float temperature, ddt_dtype dtype,
+                              const void* target_logits, const int32_t* node, const int32_t* token, float* logprob,
+                              float* entropy, int32_t* top_token, float* top_logprob, int32_t* status, void* workspace,
+                              size_t ws_bytes, ddt_stream_t stream) {
+    if (B < 1 || N < 1 || V < 1 || A < 1 || top_n < 0 || !dtype_ok(dtype)) return DDT_ERR_INVALID_ARG;
+    if (!(temperature > 0.0f) || !(1.0f / temperature < INFINITY) || !(temperature < INFINITY))
+        return DDT_ERR_INVALID_ARG;
+    if (!node && A != N) return DDT_ERR_INVALID_ARG;
+    if (top_n > kMaxTopK || top_n > V || (long)B * A > 0x7fffffffL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
+    if (!target_logits || !token || !logprob || !status || !workspace || (top_n > 0 && (!top_token || !top_logprob)))
+        return DDT_ERR_INVALID_ARG;
+    if (ws_bytes < logprobs_ws_bytes(B, A, V, top_n) || !aligned16(workspace)) return DDT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(target_logits) % (dtype == DDT_BF16 ? 2 : 4)) return DDT_ERR_INVALID_ARG;
+    return from_cuda(launch_token_logprobs(B, N, V, A, top_n, temperature, dtype, target_logits, node, token, logprob,
+                                           entropy, top_token, top_logprob, status, workspace,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -74,6 +74,22 @@ cudaError_t launch_attn_tc(int L, int B, int N, int Hq, int Hkv, int d, int Pcap
                            void* o, int32_t* status, void* ws, size_t ws_bytes, cudaStream_t st,
                            const AttnRope* rope = nullptr);
 
+size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype in, bool weight);
+cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype in, ddt_dtype out,
+                          const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                          const void* v_pages, const int32_t* prefix_len, float scale, void* o, float* weight,
+                          int32_t* status, void* ws, cudaStream_t st);
+size_t evict_ws_bytes(int L, int B, int Hkv, const AttnPaging& pg);
+cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging& pg, int keep, int n_sink,
+                         int n_recent, void* k_pages, void* v_pages, const int32_t* seq_len, float* weight,
+                         int32_t* row_pos, int32_t* prefix_len, int32_t* n_placed, int32_t* status, void* ws,
+                         cudaStream_t st);
+size_t logprobs_ws_bytes(int B, int A, int V, int top_n);
+cudaError_t launch_token_logprobs(int B, int N, int V, int A, int top_n, float temperature, ddt_dtype dtype,
+                                  const void* logits, const int32_t* node, const int32_t* token, float* logprob,
+                                  float* entropy, int32_t* top_token, float* top_logprob, int32_t* status, void* ws,
+                                  cudaStream_t st);
+
 // one bounded wait on an mbarrier nothing signals; status[0] = its outcome
 cudaError_t launch_wait_selftest(int32_t* status, cudaStream_t st);
 cudaError_t launch_rope_tree(int L, int B, int N, int Hq, int Hkv, int d, int rot, double theta, ddt_dtype dtype,

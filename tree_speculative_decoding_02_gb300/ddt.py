@@ -54,6 +54,12 @@ _SIGS = {
                                                      _c_p], _c_int),
     "ddt_tree_attn_paged_rope": ([_c_int] * 11 + [_c_p] * 10 + [_c_int, ctypes.c_double, _c_float, _c_p, _c_p, _c_p,
                                                                 _c_size, _c_p], _c_int),
+    "ddt_decode_attn_paged_workspace": ([_c_int] * 9, _c_size),
+    "ddt_decode_attn_paged": ([_c_int] * 10 + [_c_p] * 7 + [_c_float] + [_c_p] * 4 + [_c_size, _c_p], _c_int),
+    "ddt_evict_paged_workspace": ([_c_int] * 6, _c_size),
+    "ddt_evict_paged": ([_c_int] * 7 + [_c_p] + [_c_int] * 4 + [_c_p] * 9 + [_c_size, _c_p], _c_int),
+    "ddt_token_logprobs_workspace": ([_c_int] * 4, _c_size),
+    "ddt_token_logprobs": ([_c_int] * 5 + [_c_float, _c_int] + [_c_p] * 9 + [_c_size, _c_p], _c_int),
     "ddt_commit": ([_c_int] * 7 + [_c_int] + [_c_p] * 4 + [_c_int] * 6 + [_c_int] + [_c_p] * 13, _c_int),
 }
 EXPORTS = tuple(_SIGS)
@@ -562,4 +568,163 @@ def ddt_commit_paged(acc_nodes, acc_len, prefix_len, block_table, *, k_tree, v_t
                               _ptr(acc_nodes), _ptr(acc_len), _ptr(prefix_len), _ptr(res["src_row"]),
                               _ptr(res["dst_pos"]), _ptr(res["status"]), _stream())
     _check(rc, "ddt_commit_paged")
+    return res
+
+
+# ------------------------------------------------------------------ single-token decode
+def _here(t, name):
+    """The calls enqueue on the current device's current stream: refuse tensors of another one."""
+    if t.device.index != torch.cuda.current_device():
+        raise DDTError(f"{name} is on {t.device}, not on the current device")
+    return t.device
+
+
+def _need_on(dev, t, shape, dtype, name):
+    _need(t, shape, dtype, name)
+    if t.device != dev:
+        raise DDTError(f"{name} is on {t.device}, expected {dev}")
+    return t
+
+
+def _ws_bytes(dev, ws):
+    if ws.device != dev or not ws.is_contiguous():
+        raise DDTError(f"workspace must be a contiguous tensor on {dev}")
+    return ws.numel() * ws.element_size()
+
+
+def decode_attn_paged_workspace(q, k_pages, block_table, *, weights=False):
+    """A workspace for ddt_decode_attn_paged calls of these shapes (one call at a time may use it)."""
+    lib = _gpu()
+    L, B, Hq, d = q.shape
+    need = lib.ddt_decode_attn_paged_workspace(L, B, Hq, k_pages.shape[2], d, k_pages.shape[3], block_table.shape[1],
+                                               _DT[q.dtype], int(weights))
+    return _ws(need, q.device)
+
+
+def ddt_decode_attn_paged(q, k_new, v_new, k_pages, v_pages, block_table, prefix_len, *, scale: float, attn_weight=None,
+                          out_dtype=None, out=None, status=None, workspace=None):
+    """One new token a request: q [L][B][Hq][d]; k/v_new [L][B][Hkv][d] (its own row, not in the cache; or both
+    None); k/v_pages [L][num_pages][Hkv][page_size][d]; block_table [B][max_pages] int32.  attn_weight, if given:
+    [L][B][Hkv][max_pages * page_size] fp32, the running sums the rows' softmax weights are added to, in place."""
+    lib = _gpu()
+    L, B, Hq, d = q.shape
+    num_pages, Hkv, page = k_pages.shape[1], k_pages.shape[2], k_pages.shape[3]
+    max_pages = block_table.shape[1]
+    dt, dev = q.dtype, _here(q, "q")
+    if dt not in _DT:
+        raise DDTError(f"q has dtype {dt}, expected one of {list(_DT)}")
+    _need_on(dev, q, (L, B, Hq, d), dt, "q")
+    if (k_new is None) != (v_new is None):
+        raise DDTError("k_new and v_new are given together or not at all")
+    if k_new is not None:
+        _need_on(dev, k_new, (L, B, Hkv, d), dt, "k_new")
+        _need_on(dev, v_new, (L, B, Hkv, d), dt, "v_new")
+    _need_on(dev, k_pages, (L, num_pages, Hkv, page, d), dt, "k_pages")
+    _need_on(dev, v_pages, (L, num_pages, Hkv, page, d), dt, "v_pages")
+    _need_on(dev, block_table, (B, max_pages), torch.int32, "block_table")
+    _need_on(dev, prefix_len, (B,), torch.int32, "prefix_len")
+    if attn_weight is not None:
+        _need_on(dev, attn_weight, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
+    if out is not None:
+        out_dtype = out_dtype or out.dtype
+        o = _need_on(dev, out, (L, B, Hq, d), out_dtype, "out")
+    else:
+        out_dtype = out_dtype or dt
+        o = torch.empty((L, B, Hq, d), dtype=out_dtype, device=dev)
+    if out_dtype not in _DT:
+        raise DDTError(f"out has dtype {out_dtype}, expected one of {list(_DT)}")
+    st = _need_on(dev, status, (B,), torch.int32, "status") if status is not None else \
+        torch.empty((B,), dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = decode_attn_paged_workspace(q, k_pages, block_table, weights=attn_weight is not None)
+    rc = lib.ddt_decode_attn_paged(L, B, Hq, Hkv, d, page, num_pages, max_pages, _DT[dt], _DT[out_dtype], _ptr(q),
+                                   _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                   _ptr(prefix_len), float(scale), _ptr(o), _ptr(attn_weight), _ptr(st),
+                                   _ptr(workspace), _ws_bytes(dev, workspace), _stream())
+    _check(rc, "ddt_decode_attn_paged")
+    return {"o": o, "status": st}
+
+
+# ------------------------------------------------------------------------------ eviction
+def evict_paged_workspace(k_pages, block_table):
+    """A workspace for ddt_evict_paged calls of these shapes (one call at a time may use it)."""
+    lib = _gpu()
+    L, num_pages, Hkv, page, _ = k_pages.shape
+    B, max_pages = block_table.shape
+    return _ws(lib.ddt_evict_paged_workspace(L, B, Hkv, page, num_pages, max_pages), k_pages.device)
+
+
+def ddt_evict_paged(k_pages, v_pages, block_table, prefix_len, n_placed, seq_len, attn_weight, row_pos, *, keep: int,
+                    n_sink: int = 0, n_recent: int = 0, status=None, workspace=None):
+    """In place: cuts every request's cache to its `keep` rows of the largest attn_weight (the first n_sink and
+    the last n_recent positions before all others); updates the pages, prefix_len, n_placed [B], and attn_weight
+    (fp32) and row_pos (int32) [L][B][Hkv][max_pages * page_size].  seq_len [B] is read only."""
+    lib = _gpu()
+    L, num_pages, Hkv, page, d = k_pages.shape
+    B, max_pages = block_table.shape
+    dt, dev = k_pages.dtype, _here(k_pages, "k_pages")
+    if dt not in _DT:
+        raise DDTError(f"k_pages has dtype {dt}, expected one of {list(_DT)}")
+    _need_on(dev, k_pages, (L, num_pages, Hkv, page, d), dt, "k_pages")
+    _need_on(dev, v_pages, (L, num_pages, Hkv, page, d), dt, "v_pages")
+    _need_on(dev, block_table, (B, max_pages), torch.int32, "block_table")
+    for t, name in ((prefix_len, "prefix_len"), (n_placed, "n_placed"), (seq_len, "seq_len")):
+        _need_on(dev, t, (B,), torch.int32, name)
+    _need_on(dev, attn_weight, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
+    _need_on(dev, row_pos, (L, B, Hkv, max_pages * page), torch.int32, "row_pos")
+    st = _need_on(dev, status, (B,), torch.int32, "status") if status is not None else \
+        torch.empty((B,), dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = evict_paged_workspace(k_pages, block_table)
+    rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, _ptr(block_table), _DT[dt], int(keep),
+                             int(n_sink), int(n_recent), _ptr(k_pages), _ptr(v_pages), _ptr(seq_len),
+                             _ptr(attn_weight), _ptr(row_pos), _ptr(prefix_len), _ptr(n_placed), _ptr(st),
+                             _ptr(workspace), _ws_bytes(dev, workspace), _stream())
+    _check(rc, "ddt_evict_paged")
+    return {"status": st}
+
+
+# --------------------------------------------------------------------- log probabilities
+def token_logprobs_workspace(target_logits, token, *, top_n: int = 32):
+    """A workspace for ddt_token_logprobs calls of these shapes and up to top_n alternatives (one call at a
+    time may use it)."""
+    lib = _gpu()
+    B, A = token.shape
+    return _ws(lib.ddt_token_logprobs_workspace(B, A, target_logits.shape[2], int(top_n)), token.device)
+
+
+def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, temperature: float = 1.0, out=None,
+                       workspace=None):
+    """Log probabilities of token [B][A] under rows node [B][A] (None: row a, A = N) of target_logits [B][N][V],
+    the rows' entropies (nats) and their top_n tokens.  A walk's acc_nodes and emitted fit as node and token."""
+    lib = _gpu()
+    B, N, V = target_logits.shape
+    A = token.shape[1]
+    dt, dev = target_logits.dtype, _here(target_logits, "target_logits")
+    if dt not in _DT:
+        raise DDTError(f"target_logits has dtype {dt}, expected one of {list(_DT)}")
+    _need_on(dev, target_logits, (B, N, V), dt, "target_logits")
+    _need_on(dev, token, (B, A), torch.int32, "token")
+    if node is not None:
+        _need_on(dev, node, (B, A), torch.int32, "node")
+    elif A != N:
+        raise DDTError(f"token has {A} entries a request, expected {N} (one a row) without node")
+    top_n = int(top_n)
+    want = {"logprob": ((B, A), torch.float32), "entropy": ((B, A), torch.float32),
+            "status": ((B, A), torch.int32)}
+    if top_n > 0:
+        want["top_token"] = ((B, A, top_n), torch.int32)
+        want["top_logprob"] = ((B, A, top_n), torch.float32)
+    o = out or {}
+    res = {}
+    for name, (shape, dtype) in want.items():
+        t = o.get(name)
+        res[name] = _need_on(dev, t, shape, dtype, name) if t is not None else torch.empty(shape, dtype=dtype, device=dev)
+    if workspace is None:
+        workspace = token_logprobs_workspace(target_logits, token, top_n=top_n)
+    rc = lib.ddt_token_logprobs(B, N, V, A, top_n, float(temperature), _DT[dt], _ptr(target_logits), _ptr(node),
+                                _ptr(token), _ptr(res["logprob"]), _ptr(res["entropy"]), _ptr(res.get("top_token")),
+                                _ptr(res.get("top_logprob")), _ptr(res["status"]), _ptr(workspace),
+                                _ws_bytes(dev, workspace), _stream())
+    _check(rc, "ddt_token_logprobs")
     return res
