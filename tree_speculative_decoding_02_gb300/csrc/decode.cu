@@ -6,7 +6,8 @@
 // a head instead of a tree of them, so nothing is left to share a K/V row but the G query
 // heads of its kv head, and the call is bound by reading the cache once.
 //
-//   k_decode_simt   grid C: the tiles of a CTA's run, CUDA cores, any input type.
+//   k_decode_tc     grid C (decode_tc.cu): the tiles of a CTA's run on the tensor cores, bf16.
+//   k_decode_simt   grid C: the same on the CUDA cores, fp32.
 //   k_decode_join   grid L B Hq: joins a head's partials with the new token's own row:
 //                   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 //   k_decode_weight grid (L B Hkv, y): adds sum_h 2^(t_h(p) - M_h) / Z_h to the running sum
@@ -132,8 +133,9 @@ __global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams
             __syncthreads();
             // ---- softmax
             if (p.score) {
-                float* sc = p.score + ((((long long)w.l * p.B + w.b) * p.Hkv + g) * p.cap + y) * p.G + h0;
-                for (int e = tid; e < n * nh; e += kSimtThreads) sc[(long long)(e / nh) * p.G + e % nh] = s_p[e % nh][e / nh];
+                float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y;
+                for (int e = tid; e < kDecTile * nh; e += kSimtThreads)
+                    if (e % kDecTile < n) sc[(long long)(e / kDecTile) * p.cap + e % kDecTile] = s_p[e / kDecTile][e % kDecTile];
                 __syncthreads();
             }
             for (int h = warp; h < HBS; h += kSimtWarps) {
@@ -306,13 +308,13 @@ __global__ void __launch_bounds__(256) k_decode_weight(const DecodeParams p) {
     }
     if (__syncthreads_or(bad)) return;
     const int n = P + (p.k_new && P < p.cap ? 1 : 0);
-    const float* sc = p.score + lbg * p.cap * p.G;
+    const float* sc = p.score + (lb * p.Hq + (long long)g * p.G) * p.cap;
     float* wt = p.weight + lbg * p.cap;
     for (int r = blockIdx.y * blockDim.x + threadIdx.x; r < n; r += gridDim.y * blockDim.x) {
         float sum = 0.f;
         for (int h = 0; h < p.G; ++h) {
             const float4 st = s_stat[h];
-            const float t = r < P ? sc[(long long)r * p.G + h] : st.z;
+            const float t = r < P ? sc[(long long)h * p.cap + r] : st.z;
             sum = fmaf(tc::ex2(t - st.x), st.y, sum);
         }
         wt[r] += sum;
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(256) k_decode_weight(const DecodeParams p) {
 }
 
 // ------------------------------------------------------------------------------ host
+constexpr int kTcMaxCtas = 256;  // bounds the SM count from above
 static int simt_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -345,7 +348,6 @@ static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, uns
 }
 
 size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype in, bool weight) {
-    (void)in;
     DecodeParams p{};
     p.L = L;
     p.B = B;
@@ -354,7 +356,8 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
     p.G = Hq / Hkv;
     p.d = d;
     p.cap = cap;
-    return decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
+    return decode_tc_supported(d, in) ? decode_layout(p, decode_tc_heads(p.G, d), kTcMaxCtas, weight, nullptr)
+                                      : decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
 }
 
 template <typename T, int D, int HBS>
@@ -409,9 +412,17 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
     p.scale_log2 = scale * 1.4426950408889634f;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, static_cast<unsigned char*>(ws));
-    p.C = min(3 * sms, kSimtMaxCtas);
-    cudaError_t e = in == DDT_BF16 ? simt_d_go<__nv_bfloat16>(p, st) : simt_d_go<float>(p, st);
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    cudaError_t e;
+    if (decode_tc_supported(d, in)) {  // bf16: one persistent CTA an SM
+        p.C = sms < kTcMaxCtas ? sms : kTcMaxCtas;
+        decode_layout(p, decode_tc_heads(p.G, d), kTcMaxCtas, weight != nullptr, w);
+        e = launch_decode_tc(p, st);
+    } else {
+        p.C = 3 * sms < kSimtMaxCtas ? 3 * sms : kSimtMaxCtas;
+        decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, w);
+        e = simt_d_go<float>(p, st);
+    }
     if (e != cudaSuccess) return e;
     if (in == DDT_BF16) e = out == DDT_BF16 ? join_go<__nv_bfloat16, __nv_bfloat16>(p, st) : join_go<__nv_bfloat16, float>(p, st);
     else e = out == DDT_BF16 ? join_go<float, __nv_bfloat16>(p, st) : join_go<float, float>(p, st);

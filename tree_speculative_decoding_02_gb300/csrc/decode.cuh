@@ -39,7 +39,7 @@ struct DecodeParams {
     float2* part_ml;  // [U + C][HT] (reference in log2 units, sum); sum < 0: see kSeg*
     float* part_o;    // [U + C][HT][d]
     float4* stat;     // [L][B][Hq] (reference, 1 / sum, the new row's score, unused) of the joined softmax
-    float* score;     // [L B Hkv][cap][G] scores in log2 units (weight only)
+    float* score;     // [L][B][Hq][cap] scores in log2 units (weight only)
 };
 
 // values of a partial's sum that say why there is none
@@ -152,8 +152,8 @@ __device__ __forceinline__ long long dec_unit(const DecodeParams& p, const Decod
     return ((long long)w.l * p.B + w.b) * (p.Hkv * p.HB) + w.g;
 }
 
-cudaError_t launch_decode_join(const DecodeParams& p, ddt_dtype in, ddt_dtype out, cudaStream_t st);
 bool decode_tc_supported(int d, ddt_dtype in);
-cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
+int decode_tc_heads(int G, int d);
+cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st);
 
 }  // namespace ddt
