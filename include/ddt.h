@@ -490,7 +490,8 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
  *     request of the call (an eviction in place would change the other's rows).  Such a
  *     request is left as it is.
  * keep >= 1, n_sink + n_recent <= keep; page_size as in ddt_tree_attn_paged; rows of any
- * d whose bytes are a multiple of 16 (up to 16384); pages 16-byte aligned.
+ * d whose bytes are a multiple of 16 (up to 16384), num_pages * page_size < 2^31; pages,
+ * attn_weight and row_pos 16-byte aligned.
  * workspace: ddt_evict_paged_workspace(...) bytes, 16-byte aligned.
  * ------------------------------------------------------------------------------- */
 size_t ddt_evict_paged_workspace(int n_layers, int B, int Hkv, int page_size, int num_pages,
@@ -521,9 +522,10 @@ ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, i
  *     -inf (outputs NaN, top_token -1); DDT_ERR_INVALID_ARG for node >= N or token >= V
  *     (outputs as for padding).
  * Precision: terms by the hardware base-2 exponential (relative error about 2^-22), summed
- * in fp32 within 2048 entries and in fp64 across them; logprob and entropy carry an
- * absolute error of about 1e-6.  The same inputs give the same bits.
- * temperature > 0 with a finite fp32 reciprocal; 0 <= top_n <= min(32, V); V <= 2^30.
+ * in fp32 (32 at a time a thread, then pairwise); logprob and entropy carry an absolute
+ * error of about 1e-6.  The same inputs give the same bits.
+ * temperature > 0 with log2(e) / temperature finite in fp32; 0 <= top_n <= min(32, V);
+ * V <= 2^30 and B * A * (V / 1024 + 2) < 2^31.
  * workspace: ddt_token_logprobs_workspace(B, A, V, top_n) bytes, 16-byte aligned.
  * ------------------------------------------------------------------------------- */
 size_t ddt_token_logprobs_workspace(int B, int A, int V, int top_n);

@@ -452,14 +452,14 @@ ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, i
         return DDT_ERR_INVALID_ARG;
     const long row_bytes = (long)d * (kv_dtype == DDT_BF16 ? 2 : 4);
     if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
-        row_bytes % 16 != 0 || row_bytes > 16384)
+        row_bytes % 16 != 0 || row_bytes > 16384 || (long)num_pages * page_size > 0x7fffffffL)
         return DDT_ERR_UNSUPPORTED;
     if (!block_table || !k_pages || !v_pages || !seq_len || !attn_weight || !row_pos || !prefix_len || !n_placed ||
         !status || !workspace)
         return DDT_ERR_INVALID_ARG;
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
     if (ws_bytes < evict_ws_bytes(n_layers, B, Hkv, pg) || !aligned16(workspace) || !aligned16(k_pages) ||
-        !aligned16(v_pages))
+        !aligned16(v_pages) || !aligned16(attn_weight) || !aligned16(row_pos))
         return DDT_ERR_INVALID_ARG;
     return from_cuda(launch_evict(n_layers, B, Hkv, (int)row_bytes, pg, keep, n_sink, n_recent, k_pages, v_pages, seq_len,
                                   attn_weight, row_pos, prefix_len, n_placed, status, workspace,
@@ -477,10 +477,13 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
                               float* entropy, int32_t* top_token, float* top_logprob, int32_t* status, void* workspace,
                               size_t ws_bytes, ddt_stream_t stream) {
     if (B < 1 || N < 1 || V < 1 || A < 1 || top_n < 0 || !dtype_ok(dtype)) return DDT_ERR_INVALID_ARG;
-    if (!(temperature > 0.0f) || !(1.0f / temperature < INFINITY) || !(temperature < INFINITY))
+    // T > 0 with log2(e) / T finite in fp32 (the kernels scale by it)
+    if (!(temperature > 0.0f) || !((float)(1.4426950408889634 / (double)temperature) < INFINITY) ||
+        !(temperature < INFINITY))
         return DDT_ERR_INVALID_ARG;
     if (!node && A != N) return DDT_ERR_INVALID_ARG;
-    if (top_n > kMaxTopK || top_n > V || (long)B * A > 0x7fffffffL || V > (1 << 30)) return DDT_ERR_UNSUPPORTED;
+    if (top_n > kMaxTopK || top_n > V || V > (1 << 30) || (long)B * A > 0x7fffffffL / (V / 1024 + 2))
+        return DDT_ERR_UNSUPPORTED;
     if (!target_logits || !token || !logprob || !status || !workspace || (top_n > 0 && (!top_token || !top_logprob)))
         return DDT_ERR_INVALID_ARG;
     if (ws_bytes < logprobs_ws_bytes(B, A, V, top_n) || !aligned16(workspace)) return DDT_ERR_INVALID_ARG;

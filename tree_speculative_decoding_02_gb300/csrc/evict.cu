@@ -20,9 +20,8 @@
 namespace ddt {
 
 namespace {
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;             // bins of a histogram pass (the last one uses 1024)
+constexpr int kSelCache = 45 * 1024;    // rows whose keys fit in shared memory
 constexpr int kEvict = -1;  // state of a request that is over its budget
 
 struct EvictParams {
@@ -72,13 +71,15 @@ __global__ void __launch_bounds__(256) k_evict_claim(const EvictParams p) {
 // The order of the rows as an unsigned key: 0 for NaN, then the sums from the smallest to
 // the largest (-0 and +0 alike), and above them all the protected positions.
 __device__ __forceinline__ uint32_t evict_key(const EvictParams& p, float w, int pos, int sq) {
-    if (pos < p.n_sink || pos >= sq - p.n_recent) return 0xffffffffu;
-    if (w != w) return 0u;
+    // n_sink <= seq_len - n_recent: both fit in the budget, which the sequence is longer than
+    if ((uint32_t)(pos - p.n_sink) >= (uint32_t)(sq - p.n_recent - p.n_sink)) return 0xffffffffu;
     const uint32_t u = __float_as_uint(w + 0.f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return w != w ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the block and the total; the caller's shared array.
+// Exclusive prefix sum of v over the block and the total, with one barrier: the caller
+// alternates between two arrays of warp sums.
+template <int NT>
 __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = v;
@@ -87,120 +88,257 @@ __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
         const int up = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += up;
     }
-    __syncthreads();  // the array's last use is over
     if (lane == 31) s_w[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        int x = lane < kSelWarps ? s_w[lane] : 0;
+    int x = lane < NT / 32 ? s_w[lane] : 0;  // every warp sums up the warps for itself
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(kFull, x, o);
-            if (lane >= o) x += up;
-        }
-        s_w[lane] = x;
+    for (int o = 1; o < NT / 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += up;
     }
-    __syncthreads();
-    total = s_w[kSelWarps - 1];
-    return incl - v + (warp ? s_w[warp - 1] : 0);
+    total = __shfl_sync(kFull, x, NT / 32 - 1);
+    const int before = __shfl_sync(kFull, x, warp ? warp - 1 : 0);
+    return incl - v + (warp ? before : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictParams p) {
+// CACHED: the unit's keys are kept in shared memory after the first pass.  The histogram
+// passes take four consecutive rows a thread.
+template <int NT, bool CACHED>
+__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const EvictParams p) {
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ int s_hist[kBins];
-    __shared__ int s_w[32];
-    __shared__ int s_bin, s_rest;
+    __shared__ uint4 s_bits[NT];
+    __shared__ int s_w[2][32];
+    __shared__ int s_bin, s_rest, s_count, s_zeros, s_safe;
     const long long u = blockIdx.x;
     const int b = (int)(u / p.Hkv % p.B);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.state[b] != kEvict) {
         if (tid == 0) p.n_move[u] = 0;
         return;
     }
     const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b], K = p.keep;
-    int twice = 0;
-    for (int i = tid; i < (P + p.page_rows - 1) / p.page_rows; i += kSelThreads)
-        twice |= p.uses[p.block_table[(long long)b * p.max_pages + i]] > 1;
-    if (__syncthreads_or(twice)) {
-        if (tid == 0) {
-            p.n_move[u] = 0;
-            p.shared[b] = 1;
-        }
-        return;
-    }
     float* wt = p.weight + u * p.cap;
     int32_t* rp = p.row_pos + u * p.cap;
+    const int32_t* table = p.block_table + (long long)b * p.max_pages;
+    int twice = 0;  // looked at after the first pass
+    for (int i = tid; i < (P + p.page_rows - 1) / p.page_rows; i += NT) twice |= p.uses[table[i]] > 1;
+    for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
+    if (tid == 0) s_zeros = s_safe = 0;
+    __syncthreads();
     auto pos_of = [&](int i) { return i < np ? rp[i] : sq - P + i; };
-    // ---- the K-th largest key: its bits from the highest down
-    uint32_t prefix = 0;
-    int rest = K;  // how many of the keys with this prefix are kept
-    const int shift[3] = {21, 10, 0};
+    // the keys of rows i .. i + 3 (rows >= P: any)
+    auto keys4 = [&](int i, uint32_t (&key)[4]) {
+        const float4 w = *reinterpret_cast<const float4*>(wt + i);
+        int4 r = make_int4(0, 0, 0, 0);
+        if (i < np) r = *reinterpret_cast<const int4*>(rp + i);
+        const float ww[4] = {w.x, w.y, w.z, w.w};
+        const int rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) key[q] = evict_key(p, ww[q], i + q < np ? rr[q] : sq - P + i + q, sq);
+    };
+    auto key_of = [&](int i) { return CACHED ? s_key[i] : evict_key(p, wt[i], pos_of(i), sq); };
+    // ---- the K-th largest key: its bits from the highest down.  Kept are the rows above
+    //      `limit` and the first `rest` that equal it.
+    uint32_t limit = 0;
+    int rest = K;
+    bool tie = false;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int sh = shift[pass], nb = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+        const int sh = pass == 0 ? 21 : (pass == 1 ? 10 : 0), up = pass == 1 ? 21 : 10;
+        const uint32_t mask = pass == 2 ? 1023 : 2047;
+        int zeros = 0, safe = 0;  // the two keys that many rows share: counted in registers
+#pragma unroll 2
+        for (int i = tid * 4; i < P; i += NT * 4) {
+            uint32_t key[4];
+            if (CACHED && pass > 0) {
+                const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+                key[0] = k.x;
+                key[1] = k.y;
+                key[2] = k.z;
+                key[3] = k.w;
+            } else {
+                keys4(i, key);
+                if (CACHED) *reinterpret_cast<uint4*>(s_key + i) = make_uint4(key[0], key[1], key[2], key[3]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (i + q >= P || (pass > 0 && (key[q] >> up) != limit)) continue;
+                if (key[q] == 0x80000000u) ++zeros;
+                else if (key[q] == 0xffffffffu) ++safe;
+                else atomicAdd(&s_hist[(key[q] >> sh) & mask], 1);
+            }
+        }
+        zeros = __reduce_add_sync(kFull, zeros);
+        safe = __reduce_add_sync(kFull, safe);
+        if (lane == 0) {
+            if (zeros) {
+                atomicAdd(&s_hist[(0x80000000u >> sh) & mask], zeros);
+                if (pass == 0) atomicAdd(&s_zeros, zeros);
+            }
+            if (safe) {
+                atomicAdd(&s_hist[(0xffffffffu >> sh) & mask], safe);
+                if (pass == 0) atomicAdd(&s_safe, safe);
+            }
+        }
+        if (__syncthreads_or(pass == 0 && twice)) {
+            if (tid == 0) {
+                p.n_move[u] = 0;
+                p.shared[b] = 1;
+            }
+            return;
+        }
+        // warp i has the i-th run of bins from the top, and only the warp whose run holds the
+        // K-th largest looks closer
+        constexpr int kPer = kBins / NT;
+        const int top = kBins - 1 - warp * (kBins / (NT / 32)) - lane;
+        int c[kPer], sum = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            c[q] = s_hist[top - 32 * q];
+            s_hist[top - 32 * q] = 0;  // for the next pass
+            sum += c[q];
+        }
+        sum = __reduce_add_sync(kFull, sum);
+        if (lane == 0) s_w[pass & 1][warp] = sum;
         __syncthreads();
-        for (int i = tid; i < P; i += kSelThreads) {
-            const uint32_t key = evict_key(p, wt[i], pos_of(i), sq);
-            const bool in = pass == 0 || (key >> shift[pass - 1]) == prefix;
-            if (in) atomicAdd(&s_hist[(key >> sh) & (nb - 1)], 1);
+        int above = __reduce_add_sync(kFull, lane < warp ? s_w[pass & 1][lane] : 0);
+        if (above < rest && above + sum >= rest) {
+#pragma unroll 1
+            for (int q = 0; q < kPer; ++q) {
+                int here = c[0];
+#pragma unroll
+                for (int r = 1; r < kPer; ++r) here = q == r ? c[r] : here;
+                int incl = here;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up1 = __shfl_up_sync(kFull, incl, o);
+                    if (lane >= o) incl += up1;
+                }
+                const int excl = above + incl - here;
+                if (excl < rest && excl + here >= rest) {
+                    s_bin = top - 32 * q;
+                    s_rest = rest - excl;
+                    s_count = here;
+                }
+                above = __shfl_sync(kFull, above + incl, 31);
+                if (above >= rest) break;
+            }
         }
         __syncthreads();
-        // thread i looks at bins nb - 1 - 2 i and the one below: an exclusive sum from the top
-        const int hi = kBins - 1 - 2 * tid;
-        const int c0 = s_hist[hi], c1 = s_hist[hi - 1];
-        int total;
-        const int above = block_scan(c0 + c1, s_w, total);
-        if (above < rest && above + c0 >= rest) {
-            s_bin = hi;
-            s_rest = rest - above;
-        } else if (above + c0 < rest && above + c0 + c1 >= rest) {
-            s_bin = hi - 1;
-            s_rest = rest - above - c0;
-        }
-        __syncthreads();
-        prefix = pass == 0 ? (uint32_t)s_bin : (prefix << (pass == 2 ? 10 : 11)) | (uint32_t)s_bin;
+        limit = pass == 0 ? (uint32_t)s_bin : (limit << (pass == 2 ? 10 : 11)) | (uint32_t)s_bin;
         rest = s_rest;
-        __syncthreads();
+        tie = s_count > rest;
+        if (!tie) {  // all of this prefix stay
+            limit = (limit << sh) - 1u;
+            rest = 0;
+            break;
+        }
+        if (pass == 0 && limit == 0x80000000u >> 21 && s_count == s_zeros) {
+            limit = 0x80000000u;
+            break;
+        }
+        if (pass == 0 && limit == 0xffffffffu >> 21 && s_count == s_safe) {
+            limit = 0xffffffffu;
+            break;
+        }
     }
-    // ---- kept: every key above the threshold and the first `rest` equal to it
+    // ---- in index order: holes below K, and the kept rows behind it that fill them.  A bit a
+    //      row (above the limit, equal to it) by ballots, a thread a word of 32 rows for the
+    //      counts, and a warp a word for the lists.
     int32_t* src = p.src + u * p.most;
     int32_t* dst = p.dst + u * p.most;
-    int eq0 = 0, holes = 0, movers = 0;
-    for (int i0 = 0; i0 < P; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        uint32_t key = 0;
-        int pos = 0;
-        if (i < P) {
-            pos = pos_of(i);
-            key = evict_key(p, wt[i], pos, sq);
+    int eqs = 0, holes = 0, movers = 0;
+    for (int c0 = 0; c0 < P; c0 += 32 * NT) {
+        const int words = min(NT, (P - c0 + 31) / 32);
+#pragma unroll 4
+        for (int w = warp; w < words; w += NT / 32) {
+            const int i = c0 + w * 32 + lane;
+            const uint32_t key = i < P ? key_of(i) : 0u;  // no limit is below 0
+            const uint32_t gt = __ballot_sync(kFull, key > limit), eq = __ballot_sync(kFull, i < P && key == limit);
+            if (lane == 0) s_bits[w] = make_uint4(gt, eq, 0u, 0u);
         }
-        const int eq = i < P && key == prefix;
-        int n_eq;
-        const int before = block_scan(eq, s_w, n_eq);
-        const bool kept = i < P && (key > prefix || (eq && eq0 + before < rest));
-        eq0 += n_eq;
-        const int f = i >= P ? 0 : (i < K ? (kept ? 0 : 1) : (kept ? 1 << 16 : 0));
-        int both;
-        const int at = block_scan(f, s_w, both);
-        if (f == 1) dst[holes + (at & 0xffff)] = i;
-        if (f == 1 << 16) src[movers + (at >> 16)] = i;
-        if (i < K && i >= np && i < P) rp[i] = pos;
-        holes += both & 0xffff;
-        movers += both >> 16;
+        __syncthreads();
+        const uint4 x = tid < words ? s_bits[tid] : make_uint4(0u, 0u, 0u, 0u);
+        const int i = c0 + tid * 32;
+        uint32_t kept = x.x;
+        int total;
+        if (tie) {  // the first `rest` equal rows stay
+            const int before = eqs + block_scan<NT>(__popc(x.y), s_w[0], total);
+            eqs += total;
+            uint32_t eq = before < rest ? x.y : 0u;
+            while (__popc(eq) > rest - before && eq) eq &= ~(0x80000000u >> __clz(eq));
+            kept |= eq;
+        }
+        // the word's rows that exist, and those below K
+        const uint32_t live = P - i >= 32 ? ~0u : (P <= i ? 0u : (1u << (P - i)) - 1u);
+        const uint32_t low = K - i >= 32 ? ~0u : (K <= i ? 0u : (1u << (K - i)) - 1u);
+        const uint32_t hole = ~kept & live & low, mover = kept & ~low;
+        const int at = block_scan<NT>(__popc(hole) + (__popc(mover) << 16), s_w[1], total);
+        if (tid < words)
+            s_bits[tid] = make_uint4(hole, mover, (uint32_t)(holes + (at & 0xffff)), movers + ((uint32_t)at >> 16));
+        __syncthreads();
+#pragma unroll 4
+        for (int w = warp; w < words; w += NT / 32) {
+            const uint4 y = s_bits[w];
+            const int row = c0 + w * 32 + lane;
+            if (y.x >> lane & 1u) dst[y.z + __popc(y.x & ((1u << lane) - 1u))] = row;
+            if (y.y >> lane & 1u) src[y.w + __popc(y.y & ((1u << lane) - 1u))] = row;
+        }
+        holes += total & 0xffff;
+        movers += (int)((uint32_t)total >> 16);
+        __syncthreads();
     }
-    __syncthreads();
-    for (int j = tid; j < holes; j += kSelThreads) {
-        wt[dst[j]] = wt[src[j]];
-        rp[dst[j]] = pos_of(src[j]);
-    }
-    __syncthreads();
-    for (int i = K + tid; i < P; i += kSelThreads) {
-        wt[i] = 0.f;
-        rp[i] = -1;
-    }
+    for (int i = np + tid; i < K; i += NT) rp[i] = sq - P + i;
     if (tid == 0) p.n_move[u] = holes;
+    __syncthreads();
+    for (int j0 = tid; j0 < holes; j0 += 4 * NT) {  // four moves' loads are in flight
+        int s[4], d[4], pos[4], ps[4], pd[4];
+        float w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = j0 + q * NT < holes ? j0 + q * NT : j0;
+            s[q] = src[j];
+            d[q] = dst[j];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            w[q] = wt[s[q]];
+            pos[q] = pos_of(s[q]);
+            const int is = s[q] / p.page_rows, id = d[q] / p.page_rows;
+            ps[q] = table[is] * p.page_rows + s[q] - is * p.page_rows;
+            pd[q] = table[id] * p.page_rows + d[q] - id * p.page_rows;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = j0 + q * NT;
+            if (j >= holes) break;
+            wt[d[q]] = w[q];
+            rp[d[q]] = pos[q];
+            // from here on the lists hold places in the pages
+            src[j] = ps[q];
+            dst[j] = pd[q];
+        }
+    }
+    __syncthreads();
+    // rows K .. P - 1, four at a time but for the ends
+    const int k4 = min((K + 3) & ~3, P), p4 = max(P & ~3, k4);
+    for (int i = k4 + tid * 4; i < p4; i += NT * 4) {
+        *reinterpret_cast<float4*>(wt + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<int4*>(rp + i) = make_int4(-1, -1, -1, -1);
+    }
+    if (tid < 8) {
+        const int i = tid < 4 ? K + tid : p4 + tid - 4;
+        if (i < (tid < 4 ? k4 : P)) {
+            wt[i] = 0.f;
+            rp[i] = -1;
+        }
+    }
 }
 
-__global__ void __launch_bounds__(256) k_evict_move(const EvictParams p) {
+// A block moves 256 / pieces rows at a time, a thread 16 bytes of K and of V; the next
+// round's places are loaded while this one's rows are on their way.
+__global__ void __launch_bounds__(256, 8) k_evict_move(const EvictParams p) {
     const long long u = blockIdx.x;
     const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv % p.B), l = (int)(u / p.Hkv / p.B);
     if (l == 0 && g == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
@@ -212,19 +350,29 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictParams p) {
         p.status[b] = st != kEvict ? st : (p.shared[b] ? (int)DDT_ERR_INVALID_ARG : (int)DDT_OK);
     }
     const int n = p.n_move[u];
-    const int32_t* table = p.block_table + (long long)b * p.max_pages;
-    auto row = [&](int i) {
-        return ((((long long)l * p.num_pages + table[i / p.page_rows]) * p.Hkv + g) * p.page_rows + i % p.page_rows) *
-               p.pieces;
+    const int32_t* src = p.src + u * p.most;
+    const int32_t* dst = p.dst + u * p.most;
+    const int wide = min(p.pieces, 256), rows = 256 / wide, step = gridDim.y * rows;
+    int j = blockIdx.y * rows + threadIdx.x / wide;
+    if ((int)threadIdx.x >= rows * wide || j >= n) return;
+    const long long layer = (long long)l * p.num_pages;
+    // place -> 16-byte words: page * (Hkv * page_rows) + g * page_rows + row in the page
+    auto word = [&](int place) {
+        const int page = place / p.page_rows;
+        return (((layer + page) * p.Hkv + g) * p.page_rows + (place - page * p.page_rows)) * p.pieces;
     };
-    const long long all = (long long)n * p.pieces;
-    for (long long e = (long long)blockIdx.y * blockDim.x + threadIdx.x; e < all; e += (long long)gridDim.y * blockDim.x) {
-        const long long j = e / p.pieces;
-        const int c = (int)(e % p.pieces);
-        const long long from = row(p.src[u * p.most + j]) + c, to = row(p.dst[u * p.most + j]) + c;
-        const uint4 k = p.k_pages[from], v = p.v_pages[from];
-        p.k_pages[to] = k;
-        p.v_pages[to] = v;
+    int s = src[j], d = dst[j];
+    for (; j < n; j += step) {
+        const bool more = j + step < n;
+        const int s1 = more ? src[j + step] : 0, d1 = more ? dst[j + step] : 0;
+        const long long from = word(s), to = word(d);
+        for (int c = threadIdx.x % wide; c < p.pieces; c += wide) {
+            const uint4 k = p.k_pages[from + c], v = p.v_pages[from + c];
+            p.k_pages[to + c] = k;
+            p.v_pages[to + c] = v;
+        }
+        s = s1;
+        d = d1;
     }
 }
 
@@ -257,6 +405,14 @@ size_t evict_ws_bytes(int L, int B, int Hkv, const AttnPaging& pg) {
     p.num_pages = pg.num_pages;
     p.cap = pg.page_rows * pg.max_pages;
     return evict_layout(p, nullptr);
+}
+
+template <int NT>
+static cudaError_t select_go(const EvictParams& p, unsigned units, int keys, cudaStream_t st) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_evict_select<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
+    if (e == cudaSuccess) k_evict_select<NT, true><<<counted(units), NT, keys, st>>>(p);
+    return e;
 }
 
 cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging& pg, int keep, int n_sink,
@@ -292,10 +448,16 @@ cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging&
     const unsigned units = (unsigned)L * B * Hkv;
     k_evict_claim<<<counted(B), 256, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_evict_select<<<counted(units), kSelThreads, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long pieces = (long long)p.most * p.pieces;
-    const unsigned most = (unsigned)((pieces + 255) / 256), want = 8u * sms / units + 1;
+    // few units or long caches: many threads a unit, for its latency; else small blocks, so
+    // that several units share an SM and hide each other's barriers
+    const bool wide = units <= 2u * sms || p.cap > 8192, cached = p.cap <= kSelCache;
+    const int keys = cached ? (p.cap + 3) / 4 * 16 : 0;
+    if (!cached) k_evict_select<1024, false><<<counted(units), 1024, 0, st>>>(p);
+    else if (wide) e = select_go<1024>(p, units, keys, st);
+    else e = select_go<256>(p, units, keys, st);
+    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rows = 256 / (p.pieces < 256 ? p.pieces : 256);  // a block's
+    const unsigned most = (unsigned)((p.most + rows - 1) / rows), want = 8u * sms / units + 1;
     k_evict_move<<<counted(dim3(units, most < 1 ? 1 : (most < want ? most : want))), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
