@@ -446,8 +446,8 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, max_pages * page_size],
  *     DDT_ERR_INVALID_ARG if a block-table entry that the prefix needs is outside
  *     [0, num_pages); the request's output rows are then zero and its sums unchanged.
- * d in {64, 128, 256}; fp32 and bf16; Hq / Hkv <= 1024; q, k_new, v_new, the pages and o
- * 16-byte aligned.  The same inputs give the same bits.
+ * d in {64, 128, 256}; fp32 and bf16; Hq / Hkv <= 1024; q, k_new, v_new, the pages, o and
+ * attn_weight 16-byte aligned.  The same inputs give the same bits.
  * workspace: ddt_decode_attn_paged_workspace(...) bytes (want_weight: 1 with attn_weight,
  * then 4 * L * B * Hq * capacity bytes of it hold scores), 16-byte aligned.
  * ------------------------------------------------------------------------------- */

@@ -100,6 +100,58 @@ def test_ties_and_masks(dtype):
     assert _run(logits, token)["logprob"][0, 6] == float("-inf")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,N,V", [(1, 1031, 2500), (3, 500, 4099), (2, 2300, 129)])
+def test_many_rows(dtype, B, N, V):
+    """Calls of many rows (shared out over persistent warps): more rows than are listed, rows of a
+    few units cut anywhere."""
+    logits = _logits(49, B, N, V, dtype)
+    token = torch.randint(0, V, (B, N), generator=synth.gen(49, 91)).to(torch.int32)
+    _check(_run(logits, token, top_n=7, temperature=0.9), logits, token, top_n=7, T=0.9)
+
+
+@pytest.mark.parametrize("B", [20, 90])
+def test_many_padded_rows(B):
+    """Walks of many requests, most of whose entries are padding, some without a token, one that
+    names no row and one that names no token; rows of no request hold NaN."""
+    N, V, A = 60, 3001, 60
+    g = synth.gen(50, 90)
+    logits = _logits(50, B, N, V, BF)
+    node = torch.full((B, A), -1, dtype=torch.int32)
+    token = torch.full((B, A), -1, dtype=torch.int32)
+    for b in range(B):
+        n = b % 9
+        node[b, :n] = torch.randperm(N, generator=g)[:n].to(torch.int32)
+        token[b, :n] = torch.randint(-1, V, (n,), generator=g).to(torch.int32)
+        unused = torch.ones(N, dtype=torch.bool)
+        unused[node[b, :n].long()] = False
+        logits[b, unused] = float("nan")
+    r = _run(logits, token, node=node, top_n=3)
+    _check(r, logits, token, node, 3)
+    node[3, 0], token[4, 1] = N, V
+    r = _run(logits, token, node=node, top_n=3)
+    assert r["status"][3, 0] == 1 and r["status"][4, 1] == 1 and int(r["status"].sum()) == 2
+    assert r["logprob"][3, 0] == 0 and (r["top_token"][4, 1] == -1).all()
+
+
+def test_many_masked_rows():
+    """The ties of test_ties_and_masks in a call of many rows."""
+    V, N = 6001, 1100
+    logits = torch.full((1, N, V), float("-inf"), dtype=BF)
+    g = synth.gen(51, 90)
+    for i in range(N):
+        k = i % 40
+        at = torch.randperm(V, generator=g)[:k + 1]
+        logits[0, i, at] = torch.randint(0, 3, (k + 1,), generator=g).to(BF)
+    logits[0, 5] = 2.0
+    logits[0, 7] = float("-inf")
+    token = logits[0].float().argmax(-1).to(torch.int32)[None]
+    r = _run(logits, token, top_n=20)
+    assert r["status"][0, 7] == 6 and int((r["status"] != 0).sum()) == 1
+    keep = torch.arange(N) != 7
+    _check({k: v[:, keep] for k, v in r.items()}, logits[:, keep], token[:, keep], top_n=20)
+
+
 def test_statuses():
     V = 500
     logits = _logits(45, 1, 7, V, F32)

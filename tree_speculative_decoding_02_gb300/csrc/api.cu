@@ -428,7 +428,7 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
         !aligned16(workspace))
         return DDT_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
-        !aligned16(o))
+        !aligned16(o) || !aligned16(attn_weight))
         return DDT_ERR_INVALID_ARG;
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
     return from_cuda(launch_decode(n_layers, B, Hq, Hkv, d, pg, in_dtype, out_dtype, q, k_new, v_new, k_pages, v_pages,

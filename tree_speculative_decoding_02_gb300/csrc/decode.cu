@@ -8,10 +8,10 @@
 //
 //   k_decode_tc     grid C (decode_tc.cu): the tiles of a CTA's run on the tensor cores, bf16.
 //   k_decode_simt   grid C: the same on the CUDA cores, fp32.
-//   k_decode_join   grid L B Hq: joins a head's partials with the new token's own row:
-//                   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-//   k_decode_weight grid (L B Hkv, y): adds sum_h 2^(t_h(p) - M_h) / Z_h to the running sum
-//                   of row p's attention weights, from the scores the split kernel left.
+//   k_decode_finish join: a head's partials with the new token's own row,
+//                     O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s;
+//                   and, from the scores the split kernel left, sum_h 2^(t_h(p) - M_h) / Z_h
+//                   added to the running sum of row p's attention weights.
 #include <math.h>
 
 #include "decode.cuh"
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams
     const T* kp = static_cast<const T*>(p.k_pages);
     const T* vp = static_cast<const T*>(p.v_pages);
     DecodeWalk w = dec_plan<kSimtThreads>(p);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_decode_finish may be set up
     for (; w.left > 0; dec_next(p, w)) {
         const int g = w.g / p.HB, h0 = (w.g % p.HB) * HBS, nh = min(HBS, p.G - h0);
         const T* q = static_cast<const T*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D;
@@ -204,125 +205,170 @@ __global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams
     }
 }
 
-template <typename Tin, typename Tout, int D>
-__global__ void __launch_bounds__(D) k_decode_join(const DecodeParams p) {
-    __shared__ float s_w[256 / 32 * 2];
-    __shared__ float s_seg[1024];  // factors of up to 1024 segments at a time
-    const int hq = blockIdx.x % p.Hq;
-    const long long lb = blockIdx.x / p.Hq;
-    const int b = (int)(lb % p.B);
+// One head's joined softmax, by one warp.
+struct HeadJoin {
+    float ref, z, tn;  // reference, sum, the new row's score (log2 units)
+    int err;           // a status for the request, or DDT_OK
+    int ns;            // segments, from slot `first` on
+    long long first;
+};
+
+template <typename Tin, int D>
+__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, long long lb, int hq, int lane) {
+    const int b = (int)(lb % p.B), P = p.prefix_len[b];
+    HeadJoin j;
+    j.ref = j.z = 0.f;
+    j.tn = -INFINITY;
+    j.ns = 0;
+    j.first = 0;
+    j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
+    if (j.err) return j;
     const int g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
-    const int c = threadIdx.x, lane = c & 31, warp = c >> 5;
-    const int P = p.prefix_len[b];
-    Tout* out = static_cast<Tout*>(p.o) + (lb * p.Hq + hq) * D + c;
-    float4* stat = p.stat + lb * p.Hq + hq;
-    if (P < 0 || P > p.cap) {
-        *out = from_f32<Tout>(0.f);
-        if (c == 0) *stat = make_float4(0.f, -1.f, 0.f, 0.f);
-        return;
-    }
-    // the new token's own row
-    float tn = -INFINITY;
     if (p.k_new) {
-        float s = to_f32(static_cast<const Tin*>(p.q)[(lb * p.Hq + hq) * D + c]) *
-                  to_f32(static_cast<const Tin*>(p.k_new)[(lb * p.Hkv + g) * D + c]);
-        s = warp_sum(s);
-        if (lane == 0) s_w[warp] = s;
-        __syncthreads();
-        s = 0.f;
+        const Tin* q = static_cast<const Tin*>(p.q) + (lb * p.Hq + hq) * D;
+        const Tin* k = static_cast<const Tin*>(p.k_new) + (lb * p.Hkv + g) * D;
+        float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) s += s_w[w];
-        tn = s * p.scale_log2;
+        for (int e = lane; e < D; e += 32) s = fmaf(to_f32(q[e]), to_f32(k[e]), s);
+        j.tn = warp_sum(s) * p.scale_log2;
     }
-    // this unit's segments: CTAs c0 .. c1
-    const int HH = p.Hkv * p.HB;
-    const long long unit = lb * HH + g * p.HB + hb;
-    const long long all = p.pre[p.B], T = all * HH * p.L;
     const int nt = dec_tiles(P, p.cap);
-    int c0 = 0, ns = 0;
     if (nt > 0) {
+        const int HH = p.Hkv * p.HB;
+        const long long all = p.pre[p.B], T = all * HH * p.L;
         const long long first = (lb / p.B) * all * HH + p.pre[b] * HH + (long long)(g * p.HB + hb) * nt;
-        const int C = (int)min((long long)p.C, T);
-        c0 = dec_owner(T, C, first);
-        ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
+        const int C = (int)min((long long)p.C, T), c0 = dec_owner(T, C, first);
+        j.ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
+        j.first = lb * HH + g * p.HB + hb + c0;
     }
-    const float2* ml = p.part_ml + (unit + c0) * p.HT + h;
-    float M = tn, lmin = 0.f;
-    for (int s = c; s < ns; s += D) {
+    const float2* ml = p.part_ml + j.first * p.HT + h;
+    float m = j.tn, low = 0.f;
+    for (int s = lane; s < j.ns; s += 32) {
         const float2 v = ml[(long long)s * p.HT];
-        M = fmaxf(M, v.x);
-        lmin = fminf(lmin, v.y);
+        m = fmaxf(m, v.x);
+        low = fminf(low, v.y);
     }
-    M = warp_max(M);
-    lmin = -warp_max(-lmin);
-    __syncthreads();
-    if (lane == 0) {
-        s_w[warp] = M;
-        s_w[8 + warp] = lmin;
+    m = warp_max(m);
+    low = -warp_max(-low);
+    if (low < 0.f) j.err = low == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG;
+    j.ref = m == -INFINITY ? 0.f : m;
+    float z = 0.f;
+    for (int s = lane; s < j.ns; s += 32) {
+        const float2 v = ml[(long long)s * p.HT];
+        z = fmaf(tc::ex2(v.x - j.ref), v.y, z);
     }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-        M = fmaxf(M, s_w[w]);
-        lmin = fminf(lmin, s_w[8 + w]);
-    }
-    if (lmin < 0.f) {
-        *out = from_f32<Tout>(0.f);
-        if (c == 0) {
-            *stat = make_float4(0.f, -1.f, 0.f, 0.f);
-            p.status[b] = lmin == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG;
-        }
-        return;
-    }
-    const float ref = M == -INFINITY ? 0.f : M;
-    const float wn = tc::ex2(tn - ref);
-    float z = wn, acc = p.k_new ? wn * to_f32(static_cast<const Tin*>(p.v_new)[(lb * p.Hkv + g) * D + c]) : 0.f;
-    const float* po = p.part_o + ((unit + c0) * p.HT + h) * D + c;
-    for (int s0 = 0; s0 < ns; s0 += 1024) {
-        const int n = min(1024, ns - s0);
-        __syncthreads();
-        for (int s = c; s < n; s += D) s_seg[s] = tc::ex2(ml[(long long)(s0 + s) * p.HT].x - ref);
-        __syncthreads();
-#pragma unroll 8
-        for (int s = 0; s < n; ++s) {
-            z = fmaf(s_seg[s], ml[(long long)(s0 + s) * p.HT].y, z);
-            acc = fmaf(s_seg[s], po[(long long)(s0 + s) * p.HT * D], acc);
-        }
-    }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
-    *out = from_f32<Tout>(z != z ? z : acc * inv);
-    if (c == 0) *stat = make_float4(ref, inv, tn, 0.f);
+    j.z = warp_sum(z) + tc::ex2(j.tn - j.ref);
+    return j;
 }
 
-__global__ void __launch_bounds__(256) k_decode_weight(const DecodeParams p) {
-    extern __shared__ float4 s_stat[];
-    const long long lbg = blockIdx.x;
+// Blocks below n_join: WPH warps a head (1, or 8 where a head has many segments), O of the
+// head.  The others: the weight sums of 1024 rows at a time of one (layer, request, kv head).
+template <typename Tin, typename Tout, int D, int WPH>
+__global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, unsigned n_join, int chunks) {
+    constexpr int E = D / 32;
+    extern __shared__ float s_x[];  // [8][D] sums of the warps of a head, or 3 floats a head of a group
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the partials are there from here on
+    if (blockIdx.x < n_join) {
+        const long long x = WPH == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
+        const long long lb = x / p.Hq;
+        const int hq = (int)(x % p.Hq);
+        if (x >= (long long)p.L * p.B * p.Hq) return;  // (WPH 1: whole warps, no barrier follows)
+        const HeadJoin j = head_join<Tin, D>(p, lb, hq, lane);
+        Tout* out = static_cast<Tout*>(p.o) + x * D;
+        if (j.err) {
+            if (WPH == 1 || warp == 0) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(0.f);
+                if (lane == 0) p.status[lb % p.B] = j.err;
+            }
+            return;  // (WPH 8: all warps)
+        }
+        const int g = hq / p.G, h = (hq % p.G) % p.hbs;
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        if (p.k_new && (WPH == 1 || warp == 0)) {
+            const float w = tc::ex2(j.tn - j.ref);
+            const Tin* v = static_cast<const Tin*>(p.v_new) + (lb * p.Hkv + g) * D;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = w * to_f32(v[e * 32 + lane]);
+        }
+        const float2* ml = p.part_ml + j.first * p.HT + h;
+        const float* po = p.part_o + (j.first * p.HT + h) * D;
+#pragma unroll 4
+        for (int s = WPH == 1 ? 0 : warp; s < j.ns; s += WPH) {
+            const float f = tc::ex2(ml[(long long)s * p.HT].x - j.ref);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, po[(long long)s * p.HT * D + e * 32 + lane], acc[e]);
+        }
+        const float inv = j.z > 0.f ? 1.f / j.z : j.z;  // no rows at all: 0; NaN stays
+        if (WPH == 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(acc[e] * inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_x[warp * D + e * 32 + lane] = acc[e];
+            __syncthreads();
+            if (tid < D) {
+                float o = s_x[tid];
+#pragma unroll
+                for (int w = 1; w < 8; ++w) o += s_x[w * D + tid];
+                out[tid] = from_f32<Tout>(o * inv);
+            }
+        }
+        return;
+    }
+    const unsigned y = blockIdx.x - n_join;
+    const long long lbg = y / chunks;
     const int g = (int)(lbg % p.Hkv);
     const long long lb = lbg / p.Hkv;
-    const int P = p.prefix_len[lb % p.B];
-    const float4* stat = p.stat + lb * p.Hq + g * p.G;
-    int bad = P < 0 || P > p.cap;
-    for (int h = threadIdx.x; h < p.G; h += blockDim.x) {
-        s_stat[h] = stat[h];
-        bad |= s_stat[h].y < 0.f;
+    float* s_ref = s_x;
+    float* s_inv = s_ref + p.G;
+    float* s_tn = s_inv + p.G;
+    int bad = 0;
+    for (int h = warp; h < p.G; h += 8) {
+        const HeadJoin j = head_join<Tin, D>(p, lb, g * p.G + h, lane);
+        bad |= j.err;
+        if (lane == 0) {
+            s_ref[h] = j.ref;
+            s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
+            s_tn[h] = j.tn;
+        }
     }
     if (__syncthreads_or(bad)) return;
-    const int n = P + (p.k_new && P < p.cap ? 1 : 0);
+    const int P = p.prefix_len[lb % p.B];
     const float* sc = p.score + (lb * p.Hq + (long long)g * p.G) * p.cap;
     float* wt = p.weight + lbg * p.cap;
-    for (int r = blockIdx.y * blockDim.x + threadIdx.x; r < n; r += gridDim.y * blockDim.x) {
-        float sum = 0.f;
-        for (int h = 0; h < p.G; ++h) {
-            const float4 st = s_stat[h];
-            const float t = r < P ? sc[(long long)h * p.cap + r] : st.z;
-            sum = fmaf(tc::ex2(t - st.x), st.y, sum);
+    for (int r = ((int)(y % chunks) * 256 + tid) * 4; r < P; r += chunks * 1024) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int h = 0; h < p.G; ++h) {  // the rows are padded to whole pages: r + 3 < cap
+            const float4 t = *reinterpret_cast<const float4*>(sc + (long long)h * p.cap + r);
+            const float ref = s_ref[h], inv = s_inv[h];
+            sum.x = fmaf(tc::ex2(t.x - ref), inv, sum.x);
+            sum.y = fmaf(tc::ex2(t.y - ref), inv, sum.y);
+            sum.z = fmaf(tc::ex2(t.z - ref), inv, sum.z);
+            sum.w = fmaf(tc::ex2(t.w - ref), inv, sum.w);
         }
-        wt[r] += sum;
+        if (r + 3 < P) {
+            float4 w = *reinterpret_cast<float4*>(wt + r);
+            *reinterpret_cast<float4*>(wt + r) = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+        } else {  // entries past the prefix stay as they are
+            wt[r] += sum.x;
+            if (r + 1 < P) wt[r + 1] += sum.y;
+            if (r + 2 < P) wt[r + 2] += sum.z;
+        }
+    }
+    if (p.k_new && P < p.cap && y % chunks == 0 && tid == 0) {  // the new token's own row
+        float sum = 0.f;
+        for (int h = 0; h < p.G; ++h) sum = fmaf(tc::ex2(s_tn[h] - s_ref[h]), s_inv[h], sum);
+        wt[P] += sum;
     }
 }
 
 // ------------------------------------------------------------------------------ host
-constexpr int kTcMaxCtas = 256;  // bounds the SM count from above
+constexpr int kTcMaxCtas = 512;  // two an SM, for up to 256 SMs
 static int simt_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -341,7 +387,6 @@ static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, uns
     };
     p.pre = reinterpret_cast<long long*>(take(((size_t)p.B + 1) * sizeof(long long)));
     p.part_ml = reinterpret_cast<float2*>(take(slots * p.HT * sizeof(float2)));
-    p.stat = reinterpret_cast<float4*>(take((size_t)p.L * p.B * p.Hq * sizeof(float4)));
     p.part_o = reinterpret_cast<float*>(take(slots * p.HT * p.d * sizeof(float)));
     p.score = weight ? reinterpret_cast<float*>(take(units * p.cap * p.G * sizeof(float))) : nullptr;
     return at;
@@ -375,13 +420,34 @@ static cudaError_t simt_d_go(DecodeParams& p, cudaStream_t st) {
                      : (p.d == 128 ? simt_heads_go<T, 128>(p, st) : simt_heads_go<T, 256>(p, st));
 }
 
+template <typename Tin, typename Tout, int D, int WPH>
+static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st) {
+    const size_t heads = (size_t)p.L * p.B * p.Hq;
+    const unsigned n_join = (unsigned)(WPH == 1 ? (heads + 7) / 8 : heads), units = (unsigned)p.L * p.B * p.Hkv;
+    const unsigned most = (p.cap + 1023) / 1024, want = 6u * sms / units + 1;
+    const int chunks = (int)(most < want ? most : want);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(counted(n_join + (p.weight ? units * chunks : 0)));
+    cfg.blockDim = dim3(256);
+    const size_t join_smem = WPH == 1 ? 0 : 8 * D * sizeof(float), weight_smem = p.weight ? 3 * p.G * sizeof(float) : 0;
+    cfg.dynamicSmemBytes = join_smem > weight_smem ? join_smem : weight_smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};  // may be set up while the split kernel ends
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_decode_finish<Tin, Tout, D, WPH>, p, n_join, chunks);
+}
 template <typename Tin, typename Tout>
-static cudaError_t join_go(const DecodeParams& p, cudaStream_t st) {
-    const unsigned n = counted((unsigned)p.L * p.B * p.Hq);
-    if (p.d == 64) k_decode_join<Tin, Tout, 64><<<n, 64, 0, st>>>(p);
-    else if (p.d == 128) k_decode_join<Tin, Tout, 128><<<n, 128, 0, st>>>(p);
-    else k_decode_join<Tin, Tout, 256><<<n, 256, 0, st>>>(p);
-    return cudaGetLastError();
+static cudaError_t finish_go(const DecodeParams& p, int sms, cudaStream_t st) {
+    // segments a head: C / (units) + 1 or so
+    const bool many = p.C >= 12L * p.L * p.B * p.Hkv * p.HB;
+    switch (p.d) {
+        case 64: return many ? finish_launch<Tin, Tout, 64, 8>(p, sms, st) : finish_launch<Tin, Tout, 64, 1>(p, sms, st);
+        case 128: return many ? finish_launch<Tin, Tout, 128, 8>(p, sms, st) : finish_launch<Tin, Tout, 128, 1>(p, sms, st);
+    }
+    return many ? finish_launch<Tin, Tout, 256, 8>(p, sms, st) : finish_launch<Tin, Tout, 256, 1>(p, sms, st);
 }
 
 cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype in, ddt_dtype out,
@@ -414,8 +480,8 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     unsigned char* w = static_cast<unsigned char*>(ws);
     cudaError_t e;
-    if (decode_tc_supported(d, in)) {  // bf16: one persistent CTA an SM
-        p.C = sms < kTcMaxCtas ? sms : kTcMaxCtas;
+    if (decode_tc_supported(d, in)) {  // bf16: persistent CTAs
+        p.C = sms < kTcMaxCtas / 2 ? sms : kTcMaxCtas / 2;
         decode_layout(p, decode_tc_heads(p.G, d), kTcMaxCtas, weight != nullptr, w);
         e = launch_decode_tc(p, st);
     } else {
@@ -424,13 +490,10 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
         e = simt_d_go<float>(p, st);
     }
     if (e != cudaSuccess) return e;
-    if (in == DDT_BF16) e = out == DDT_BF16 ? join_go<__nv_bfloat16, __nv_bfloat16>(p, st) : join_go<__nv_bfloat16, float>(p, st);
-    else e = out == DDT_BF16 ? join_go<float, __nv_bfloat16>(p, st) : join_go<float, float>(p, st);
-    if (e != cudaSuccess || !weight) return e;
-    const unsigned units = (unsigned)L * B * Hkv;
-    const unsigned most = (p.cap + 255) / 256, want = (unsigned)sms * 8 / units + 1;
-    k_decode_weight<<<counted(dim3(units, most < want ? most : want)), 256, p.G * sizeof(float4), st>>>(p);
-    return cudaGetLastError();
+    if (in == DDT_BF16)
+        return out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16>(p, sms, st)
+                               : finish_go<__nv_bfloat16, float>(p, sms, st);
+    return out == DDT_BF16 ? finish_go<float, __nv_bfloat16>(p, sms, st) : finish_go<float, float>(p, sms, st);
 }
 
 }  // namespace ddt

@@ -38,7 +38,6 @@ struct DecodeParams {
     long long* pre;   // [B + 1] tiles of the requests before b
     float2* part_ml;  // [U + C][HT] (reference in log2 units, sum); sum < 0: see kSeg*
     float* part_o;    // [U + C][HT][d]
-    float4* stat;     // [L][B][Hq] (reference, 1 / sum, the new row's score, unused) of the joined softmax
     float* score;     // [L][B][Hq][cap] scores in log2 units (weight only)
 };
 
@@ -154,6 +153,6 @@ __device__ __forceinline__ long long dec_unit(const DecodeParams& p, const Decod
 
 bool decode_tc_supported(int d, ddt_dtype in);
 int decode_tc_heads(int G, int d);
-cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st);
+cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
 
 }  // namespace ddt

@@ -14,11 +14,12 @@
 //   warp 0      producer: block-table entries, TMA of K and V tiles (128 rows, 128-byte
 //               swizzle, a box a page slice, a lane a box) into one ring, Q by TMA
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
-//   warps 4-7   softmax: a thread a cached row; the tile's maximum of each head by a warp
+//   warps 2-5   softmax: a thread a cached row; the tile's maximum of each head by a warp
 //               reduction and one exchange; O is rescaled only when a maximum grows by
-//               more than 2^8
-//   warps 8-11  the segment's partial from tensor memory to the workspace, behind the next
-//               segment's first tiles
+//               more than 2^8.  At a segment's end the same warps write its partial.
+// Up to eight heads and head sizes 64 and 128: two CTAs an SM, each with half the ring, so
+// that one's softmax chain (about 2000 cycles a tile, as long as an SM's share of HBM takes
+// for 32 KB) hides behind the other's.
 // Every wait is bounded; after one gives up the CTA drains its copies and MMAs, and its
 // unfinished segments say so to the join.
 #include <cuda.h>
@@ -33,26 +34,30 @@ namespace ddt {
 
 namespace {
 
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 192;
 constexpr float kTau = 8.f;  // rescale O only when a head's maximum grows by more than 2^kTau
 
 template <int D, int HP>
 struct DecCfg {
     static constexpr int kBlocks = D / 64;                 // 128-byte swizzle blocks of a row
     static constexpr int kStageBytes = kDecTile * D * 2;   // a K or V tile
-    static constexpr int kStages = (HP == 32 ? 163840 : 196608) / kStageBytes;
+    static constexpr int kCtas = HP == 8 && D <= 128 ? 2 : 1;  // an SM
+    static constexpr int kRing = kCtas == 2 ? 98304 : (HP == 32 ? 163840 : 196608);
+    static constexpr int kStages = kRing / kStageBytes;
     static constexpr int NQ = HP < 16 ? 16 : HP;           // N of Q K^T
     static constexpr int NP = 2 * HP;                      // N of P V: both parts
-    static constexpr int kQBytes = NQ * D * 2;
+    static constexpr int kQPitch = HP * 128;               // a 64-channel block of Q: HP rows (for 8 of
+                                                           // them N = 16 reads on: columns not used)
+    static constexpr int kQBytes = HP * D * 2;
     static constexpr int kPBytes = NP * kDecTile * 2;
     static constexpr int kMB = D > 128 ? D / 128 : 1;      // M blocks of P V
-    static constexpr int kOCol = 2 * NQ;                   // tensor memory: S x 2, O x 2
-    static constexpr int kCols = 2 * NQ + 2 * kMB * NP;
-    static constexpr int kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
-    static constexpr int kCtl = (2 * kStages + 22) * 8 + 18 * HP * 4;  // barriers and small arrays
+    static constexpr int kOCol = 2 * NQ;                   // tensor memory: S x 2, O
+    static constexpr int kCols = 2 * NQ + kMB * NP;
+    static constexpr int kTmemCols = kCols <= 64 ? 64 : 128;
+    static constexpr int kCtl = (2 * kStages + 16) * 8 + 12 * HP * 4;  // barriers and small arrays
     static constexpr int kSmem = 1024 + kStages * kStageBytes + 2 * kQBytes + 2 * kPBytes + kCtl;
-    static_assert(kSmem <= 227 * 1024 - 256, "shared memory of a CTA (the plan has a little of its own)");
-    static_assert(kCols <= 256, "tensor memory");
+    static_assert(kCtas * (kSmem + 1024 + 256) <= 228 * 1024, "shared memory of an SM (the plan has a little of its own)");
+    static_assert(kCols <= 128, "tensor memory");
 };
 
 struct DecTcArgs {
@@ -84,7 +89,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 }  // namespace
 
 template <int D, int HP>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
     k_decode_tc(const DecodeParams p, const DecTcArgs a, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q) {
     using Cfg = DecCfg<D, HP>;
@@ -100,16 +105,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t* s_full = q_free + 2;       // [2] S of a tile in tensor memory
     uint64_t* p_full = s_full + 2;       // [2] P of a tile in shared memory (4 warps)
     uint64_t* p_free = p_full + 2;       // [2] its P V is done
-    uint64_t* o_full = p_free + 2;       // [2] O of a segment is complete
-    uint64_t* o_free = o_full + 2;       // [2] and has been read (4 warps)
-    uint64_t* ml_full = o_free + 2;      // [2] its references and sums are in shared memory (4 warps)
-    uint64_t* drain = ml_full + 2;
+    uint64_t* drain = p_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     int* bad_tile = abort_flag + 1;                            // [8] a page of the tile does not exist
     float* xm = reinterpret_cast<float*>(bad_tile + 8);        // [2][4][HP] warps' tile maxima
-    float* sm_m = xm + 2 * 4 * HP;                             // [2][HP]
-    float* sm_l = sm_m + 2 * HP;                               // [2][4][HP]
+    float* sm_l = xm + 2 * 4 * HP;                             // [4][HP] warps' sums of a segment
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -120,9 +121,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4);
             tc::mbar_init(p_free + i, 1);
-            tc::mbar_init(o_full + i, 1);
-            tc::mbar_init(o_free + i, 4);
-            tc::mbar_init(ml_full + i, 4);
         }
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -141,6 +139,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     volatile int* abort = abort_flag;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_decode_finish may be set up
 
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const long long row = ((long long)w.l * p.B + w.b) * p.Hq + g * p.G + (w.g % p.HB) * HP;
 #pragma unroll
                 for (int blk = 0; blk < Cfg::kBlocks; ++blk)
-                    tc::tma_load_2d(sQ + (seg & 1) * Cfg::kQBytes + blk * (NQ * 128), &tm_q, q_full + (seg & 1),
+                    tc::tma_load_2d(sQ + (seg & 1) * Cfg::kQBytes + blk * Cfg::kQPitch, &tm_q, q_full + (seg & 1),
                                     blk * 64, (int)row);
             }
             for (int t = w.t; t < w.t + n_seg; ++t, ++j) {
@@ -209,30 +208,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t pdesc = tc::desc_sw128(tc::smem_u32(sP), 16, 1024);
             int j = 0, seg = 0;
             bool ok = true;
-            // P V of tile i, the first (or last) of segment s
-            auto pv = [&](int i, int s, bool first, bool last) {
-                if (first && !tc::mbar_wait(o_free + (s & 1), ((s >> 1) & 1) ^ 1, abort)) return false;
+            // P V of tile i; `first`: of a segment, so O starts anew (its warps have read the
+            // last segment's O before they hand over this P)
+            auto pv = [&](int i, bool first) {
                 const int st = (2 * i + 1) % kStages;
                 if (!tc::mbar_wait(full + st, ((2 * i + 1) / kStages) & 1, abort)) return false;
                 if (!tc::mbar_wait(p_full + (i & 1), (i >> 1) & 1, abort)) return false;
                 tc::tc_fence_after();
                 const uint64_t vd = vdesc + (uint64_t)((st * Cfg::kStageBytes) >> 4);
                 const uint64_t pd = pdesc + (uint64_t)(((i & 1) * Cfg::kPBytes) >> 4);
-                const uint32_t od = tmem + Cfg::kOCol + (s & 1) * kMB * NP;
 #pragma unroll
                 for (int kk = 0; kk < kDecTile / 16; ++kk)
 #pragma unroll
                     for (int mb = 0; mb < kMB; ++mb)
-                        tc::mma_f16_ss(od + mb * NP, vd + (uint64_t)((mb * 2 * kDecTile * 128 + kk * 2048) >> 4),
+                        tc::mma_f16_ss(tmem + Cfg::kOCol + mb * NP,
+                                       vd + (uint64_t)((mb * 2 * kDecTile * 128 + kk * 2048) >> 4),
                                        pd + (uint64_t)(((kk >> 2) * (NP * 128) + (kk & 3) * 32) >> 4), idesc_pv,
                                        !first || kk > 0);
                 tc::mma_commit(empty + st);
                 tc::mma_commit(p_free + (i & 1));
-                if (last) tc::mma_commit(o_full + (s & 1));
                 return true;
             };
-            bool prev_first = false, prev_last = false;
-            int prev_seg = 0;
+            bool prev_first = false;
             for (; w.left > 0 && ok; dec_next(p, w), ++seg) {
                 const int n_seg = dec_seg_tiles(w);
                 ok = tc::mbar_wait(q_full + (seg & 1), (seg >> 1) & 1, abort);
@@ -247,28 +244,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int kk = 0; kk < D / 16; ++kk)
                         tc::mma_f16_ss(tmem + (j & 1) * NQ,
                                        kd + (uint64_t)(((kk >> 2) * (kDecTile * 128) + (kk & 3) * 32) >> 4),
-                                       qd + (uint64_t)(((kk >> 2) * (NQ * 128) + (kk & 3) * 32) >> 4), idesc_qk, kk > 0);
+                                       qd + (uint64_t)(((kk >> 2) * Cfg::kQPitch + (kk & 3) * 32) >> 4), idesc_qk, kk > 0);
                     tc::mma_commit(empty + st);
                     tc::mma_commit(s_full + (j & 1));
                     if (i == n_seg - 1) tc::mma_commit(q_free + (seg & 1));
                     // S of tile j + 1 may overwrite that of tile j - 1 once P of j - 1 is there
-                    if (j > 0) ok = pv(j - 1, prev_seg, prev_first, prev_last);
-                    prev_seg = seg;
+                    if (j > 0) ok = pv(j - 1, prev_first);
                     prev_first = i == 0;
-                    prev_last = i == n_seg - 1;
                 }
             }
-            if (ok && j > 0) pv(j - 1, prev_seg, prev_first, prev_last);
+            if (ok && j > 0) pv(j - 1, prev_first);
             tc::mma_commit(drain);
             drain_wait(drain, 0);
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ------------------------------------------------------------------- softmax
-        const int ws = warp - 4, r = 32 * ws + lane;
+    } else {
+        // -------------------------------------------------- softmax, and the segments' partials
+        const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
         const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
-        int j = 0, seg = 0;
+        int j = 0;
         bool ok = true;
-        for (; w.left > 0 && ok; dec_next(p, w), ++seg) {
+        for (; w.left > 0; dec_next(p, w)) {
             const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0), n_seg = dec_seg_tiles(w);
             float m[HP], l[HP];
 #pragma unroll
@@ -277,34 +272,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l[h] = 0.f;
             }
             int bad = 0;
-            for (int i = 0; i < n_seg && ok; ++i, ++j) {
+            for (int i = 0; i < n_seg; ++i, ++j) {
                 const int y = (w.t + i) * kDecTile, n = min(kDecTile, w.P - y);
-                ok = __all_sync(kFull, tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort));
-                if (!ok) break;
-                tc::tc_fence_after();
-                uint32_t sr[NQ];
-#pragma unroll
-                for (int c = 0; c < NQ; c += 16) tmem_ld16(tmem + lane_base + (j & 1) * NQ + c, sr + c);
-                tc::tmem_wait_ld();
-                bad |= bad_tile[j & 7];
+                // a warp that gave up still takes part in the barriers
+                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
+                ok = __all_sync(kFull, ok);
                 float t[HP], mine = -INFINITY;
+                float* x = xm + (j & 1) * 4 * HP;
+                if (ok) {
+                    tc::tc_fence_after();
+                    uint32_t sr[NQ];
 #pragma unroll
-                for (int h = 0; h < HP; ++h) {
-                    t[h] = r < n ? __uint_as_float(sr[h]) * p.scale_log2 : -INFINITY;
-                    if (h < nh) {
-                        const float x = redux_max(t[h]);
-                        if (lane == h) mine = x;
+                    for (int c = 0; c < NQ; c += 16) tmem_ld16(tmem + lane_base + (j & 1) * NQ + c, sr + c);
+                    tc::tmem_wait_ld();
+                    bad |= bad_tile[j & 7];
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        t[h] = r < n ? __uint_as_float(sr[h]) * p.scale_log2 : -INFINITY;
+                        if (h < nh) {
+                            const float v = redux_max(t[h]);
+                            if (lane == h) mine = v;
+                        }
+                    }
+                    if (p.score && r < n) {
+                        float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y + r;
+#pragma unroll
+                        for (int h = 0; h < HP; ++h)
+                            if (h < nh) sc[(long long)h * p.cap] = t[h];
                     }
                 }
-                float* x = xm + (j & 1) * 4 * HP;
                 if (lane < HP) x[ws * HP + lane] = mine;
-                if (p.score && r < n) {
-                    float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y + r;
-#pragma unroll
-                    for (int h = 0; h < HP; ++h)
-                        if (h < nh) sc[(long long)h * p.cap] = t[h];
-                }
                 tc::named_bar(1, 128);
+                if (!ok) continue;
                 float mt[HP];
 #pragma unroll
                 for (int h = 0; h < HP; h += 4) {
@@ -335,12 +334,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     if (i > 0) {  // O holds earlier tiles of the segment: once their P V are done
                         ok = __all_sync(kFull, tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort));
-                        if (!ok) break;
+                        if (!ok) continue;
                         tc::tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < kMB * NP; c += 16) {
                             uint32_t o[16];
-                            const uint32_t at = tmem + lane_base + Cfg::kOCol + (seg & 1) * kMB * NP + c;
+                            const uint32_t at = tmem + lane_base + Cfg::kOCol + c;
                             tmem_ld16(at, o);
                             tc::tmem_wait_ld();
 #pragma unroll
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 // the P buffer is free once P V of tile j - 2 is done
                 ok = __all_sync(kFull, tc::mbar_wait(p_free + (j & 1), ((j >> 1) & 1) ^ 1, abort));
-                if (!ok) break;
+                if (!ok) continue;
                 unsigned char* pb = sP + (j & 1) * Cfg::kPBytes + (r >> 6) * (NP * 128);
 #pragma unroll
                 for (int h = 0; h < HP; ++h)
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // does not cancel NaN: zero them before the MMA reads them
                     const int st = (2 * j + 1) % kStages;
                     ok = __all_sync(kFull, tc::mbar_wait(full + st, ((2 * j + 1) / kStages) & 1, abort));
-                    if (!ok) break;
+                    if (!ok) continue;
                     unsigned char* v = ring + st * Cfg::kStageBytes;
                     const int per = (kDecTile - n) * 8;
                     for (int e = r; e < per * Cfg::kBlocks; e += 128)
@@ -382,50 +381,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(p_full + (j & 1));
             }
-            if (!ok) break;
-            // references and sums for the epilogue, whose last use of these places is over
-            ok = __all_sync(kFull, tc::mbar_wait(o_free + (seg & 1), ((seg >> 1) & 1) ^ 1, abort));
-            if (!ok) break;
+            // ---- the partial: sums through shared memory, O once the last P V is done
             float sum = 0.f, ref = 0.f;
 #pragma unroll
             for (int h = 0; h < HP; ++h)
                 if (h < nh) {
                     const float x = warp_sum(l[h]);
-                    if (lane == h) {
-                        sum = x;
-                        ref = m[h];
-                    }
+                    if (lane == h) sum = x;
+                    if (r == h) ref = m[h];
                 }
-            if (lane < HP) {
-                sm_l[((seg & 1) * 4 + ws) * HP + lane] = bad ? -1.f : sum;
-                if (ws == 0) sm_m[(seg & 1) * HP + lane] = ref;
-            }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(ml_full + (seg & 1));
-        }
-    } else if (warp >= 8) {
-        // ------------------------------------------------------------------- partials
-        const int ws = warp - 8, r = 32 * ws + lane;
-        const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
-        int seg = 0;
-        bool ok = true;
-        for (; w.left > 0; dec_next(p, w), ++seg) {
-            const int h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0);
-            const long long slot = dec_unit(p, w) + blockIdx.x;
-            if (ok) ok = tc::mbar_wait(ml_full + (seg & 1), (seg >> 1) & 1, abort);
-            if (ok) ok = tc::mbar_wait(o_full + (seg & 1), (seg >> 1) & 1, abort);
+            if (lane < HP) sm_l[ws * HP + lane] = sum;
+            if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
             ok = __all_sync(kFull, ok);
-            if (!ok) {
-                if (r < nh) p.part_ml[slot * p.HT + r] = make_float2(0.f, kSegTimeout);
-                continue;
+            tc::named_bar(1, 128);
+            const long long slot = dec_unit(p, w) + blockIdx.x;
+            if (r < nh) {
+                const float z = (sm_l[r] + sm_l[HP + r]) + (sm_l[2 * HP + r] + sm_l[3 * HP + r]);
+                p.part_ml[slot * p.HT + r] = make_float2(ref, !ok ? kSegTimeout : (bad ? kSegBadPage : z));
             }
+            if (!ok) continue;
             tc::tc_fence_after();
 #pragma unroll
             for (int mb = 0; mb < kMB; ++mb) {
                 uint32_t o[NP];
 #pragma unroll
-                for (int c = 0; c < NP; c += 16)
-                    tmem_ld16(tmem + lane_base + Cfg::kOCol + ((seg & 1) * kMB + mb) * NP + c, o + c);
+                for (int c = 0; c < NP; c += 16) tmem_ld16(tmem + lane_base + Cfg::kOCol + mb * NP + c, o + c);
                 tc::tmem_wait_ld();
                 if (D >= 128 || r < D) {
                     float* out = p.part_o + slot * p.HT * D + mb * 128 + r;
@@ -434,20 +414,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (h < nh) out[h * D] = __uint_as_float(o[h]) + __uint_as_float(o[HP + h]);
                 }
             }
-            if (r < nh) {
-                float sum = 0.f;
-                bool bad = false;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float x = sm_l[((seg & 1) * 4 + q) * HP + r];
-                    bad |= x < 0.f;
-                    sum += x;
-                }
-                p.part_ml[slot * p.HT + r] = make_float2(sm_m[(seg & 1) * HP + r], bad ? kSegBadPage : sum);
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(o_free + (seg & 1));
         }
     }
 
@@ -481,10 +447,11 @@ EncodeTiledFn encode_fn() {
 }
 
 template <int D, int HP>
-cudaError_t tc_go(const DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, cudaStream_t st) {
+cudaError_t tc_go(DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, cudaStream_t st) {
     constexpr int smem = DecCfg<D, HP>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    p.C *= DecCfg<D, HP>::kCtas;
     k_decode_tc<D, HP><<<counted(p.C), kTcThreads, smem, st>>>(p, a, maps[0], maps[1], maps[2]);
     return cudaGetLastError();
 }
@@ -497,7 +464,8 @@ bool decode_tc_supported(int d, ddt_dtype in) { return in == DDT_BF16 && (d == 6
 // where shared memory has no room for more)
 int decode_tc_heads(int G, int d) { return G <= 8 ? 8 : (G <= 16 || d == 256 ? 16 : 32); }
 
-cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
+// p.C: SMs on entry, CTAs on return
+cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     DecTcArgs a;

@@ -8,7 +8,7 @@
 // destinations (< keep) never meet, so the moves run in place and in any order, and a
 // request that is r rows over its budget moves at most r rows however long its cache is.
 //
-//   k_evict_claim   grid B: lengths and block table checked, uses of each page counted.
+//   k_evict_claim   grid B: lengths and block table checked, pages that are used twice found.
 //   k_evict_select  grid L B Hkv: the keep-th largest key by three histogram passes (11, 11
 //                   and 10 bits), then one pass in index order for the holes and the rows
 //                   that fill them; sums and positions follow at once.
@@ -22,6 +22,8 @@ namespace ddt {
 namespace {
 constexpr int kBins = 2048;             // bins of a histogram pass (the last one uses 1024)
 constexpr int kSelCache = 45 * 1024;    // rows whose keys fit in shared memory
+constexpr int kClaimThreads = 512;
+constexpr int kWindow = 1 << 20;        // pages a bitmap in shared memory covers
 constexpr int kEvict = -1;  // state of a request that is over its budget
 
 struct EvictParams {
@@ -38,34 +40,53 @@ struct EvictParams {
     int32_t* n_placed;
     int32_t* status;
     // workspace
-    int32_t* uses;    // [num_pages]
     int32_t* state;   // [B] kEvict, DDT_OK (within the budget), or an error
-    int32_t* shared;  // [B] 1: a page of the request is used more than once
     int32_t* n_move;  // [U]
     int32_t* src;     // [U][most]
     int32_t* dst;     // [U][most]
 };
 }  // namespace
 
-__global__ void __launch_bounds__(256) k_evict_claim(const EvictParams p) {
-    const int b = blockIdx.x;
+// Checks one request.  A page that it would rewrite may be used once only: its own pages are
+// marked in a bitmap in shared memory (a window of the pages at a time, one window but for
+// pools of over a million pages), and every page of the other requests is looked up there.
+__global__ void __launch_bounds__(kClaimThreads) k_evict_claim(const EvictParams p) {
+    extern __shared__ uint32_t s_used[];
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b];
     int st = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : ((np < 0 || np > P || sq < P) ? DDT_ERR_INVALID_ARG : DDT_OK);
+    auto pages = [&](int rows) { return rows < 0 || rows > p.cap ? 0 : (rows + p.page_rows - 1) / p.page_rows; };
+    const int32_t* mine = p.block_table + (long long)b * p.max_pages;
+    const int n = st == DDT_ERR_CAPACITY ? 0 : pages(P);
     int bad = 0;
-    if (st != DDT_ERR_CAPACITY) {
-        const int n = (P + p.page_rows - 1) / p.page_rows;
-        for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const int pg = p.block_table[(long long)b * p.max_pages + i];
-            if (pg < 0 || pg >= p.num_pages) bad = 1;
-            else atomicAdd(p.uses + pg, 1);
+    for (int i = tid; i < n; i += kClaimThreads) bad |= mine[i] < 0 || mine[i] >= p.num_pages;
+    if (__syncthreads_or(bad)) st = DDT_ERR_INVALID_ARG;
+    if (st == DDT_OK && P > p.keep) {
+        int twice = 0;
+        for (int w0 = 0; w0 < p.num_pages; w0 += kWindow) {
+            const int len = min(kWindow, p.num_pages - w0);
+            auto marked = [&](int page, bool set) {
+                const unsigned at = (unsigned)(page - w0);
+                if (at >= (unsigned)len) return 0u;
+                const uint32_t bit = 1u << (at & 31);
+                return (set ? atomicOr(&s_used[at >> 5], bit) : s_used[at >> 5]) & bit;
+            };
+            for (int i = tid; i < (len + 31) / 32; i += kClaimThreads) s_used[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kClaimThreads) twice |= marked(mine[i], true) != 0;
+            __syncthreads();
+            for (int o = warp; o < p.B; o += kClaimThreads / 32) {
+                if (o == b) continue;
+                const int32_t* other = p.block_table + (long long)o * p.max_pages;
+                const int no = pages(p.prefix_len[o]);
+#pragma unroll 4
+                for (int i = lane; i < no; i += 32) twice |= marked(other[i], false) != 0;
+            }
+            __syncthreads();
         }
+        st = __syncthreads_or(twice) ? (int)DDT_ERR_INVALID_ARG : kEvict;
     }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        if (bad) st = DDT_ERR_INVALID_ARG;
-        p.state[b] = st != DDT_OK ? st : (P > p.keep ? kEvict : DDT_OK);
-        p.shared[b] = 0;
-    }
+    if (tid == 0) p.state[b] = st;
 }
 
 // The order of the rows as an unsigned key: 0 for NaN, then the sums from the smallest to
@@ -121,8 +142,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     float* wt = p.weight + u * p.cap;
     int32_t* rp = p.row_pos + u * p.cap;
     const int32_t* table = p.block_table + (long long)b * p.max_pages;
-    int twice = 0;  // looked at after the first pass
-    for (int i = tid; i < (P + p.page_rows - 1) / p.page_rows; i += NT) twice |= p.uses[table[i]] > 1;
     for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
     if (tid == 0) s_zeros = s_safe = 0;
     __syncthreads();
@@ -181,13 +200,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
                 if (pass == 0) atomicAdd(&s_safe, safe);
             }
         }
-        if (__syncthreads_or(pass == 0 && twice)) {
-            if (tid == 0) {
-                p.n_move[u] = 0;
-                p.shared[b] = 1;
-            }
-            return;
-        }
+        __syncthreads();
         // warp i has the i-th run of bins from the top, and only the warp whose run holds the
         // K-th largest looks closer
         constexpr int kPer = kBins / NT;
@@ -343,11 +356,11 @@ __global__ void __launch_bounds__(256, 8) k_evict_move(const EvictParams p) {
     const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv % p.B), l = (int)(u / p.Hkv / p.B);
     if (l == 0 && g == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         const int st = p.state[b];
-        if (st == kEvict && !p.shared[b]) {
+        if (st == kEvict) {
             p.prefix_len[b] = p.keep;
             p.n_placed[b] = p.keep;
         }
-        p.status[b] = st != kEvict ? st : (p.shared[b] ? (int)DDT_ERR_INVALID_ARG : (int)DDT_OK);
+        p.status[b] = st != kEvict ? st : (int)DDT_OK;
     }
     const int n = p.n_move[u];
     const int32_t* src = p.src + u * p.most;
@@ -388,9 +401,7 @@ static size_t evict_layout(EvictParams& p, unsigned char* ws) {
         return reinterpret_cast<int32_t*>(r);
     };
     p.most = p.cap / 2;  // min(keep, cap - keep) whatever `keep` is
-    p.uses = take(p.num_pages);
     p.state = take(p.B);
-    p.shared = take(p.B);
     p.n_move = take(units);
     p.src = take(units * p.most);
     p.dst = take(units * p.most);
@@ -443,10 +454,10 @@ cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging&
     evict_layout(p, static_cast<unsigned char*>(ws));
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaMemsetAsync(p.uses, 0, (size_t)p.num_pages * sizeof(int32_t), st);
-    if (e != cudaSuccess) return e;
     const unsigned units = (unsigned)L * B * Hkv;
-    k_evict_claim<<<counted(B), 256, 0, st>>>(p);
+    cudaError_t e = cudaFuncSetAttribute(k_evict_claim, cudaFuncAttributeMaxDynamicSharedMemorySize, kWindow / 8);
+    if (e != cudaSuccess) return e;
+    k_evict_claim<<<counted(B), kClaimThreads, ((pg.num_pages < kWindow ? pg.num_pages : kWindow) + 31) / 32 * 4, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // few units or long caches: many threads a unit, for its latency; else small blocks, so
     // that several units share an SM and hide each other's barriers

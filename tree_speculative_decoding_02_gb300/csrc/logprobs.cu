@@ -6,14 +6,18 @@
 // so one pass that carries (m, Z, sum 2^w w) is enough; the top tokens need a second look at
 // a few entries only.
 //
-//   k_lp_unit   persistent warps over the (row, 4096-byte unit) pairs of the rows that are
-//               asked for: one pass, the next unit's 16-byte words in registers while this
-//               one's are worked on.  Packed maxima and minima on the raw words, packed fp32
-//               pairs for the rest: about 4.5 instructions an entry.  Each lane's largest
-//               entry goes to the second kernel.
-//   k_lp_join   grid B A: joins a row's units; the n-th largest of the units' largest entries
-//               bounds the n-th best entry of the row from below, so only the lanes that
-//               reach it are read again (somewhat over n of 2400).
+// k_token_logprobs: a CTA a row, or a cluster of up to eight CTAs a row in calls of few rows,
+// which are bound by latency.
+//   stream  the row is cut into 4096-byte units, a warp a unit.  A warp keeps two units on
+//           their way into shared memory (cp.async, each thread its own words, so no barrier).
+//           Each thread carries a reference near its largest entry, moved only when an entry is
+//           2^8 above it, and its two sums: packed maxima on the raw words, packed fp32 pairs
+//           for the rest, nothing across the warp.  It leaves its share of the row's sums, and
+//           its largest entry of every unit.
+//   finish  joins the shares; the n-th largest of the threads' largest entries bounds the n-th
+//           best entry of the row from below, so only the few (unit, thread) words that hold
+//           an entry that reaches it are read again.  Six CTAs an SM: most stream while one or
+//           two finish their rows (a chain of reads that depend on one another).
 #include <limits.h>
 #include <math.h>
 
@@ -24,20 +28,22 @@
 namespace ddt {
 
 namespace {
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpCtas = 2;      // CTAs an SM of the first kernel, all resident
-constexpr int kLpRows = 4096;   // rows it lists
-constexpr int kLpLists = 512;   // lanes read again
-constexpr int kLpCand = 1024;   // entries ranked
+constexpr int kLpWarps = 4;
+constexpr int kLpThreads = kLpWarps * 32;
+constexpr int kLpCtas = 6;      // CTAs an SM
+constexpr int kLpStages = 2;    // units on their way a warp
+constexpr int kLpClusters = 2 * 256 * kLpCtas;  // CTAs of a call with several a row, at most
+constexpr int kLpLists = 256;   // (unit, thread) pairs read again
+constexpr int kLpCand = 512;    // entries ranked
 constexpr float kLpLow = -200.f;  // 2^w is 0 from here down
 }  // namespace
 
+// A thread's share of a row.
 struct LpPartial {
-    float m;  // the unit's largest logit
-    float s;  // sum of 2^w; 0: nothing above -inf; NaN: a NaN or +inf logit
-    float t;  // sum of 2^w w
-    float pad;
+    float m;   // reference, a logit (-inf: no entry above -inf so far)
+    float s;   // sum of 2^w with this reference; 0: nothing above -inf; NaN: a NaN or +inf logit
+    float t;   // sum of 2^w w
+    float mx;  // largest entry
 };
 
 // A unit is 4096 bytes of a row: 8 words of 16 bytes a lane, word j of lane i being word
@@ -51,6 +57,10 @@ struct LpUnit {
     __device__ static int entry(int unit, int j, int lane, int lead) {
         return unit * kEntries + (j * 32 + lane) * VE - lead;
     }
+    // all of the unit's words lie within the row
+    __device__ static bool whole(int unit, int lead, int V) {
+        return unit * kEntries >= lead && (unit + 1) * kEntries - lead <= V;
+    }
 };
 static inline int lp_units(int V, size_t esz) {
     const int per = 4096 / (int)esz, gap = 16 / (int)esz - 1;
@@ -58,10 +68,16 @@ static inline int lp_units(int V, size_t esz) {
 }
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// shares: those of a CTA a row, or of kLpClusters CTAs where rows have several
+static size_t lp_part_bytes(size_t rows) {
+    return (rows > kLpClusters ? rows : kLpClusters) * kLpThreads * sizeof(LpPartial);
+}
+
+// workspace: shares, the threads' largest entries of every unit.  fp32 rows have twice the
+// units of bf16 rows: the size covers both.
 size_t logprobs_ws_bytes(int B, int A, int V, int top_n) {
-    // fp32 rows have twice the units of bf16 rows: the workspace covers both
-    const size_t n = (size_t)B * A * lp_units(V, 4);
-    return al256(n * sizeof(LpPartial)) + (top_n > 0 ? al256(n * 32 * sizeof(float)) : 0);
+    const size_t rows = (size_t)B * A;
+    return lp_part_bytes(rows) + (top_n > 0 ? al256(rows * lp_units(V, 4) * 32 * sizeof(float)) : 0);
 }
 
 // The word at entry e of the row; entries outside [0, V) are -inf.
@@ -87,49 +103,29 @@ __device__ __forceinline__ float lp_at(const uint4& w, int q, const __nv_bfloat1
 __device__ __forceinline__ float lp_at(const uint4& w, int q, const float*) {
     return __uint_as_float(q < 1 ? w.x : (q < 2 ? w.y : (q < 3 ? w.z : w.w)));
 }
-// running maximum and minimum of a lane's words (NaN entries are passed over here: they turn
-// the sums NaN)
-struct LpRangeBf16 {
-    __nv_bfloat162 hi, lo;
-    __device__ __forceinline__ void init() {
-        hi = __float2bfloat162_rn(-INFINITY);
-        lo = __float2bfloat162_rn(INFINITY);
-    }
+// running maximum of a lane's words (NaN entries are passed over here: they turn the sums NaN)
+template <typename T>
+struct LpMax;
+template <>
+struct LpMax<__nv_bfloat16> {
+    __nv_bfloat162 hi = __float2bfloat162_rn(-INFINITY);
     __device__ __forceinline__ void see(const uint4& w) {
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&v[i]);
-            hi = __hmax2(hi, x);
-            lo = __hmin2(lo, x);
-        }
+        for (int i = 0; i < 4; ++i) hi = __hmax2(hi, *reinterpret_cast<const __nv_bfloat162*>(&v[i]));
     }
     __device__ __forceinline__ float max() const { return fmaxf(__low2float(hi), __high2float(hi)); }
-    __device__ __forceinline__ float min() const { return fminf(__low2float(lo), __high2float(lo)); }
 };
-struct LpRangeF32 {
-    float hi, lo;
-    __device__ __forceinline__ void init() {
-        hi = -INFINITY;
-        lo = INFINITY;
-    }
+template <>
+struct LpMax<float> {
+    float hi = -INFINITY;
     __device__ __forceinline__ void see(const uint4& w) {
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi = fmaxf(hi, __uint_as_float(v[i]));
-            lo = fminf(lo, __uint_as_float(v[i]));
-        }
+        for (int i = 0; i < 4; ++i) hi = fmaxf(hi, __uint_as_float(v[i]));
     }
     __device__ __forceinline__ float max() const { return hi; }
-    __device__ __forceinline__ float min() const { return lo; }
 };
-template <typename T>
-struct LpRange;
-template <>
-struct LpRange<__nv_bfloat16> : LpRangeBf16 {};
-template <>
-struct LpRange<float> : LpRangeF32 {};
 
 // two fp32 values in one 64-bit register, for the packed fp32 instructions
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -161,315 +157,386 @@ __device__ __forceinline__ float redux_max(float x) {
     return y;
 }
 
-// One unit's words -> its partial (lane 0 writes) and the lane's largest entry.
+// A thread's running share of a row.
+struct LpRun {
+    float m, ref, s, t, mx;  // ref = m log2(e) / T as rounded, which the terms take as it is
+    __device__ __forceinline__ void start() {
+        m = ref = mx = -INFINITY;
+        s = t = 0.f;
+    }
+};
+constexpr float kLpFar = 1e30f;  // references beyond it are taken before scaling
+
+// One unit's words of this thread, from shared memory (read twice: keeping them in registers
+// costs a third of the warps); returns the largest entry.
 template <typename T>
-__device__ __forceinline__ void lp_reduce(const uint4 (&w)[8], float s2, int lane, LpPartial* part, T* lane_max) {
+__device__ __forceinline__ float lp_add(LpRun& r, const uint4* from, float s2) {
     constexpr int VE = LpUnit<T>::VE;
-    LpRange<T> range;
-    range.init();
+    const T* kT = nullptr;
+    LpMax<T> top;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) range.see(w[j]);
-    const float mt = range.max();
-    const float m = redux_max(mt);
-    const float ref = m * s2, base = m == -INFINITY ? 0.f : m;
-    // rows with masked entries (-inf or the type's lowest) or out of fp32's range once scaled
-    const bool low = !(fmaf(range.min(), s2, -ref) > kLpLow && fabsf(ref) < 1e30f);
+    for (int j = 0; j < 8; ++j) top.see(from[j * 32]);
+    const float mt = top.max();
+    r.mx = fmaxf(r.mx, mt);
+    if ((mt - r.m) * s2 > 8.f) {  // the first unit, or an entry far above the reference
+        const float ref = mt * s2;
+        if (r.s != 0.f) {
+            const float d = fabsf(ref) < kLpFar && fabsf(r.ref) < kLpFar ? r.ref - ref : fmaxf((r.m - mt) * s2, kLpLow);
+            const float f = tc::ex2(d);
+            r.t = f * fmaf(d, r.s, r.t);
+            r.s *= f;
+        }
+        r.m = mt;
+        r.ref = ref;
+    }
+    const uint64_t k2 = pack2(s2, s2), r2 = pack2(-r.ref, -r.ref);
     uint64_t s[2] = {0, 0}, t[2] = {0, 0};
-    float off = 0.f;
-    const uint64_t k2 = pack2(s2, s2), r2 = pack2(-ref, -ref);
-    if (!__any_sync(kFull, low)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 8; ++j) {
+        const uint4 w = from[j * 32];
 #pragma unroll
-            for (int q = 0; q < VE; q += 2) {
-                const uint64_t x = pack2(lp_at(w[j], q, static_cast<const T*>(nullptr)),
-                                         lp_at(w[j], q + 1, static_cast<const T*>(nullptr)));
-                const uint64_t v = fma2(x, k2, r2);
-                float a, b;
-                unpack2(v, a, b);
-                const uint64_t e = pack2(tc::ex2(a), tc::ex2(b));
-                s[(q >> 1) & 1] = add2(s[(q >> 1) & 1], e);
-                t[(q >> 1) & 1] = fma2(e, v, t[(q >> 1) & 1]);
-            }
-        // the terms took m s2 as rounded for their reference: to the exact one, 2^-24 m s2
-        // away at most (its square is nothing)
-        off = fmaf(m, s2, -ref);
-    } else {
-        // the bound keeps 0 * -inf out of t
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int q = 0; q < VE; q += 2) {
-                const float a = max_nan((lp_at(w[j], q, static_cast<const T*>(nullptr)) - base) * s2, kLpLow);
-                const float b = max_nan((lp_at(w[j], q + 1, static_cast<const T*>(nullptr)) - base) * s2, kLpLow);
-                const uint64_t e = pack2(tc::ex2(a), tc::ex2(b));
-                s[(q >> 1) & 1] = add2(s[(q >> 1) & 1], e);
-                t[(q >> 1) & 1] = fma2(e, pack2(a, b), t[(q >> 1) & 1]);
-            }
+        for (int q = 0; q < VE; q += 2) {
+            const uint64_t v = fma2(pack2(lp_at(w, q, kT), lp_at(w, q + 1, kT)), k2, r2);
+            float a, b;
+            unpack2(v, a, b);
+            const uint64_t e = pack2(tc::ex2(a), tc::ex2(b));
+            s[(q >> 1) & 1] = add2(s[(q >> 1) & 1], e);
+            t[(q >> 1) & 1] = fma2(e, v, t[(q >> 1) & 1]);
+        }
     }
     float s0, s1, t0, t1;
     unpack2(add2(s[0], s[1]), s0, s1);
     unpack2(add2(t[0], t[1]), t0, t1);
-    const float ss = warp_sum(s0 + s1), tt = warp_sum(t0 + t1);
-    const float c = 1.f - 0.6931471805599453f * off;
-    if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(m, ss * c, fmaf(-off, ss, tt) * c, 0.f);
-    if (lane_max) lane_max[lane] = from_f32<T>(mt);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas) k_lp_unit(const T* __restrict__ logits, int rows, int N, int V,
-                                                                 int A, int nunits, float s2,
-                                                                 const int32_t* __restrict__ node,
-                                                                 LpPartial* __restrict__ part,
-                                                                 T* __restrict__ lane_max) {
-    __shared__ int s_row[kLpRows];
-    __shared__ int s_n;
-    const int lane = threadIdx.x & 31;
-    // a walk's rows are mostly padding: the ones that are asked for are listed first (in no
-    // order: the partials go to the rows' own places), so that all warps share them evenly
-    const bool listed = node && rows <= kLpRows;
-    if (listed) {
-        if (threadIdx.x == 0) s_n = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows; i += kLpThreads) {
-            const int r = node[i];
-            if (r >= 0 && r < N) s_row[atomicAdd(&s_n, 1)] = i;
+    s0 += s1;
+    t0 += t1;
+    if (__any_sync(kFull, t0 != t0 || !(fabsf(r.ref) < kLpFar))) {
+        // masked entries (0 * -inf in t), or out of fp32's range once scaled (the type's lowest
+        // value as a mask): again, term by term and with a bound
+        const bool far = !(fabsf(r.ref) < kLpFar);
+        const float base = r.m == -INFINITY ? 0.f : r.m;
+        s0 = t0 = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            const uint4 w = from[j * 32];
+#pragma unroll
+            for (int q = 0; q < VE; ++q) {
+                const float x = lp_at(w, q, kT);
+                const float a = max_nan(far ? (x - base) * s2 : fmaf(x, s2, -r.ref), kLpLow), e = tc::ex2(a);
+                s0 += e;
+                t0 = fmaf(e, a, t0);
+            }
         }
-        __syncthreads();
     }
-    // rows * nunits < 2^31
-    const unsigned total = (unsigned)(listed ? s_n : rows) * nunits, step = gridDim.x * kLpWarps;
-    // the words of pair x, if its row is asked for; `at`: the place of its results
-    auto load = [&](unsigned x, uint4 (&w)[8], unsigned& at) {
-        unsigned i = x / nunits;
-        const int u = (int)(x - i * nunits);
-        if (listed) i = s_row[i];
-        const int r = node ? node[i] : (int)(i % A);
-        at = i * nunits + u;
-        if (r < 0 || r >= N) return false;
-        const T* row = logits + ((long long)(i / A) * N + r) * V;
-        const int e0 = LpUnit<T>::entry(u, 0, lane, LpUnit<T>::lead(row));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = lp_word(row, e0 + j * 32 * LpUnit<T>::VE, V);
-        return true;
-    };
-    unsigned x = blockIdx.x * kLpWarps + (threadIdx.x >> 5), at = 0, at1 = 0;
-    uint4 w[8];
-    bool have = x < total && load(x, w, at);
-    for (; x < total; x += step) {
-        uint4 next[8];
-        const bool more = x + step < total && load(x + step, next, at1);
-        if (have) lp_reduce<T>(w, s2, lane, part + at, lane_max ? lane_max + (long long)at * 32 : nullptr);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = next[j];
-        have = more;
-        at = at1;
+    r.s += s0;
+    r.t += t0;
+    return mt;
+}
+
+// The share with the exact reference m: the terms took 2^-24 m s2 at most of it too much (whose
+// square is nothing).
+__device__ __forceinline__ float4 lp_share(const LpRun& r, float s2) {
+    const float off = fabsf(r.ref) < kLpFar ? fmaf(r.m, s2, -r.ref) : 0.f, c = 1.f - 0.6931471805599453f * off;
+    return make_float4(r.m, r.s * c, fmaf(-off, r.s, r.t) * c, r.mx);
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
+struct LpArgs {
+    int rows, N, V, A, nunits, top_n;
+    float s2, inv_t;
+    const int32_t* node;
+    const int32_t* token;
+    float4* part;    // LpPartial
+    float* logprob;
+    float* entropy;
+    int32_t* top_token;
+    float* top_logprob;
+    int32_t* status;
+};
+
+__device__ __forceinline__ int lp_node(const LpArgs& p, int i) { return p.node ? p.node[i] : i % p.A; }
+// entry i names a row and no impossible token
+__device__ __forceinline__ bool lp_asked(const LpArgs& p, int i) {
+    const int r = lp_node(p, i);
+    return r >= 0 && r < p.N && p.token[i] < p.V;
+}
+template <typename T>
+__device__ __forceinline__ const T* lp_row(const LpArgs& p, const T* logits, int i) {
+    return logits + ((long long)(i / p.A) * p.N + lp_node(p, i)) * p.V;
+}
+// the results of an entry that does not
+__device__ __forceinline__ void lp_padding(const LpArgs& p, int i, int tid) {
+    if (tid == 0) {
+        p.logprob[i] = 0.f;
+        if (p.entropy) p.entropy[i] = 0.f;
+        p.status[i] = lp_node(p, i) < 0 ? DDT_OK : DDT_ERR_INVALID_ARG;
+    }
+    if (tid < p.top_n) {
+        p.top_token[(long long)i * p.top_n + tid] = -1;
+        p.top_logprob[(long long)i * p.top_n + tid] = 0.f;
     }
 }
 
+struct LpScratch {
+    float m[kLpWarps], z[kLpWarps], t[kLpWarps], sorted[kLpThreads];
+    int list[kLpLists];
+    float cv[kLpCand];
+    int ci[kLpCand];
+    int nl, nc;
+};
+
+// A unit's words: on their way into a warp's place of the ring, and from there.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) k_lp_join(const T* __restrict__ logits, int N, int V, int A, int nunits,
-                                                        int top_n, float s2, float inv_t,
-                                                        const int32_t* __restrict__ node,
-                                                        const int32_t* __restrict__ token,
-                                                        const LpPartial* __restrict__ part,
-                                                        const T* __restrict__ lane_max, float* __restrict__ logprob,
-                                                        float* __restrict__ entropy, int32_t* __restrict__ top_token,
-                                                        float* __restrict__ top_logprob, int32_t* __restrict__ status) {
+__device__ __forceinline__ void lp_fetch(uint4* dst, const T* row, int u, int lane, int V) {
     constexpr int VE = LpUnit<T>::VE;
-    __shared__ float s_m[kLpWarps], s_z[kLpWarps], s_t[kLpWarps];
-    __shared__ float s_sorted[kLpWarps * 32];
-    __shared__ int s_list[kLpLists];
-    __shared__ float s_cv[kLpCand];
-    __shared__ int s_ci[kLpCand];
-    __shared__ int s_nl, s_nc;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long i = blockIdx.x;
-    const int b = (int)(i / A);
-    const int r = node ? node[i] : (int)(i % A), tok = token[i];
-    int32_t* tt = top_token + i * top_n;
-    float* tl = top_logprob + i * top_n;
-    const bool outside = r >= N || (r >= 0 && tok >= V);
-    if (r < 0 || outside) {  // a padding entry, or one that names no row or no token
-        for (int j = tid; j < top_n; j += kLpThreads) {
-            tt[j] = -1;
-            tl[j] = 0.f;
+    const int lead = LpUnit<T>::lead(row), e0 = LpUnit<T>::entry(u, 0, lane, lead);
+    if (LpUnit<T>::whole(u, lead, V)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cp_async16(dst + j * 32 + lane, row + e0 + j * 32 * VE);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = e0 + j * 32 * VE;
+            if (e >= 0 && e + VE <= V) cp_async16(dst + j * 32 + lane, row + e);
         }
-        if (tid == 0) {
-            logprob[i] = 0.f;
-            if (entropy) entropy[i] = 0.f;
-            status[i] = outside ? DDT_ERR_INVALID_ARG : DDT_OK;
-        }
-        return;
     }
-    const T* row = logits + ((long long)b * N + r) * V;
+}
+// The words at the row's ends, which no copy brings, into their places.
+template <typename T>
+__device__ __forceinline__ void lp_ends(uint4* to, const T* row, int u, int lane, int V) {
+    constexpr int VE = LpUnit<T>::VE;
+    const int lead = LpUnit<T>::lead(row);
+    if (LpUnit<T>::whole(u, lead, V)) return;
+    const int e0 = LpUnit<T>::entry(u, 0, lane, lead);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int e = e0 + j * 32 * VE;
+        if (e < 0 || e + VE > V) to[j * 32 + lane] = lp_word(row, e, V);
+    }
+}
+__device__ __forceinline__ void lp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void lp_wait() {  // for the oldest of the stages
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLpStages - 1) : "memory");
+}
+
+// The top n of a row by one warp where the quick way does not do: few units, or many entries
+// at its bound (a masked row, say).  The n-th largest of the lanes' largest entries: fewer
+// than n lanes have entries above it, and of the entries that equal it the first n in order
+// are enough.
+template <typename T>
+__device__ __noinline__ void lp_top_slow(const T* __restrict__ row, const T* LM, int V, int nunits, int n, int lane,
+                                         float& bv, int& bi) {
+    constexpr int VE = LpUnit<T>::VE;
+    const int lead = LpUnit<T>::lead(row);
+    const VId none = vid_empty();
+    float best = -INFINITY;
+#pragma unroll 4
+    for (int u = 0; u < nunits; ++u) {
+        float v = to_f32(LM[u * 32 + lane]);
+        int id = lane, bid = lane;
+        if (!__any_sync(kFull, v > __shfl_sync(kFull, best, 31))) continue;
+        warp_sort_best_first(v, id);
+        warp_merge_best_first(best, bid, v, id);
+    }
+    const float tau = __shfl_sync(kFull, best, n - 1);
+    WarpTopK top;
+    top.init(32);
+    int equal = 0;
+    for (int u = 0; u < nunits; ++u) {
+        const float v = to_f32(LM[u * 32 + lane]);
+        const bool above = __any_sync(kFull, v > tau), same = __any_sync(kFull, v >= tau);
+        if (!above && (!same || equal >= n)) continue;
+        for (int j = 0; j < 8; ++j) {
+            const int e = LpUnit<T>::entry(u, j, lane, lead);
+            const uint4 w = lp_word(row, e, V);
+            int eq = 0;
+#pragma unroll
+            for (int q = 0; q < VE; ++q) {
+                const bool in = e + q >= 0 && e + q < V;
+                const float y = lp_at(w, q, static_cast<const T*>(nullptr));
+                const bool is = in && y == tau;
+                eq += is;
+                const bool take = (in && y > tau) || (is && equal < n);
+                if (__any_sync(kFull, take)) top.insert(take ? y : none.v, take ? e + q : none.id);
+            }
+            equal += __reduce_add_sync(kFull, eq);
+        }
+    }
+    bv = top.v;
+    bi = top.id;
+}
+
+// One row's results from its n_t shares (a multiple of 32), by the whole block.
+template <typename T>
+__device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T* __restrict__ row, const T* LM,
+                                          const float4* P, int n_t, int i) {
+    constexpr int VE = LpUnit<T>::VE, NT = kLpThreads, kWarps = kLpWarps;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int V = p.V, nunits = p.nunits, top_n = p.top_n, lead = LpUnit<T>::lead(row);
+    const int tok = p.token[i];
     const float xt = tok >= 0 ? to_f32(row[tok]) : 0.f;
-    const float4* P = reinterpret_cast<const float4*>(part + i * nunits);
-    // ---- the row's maximum, Z and sum 2^w w (a NaN sum stays NaN)
-    float m = -INFINITY;
-    for (int u = tid; u < nunits; u += kLpThreads) m = fmaxf(m, P[u].x);
+    // ---- the row's reference, and the threads' largest entries in order
+    float m = -INFINITY, best = -INFINITY;
+    int id = lane;
+    for (int u = tid; u < n_t; u += NT) {
+        const float4 x = P[u];
+        m = fmaxf(m, x.x);
+        best = fmaxf(best, x.w);
+    }
+    if (top_n && warp * 32 < n_t) warp_sort_best_first(best, id);
     m = redux_max(m);
-    if (lane == 0) s_m[warp] = m;
-    if (tid == 0) s_nl = s_nc = 0;
+    S.sorted[tid] = best;
+    if (lane == 0) S.m[warp] = m;
+    if (tid == 0) S.nl = S.nc = 0;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) m = fmaxf(m, s_m[w]);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, S.m[w]);
+    // ---- Z and sum 2^w w (a NaN sum stays NaN)
     float z = 0.f, t = 0.f;
-    for (int u = tid; u < nunits; u += kLpThreads) {
-        const float4 p = P[u];
-        if (p.y == 0.f) continue;
-        const float d = fmaxf((p.x - m) * s2, kLpLow), f = tc::ex2(d);
-        z = fmaf(f, p.y, z);
-        t = fmaf(f, fmaf(d, p.y, p.z), t);
+    for (int u = tid; u < n_t; u += NT) {
+        const float4 x = P[u];
+        if (x.y == 0.f) continue;
+        const float d = fmaxf((x.x - m) * p.s2, kLpLow), f = tc::ex2(d);
+        z = fmaf(f, x.y, z);
+        t = fmaf(f, fmaf(d, x.y, x.z), t);
     }
     z = warp_sum(z);
     t = warp_sum(t);
     if (lane == 0) {
-        s_z[warp] = z;
-        s_t[warp] = t;
+        S.z[warp] = z;
+        S.t[warp] = t;
     }
-    __syncthreads();
-    z = t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) {
-        z += s_z[w];
-        t += s_t[w];
-    }
-    if (!(z > 0.f)) {  // NaN, +inf, or nothing above -inf
-        for (int j = tid; j < top_n; j += kLpThreads) {
-            tt[j] = -1;
-            tl[j] = NAN;
-        }
-        if (tid == 0) {
-            logprob[i] = NAN;
-            if (entropy) entropy[i] = NAN;
-            status[i] = DDT_ERR_NONFINITE;
-        }
-        return;
-    }
-    const float LN2 = 0.6931471805599453f, lz = log2f(z);
-    if (tid == 0) {
-        logprob[i] = tok >= 0 ? (xt - m) * inv_t - lz * LN2 : 0.f;
-        if (entropy) entropy[i] = (lz - t / z) * LN2;
-        status[i] = DDT_OK;
-    }
-    if (top_n == 0) return;
-    // ---- a bound from below on the row's n-th best value: the n-th largest of the units'
-    //      largest entries, or of the threads' where there are few units (each of those n has
-    //      an entry that reaches it)
-    const T* LM = lane_max + i * nunits * 32;
-    const bool by_unit = nunits >= top_n;
-    float tm = -INFINITY;
-    if (by_unit) {
-        for (int u = tid; u < nunits; u += kLpThreads) tm = fmaxf(tm, P[u].x);
-    } else {
-        for (int x = tid * VE; x < nunits * 32; x += kLpThreads * VE) {
-            const uint4 v = *reinterpret_cast<const uint4*>(LM + x);
-#pragma unroll
-            for (int q = 0; q < VE; ++q) tm = fmaxf(tm, lp_at(v, q, static_cast<const T*>(nullptr)));
-        }
-    }
-    float sv = tm;
-    int si = lane;
-    warp_sort_best_first(sv, si);
-    s_sorted[warp * 32 + lane] = sv;
-    __syncthreads();
+    // ---- a bound from below on the row's n-th best value: the n-th largest of the threads'
+    //      largest entries (each of those n has an entry that reaches it); the (unit, thread)
+    //      pairs that reach it
     float tau = -INFINITY;
-    {
-        int at = 0;
-        float head = lane < kLpWarps ? s_sorted[lane * 32] : -INFINITY;
-        for (int n = 0; n < top_n; ++n) {
-            tau = redux_max(head);
-            const unsigned who = __ballot_sync(kFull, head == tau);
-            if (lane == __ffs(who) - 1) head = ++at < 32 ? s_sorted[lane * 32 + at] : -INFINITY;
-        }
-    }
-    // ---- the lanes that reach it, and their entries that do
-    const int lead = LpUnit<T>::lead(row);
-    if (by_unit) {  // a warp looks at the lanes of one unit at a time
-        for (int u = warp; u < nunits; u += kLpWarps) {
-            if (!(P[u].x >= tau)) continue;
-            if (to_f32(LM[u * 32 + lane]) >= tau) {
-                const int at = atomicAdd(&s_nl, 1);
-                if (at < kLpLists) s_list[at] = u * 32 + lane;
-            }
-        }
-    } else if (tm >= tau) {
-        for (int x = tid * VE; x < nunits * 32; x += kLpThreads * VE) {
+    if (top_n) {
+        best = S.sorted[lane];
+        for (int w = 1; w < kWarps && w * 32 < n_t; ++w) warp_merge_best_first(best, id, S.sorted[w * 32 + lane], lane);
+        tau = __shfl_sync(kFull, best, top_n - 1);
+#pragma unroll 2
+        for (int x = tid * VE; x < nunits * 32; x += NT * VE) {
             const uint4 v = *reinterpret_cast<const uint4*>(LM + x);
 #pragma unroll
             for (int q = 0; q < VE; ++q)
                 if (lp_at(v, q, static_cast<const T*>(nullptr)) >= tau) {
-                    const int at = atomicAdd(&s_nl, 1);
-                    if (at < kLpLists) s_list[at] = x + q;
+                    const int at = atomicAdd(&S.nl, 1);
+                    if (at < kLpLists) S.list[at] = x + q;
                 }
         }
     }
     __syncthreads();
-    const int nl = s_nl;
-    if (nl <= kLpLists)
-        for (int x = tid; x < nl * 8; x += kLpThreads) {
-            const int l = s_list[x >> 3];
+    z = t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        z += S.z[w];
+        t += S.t[w];
+    }
+    int32_t* tt = p.top_token + (long long)i * top_n;
+    float* tl = p.top_logprob + (long long)i * top_n;
+    const bool bad = !(z > 0.f);  // NaN, +inf, or nothing above -inf
+    const float LN2 = 0.6931471805599453f, lz = log2f(z);
+    if (tid == 0) {
+        p.logprob[i] = bad ? NAN : (tok >= 0 ? (xt - m) * p.inv_t - lz * LN2 : 0.f);
+        if (p.entropy) p.entropy[i] = bad ? NAN : (lz - t / z) * LN2;
+        p.status[i] = bad ? DDT_ERR_NONFINITE : DDT_OK;
+    }
+    if (bad && tid < top_n) {
+        tt[tid] = -1;
+        tl[tid] = NAN;
+    }
+    if (bad || top_n == 0) return;  // the same for the whole block
+    // ---- their entries that reach it, ranked by one warp
+    const int nl = S.nl;
+    if (nl <= kLpLists) {
+#pragma unroll 2
+        for (int x = tid; x < nl * 8; x += NT) {
+            const int l = S.list[x >> 3];
             const int e = LpUnit<T>::entry(l >> 5, x & 7, l & 31, lead);
             const uint4 v = lp_word(row, e, V);
 #pragma unroll
             for (int q = 0; q < VE; ++q) {
                 const float y = lp_at(v, q, static_cast<const T*>(nullptr));
                 if (y >= tau && e + q >= 0 && e + q < V) {
-                    const int at = atomicAdd(&s_nc, 1);
+                    const int at = atomicAdd(&S.nc, 1);
                     if (at < kLpCand) {
-                        s_cv[at] = y;
-                        s_ci[at] = e + q;
+                        S.cv[at] = y;
+                        S.ci[at] = e + q;
                     }
                 }
             }
         }
+    }
     __syncthreads();
+    if (warp) return;
     const VId none = vid_empty();
+    const int nc = S.nc;
     float bv = none.v;
     int bi = none.id;
-    if (nl > kLpLists || s_nc > kLpCand) {
-        // many entries tie with the bound (a masked row, say): every warp ranks its part of
-        // the whole row, and the first warp merges the warps' lists
-        WarpTopK k;
-        k.init(32);
-        for (int e0 = warp * 32 * VE - lead; e0 < V; e0 += kLpThreads * VE) {
-            const int e = e0 + lane * VE;
-            const uint4 v = lp_word(row, e, V);
-            float most = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < VE; ++q) most = fmaxf(most, lp_at(v, q, static_cast<const T*>(nullptr)));
-            const float last = __shfl_sync(kFull, k.v, 31);
-            const int last_id = __shfl_sync(kFull, k.id, 31);
-            if (__any_sync(kFull, most > last || (most == last && e < last_id)))
-#pragma unroll
-                for (int q = 0; q < VE; ++q) {
-                    const bool in = e + q >= 0 && e + q < V;
-                    k.insert(in ? lp_at(v, q, static_cast<const T*>(nullptr)) : none.v, in ? e + q : none.id);
-                }
-        }
-        __syncthreads();
-        s_cv[warp * 32 + lane] = k.v;
-        s_ci[warp * 32 + lane] = k.id;
-        __syncthreads();
-        if (warp) return;
-        bv = k.v;
-        bi = k.id;
-        for (int w = 1; w < kLpWarps; ++w) warp_merge_best_first(bv, bi, s_cv[w * 32 + lane], s_ci[w * 32 + lane]);
-    } else {
-        if (warp) return;
-        const int nc = s_nc;
-        for (int c0 = 0; c0 < nc; c0 += 32) {
-            float cv = c0 + lane < nc ? s_cv[c0 + lane] : none.v;
-            int ci = c0 + lane < nc ? s_ci[c0 + lane] : none.id;
+    if (nl <= kLpLists && nc <= kLpCand) {
+        for (int x = 0; x < nc; x += 32) {
+            float cv = x + lane < nc ? S.cv[x + lane] : none.v;
+            int ci = x + lane < nc ? S.ci[x + lane] : none.id;
             warp_sort_best_first(cv, ci);
             warp_merge_best_first(bv, bi, cv, ci);
         }
+    } else {
+        lp_top_slow<T>(row, LM, V, nunits, top_n, lane, bv, bi);
     }
     if (lane < top_n) {
         tt[lane] = bi;
-        tl[lane] = (bv - m) * inv_t - lz * LN2;
+        tl[lane] = (bv - m) * p.inv_t - lz * LN2;
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) k_token_logprobs(const T* __restrict__ logits, T* lane_max, const LpArgs p) {
+    extern __shared__ __align__(16) uint4 s_ring[];  // [kLpWarps][kLpStages][256]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int cl, rank;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int i = blockIdx.x / cl;
+    if (!lp_asked(p, i)) {  // the whole cluster
+        if (rank == 0) lp_padding(p, i, threadIdx.x);
+        return;
+    }
+    const T* row = lp_row(p, logits, i);
+    const int V = p.V, nunits = p.nunits, wid = rank * kLpWarps + warp, n_w = cl * kLpWarps;
+    uint4* ring = s_ring + warp * kLpStages * 256;
+    T* LM = lane_max + (long long)i * nunits * 32;
+    int fu = wid, stage = 0;
+    auto fetch = [&](int s) {
+        if (fu < nunits) lp_fetch<T>(ring + s * 256, row, fu, lane, V);
+        fu += n_w;
+        lp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kLpStages; ++s) fetch(s);
+    LpRun run;
+    run.start();
+    for (int u = wid; u < nunits; u += n_w) {
+        uint4* at = ring + stage * 256;
+        lp_wait();
+        lp_ends<T>(at, row, u, lane, V);
+        const float mt = lp_add<T>(run, at + lane, p.s2);
+        fetch(stage);
+        if (p.top_n) LM[u * 32 + lane] = from_f32<T>(mt);
+        stage = stage + 1 == kLpStages ? 0 : stage + 1;
+    }
+    float4* P = p.part + (long long)i * n_w * 32;
+    P[wid * 32 + lane] = lp_share(run, p.s2);
+    // the shares of all CTAs are visible to the cluster's first one
+    if (cl > 1) {
+        tc::cluster_sync();
+        if (rank) return;
+    } else {
+        __syncthreads();
+    }
+    // every copy has landed and been read: the ring becomes the scratch
+    lp_finish<T>(p, *reinterpret_cast<LpScratch*>(s_ring), row, LM, P, n_w * 32, i);
 }
 
 template <typename T>
@@ -477,23 +544,33 @@ static cudaError_t lp_go(int B, int N, int V, int A, int top_n, float temperatur
                          const int32_t* node, const int32_t* token, float* logprob, float* entropy,
                          int32_t* top_token, float* top_logprob, int32_t* status, void* ws, cudaStream_t st) {
     const int nunits = lp_units(V, sizeof(T)), rows = B * A;
-    LpPartial* part = static_cast<LpPartial*>(ws);
-    T* lane_max = top_n > 0 ? reinterpret_cast<T*>(static_cast<unsigned char*>(ws) +
-                                                   al256((size_t)rows * nunits * sizeof(LpPartial)))
-                            : nullptr;
-    const float s2 = (float)(1.4426950408889634 / (double)temperature);
-    const T* x = static_cast<const T*>(logits);
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    const LpArgs a{rows,  N,     V,       A,       nunits,    top_n,       (float)(1.4426950408889634 / (double)temperature),
+                   (float)(1.0 / (double)temperature), node, token, reinterpret_cast<float4*>(w), logprob, entropy,
+                   top_token, top_logprob, status};
+    T* lane_max = reinterpret_cast<T*>(w + lp_part_bytes(rows));
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long want = ((long long)rows * nunits + kLpWarps - 1) / kLpWarps;
-    const int grid = (int)(want < (long long)kLpCtas * sms ? want : (long long)kLpCtas * sms);
-    k_lp_unit<T><<<counted(grid), kLpThreads, 0, st>>>(x, rows, N, V, A, nunits, s2, node, part, lane_max);
-    cudaError_t e = cudaGetLastError();
+    if (sms > 256) sms = 256;
+    constexpr int ring = kLpWarps * kLpStages * 4096;
+    static_assert(kLpCtas * (ring + 1024) <= 228 * 1024 && sizeof(LpScratch) <= ring, "shared memory of an SM");
+    // as many CTAs a row as are resident together; of a walk's entries half or more are padding
+    int cl = 1;
+    while (cl < 8 && rows * 2LL * cl <= (node ? 2LL : 1LL) * kLpCtas * sms && cl * kLpWarps < nunits) cl *= 2;
+    const cudaError_t e = cudaFuncSetAttribute(k_token_logprobs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
-    k_lp_join<T><<<counted((unsigned)rows), kLpThreads, 0, st>>>(x, N, V, A, nunits, top_n, s2,
-                                                               (float)(1.0 / (double)temperature), node, token, part, lane_max,
-                                                               logprob, entropy, top_token, top_logprob, status);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(counted((unsigned)rows * cl));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = ring;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cl;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_token_logprobs<T>, static_cast<const T*>(logits), lane_max, a);
 }
 
 cudaError_t launch_token_logprobs(int B, int N, int V, int A, int top_n, float temperature, ddt_dtype dtype,

@@ -572,24 +572,36 @@ def ddt_commit_paged(acc_nodes, acc_len, prefix_len, block_table, *, k_tree, v_t
 
 
 # ------------------------------------------------------------------ single-token decode
+# These calls are made once a token and finish in a few microseconds, so their argument
+# checks are kept short: _at() is one pass over a tensor's properties and gives its address.
 def _here(t, name):
     """The calls enqueue on the current device's current stream: refuse tensors of another one."""
-    if t.device.index != torch.cuda.current_device():
-        raise DDTError(f"{name} is on {t.device}, not on the current device")
-    return t.device
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise DDTError(f"{name} is on {t.device}, not on the current CUDA device")
+    return dev
 
 
-def _need_on(dev, t, shape, dtype, name):
-    _need(t, shape, dtype, name)
-    if t.device != dev:
-        raise DDTError(f"{name} is on {t.device}, expected {dev}")
-    return t
+def _at(t, dev, shape, dtype, name):
+    """The address of a contiguous tensor of this shape and type on device `dev`."""
+    if t is None:
+        raise DDTError(f"{name} is required")
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, shape, dtype, name)
+        raise DDTError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
 
 
-def _ws_bytes(dev, ws):
-    if ws.device != dev or not ws.is_contiguous():
-        raise DDTError(f"workspace must be a contiguous tensor on {dev}")
-    return ws.numel() * ws.element_size()
+def _ws_at(dev, ws):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise DDTError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _code(dtype, name):
+    if dtype not in _DT:
+        raise DDTError(f"{name} has dtype {dtype}, expected one of {list(_DT)}")
+    return _DT[dtype]
 
 
 def decode_attn_paged_workspace(q, k_pages, block_table, *, weights=False):
@@ -606,43 +618,42 @@ def ddt_decode_attn_paged(q, k_new, v_new, k_pages, v_pages, block_table, prefix
     """One new token a request: q [L][B][Hq][d]; k/v_new [L][B][Hkv][d] (its own row, not in the cache; or both
     None); k/v_pages [L][num_pages][Hkv][page_size][d]; block_table [B][max_pages] int32.  attn_weight, if given:
     [L][B][Hkv][max_pages * page_size] fp32, the running sums the rows' softmax weights are added to, in place."""
-    lib = _gpu()
+    lib = _lib or _gpu()
     L, B, Hq, d = q.shape
-    num_pages, Hkv, page = k_pages.shape[1], k_pages.shape[2], k_pages.shape[3]
+    _, num_pages, Hkv, page, _ = pages = k_pages.shape
     max_pages = block_table.shape[1]
-    dt, dev = q.dtype, _here(q, "q")
-    if dt not in _DT:
-        raise DDTError(f"q has dtype {dt}, expected one of {list(_DT)}")
-    _need_on(dev, q, (L, B, Hq, d), dt, "q")
-    if (k_new is None) != (v_new is None):
-        raise DDTError("k_new and v_new are given together or not at all")
-    if k_new is not None:
-        _need_on(dev, k_new, (L, B, Hkv, d), dt, "k_new")
-        _need_on(dev, v_new, (L, B, Hkv, d), dt, "v_new")
-    _need_on(dev, k_pages, (L, num_pages, Hkv, page, d), dt, "k_pages")
-    _need_on(dev, v_pages, (L, num_pages, Hkv, page, d), dt, "v_pages")
-    _need_on(dev, block_table, (B, max_pages), torch.int32, "block_table")
-    _need_on(dev, prefix_len, (B,), torch.int32, "prefix_len")
-    if attn_weight is not None:
-        _need_on(dev, attn_weight, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
-    if out is not None:
-        out_dtype = out_dtype or out.dtype
-        o = _need_on(dev, out, (L, B, Hq, d), out_dtype, "out")
-    else:
-        out_dtype = out_dtype or dt
-        o = torch.empty((L, B, Hq, d), dtype=out_dtype, device=dev)
-    if out_dtype not in _DT:
-        raise DDTError(f"out has dtype {out_dtype}, expected one of {list(_DT)}")
-    st = _need_on(dev, status, (B,), torch.int32, "status") if status is not None else \
-        torch.empty((B,), dtype=torch.int32, device=dev)
+    dev, dt = _here(q, "q"), q.dtype
+    in_code = _code(dt, "q")
+    heads = (L, B, Hq, d)
+    pq = _at(q, dev, heads, dt, "q")
+    pk = pv = None
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise DDTError("k_new and v_new are given together or not at all")
+        pk = _at(k_new, dev, (L, B, Hkv, d), dt, "k_new")
+        pv = _at(v_new, dev, (L, B, Hkv, d), dt, "v_new")
+    pkp = _at(k_pages, dev, (L, num_pages, Hkv, page, d), dt, "k_pages")
+    pvp = _at(v_pages, dev, pages, dt, "v_pages")
+    ptab = _at(block_table, dev, (B, max_pages), torch.int32, "block_table")
+    plen = _at(prefix_len, dev, (B,), torch.int32, "prefix_len")
+    pw = None if attn_weight is None else _at(attn_weight, dev, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
+    if out is None:
+        out = torch.empty(heads, dtype=out_dtype or dt, device=q.device)
+    out_dtype = out_dtype or out.dtype
+    out_code = _code(out_dtype, "out")
+    po = _at(out, dev, heads, out_dtype, "out")
+    if status is None:
+        status = torch.empty((B,), dtype=torch.int32, device=q.device)
+    pst = _at(status, dev, (B,), torch.int32, "status")
     if workspace is None:
         workspace = decode_attn_paged_workspace(q, k_pages, block_table, weights=attn_weight is not None)
-    rc = lib.ddt_decode_attn_paged(L, B, Hq, Hkv, d, page, num_pages, max_pages, _DT[dt], _DT[out_dtype], _ptr(q),
-                                   _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
-                                   _ptr(prefix_len), float(scale), _ptr(o), _ptr(attn_weight), _ptr(st),
-                                   _ptr(workspace), _ws_bytes(dev, workspace), _stream())
-    _check(rc, "ddt_decode_attn_paged")
-    return {"o": o, "status": st}
+    pws, ws_bytes = _ws_at(dev, workspace)
+    rc = lib.ddt_decode_attn_paged(L, B, Hq, Hkv, d, page, num_pages, max_pages, in_code, out_code, pq, pk, pv, pkp, pvp,
+                                   ptab, plen, scale, po, pw, pst, pws, ws_bytes,
+                                   torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check(rc, "ddt_decode_attn_paged")
+    return {"o": out, "status": status}
 
 
 # ------------------------------------------------------------------------------ eviction
@@ -659,29 +670,31 @@ def ddt_evict_paged(k_pages, v_pages, block_table, prefix_len, n_placed, seq_len
     """In place: cuts every request's cache to its `keep` rows of the largest attn_weight (the first n_sink and
     the last n_recent positions before all others); updates the pages, prefix_len, n_placed [B], and attn_weight
     (fp32) and row_pos (int32) [L][B][Hkv][max_pages * page_size].  seq_len [B] is read only."""
-    lib = _gpu()
-    L, num_pages, Hkv, page, d = k_pages.shape
+    lib = _lib or _gpu()
+    L, num_pages, Hkv, page, d = pages = k_pages.shape
     B, max_pages = block_table.shape
-    dt, dev = k_pages.dtype, _here(k_pages, "k_pages")
-    if dt not in _DT:
-        raise DDTError(f"k_pages has dtype {dt}, expected one of {list(_DT)}")
-    _need_on(dev, k_pages, (L, num_pages, Hkv, page, d), dt, "k_pages")
-    _need_on(dev, v_pages, (L, num_pages, Hkv, page, d), dt, "v_pages")
-    _need_on(dev, block_table, (B, max_pages), torch.int32, "block_table")
-    for t, name in ((prefix_len, "prefix_len"), (n_placed, "n_placed"), (seq_len, "seq_len")):
-        _need_on(dev, t, (B,), torch.int32, name)
-    _need_on(dev, attn_weight, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
-    _need_on(dev, row_pos, (L, B, Hkv, max_pages * page), torch.int32, "row_pos")
-    st = _need_on(dev, status, (B,), torch.int32, "status") if status is not None else \
-        torch.empty((B,), dtype=torch.int32, device=dev)
+    dev, dt = _here(k_pages, "k_pages"), k_pages.dtype
+    code = _code(dt, "k_pages")
+    rows = (L, B, Hkv, max_pages * page)
+    pk = _at(k_pages, dev, pages, dt, "k_pages")
+    pv = _at(v_pages, dev, pages, dt, "v_pages")
+    ptab = _at(block_table, dev, (B, max_pages), torch.int32, "block_table")
+    plen = _at(prefix_len, dev, (B,), torch.int32, "prefix_len")
+    pnp = _at(n_placed, dev, (B,), torch.int32, "n_placed")
+    psq = _at(seq_len, dev, (B,), torch.int32, "seq_len")
+    pw = _at(attn_weight, dev, rows, torch.float32, "attn_weight")
+    prp = _at(row_pos, dev, rows, torch.int32, "row_pos")
+    if status is None:
+        status = torch.empty((B,), dtype=torch.int32, device=k_pages.device)
+    pst = _at(status, dev, (B,), torch.int32, "status")
     if workspace is None:
         workspace = evict_paged_workspace(k_pages, block_table)
-    rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, _ptr(block_table), _DT[dt], int(keep),
-                             int(n_sink), int(n_recent), _ptr(k_pages), _ptr(v_pages), _ptr(seq_len),
-                             _ptr(attn_weight), _ptr(row_pos), _ptr(prefix_len), _ptr(n_placed), _ptr(st),
-                             _ptr(workspace), _ws_bytes(dev, workspace), _stream())
-    _check(rc, "ddt_evict_paged")
-    return {"status": st}
+    pws, ws_bytes = _ws_at(dev, workspace)
+    rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, ptab, code, keep, n_sink, n_recent, pk, pv, psq, pw,
+                             prp, plen, pnp, pst, pws, ws_bytes, torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check(rc, "ddt_evict_paged")
+    return {"status": status}
 
 
 # --------------------------------------------------------------------- log probabilities
@@ -697,34 +710,38 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
                        workspace=None):
     """Log probabilities of token [B][A] under rows node [B][A] (None: row a, A = N) of target_logits [B][N][V],
     the rows' entropies (nats) and their top_n tokens.  A walk's acc_nodes and emitted fit as node and token."""
-    lib = _gpu()
+    lib = _lib or _gpu()
     B, N, V = target_logits.shape
     A = token.shape[1]
-    dt, dev = target_logits.dtype, _here(target_logits, "target_logits")
-    if dt not in _DT:
-        raise DDTError(f"target_logits has dtype {dt}, expected one of {list(_DT)}")
-    _need_on(dev, target_logits, (B, N, V), dt, "target_logits")
-    _need_on(dev, token, (B, A), torch.int32, "token")
+    dev, dt = _here(target_logits, "target_logits"), target_logits.dtype
+    code = _code(dt, "target_logits")
+    px = _at(target_logits, dev, (B, N, V), dt, "target_logits")
+    each = (B, A)
+    pt = _at(token, dev, each, torch.int32, "token")
+    pn = None
     if node is not None:
-        _need_on(dev, node, (B, A), torch.int32, "node")
+        pn = _at(node, dev, each, torch.int32, "node")
     elif A != N:
         raise DDTError(f"token has {A} entries a request, expected {N} (one a row) without node")
-    top_n = int(top_n)
-    want = {"logprob": ((B, A), torch.float32), "entropy": ((B, A), torch.float32),
-            "status": ((B, A), torch.int32)}
-    if top_n > 0:
-        want["top_token"] = ((B, A, top_n), torch.int32)
-        want["top_logprob"] = ((B, A, top_n), torch.float32)
     o = out or {}
     res = {}
-    for name, (shape, dtype) in want.items():
+
+    def give(name, shape, dtype):
         t = o.get(name)
-        res[name] = _need_on(dev, t, shape, dtype, name) if t is not None else torch.empty(shape, dtype=dtype, device=dev)
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=token.device)
+        res[name] = t
+        return _at(t, dev, shape, dtype, name)
+    plp, pen = give("logprob", each, torch.float32), give("entropy", each, torch.float32)
+    ptt = ptl = None
+    if top_n > 0:
+        ptt, ptl = give("top_token", (B, A, top_n), torch.int32), give("top_logprob", (B, A, top_n), torch.float32)
+    pst = give("status", each, torch.int32)
     if workspace is None:
         workspace = token_logprobs_workspace(target_logits, token, top_n=top_n)
-    rc = lib.ddt_token_logprobs(B, N, V, A, top_n, float(temperature), _DT[dt], _ptr(target_logits), _ptr(node),
-                                _ptr(token), _ptr(res["logprob"]), _ptr(res["entropy"]), _ptr(res.get("top_token")),
-                                _ptr(res.get("top_logprob")), _ptr(res["status"]), _ptr(workspace),
-                                _ws_bytes(dev, workspace), _stream())
-    _check(rc, "ddt_token_logprobs")
+    pws, ws_bytes = _ws_at(dev, workspace)
+    rc = lib.ddt_token_logprobs(B, N, V, A, top_n, temperature, code, px, pn, pt, plp, pen, ptt, ptl, pst, pws, ws_bytes,
+                                torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check(rc, "ddt_token_logprobs")
     return res
