@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams
     constexpr int kSets = kSimtThreads / (D / 4);  // row sets of the value phase
     __shared__ __align__(16) float s_q[HBS][D];
     __shared__ __align__(16) float s_p[HBS][kDecTile];
+    __shared__ __align__(16) float s_sum[(D == 64 ? kSets / 2 : kSets) * 4 * D];
     __shared__ long long s_row[kDecTile];
     __shared__ float s_m[HBS], s_l[HBS], s_f[HBS];
     __shared__ int s_bad;
@@ -187,20 +188,33 @@ __global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams
                 }
             }
         }
-        // ---- the segment's partial: the row sets' sums, through the query array (done with)
+        // ---- the segment's partial: the row sets' sums, four heads at a time, a warp's own two
+        //      sets (head size 64) by a shuffle
         const long long slot = dec_unit(p, w) + blockIdx.x;
-        const int c4 = (tid % (D / 4)) * 4, set = tid / (D / 4);
-        for (int s = 0; s < kSets; ++s) {
+        constexpr int kLeft = D == 64 ? kSets / 2 : kSets;  // sets that go through shared memory
+        const int c4 = (tid % (D / 4)) * 4, set = D == 64 ? warp : tid / (D / 4);
+#pragma unroll
+        for (int h4 = 0; h4 < HBS; h4 += 4) {
             __syncthreads();
-            if (set == s) {
 #pragma unroll
-                for (int h = 0; h < HBS; ++h)
+            for (int h = 0; h < 4; ++h) {
+                float v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s_q[h][c4 + i] = acc[h][i] + (s ? s_q[h][c4 + i] : 0.f);
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = acc[h4 + h][i];
+                    if (D == 64) v[i] += __shfl_xor_sync(kFull, v[i], 16);
+                }
+                if (D != 64 || lane < 16)
+                    *reinterpret_cast<float4*>(s_sum + (set * 4 + h) * D + c4) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            __syncthreads();
+            for (int e = tid; e < 4 * D; e += kSimtThreads) {
+                float o = 0.f;
+#pragma unroll
+                for (int s = 0; s < kLeft; ++s) o += s_sum[s * 4 * D + e];
+                if (h4 + e / D < nh) p.part_o[(slot * p.HT + h4) * D + e] = o;
             }
         }
-        __syncthreads();
-        for (int e = tid; e < nh * D; e += kSimtThreads) p.part_o[slot * p.HT * D + e] = s_q[e / D][e % D];
         if (tid < nh) p.part_ml[slot * p.HT + tid] = make_float2(s_m[tid], s_bad ? kSegBadPage : s_l[tid]);
     }
 }
@@ -214,32 +228,33 @@ struct HeadJoin {
 };
 
 template <typename Tin, int D>
-__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, long long lb, int hq, int lane) {
-    const int b = (int)(lb % p.B), P = p.prefix_len[b];
+__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, int lane) {
+    const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
+    // loads that do not wait for one another first
+    const int P = p.prefix_len[b];
+    const long long pre = p.pre[b], all = p.pre[p.B];
+    float s = 0.f;
+    if (p.k_new) {
+        const Tin* q = static_cast<const Tin*>(p.q) + ((long long)lb * p.Hq + hq) * D;
+        const Tin* k = static_cast<const Tin*>(p.k_new) + ((long long)lb * p.Hkv + g) * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) s = fmaf(to_f32(q[e * 32 + lane]), to_f32(k[e * 32 + lane]), s);
+    }
     HeadJoin j;
     j.ref = j.z = 0.f;
-    j.tn = -INFINITY;
+    j.tn = p.k_new ? warp_sum(s) * p.scale_log2 : -INFINITY;
     j.ns = 0;
     j.first = 0;
     j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
     if (j.err) return j;
-    const int g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
-    if (p.k_new) {
-        const Tin* q = static_cast<const Tin*>(p.q) + (lb * p.Hq + hq) * D;
-        const Tin* k = static_cast<const Tin*>(p.k_new) + (lb * p.Hkv + g) * D;
-        float s = 0.f;
-#pragma unroll
-        for (int e = lane; e < D; e += 32) s = fmaf(to_f32(q[e]), to_f32(k[e]), s);
-        j.tn = warp_sum(s) * p.scale_log2;
-    }
     const int nt = dec_tiles(P, p.cap);
     if (nt > 0) {
         const int HH = p.Hkv * p.HB;
-        const long long all = p.pre[p.B], T = all * HH * p.L;
-        const long long first = (lb / p.B) * all * HH + p.pre[b] * HH + (long long)(g * p.HB + hb) * nt;
+        const long long T = all * HH * p.L;
+        const long long first = l * all * HH + pre * HH + (long long)(g * p.HB + hb) * nt;
         const int C = (int)min((long long)p.C, T), c0 = dec_owner(T, C, first);
         j.ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
-        j.first = lb * HH + g * p.HB + hb + c0;
+        j.first = (long long)lb * HH + g * p.HB + hb + c0;
     }
     const float2* ml = p.part_ml + j.first * p.HT + h;
     float m = j.tn, low = 0.f;
@@ -262,20 +277,19 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, long long l
 }
 
 // Blocks below n_join: WPH warps a head (1, or 8 where a head has many segments), O of the
-// head.  The others: the weight sums of 1024 rows at a time of one (layer, request, kv head).
+// head.  The others: the weight sums of some rows of one (layer, request, kv head).
 template <typename Tin, typename Tout, int D, int WPH>
-__global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, unsigned n_join, int chunks) {
+__global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, unsigned n_join, int chunks) {
     constexpr int E = D / 32;
     extern __shared__ float s_x[];  // [8][D] sums of the warps of a head, or 3 floats a head of a group
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the partials are there from here on
     if (blockIdx.x < n_join) {
-        const long long x = WPH == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
-        const long long lb = x / p.Hq;
-        const int hq = (int)(x % p.Hq);
-        if (x >= (long long)p.L * p.B * p.Hq) return;  // (WPH 1: whole warps, no barrier follows)
+        const unsigned x = WPH == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
+        const int lb = (int)(x / p.Hq), hq = (int)(x - (unsigned)lb * p.Hq);
+        if (lb >= p.L * p.B) return;  // (WPH 1: whole warps, no barrier follows)
         const HeadJoin j = head_join<Tin, D>(p, lb, hq, lane);
-        Tout* out = static_cast<Tout*>(p.o) + x * D;
+        Tout* out = static_cast<Tout*>(p.o) + (long long)x * D;
         if (j.err) {
             if (WPH == 1 || warp == 0) {
 #pragma unroll
@@ -290,7 +304,7 @@ __global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, uns
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         if (p.k_new && (WPH == 1 || warp == 0)) {
             const float w = tc::ex2(j.tn - j.ref);
-            const Tin* v = static_cast<const Tin*>(p.v_new) + (lb * p.Hkv + g) * D;
+            const Tin* v = static_cast<const Tin*>(p.v_new) + ((long long)lb * p.Hkv + g) * D;
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = w * to_f32(v[e * 32 + lane]);
         }
@@ -320,12 +334,13 @@ __global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, uns
         return;
     }
     const unsigned y = blockIdx.x - n_join;
-    const long long lbg = y / chunks;
-    const int g = (int)(lbg % p.Hkv);
-    const long long lb = lbg / p.Hkv;
+    const int lbg = (int)(y / chunks), part = (int)(y - (unsigned)lbg * chunks), lb = lbg / p.Hkv, g = lbg - lb * p.Hkv;
     float* s_ref = s_x;
     float* s_inv = s_ref + p.G;
     float* s_tn = s_inv + p.G;
+    const int P = p.prefix_len[lb % p.B];
+    // blocks behind the unit's rows (the first also has the new token's)
+    if (part && part * 1024LL >= P) return;
     int bad = 0;
     for (int h = warp; h < p.G; h += 8) {
         const HeadJoin j = head_join<Tin, D>(p, lb, g * p.G + h, lane);
@@ -337,19 +352,24 @@ __global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, uns
         }
     }
     if (__syncthreads_or(bad)) return;
-    const int P = p.prefix_len[lb % p.B];
-    const float* sc = p.score + (lb * p.Hq + (long long)g * p.G) * p.cap;
-    float* wt = p.weight + lbg * p.cap;
-    for (int r = ((int)(y % chunks) * 256 + tid) * 4; r < P; r += chunks * 1024) {
+    const float* sc = p.score + ((long long)lb * p.Hq + g * p.G) * p.cap;
+    float* wt = p.weight + (long long)lbg * p.cap;
+    for (int r = (part * 256 + tid) * 4; r < P; r += chunks * 1024) {
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int h = 0; h < p.G; ++h) {  // the rows are padded to whole pages: r + 3 < cap
-            const float4 t = *reinterpret_cast<const float4*>(sc + (long long)h * p.cap + r);
-            const float ref = s_ref[h], inv = s_inv[h];
-            sum.x = fmaf(tc::ex2(t.x - ref), inv, sum.x);
-            sum.y = fmaf(tc::ex2(t.y - ref), inv, sum.y);
-            sum.z = fmaf(tc::ex2(t.z - ref), inv, sum.z);
-            sum.w = fmaf(tc::ex2(t.w - ref), inv, sum.w);
+        for (int h0 = 0; h0 < p.G; h0 += 4) {  // four heads' scores are in flight
+            float4 t[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)  // the rows are padded to whole pages: r + 3 < cap
+                if (h0 + h < p.G) t[h] = *reinterpret_cast<const float4*>(sc + (long long)(h0 + h) * p.cap + r);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (h0 + h < p.G) {
+                    const float ref = s_ref[h0 + h], inv = s_inv[h0 + h];
+                    sum.x = fmaf(tc::ex2(t[h].x - ref), inv, sum.x);
+                    sum.y = fmaf(tc::ex2(t[h].y - ref), inv, sum.y);
+                    sum.z = fmaf(tc::ex2(t[h].z - ref), inv, sum.z);
+                    sum.w = fmaf(tc::ex2(t[h].w - ref), inv, sum.w);
+                }
         }
         if (r + 3 < P) {
             float4 w = *reinterpret_cast<float4*>(wt + r);
@@ -360,7 +380,7 @@ __global__ void __launch_bounds__(256) k_decode_finish(const DecodeParams p, uns
             if (r + 2 < P) wt[r + 2] += sum.z;
         }
     }
-    if (p.k_new && P < p.cap && y % chunks == 0 && tid == 0) {  // the new token's own row
+    if (p.k_new && P < p.cap && part == 0 && tid == 0) {  // the new token's own row
         float sum = 0.f;
         for (int h = 0; h < p.G; ++h) sum = fmaf(tc::ex2(s_tn[h] - s_ref[h]), s_inv[h], sum);
         wt[P] += sum;
@@ -424,8 +444,10 @@ template <typename Tin, typename Tout, int D, int WPH>
 static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st) {
     const size_t heads = (size_t)p.L * p.B * p.Hq;
     const unsigned n_join = (unsigned)(WPH == 1 ? (heads + 7) / 8 : heads), units = (unsigned)p.L * p.B * p.Hkv;
-    const unsigned most = (p.cap + 1023) / 1024, want = 6u * sms / units + 1;
-    const int chunks = (int)(most < want ? most : want);
+    // 2048 rows a block, so that long requests get more of them; not too many for units that may
+    // be short
+    const unsigned most = (p.cap + 2047) / 2048, room = 24u * sms / units + 1;
+    const int chunks = (int)(most < room ? most : room);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(counted(n_join + (p.weight ? units * chunks : 0)));
     cfg.blockDim = dim3(256);

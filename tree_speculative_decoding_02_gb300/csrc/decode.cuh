@@ -58,8 +58,14 @@ struct DecodeWalk {
 
 // First tile of CTA c, and the CTA that owns tile x, of T tiles over C CTAs, every one of
 // which has a tile (where T < C the CTAs from T on have none: C is then T).
-__device__ __forceinline__ long long dec_first(long long T, int C, int c) { return T * c / C; }
-__device__ __forceinline__ int dec_owner(long long T, int C, long long x) { return (int)(((x + 1) * C - 1) / T); }
+// (A 64-bit division takes about 100 instructions; ordinary calls fit in 32 bits.)
+__device__ __forceinline__ long long dec_first(long long T, int C, int c) {
+    return T <= 0xffffffffu / (unsigned)C ? (unsigned)T * (unsigned)c / (unsigned)C : T * c / C;
+}
+__device__ __forceinline__ int dec_owner(long long T, int C, long long x) {
+    return T <= 0xffffffffu / (unsigned)C ? (int)(((unsigned)(x + 1) * (unsigned)C - 1u) / (unsigned)T)
+                                          : (int)(((x + 1) * C - 1) / T);
+}
 
 // All threads of the block: finds this CTA's run.  CTA 0 also writes pre[] and the statuses.
 template <int NT>

@@ -582,6 +582,11 @@ def _here(t, name):
     return dev
 
 
+# the current stream's handle of a device, without making a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _at(t, dev, shape, dtype, name):
     """The address of a contiguous tensor of this shape and type on device `dev`."""
     if t is None:
@@ -650,7 +655,7 @@ def ddt_decode_attn_paged(q, k_new, v_new, k_pages, v_pages, block_table, prefix
     pws, ws_bytes = _ws_at(dev, workspace)
     rc = lib.ddt_decode_attn_paged(L, B, Hq, Hkv, d, page, num_pages, max_pages, in_code, out_code, pq, pk, pv, pkp, pvp,
                                    ptab, plen, scale, po, pw, pst, pws, ws_bytes,
-                                   torch.cuda.current_stream().cuda_stream)
+                                   _raw_stream(dev))
     if rc:
         _check(rc, "ddt_decode_attn_paged")
     return {"o": out, "status": status}
@@ -691,7 +696,7 @@ def ddt_evict_paged(k_pages, v_pages, block_table, prefix_len, n_placed, seq_len
         workspace = evict_paged_workspace(k_pages, block_table)
     pws, ws_bytes = _ws_at(dev, workspace)
     rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, ptab, code, keep, n_sink, n_recent, pk, pv, psq, pw,
-                             prp, plen, pnp, pst, pws, ws_bytes, torch.cuda.current_stream().cuda_stream)
+                             prp, plen, pnp, pst, pws, ws_bytes, _raw_stream(dev))
     if rc:
         _check(rc, "ddt_evict_paged")
     return {"status": status}
@@ -741,7 +746,7 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
         workspace = token_logprobs_workspace(target_logits, token, top_n=top_n)
     pws, ws_bytes = _ws_at(dev, workspace)
     rc = lib.ddt_token_logprobs(B, N, V, A, top_n, temperature, code, px, pn, pt, plp, pen, ptt, ptl, pst, pws, ws_bytes,
-                                torch.cuda.current_stream().cuda_stream)
+                                _raw_stream(dev))
     if rc:
         _check(rc, "ddt_token_logprobs")
     return res
