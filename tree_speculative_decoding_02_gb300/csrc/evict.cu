@@ -53,40 +53,44 @@ struct EvictParams {
 __global__ void __launch_bounds__(kClaimThreads) k_evict_claim(const EvictParams p) {
     extern __shared__ uint32_t s_used[];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the selection may begin
     const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b];
     int st = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : ((np < 0 || np > P || sq < P) ? DDT_ERR_INVALID_ARG : DDT_OK);
     auto pages = [&](int rows) { return rows < 0 || rows > p.cap ? 0 : (rows + p.page_rows - 1) / p.page_rows; };
     const int32_t* mine = p.block_table + (long long)b * p.max_pages;
     const int n = st == DDT_ERR_CAPACITY ? 0 : pages(P);
-    int bad = 0;
-    for (int i = tid; i < n; i += kClaimThreads) bad |= mine[i] < 0 || mine[i] >= p.num_pages;
-    if (__syncthreads_or(bad)) st = DDT_ERR_INVALID_ARG;
-    if (st == DDT_OK && P > p.keep) {
-        int twice = 0;
-        for (int w0 = 0; w0 < p.num_pages; w0 += kWindow) {
-            const int len = min(kWindow, p.num_pages - w0);
-            auto marked = [&](int page, bool set) {
-                const unsigned at = (unsigned)(page - w0);
-                if (at >= (unsigned)len) return 0u;
-                const uint32_t bit = 1u << (at & 31);
-                return (set ? atomicOr(&s_used[at >> 5], bit) : s_used[at >> 5]) & bit;
-            };
+    const bool cut = st == DDT_OK && P > p.keep;
+    int bad = 0, twice = 0;
+    for (int w0 = 0; w0 < p.num_pages && (cut || w0 == 0); w0 += kWindow) {
+        const int len = min(kWindow, p.num_pages - w0);
+        auto marked = [&](int page, bool set) {
+            const unsigned at = (unsigned)(page - w0);
+            if (at >= (unsigned)len) return 0u;
+            const uint32_t bit = 1u << (at & 31);
+            return (set ? atomicOr(&s_used[at >> 5], bit) : s_used[at >> 5]) & bit;
+        };
+        if (cut)
             for (int i = tid; i < (len + 31) / 32; i += kClaimThreads) s_used[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += kClaimThreads) twice |= marked(mine[i], true) != 0;
-            __syncthreads();
-            for (int o = warp; o < p.B; o += kClaimThreads / 32) {
-                if (o == b) continue;
-                const int32_t* other = p.block_table + (long long)o * p.max_pages;
-                const int no = pages(p.prefix_len[o]);
-#pragma unroll 4
-                for (int i = lane; i < no; i += 32) twice |= marked(other[i], false) != 0;
-            }
-            __syncthreads();
+        __syncthreads();
+#pragma unroll 2
+        for (int i = tid; i < n; i += kClaimThreads) {
+            const int page = mine[i];
+            bad |= page < 0 || page >= p.num_pages;
+            if (cut) twice |= marked(page, true) != 0;
         }
-        st = __syncthreads_or(twice) ? (int)DDT_ERR_INVALID_ARG : kEvict;
+        __syncthreads();
+        if (!cut) break;
+        for (int o = warp; o < p.B; o += kClaimThreads / 32) {
+            const int32_t* other = p.block_table + (long long)o * p.max_pages;
+            const int no = o == b ? 0 : pages(p.prefix_len[o]);
+#pragma unroll 4
+            for (int i = lane; i < no; i += 32) twice |= marked(other[i], false) != 0;
+        }
+        __syncthreads();
     }
-    if (tid == 0) p.state[b] = st;
+    bad = __syncthreads_or(bad);
+    twice = __syncthreads_or(twice);
+    if (tid == 0) p.state[b] = st != DDT_OK ? st : (bad || twice ? (int)DDT_ERR_INVALID_ARG : (cut ? kEvict : (int)DDT_OK));
 }
 
 // The order of the rows as an unsigned key: 0 for NaN, then the sums from the smallest to
@@ -134,11 +138,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     const long long u = blockIdx.x;
     const int b = (int)(u / p.Hkv % p.B);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (p.state[b] != kEvict) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moves may be set up
+    const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b], K = p.keep;
+    // lengths that make no sense are refused by k_evict_claim, which may still be running: it
+    // has the last word before anything is written
+    const bool cut = P > K && P <= p.cap && np >= 0 && np <= P && sq >= P;
+    if (!cut) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (tid == 0) p.n_move[u] = 0;
         return;
     }
-    const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b], K = p.keep;
     float* wt = p.weight + u * p.cap;
     int32_t* rp = p.row_pos + u * p.cap;
     const int32_t* table = p.block_table + (long long)b * p.max_pages;
@@ -256,6 +265,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
             break;
         }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.state[b] != kEvict) {
+        if (tid == 0) p.n_move[u] = 0;
+        return;
+    }
     // ---- in index order: holes below K, and the kept rows behind it that fill them.  A bit a
     //      row (above the limit, equal to it) by ballots, a thread a word of 32 rows for the
     //      counts, and a warp a word for the lists.
@@ -352,6 +366,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
 // A block moves 256 / pieces rows at a time, a thread 16 bytes of K and of V; the next
 // round's places are loaded while this one's rows are on their way.
 __global__ void __launch_bounds__(256, 8) k_evict_move(const EvictParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long u = blockIdx.x;
     const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv % p.B), l = (int)(u / p.Hkv / p.B);
     if (l == 0 && g == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
@@ -418,12 +433,27 @@ size_t evict_ws_bytes(int L, int B, int Hkv, const AttnPaging& pg) {
     return evict_layout(p, nullptr);
 }
 
+// a launch that may be set up while the kernel before it ends
+static cudaError_t launch_behind(void (*kernel)(EvictParams), dim3 grid, int threads, int smem, const EvictParams& p,
+                                 cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = counted(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int NT>
 static cudaError_t select_go(const EvictParams& p, unsigned units, int keys, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(k_evict_select<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
-    if (e == cudaSuccess) k_evict_select<NT, true><<<counted(units), NT, keys, st>>>(p);
-    return e;
+    return e != cudaSuccess ? e : launch_behind(k_evict_select<NT, true>, dim3(units), NT, keys, p, st);
 }
 
 cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging& pg, int keep, int n_sink,
@@ -463,14 +493,13 @@ cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging&
     // that several units share an SM and hide each other's barriers
     const bool wide = units <= 2u * sms || p.cap > 8192, cached = p.cap <= kSelCache;
     const int keys = cached ? (p.cap + 3) / 4 * 16 : 0;
-    if (!cached) k_evict_select<1024, false><<<counted(units), 1024, 0, st>>>(p);
+    if (!cached) e = launch_behind(k_evict_select<1024, false>, dim3(units), 1024, 0, p, st);
     else if (wide) e = select_go<1024>(p, units, keys, st);
     else e = select_go<256>(p, units, keys, st);
-    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     const int rows = 256 / (p.pieces < 256 ? p.pieces : 256);  // a block's
     const unsigned most = (unsigned)((p.most + rows - 1) / rows), want = 8u * sms / units + 1;
-    k_evict_move<<<counted(dim3(units, most < 1 ? 1 : (most < want ? most : want))), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_behind(k_evict_move, dim3(units, most < 1 ? 1 : (most < want ? most : want)), 256, 0, p, st);
 }
 
 }  // namespace ddt
