@@ -654,7 +654,7 @@ def ddt_decode_attn_paged(q, k_new, v_new, k_pages, v_pages, block_table, prefix
         workspace = decode_attn_paged_workspace(q, k_pages, block_table, weights=attn_weight is not None)
     pws, ws_bytes = _ws_at(dev, workspace)
     rc = lib.ddt_decode_attn_paged(L, B, Hq, Hkv, d, page, num_pages, max_pages, in_code, out_code, pq, pk, pv, pkp, pvp,
-                                   ptab, plen, scale, po, pw, pst, pws, ws_bytes,
+                                   ptab, plen, float(scale), po, pw, pst, pws, ws_bytes,
                                    _raw_stream(dev))
     if rc:
         _check(rc, "ddt_decode_attn_paged")
@@ -695,8 +695,8 @@ def ddt_evict_paged(k_pages, v_pages, block_table, prefix_len, n_placed, seq_len
     if workspace is None:
         workspace = evict_paged_workspace(k_pages, block_table)
     pws, ws_bytes = _ws_at(dev, workspace)
-    rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, ptab, code, keep, n_sink, n_recent, pk, pv, psq, pw,
-                             prp, plen, pnp, pst, pws, ws_bytes, _raw_stream(dev))
+    rc = lib.ddt_evict_paged(L, B, Hkv, d, page, num_pages, max_pages, ptab, code, int(keep), int(n_sink), int(n_recent), pk, pv,
+                             psq, pw, prp, plen, pnp, pst, pws, ws_bytes, _raw_stream(dev))
     if rc:
         _check(rc, "ddt_evict_paged")
     return {"status": status}
@@ -728,8 +728,7 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
         pn = _at(node, dev, each, torch.int32, "node")
     elif A != N:
         raise DDTError(f"token has {A} entries a request, expected {N} (one a row) without node")
-    o = out or {}
-    res = {}
+    o, res, top_n = out or {}, {}, int(top_n)
 
     def give(name, shape, dtype):
         t = o.get(name)
@@ -745,7 +744,7 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
     if workspace is None:
         workspace = token_logprobs_workspace(target_logits, token, top_n=top_n)
     pws, ws_bytes = _ws_at(dev, workspace)
-    rc = lib.ddt_token_logprobs(B, N, V, A, top_n, temperature, code, px, pn, pt, plp, pen, ptt, ptl, pst, pws, ws_bytes,
+    rc = lib.ddt_token_logprobs(B, N, V, A, top_n, float(temperature), code, px, pn, pt, plp, pen, ptt, ptl, pst, pws, ws_bytes,
                                 _raw_stream(dev))
     if rc:
         _check(rc, "ddt_token_logprobs")

@@ -162,6 +162,12 @@ class Round:
             ddt.ddt_walk_accept(t["token"], t["parent"], t["n_nodes"], self.A - 1, target_logits=self.target_logits,
                                 out=self.walk, workspace=self.walk_ws, flat=bool(self.cfg.get("flat", False)))
 
+    def emitted_logprobs(self, top_n=0):
+        """Log probabilities of the round's emitted tokens (accepted ones and the bonus) under the
+        target, their rows' entropies and top_n alternatives; after the walk."""
+        return ddt.ddt_token_logprobs(self.target_logits, self.walk["emitted"], node=self.walk["acc_nodes"], top_n=top_n,
+                                      temperature=self.temperature or 1.0)
+
     def attention(self):
         """The round's attention call.  With cfg["rope"] (rotated channels) q and the tree
         keys are taken before rotary embedding: the keys are rotated in place at their
