@@ -14,9 +14,10 @@
 //   warp 0      producer: block-table entries, TMA of K and V tiles (128 rows, 128-byte
 //               swizzle, a box a page slice, a lane a box) into one ring, Q by TMA
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
-//   warps 2-5   softmax: a thread a cached row; the tile's maximum of each head by a warp
-//               reduction and one exchange; O is rescaled only when a maximum grows by
-//               more than 2^8.  At a segment's end the same warps write its partial.
+//   warps 2-5   softmax: a thread a cached row.  The exponents' reference of a head is the
+//               maximum of the segment's first tile, and moves (with O rescaled) only when a
+//               score is 2^8 above it: one vote a tile instead of its maxima.  At a segment's
+//               end the same warps write its partial.
 // Up to eight heads and head sizes 64 and 128: two CTAs an SM, each with half the ring, so
 // that one's softmax chain (about 2000 cycles a tile, as long as an SM's share of HBM takes
 // for 32 KB) hides behind the other's.
@@ -75,6 +76,17 @@ __device__ __forceinline__ float redux_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// barrier of the 128 softmax threads that also tells whether any of them passed true
+__device__ __forceinline__ bool bar_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // 16 consecutive 32-bit columns of this thread's lane
@@ -277,8 +289,8 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                 // a warp that gave up still takes part in the barriers
                 if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
                 ok = __all_sync(kFull, ok);
-                float t[HP], mine = -INFINITY;
-                float* x = xm + (j & 1) * 4 * HP;
+                float t[HP];
+                bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
                     uint32_t sr[NQ];
@@ -289,10 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
 #pragma unroll
                     for (int h = 0; h < HP; ++h) {
                         t[h] = r < n ? __uint_as_float(sr[h]) * p.scale_log2 : -INFINITY;
-                        if (h < nh) {
-                            const float v = redux_max(t[h]);
-                            if (lane == h) mine = v;
-                        }
+                        if (h < nh) above |= t[h] > m[h] + kTau;
                     }
                     if (p.score && r < n) {
                         float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y + r;
@@ -301,54 +310,53 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                             if (h < nh) sc[(long long)h * p.cap] = t[h];
                     }
                 }
-                if (lane < HP) x[ws * HP + lane] = mine;
-                tc::named_bar(1, 128);
+                if (bar_any(1, above)) {
+                    // the segment's first tile, or a growing maximum: new references, the tile's
+                    // maxima, for the heads that need them
+                    float* x = xm + (j & 1) * 4 * HP;
+                    float mine = -INFINITY;
+                    if (ok)
+#pragma unroll
+                        for (int h = 0; h < HP; ++h)
+                            if (h < nh) {
+                                const float v = redux_max(t[h]);
+                                if (lane == h) mine = v;
+                            }
+                    if (lane < HP) x[ws * HP + lane] = mine;
+                    tc::named_bar(1, 128);
+                    if (ok) {
+                        float f[HP];
+#pragma unroll
+                        for (int h = 0; h < HP; ++h) {
+                            const float mt = fmaxf(fmaxf(x[h], x[HP + h]), fmaxf(x[2 * HP + h], x[3 * HP + h]));
+                            f[h] = 1.f;
+                            if (mt > m[h] + kTau) {
+                                f[h] = tc::ex2(m[h] - mt);
+                                l[h] *= f[h];
+                                m[h] = mt;
+                            }
+                        }
+                        if (i > 0) {  // O holds earlier tiles of the segment: once their P V are done
+                            ok = __all_sync(kFull, tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort));
+                            if (ok) {
+                                tc::tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < kMB * NP; c += 16) {
+                                    uint32_t o[16];
+                                    const uint32_t at = tmem + lane_base + Cfg::kOCol + c;
+                                    tmem_ld16(at, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(c + e) % HP]);
+                                    tc::tmem_st16(at, o);
+                                }
+                                tc::tmem_wait_st();
+                            }
+                        }
+                    }
+                }
                 if (!ok) continue;
-                float mt[HP];
-#pragma unroll
-                for (int h = 0; h < HP; h += 4) {
-                    float4 v = *reinterpret_cast<const float4*>(x + h);
-#pragma unroll
-                    for (int q = 1; q < 4; ++q) {
-                        const float4 o = *reinterpret_cast<const float4*>(x + q * HP + h);
-                        v = make_float4(fmaxf(v.x, o.x), fmaxf(v.y, o.y), fmaxf(v.z, o.z), fmaxf(v.w, o.w));
-                    }
-                    mt[h] = v.x;
-                    mt[h + 1] = v.y;
-                    mt[h + 2] = v.z;
-                    mt[h + 3] = v.w;
-                }
-                bool grow = false;
-#pragma unroll
-                for (int h = 0; h < HP; ++h) grow |= mt[h] > m[h] + kTau;  // the same in all 128 threads
-                if (grow) {
-                    float f[HP];
-#pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        f[h] = 1.f;
-                        if (mt[h] > m[h] + kTau) {
-                            f[h] = tc::ex2(m[h] - mt[h]);
-                            l[h] *= f[h];
-                            m[h] = mt[h];
-                        }
-                    }
-                    if (i > 0) {  // O holds earlier tiles of the segment: once their P V are done
-                        ok = __all_sync(kFull, tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort));
-                        if (!ok) continue;
-                        tc::tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < kMB * NP; c += 16) {
-                            uint32_t o[16];
-                            const uint32_t at = tmem + lane_base + Cfg::kOCol + c;
-                            tmem_ld16(at, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(c + e) % HP]);
-                            tc::tmem_st16(at, o);
-                        }
-                        tc::tmem_wait_st();
-                    }
-                }
                 // the P buffer is free once P V of tile j - 2 is done
                 ok = __all_sync(kFull, tc::mbar_wait(p_free + (j & 1), ((j >> 1) & 1) ^ 1, abort));
                 if (!ok) continue;
