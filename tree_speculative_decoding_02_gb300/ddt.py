@@ -574,39 +574,41 @@ def ddt_commit_paged(acc_nodes, acc_len, prefix_len, block_table, *, k_tree, v_t
 # ------------------------------------------------------------------ single-token decode
 # These calls are made once a token and finish in a few microseconds, so their argument
 # checks are kept short: _at() is one pass over a tensor's properties and gives its address.
+# The two handles below are torch.cuda.current_device() and current_stream(dev).cuda_stream
+# without the Python objects around them.
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_I32 = torch.int32
+
+
 def _here(t, name):
     """The calls enqueue on the current device's current stream: refuse tensors of another one."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _device_now():
         raise DDTError(f"{name} is on {t.device}, not on the current CUDA device")
     return dev
 
 
-# the current stream's handle of a device, without making a Stream object
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
 def _at(t, dev, shape, dtype, name):
     """The address of a contiguous tensor of this shape and type on device `dev`."""
-    if t is None:
-        raise DDTError(f"{name} is required")
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _need(t, shape, dtype, name)
-        raise DDTError(f"{name} is on {t.device}, expected cuda:{dev}")
-    return t.data_ptr()
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, shape, dtype, name)
+    raise DDTError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _ws_at(dev, ws):
     if ws.get_device() != dev or not ws.is_contiguous():
         raise DDTError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _code(dtype, name):
-    if dtype not in _DT:
+    code = _DT.get(dtype)
+    if code is None:
         raise DDTError(f"{name} has dtype {dtype}, expected one of {list(_DT)}")
-    return _DT[dtype]
+    return code
 
 
 def decode_attn_paged_workspace(q, k_pages, block_table, *, weights=False):
@@ -639,17 +641,18 @@ def ddt_decode_attn_paged(q, k_new, v_new, k_pages, v_pages, block_table, prefix
         pv = _at(v_new, dev, (L, B, Hkv, d), dt, "v_new")
     pkp = _at(k_pages, dev, (L, num_pages, Hkv, page, d), dt, "k_pages")
     pvp = _at(v_pages, dev, pages, dt, "v_pages")
-    ptab = _at(block_table, dev, (B, max_pages), torch.int32, "block_table")
-    plen = _at(prefix_len, dev, (B,), torch.int32, "prefix_len")
+    ptab = _at(block_table, dev, (B, max_pages), _I32, "block_table")
+    each = (B,)
+    plen = _at(prefix_len, dev, each, _I32, "prefix_len")
     pw = None if attn_weight is None else _at(attn_weight, dev, (L, B, Hkv, max_pages * page), torch.float32, "attn_weight")
     if out is None:
         out = torch.empty(heads, dtype=out_dtype or dt, device=q.device)
     out_dtype = out_dtype or out.dtype
-    out_code = _code(out_dtype, "out")
+    out_code = in_code if out_dtype is dt else _code(out_dtype, "out")
     po = _at(out, dev, heads, out_dtype, "out")
     if status is None:
-        status = torch.empty((B,), dtype=torch.int32, device=q.device)
-    pst = _at(status, dev, (B,), torch.int32, "status")
+        status = torch.empty(each, dtype=_I32, device=q.device)
+    pst = _at(status, dev, each, _I32, "status")
     if workspace is None:
         workspace = decode_attn_paged_workspace(q, k_pages, block_table, weights=attn_weight is not None)
     pws, ws_bytes = _ws_at(dev, workspace)
@@ -683,15 +686,15 @@ def ddt_evict_paged(k_pages, v_pages, block_table, prefix_len, n_placed, seq_len
     rows = (L, B, Hkv, max_pages * page)
     pk = _at(k_pages, dev, pages, dt, "k_pages")
     pv = _at(v_pages, dev, pages, dt, "v_pages")
-    ptab = _at(block_table, dev, (B, max_pages), torch.int32, "block_table")
-    plen = _at(prefix_len, dev, (B,), torch.int32, "prefix_len")
-    pnp = _at(n_placed, dev, (B,), torch.int32, "n_placed")
-    psq = _at(seq_len, dev, (B,), torch.int32, "seq_len")
+    ptab = _at(block_table, dev, (B, max_pages), _I32, "block_table")
+    plen = _at(prefix_len, dev, (B,), _I32, "prefix_len")
+    pnp = _at(n_placed, dev, (B,), _I32, "n_placed")
+    psq = _at(seq_len, dev, (B,), _I32, "seq_len")
     pw = _at(attn_weight, dev, rows, torch.float32, "attn_weight")
-    prp = _at(row_pos, dev, rows, torch.int32, "row_pos")
+    prp = _at(row_pos, dev, rows, _I32, "row_pos")
     if status is None:
         status = torch.empty((B,), dtype=torch.int32, device=k_pages.device)
-    pst = _at(status, dev, (B,), torch.int32, "status")
+    pst = _at(status, dev, (B,), _I32, "status")
     if workspace is None:
         workspace = evict_paged_workspace(k_pages, block_table)
     pws, ws_bytes = _ws_at(dev, workspace)
@@ -722,10 +725,10 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
     code = _code(dt, "target_logits")
     px = _at(target_logits, dev, (B, N, V), dt, "target_logits")
     each = (B, A)
-    pt = _at(token, dev, each, torch.int32, "token")
+    pt = _at(token, dev, each, _I32, "token")
     pn = None
     if node is not None:
-        pn = _at(node, dev, each, torch.int32, "node")
+        pn = _at(node, dev, each, _I32, "node")
     elif A != N:
         raise DDTError(f"token has {A} entries a request, expected {N} (one a row) without node")
     o, res, top_n = out or {}, {}, int(top_n)
