@@ -7,7 +7,7 @@
 // heads of its kv head, and the call is bound by reading the cache once.
 //
 //   k_decode_tc     grid C (decode_tc.cu): the tiles of a CTA's run on the tensor cores, bf16.
-//   k_decode_simt   grid C: the same on the CUDA cores, fp32.
+//   k_decode_simt   grid C: the same on the CUDA cores, fp32 caches.
 //   k_decode_finish join: a head's partials with the new token's own row,
 //                     O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s;
 //                   and, from the scores the split kernel left, sum_h 2^(t_h(p) - M_h) / Z_h
@@ -22,200 +22,265 @@ namespace ddt {
 namespace {
 constexpr int kSimtThreads = 256;
 constexpr int kSimtWarps = kSimtThreads / 32;
-constexpr int kSimtMaxCtas = 1024;
+constexpr int kSimtMaxCtas = 512;
 }  // namespace
 
-// 16 bytes of a row as floats.
-__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[4], const float*) {
-    v[0] = __uint_as_float(u.x);
-    v[1] = __uint_as_float(u.y);
-    v[2] = __uint_as_float(u.z);
-    v[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[8], const __nv_bfloat16*) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-// Four consecutive elements as floats.
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = a.z;
-    v[3] = a.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
-    v[0] = __uint_as_float(a.x << 16);
-    v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16);
-    v[3] = __uint_as_float(a.y & 0xffff0000u);
-}
+// Tiles of 32 KB of K and V (R rows), three on their way by cp.async; two barriers a tile.
+//   scores   D / 16 lanes a row, 16 channels a lane, all heads; the sums over the lanes scatter
+//            the heads over them, so a lane ends up with the scores (and the exponentials) of
+//            its row for a few heads
+//   values   a thread owns four channels and four consecutive rows of the tile
+// As in the tensor-core kernel the exponents' reference moves only when a score is 2^8 above it.
+template <int D, int HBS>
+struct SimtCfg {
+    static constexpr int R = 4096 / D;                       // rows a tile
+    static constexpr int LPR = D / 16;                       // lanes a row
+    static constexpr int kStages = D == 256 && HBS == 16 ? 2 : 3;
+    static constexpr int NV = HBS > LPR ? HBS / LPR : 1;     // heads a lane ends up with
+    static constexpr int kSets = kSimtThreads / (D / 4);     // row sets of the values
+    static constexpr int kLeft = D == 64 ? kSets / 2 : kSets;  // of them through shared memory at a segment's end
+    static constexpr int kQ = HBS * D > 1024 ? HBS * D : 1024;  // floats: the queries, then those sums
+    static constexpr int kSumHeads = kQ / (kLeft * D) < HBS ? kQ / (kLeft * D) : HBS;  // heads at a time
+    static constexpr int kSmem = kStages * 32768 + kQ * 4 + 2 * HBS * R * 4;
+    static_assert(2 * (kSmem + 2048) <= 228 * 1024 && kSumHeads >= 1 && HBS % kSumHeads == 0, "shared memory");
+};
 
-// One tile of 128 rows at a time, three phases between barriers:
-//   scores   eight lanes a row: each takes every eighth 16-byte piece of the K row and of
-//            the queries (shared memory, fp32), three shuffles add up the eight
-//   softmax  a warp a head: tile maximum, running reference, exponentials, sum
-//   values   a thread owns four channels and every (1024 / D)-th row of the tile
-template <typename T, int D, int HBS>
-__global__ void __launch_bounds__(kSimtThreads) k_decode_simt(const DecodeParams p) {
-    constexpr int VE = 16 / (int)sizeof(T);
-    constexpr int kVec = D / (8 * VE);           // 16-byte pieces a lane takes of a row
-    constexpr int kSets = kSimtThreads / (D / 4);  // row sets of the value phase
-    __shared__ __align__(16) float s_q[HBS][D];
-    __shared__ __align__(16) float s_p[HBS][kDecTile];
-    __shared__ __align__(16) float s_sum[(D == 64 ? kSets / 2 : kSets) * 4 * D];
-    __shared__ long long s_row[kDecTile];
-    __shared__ float s_m[HBS], s_l[HBS], s_f[HBS];
-    __shared__ int s_bad;
+template <int D, int HBS>
+__global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodeParams p) {
+    using Cfg = SimtCfg<D, HBS>;
+    constexpr int R = Cfg::R, LPR = Cfg::LPR, NV = Cfg::NV, kStages = Cfg::kStages;
+    extern __shared__ __align__(16) float s_ring[];   // [kStages][K, V][R][D]
+    float* s_q = s_ring + kStages * 8192;             // [HBS][D]
+    float* s_p = s_q + Cfg::kQ;                       // [HBS][R] exponentials
+    float* s_t = s_p + HBS * R;                       // [HBS][R] scores
+    __shared__ float s_m[HBS], s_f[HBS], s_l[kSimtWarps][HBS];
+    __shared__ long long s_row[4][R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const T* kp = static_cast<const T*>(p.k_pages);
-    const T* vp = static_cast<const T*>(p.v_pages);
+    const float* kp = static_cast<const float*>(p.k_pages);
+    const float* vp = static_cast<const float*>(p.v_pages);
     DecodeWalk w = dec_plan<kSimtThreads>(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_decode_finish may be set up
-    for (; w.left > 0; dec_next(p, w)) {
-        const int g = w.g / p.HB, h0 = (w.g % p.HB) * HBS, nh = min(HBS, p.G - h0);
-        const T* q = static_cast<const T*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D;
-        __syncthreads();  // the previous segment is done with shared memory
-        for (int e = tid; e < HBS * D; e += kSimtThreads) s_q[e / D][e % D] = e < nh * D ? to_f32(q[e]) : 0.f;
-        if (tid < HBS) {
-            s_m[tid] = -INFINITY;
-            s_l[tid] = 0.f;
+
+    // ---- the copies, kStages - 1 tiles ahead of the sums, and one tile ahead of them the rows'
+    //      places: the tile at row fy of segment f
+    DecodeWalk f = w;
+    auto seg_end = [&](const DecodeWalk& x) { return min(x.P, (x.t + dec_seg_tiles(x)) * kDecTile); };
+    int fy = f.t * kDecTile, seg_f = 0, seg_w = 0;
+    int bad_bits = 0;  // bit (segment & 31): this thread met a page that does not exist
+    uint32_t there = 0;  // bit slot: it holds a tile's places
+    auto places = [&](int slot) {
+        there &= ~(1u << slot);
+        if (f.left <= 0) return;
+        there |= 1u << slot;
+        const int end = seg_end(f), y = fy + tid;
+        if (tid < R) {
+            long long row = -1;  // not there: zeros
+            if (y < end) {
+                const int lp = y / p.page_rows, phys = p.block_table[(long long)f.b * p.max_pages + lp];
+                if (phys >= 0 && phys < p.num_pages)
+                    row = ((((long long)f.l * p.num_pages + phys) * p.Hkv + f.g / p.HB) * p.page_rows + (y - lp * p.page_rows)) * D;
+                else
+                    bad_bits |= 1 << (seg_f & 31);
+            }
+            s_row[slot][tid] = row;
         }
-        if (tid == 0) s_bad = 0;
-        float acc[HBS][4];
+        fy += R;
+        if (fy >= end) {
+            dec_next(p, f);
+            fy = f.t * kDecTile;
+            ++seg_f;
+        }
+    };
+    auto fetch = [&](int stage, int slot) {
+        if (there >> slot & 1u) {
+            const uint32_t dst = tc::smem_u32(s_ring + stage * 8192 + tid * 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = tid + q * kSimtThreads;
+                const long long row = s_row[slot][e / (D / 4)];
+                const uint32_t n = row >= 0 ? 16 : 0, to = dst + q * kSimtThreads * 16;
+                const long long at = (row >= 0 ? row : 0) + (e % (D / 4)) * 4;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(kp + at), "r"(n) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + R * D * 4), "l"(vp + at), "r"(n) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) places(s);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(s, s);
+    int stage = 0, slot = kStages - 1;  // the next tile's places
+
+    const int r = tid / LPR, lr = tid % LPR;           // scores: this lane's row and place in it
+    const int c4 = (tid % (D / 4)) * 4, set = tid / (D / 4);  // values: channels, rows 4 set ..
+    int hb = 0;  // scores: first of the heads this lane ends up with
+#pragma unroll
+    for (int o = LPR / 2, nv = HBS; o > 0; o >>= 1)
+        if (nv > 1) {
+            nv >>= 1;
+            if (lane & o) hb += nv;
+        }
+    // of lanes with the same heads (fewer heads than lanes) the first one counts
+    const bool owner = HBS >= LPR || (lr % (LPR / (HBS < LPR ? HBS : LPR))) == 0;
+    for (; w.left > 0; dec_next(p, w), ++seg_w) {
+        const int g = w.g / p.HB, h0 = (w.g % p.HB) * HBS, nh = min(HBS, p.G - h0), end = seg_end(w);
+        const float* q = static_cast<const float*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D;
+        __syncthreads();  // the previous segment is done with shared memory
+        for (int e = tid; e < HBS * D; e += kSimtThreads) s_q[e] = e < nh * D ? q[e] : 0.f;
+        if (tid < HBS) s_m[tid] = -INFINITY;
+        float acc[HBS][4], l[NV];
 #pragma unroll
         for (int h = 0; h < HBS; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[h][i] = 0.f;
-        const int n_seg = dec_seg_tiles(w);
-        for (int j = 0; j < n_seg; ++j) {
-            const int y = (w.t + j) * kDecTile, n = min(kDecTile, w.P - y);
-            __syncthreads();
-            if (tid < kDecTile) {
-                long long row = -1;
-                if (tid < n) {
-                    const int lp = (y + tid) / p.page_rows, in = (y + tid) % p.page_rows;
-                    const int phys = p.block_table[(long long)w.b * p.max_pages + lp];
-                    if (phys < 0 || phys >= p.num_pages) s_bad = 1;
-                    else row = ((((long long)w.l * p.num_pages + phys) * p.Hkv + g) * p.page_rows + in) * D;
-                }
-                s_row[tid] = row;
-            }
-            __syncthreads();
-            // ---- scores
-#pragma unroll 2
-            for (int r0 = warp * 4; r0 < kDecTile; r0 += kSimtWarps * 4) {
-                const int r = r0 + (lane >> 3);
-                const long long row = s_row[r];
-                float kv[kVec][VE];
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (row >= 0) u = ld_stream_u4(kp + row + ((lane & 7) + 8 * i) * VE);
-                    unpack16(u, kv[i], static_cast<const T*>(nullptr));
-                }
+        for (int v = 0; v < NV; ++v) l[v] = 0.f;
+        for (int y = w.t * kDecTile; y < end; y += R) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncthreads();  // everyone's copies have landed, and the tile before is done with
+            fetch((stage + kStages - 1) % kStages, slot);
+            slot = (slot + 1) & 3;
+            places(slot);
+            const float* K = s_ring + stage * 8192;
+            const float* V = K + R * D;
+            stage = (stage + 1) % kStages;
+            // ---- scores
+            float s[HBS];
+#pragma unroll
+            for (int h = 0; h < HBS; ++h) s[h] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // (head size 64: rows of the other parity take the pieces in another order, so
+                // that the two rows of a quarter warp are in different banks)
+                const int c = (lr + LPR * (D == 64 ? i ^ (r & 1) : i)) * 4;
+                const float4 k = *reinterpret_cast<const float4*>(K + r * D + c);
 #pragma unroll
                 for (int h = 0; h < HBS; ++h) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) s = fmaf(kv[i][e], s_q[h][((lane & 7) + 8 * i) * VE + e], s);
-                    s += __shfl_xor_sync(kFull, s, 1);
-                    s += __shfl_xor_sync(kFull, s, 2);
-                    s += __shfl_xor_sync(kFull, s, 4);
-                    if ((lane & 7) == 0) s_p[h][r] = row >= 0 ? s * p.scale_log2 : -INFINITY;
+                    const float4 x = *reinterpret_cast<const float4*>(s_q + h * D + c);
+                    s[h] = fmaf(k.x, x.x, fmaf(k.y, x.y, fmaf(k.z, x.z, fmaf(k.w, x.w, s[h]))));
                 }
             }
-            __syncthreads();
-            // ---- softmax
-            if (p.score) {
-                float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y;
-                for (int e = tid; e < kDecTile * nh; e += kSimtThreads)
-                    if (e % kDecTile < n) sc[(long long)(e / kDecTile) * p.cap + e % kDecTile] = s_p[e / kDecTile][e % kDecTile];
+#pragma unroll
+            for (int o = LPR / 2, nv = HBS; o > 0; o >>= 1) {
+                if (nv > 1) {
+                    nv >>= 1;
+#pragma unroll
+                    for (int v = 0; v < HBS / 2; ++v)
+                        if (v < nv) {
+                            const float send = (lane & o) ? s[v] : s[v + nv], keep = (lane & o) ? s[v + nv] : s[v];
+                            s[v] = keep + __shfl_xor_sync(kFull, send, o);
+                        }
+                } else {
+                    s[0] += __shfl_xor_sync(kFull, s[0], o);
+                }
+            }
+            bool above = false;
+            float e[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float m = s_m[hb + v];
+                s[v] = y + r < end ? s[v] * p.scale_log2 : -INFINITY;
+                above |= s[v] > m + 8.f;
+                e[v] = tc::ex2(s[v] - m);
+                if (owner) {
+                    s_p[(hb + v) * R + r] = e[v];
+                    if (p.score) s_t[(hb + v) * R + r] = s[v];
+                }
+            }
+            if (__syncthreads_or(above)) {
+                // the segment's first tile, or a growing maximum: new references
+                if (owner)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) s_t[(hb + v) * R + r] = s[v];
+                __syncthreads();
+                for (int h = warp; h < HBS; h += kSimtWarps) {
+                    float m = -INFINITY;
+                    for (int x = lane; x < R; x += 32) m = fmaxf(m, s_t[h * R + x]);
+                    m = warp_max(m);
+                    const float old = s_m[h];
+                    __syncwarp();
+                    if (lane == 0) {
+                        s_f[h] = m > old + 8.f ? tc::ex2(old - m) : 1.f;
+                        if (m > old + 8.f) s_m[h] = m;
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    e[v] = tc::ex2(s[v] - s_m[hb + v]);
+                    l[v] *= s_f[hb + v];
+                    if (owner) s_p[(hb + v) * R + r] = e[v];
+                }
+#pragma unroll
+                for (int h = 0; h < HBS; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[h][i] *= s_f[h];
                 __syncthreads();
             }
-            for (int h = warp; h < HBS; h += kSimtWarps) {
-                float v[kDecTile / 32], mt = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kDecTile / 32; ++i) {
-                    v[i] = s_p[h][lane + 32 * i];
-                    mt = fmaxf(mt, v[i]);
-                }
-                mt = warp_max(mt);
-                const float m0 = s_m[h], m1 = fmaxf(m0, mt);
-                const float ref = m1 == -INFINITY ? 0.f : m1;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < kDecTile / 32; ++i) {
-                    v[i] = tc::ex2(v[i] - ref);
-                    sum += v[i];
-                    s_p[h][lane + 32 * i] = v[i];
-                }
-                sum = warp_sum(sum);
-                __syncwarp();
-                if (lane == 0) {
-                    const float f = m0 == -INFINITY ? 0.f : tc::ex2(m0 - m1);
-                    s_f[h] = f;
-                    s_l[h] = s_l[h] * f + sum;
-                    s_m[h] = m1;
-                }
+            for (int v = 0; v < NV; ++v) l[v] += e[v];
+            if (p.score) {
+                float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y;
+                const int n = min(R, end - y);
+                for (int x = tid; x < nh * R; x += kSimtThreads)
+                    if (x % R < n) sc[(long long)(x / R) * p.cap + x % R] = s_t[x];
             }
-            __syncthreads();
             // ---- values
+            float4 v4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v4[i] = *reinterpret_cast<const float4*>(V + (set * 4 + i) * D + c4);
 #pragma unroll
             for (int h = 0; h < HBS; ++h) {
-                const float f = s_f[h];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[h][i] *= f;
-            }
-            const int c4 = (tid % (D / 4)) * 4;
-#pragma unroll 4
-            for (int r = tid / (D / 4); r < n; r += kSets) {
-                const long long row = s_row[r];
-                float vv[4] = {0.f, 0.f, 0.f, 0.f};
-                if (row >= 0) load4(vp + row + c4, vv);
-#pragma unroll
-                for (int h = 0; h < HBS; ++h) {
-                    const float pr = s_p[h][r];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[h][i] = fmaf(pr, vv[i], acc[h][i]);
-                }
+                const float4 x = *reinterpret_cast<const float4*>(s_p + h * R + set * 4);
+                acc[h][0] = fmaf(x.x, v4[0].x, fmaf(x.y, v4[1].x, fmaf(x.z, v4[2].x, fmaf(x.w, v4[3].x, acc[h][0]))));
+                acc[h][1] = fmaf(x.x, v4[0].y, fmaf(x.y, v4[1].y, fmaf(x.z, v4[2].y, fmaf(x.w, v4[3].y, acc[h][1]))));
+                acc[h][2] = fmaf(x.x, v4[0].z, fmaf(x.y, v4[1].z, fmaf(x.z, v4[2].z, fmaf(x.w, v4[3].z, acc[h][2]))));
+                acc[h][3] = fmaf(x.x, v4[0].w, fmaf(x.y, v4[1].w, fmaf(x.z, v4[2].w, fmaf(x.w, v4[3].w, acc[h][3]))));
             }
         }
-        // ---- the segment's partial: the row sets' sums, four heads at a time, a warp's own two
-        //      sets (head size 64) by a shuffle
+        // ---- the segment's partial: sums of the exponentials over the rows of a warp, then of
+        //      the warps; the row sets' O a few heads at a time, a warp's own two sets (head
+        //      size 64) by a shuffle
         const long long slot = dec_unit(p, w) + blockIdx.x;
-        constexpr int kLeft = D == 64 ? kSets / 2 : kSets;  // sets that go through shared memory
-        const int c4 = (tid % (D / 4)) * 4, set = D == 64 ? warp : tid / (D / 4);
 #pragma unroll
-        for (int h4 = 0; h4 < HBS; h4 += 4) {
-            __syncthreads();
+        for (int v = 0; v < NV; ++v) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float v[4];
+            for (int o = LPR; o < 32; o <<= 1) l[v] += __shfl_xor_sync(kFull, l[v], o);
+            if (lane < LPR && owner) s_l[warp][hb + v] = l[v];
+        }
+        const int bad = __syncthreads_or(bad_bits >> (seg_w & 31) & 1);
+        bad_bits &= ~(1 << (seg_w & 31));
+#pragma unroll
+        for (int h4 = 0; h4 < HBS; h4 += Cfg::kSumHeads) {
+            if (h4) __syncthreads();
+            const int to = D == 64 ? warp : set;
+#pragma unroll
+            for (int h = 0; h < Cfg::kSumHeads; ++h) {
+                float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = acc[h4 + h][i];
-                    if (D == 64) v[i] += __shfl_xor_sync(kFull, v[i], 16);
+                    x[i] = acc[h4 + h][i];
+                    if (D == 64) x[i] += __shfl_xor_sync(kFull, x[i], 16);
                 }
                 if (D != 64 || lane < 16)
-                    *reinterpret_cast<float4*>(s_sum + (set * 4 + h) * D + c4) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(s_q + (to * Cfg::kSumHeads + h) * D + c4) = make_float4(x[0], x[1], x[2], x[3]);
             }
             __syncthreads();
-            for (int e = tid; e < 4 * D; e += kSimtThreads) {
+            for (int x = tid; x < Cfg::kSumHeads * D; x += kSimtThreads) {
                 float o = 0.f;
 #pragma unroll
-                for (int s = 0; s < kLeft; ++s) o += s_sum[s * 4 * D + e];
-                if (h4 + e / D < nh) p.part_o[(slot * p.HT + h4) * D + e] = o;
+                for (int s = 0; s < Cfg::kLeft; ++s) o += s_q[s * Cfg::kSumHeads * D + x];
+                if (h4 + x / D < nh) p.part_o[(slot * p.HT + h4) * D + x] = o;
             }
         }
-        if (tid < nh) p.part_ml[slot * p.HT + tid] = make_float2(s_m[tid], s_bad ? kSegBadPage : s_l[tid]);
+        if (tid < nh) {
+            float z = 0.f;
+#pragma unroll
+            for (int x = 0; x < kSimtWarps; ++x) z += s_l[x][tid];
+            p.part_ml[slot * p.HT + tid] = make_float2(s_m[tid], bad ? kSegBadPage : z);
+        }
     }
 }
 
@@ -425,19 +490,20 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
                                       : decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
 }
 
-template <typename T, int D, int HBS>
+template <int D, int HBS>
 static cudaError_t simt_go(DecodeParams& p, cudaStream_t st) {
-    k_decode_simt<T, D, HBS><<<counted(p.C), kSimtThreads, 0, st>>>(p);
+    constexpr int smem = SimtCfg<D, HBS>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(k_decode_simt<D, HBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    k_decode_simt<D, HBS><<<counted(p.C), kSimtThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int D>
+template <int D>
 static cudaError_t simt_heads_go(DecodeParams& p, cudaStream_t st) {
-    return p.hbs == 4 ? simt_go<T, D, 4>(p, st) : (p.hbs == 8 ? simt_go<T, D, 8>(p, st) : simt_go<T, D, 16>(p, st));
+    return p.hbs == 4 ? simt_go<D, 4>(p, st) : (p.hbs == 8 ? simt_go<D, 8>(p, st) : simt_go<D, 16>(p, st));
 }
-template <typename T>
 static cudaError_t simt_d_go(DecodeParams& p, cudaStream_t st) {
-    return p.d == 64 ? simt_heads_go<T, 64>(p, st)
-                     : (p.d == 128 ? simt_heads_go<T, 128>(p, st) : simt_heads_go<T, 256>(p, st));
+    return p.d == 64 ? simt_heads_go<64>(p, st) : (p.d == 128 ? simt_heads_go<128>(p, st) : simt_heads_go<256>(p, st));
 }
 
 template <typename Tin, typename Tout, int D, int WPH>
@@ -507,9 +573,9 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
         decode_layout(p, decode_tc_heads(p.G, d), kTcMaxCtas, weight != nullptr, w);
         e = launch_decode_tc(p, st);
     } else {
-        p.C = 3 * sms < kSimtMaxCtas ? 3 * sms : kSimtMaxCtas;
+        p.C = 2 * sms < kSimtMaxCtas ? 2 * sms : kSimtMaxCtas;
         decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, w);
-        e = simt_d_go<float>(p, st);
+        e = simt_d_go(p, st);
     }
     if (e != cudaSuccess) return e;
     if (in == DDT_BF16)
