@@ -192,6 +192,32 @@ def test_equals_the_tree_call_on_a_root():
     assert (t["o"][:, :, 0] - r["o"]).abs().max() <= 2e-3 * r["o"].abs().max()
 
 
+# One launch (a cluster of 1, 2, 4 or 8 blocks a unit joins its own partials) or two (the table's
+# rows are too many for that): either is chosen by the table's capacity, not by the lengths.
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,d,B", [(8, 1, 64, 1), (6, 2, 128, 30), (24, 4, 256, 20), (16, 16, 64, 13)])
+@pytest.mark.parametrize("cap_rows", [120, 300, 900, 5000])
+def test_any_table_capacity(dtype, Hq, Hkv, d, B, cap_rows):
+    lens = [(37 * i + 1) * 53 % (min(cap_rows, 900) + 1) for i in range(B)]
+    lens[-1] = min(cap_rows, 900) - 1
+    c = _case(24, 1, B, Hq, Hkv, d, lens, 16, dtype, cap_rows=cap_rows)
+    w = torch.zeros((1, B, Hkv, c["table"].shape[1] * 16), device="cuda")
+    r = _run(c, weight=w, out_dtype=F32)
+    _check(c, r, w)
+    if B > 2:  # flagged requests beside others
+        c["table"] = c["table"].clone()
+        c["table"][1, 0] = -7
+        lens[1], lens[2] = 16, c["table"].shape[1] * 16 + 1
+        w2 = torch.zeros_like(w)
+        bad = _run(c, weight=w2, out_dtype=F32)
+        assert bad["status"].cpu().tolist() == [0, 1, 3] + [0] * (B - 3)
+        assert (bad["o"][:, 1:3] == 0).all() and (w2[:, 1:3] == 0).all()
+        # (not bit for bit: where two launches split the rows, the split follows all lengths)
+        rest = [0] + list(range(3, B))
+        c2 = dict(c, lens=[lens[b] for b in rest], table=c["table"][rest], **{k: c[k][:, rest] for k in ("q", "k_new", "v_new")})
+        _check(c2, {"o": bad["o"][:, rest], "status": bad["status"][rest]}, w2[:, rest])
+
+
 def test_side_stream_and_graph_replay_follow_the_lengths():
     """A captured call runs on its stream, and a replay takes the lengths it finds."""
     lens = [500, 40, 0]

@@ -8,6 +8,7 @@
 //
 //   k_decode_tc     grid C (decode_tc.cu): the tiles of a CTA's run on the tensor cores, bf16.
 //   k_decode_simt   grid C: the same on the CUDA cores, fp32 caches.
+//                   (small calls: a cluster a unit, which joins by itself, decode.cuh)
 //   k_decode_finish join: a head's partials with the new token's own row,
 //                     O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s;
 //                   and, from the scores the split kernel left, sum_h 2^(t_h(p) - M_h) / Z_h
@@ -58,7 +59,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float* kp = static_cast<const float*>(p.k_pages);
     const float* vp = static_cast<const float*>(p.v_pages);
-    DecodeWalk w = dec_plan<kSimtThreads>(p);
+    const DecodeWalk mine = dec_plan<kSimtThreads>(p);
+    DecodeWalk w = mine;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_decode_finish may be set up
 
     // ---- the copies, kStages - 1 tiles ahead of the sums, and one tile ahead of them the rows'
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
         // ---- the segment's partial: sums of the exponentials over the rows of a warp, then of
         //      the warps; the row sets' O a few heads at a time, a warp's own two sets (head
         //      size 64) by a shuffle
-        const long long slot = dec_unit(p, w) + blockIdx.x;
+        const long long slot = dec_slot(p, w);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
@@ -282,63 +284,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
             p.part_ml[slot * p.HT + tid] = make_float2(s_m[tid], bad ? kSegBadPage : z);
         }
     }
-}
-
-// One head's joined softmax, by one warp.
-struct HeadJoin {
-    float ref, z, tn;  // reference, sum, the new row's score (log2 units)
-    int err;           // a status for the request, or DDT_OK
-    int ns;            // segments, from slot `first` on
-    long long first;
-};
-
-template <typename Tin, int D>
-__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, int lane) {
-    const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
-    // loads that do not wait for one another first
-    const int P = p.prefix_len[b];
-    const long long pre = p.pre[b], all = p.pre[p.B];
-    float s = 0.f;
-    if (p.k_new) {
-        const Tin* q = static_cast<const Tin*>(p.q) + ((long long)lb * p.Hq + hq) * D;
-        const Tin* k = static_cast<const Tin*>(p.k_new) + ((long long)lb * p.Hkv + g) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) s = fmaf(to_f32(q[e * 32 + lane]), to_f32(k[e * 32 + lane]), s);
+    if (p.cl) {
+        if (p.cl > 1) tc::cluster_sync();
+        else __syncthreads();
+        dec_finish<float, D, kSimtThreads>(p, mine, p.out, s_q);
     }
-    HeadJoin j;
-    j.ref = j.z = 0.f;
-    j.tn = p.k_new ? warp_sum(s) * p.scale_log2 : -INFINITY;
-    j.ns = 0;
-    j.first = 0;
-    j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
-    if (j.err) return j;
-    const int nt = dec_tiles(P, p.cap);
-    if (nt > 0) {
-        const int HH = p.Hkv * p.HB;
-        const long long T = all * HH * p.L;
-        const long long first = l * all * HH + pre * HH + (long long)(g * p.HB + hb) * nt;
-        const int C = (int)min((long long)p.C, T), c0 = dec_owner(T, C, first);
-        j.ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
-        j.first = (long long)lb * HH + g * p.HB + hb + c0;
-    }
-    const float2* ml = p.part_ml + j.first * p.HT + h;
-    float m = j.tn, low = 0.f;
-    for (int s = lane; s < j.ns; s += 32) {
-        const float2 v = ml[(long long)s * p.HT];
-        m = fmaxf(m, v.x);
-        low = fminf(low, v.y);
-    }
-    m = warp_max(m);
-    low = -warp_max(-low);
-    if (low < 0.f) j.err = low == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG;
-    j.ref = m == -INFINITY ? 0.f : m;
-    float z = 0.f;
-    for (int s = lane; s < j.ns; s += 32) {
-        const float2 v = ml[(long long)s * p.HT];
-        z = fmaf(tc::ex2(v.x - j.ref), v.y, z);
-    }
-    j.z = warp_sum(z) + tc::ex2(j.tn - j.ref);
-    return j;
 }
 
 // Blocks below n_join: WPH warps a head (1, or 8 where a head has many segments), O of the
@@ -490,13 +440,42 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
                                       : decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
 }
 
+// The grid of a split kernel with `ctas` CTAs an SM.  A call is small if the tiles that its units
+// can have are no more than four (fp32, whose tiles take four times as long: one) for every CTA
+// of a cluster a unit, all of them resident: the split over more CTAs would then gain less than
+// the second kernel costs.  Replayed from a graph, as a cluster and as two kernels: one request of
+// 1000 rows, 24 heads of 256, 9.7 and 11.7 us; of 4000 rows, 32 heads of 128, 12.4 and 14.5;
+// fp32, one request of 1000 rows 13.6 and 15.4, two of up to 2000 rows 19.5 and 16.0.
+cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
+                                 cudaStream_t st) {
+    p.C *= ctas;
+    const long units = (long)p.L * p.B * p.Hkv;
+    const int nt = (p.cap + kDecTile - 1) / kDecTile;
+    int cl = 1;
+    while (cl < 8 && units * 2 * cl <= p.C && cl < nt) cl *= 2;
+    p.cl = p.HB == 1 && units * cl <= p.C && nt <= (fp32 ? 1 : 4) * cl ? cl : 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(counted(p.cl ? (unsigned)(units * cl) : (unsigned)p.C));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at = cudaLaunchAttribute{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.cl ? p.cl : 1;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 template <int D, int HBS>
 static cudaError_t simt_go(DecodeParams& p, cudaStream_t st) {
     constexpr int smem = SimtCfg<D, HBS>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(k_decode_simt<D, HBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k_decode_simt<D, HBS><<<counted(p.C), kSimtThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    cudaLaunchConfig_t cfg = decode_config(p, true, 2, kSimtThreads, smem, at, st);
+    return cudaLaunchKernelEx(&cfg, k_decode_simt<D, HBS>, p);
 }
 template <int D>
 static cudaError_t simt_heads_go(DecodeParams& p, cudaStream_t st) {
@@ -563,6 +542,7 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
     p.o = o;
     p.weight = weight;
     p.status = status;
+    p.out = out;
     p.scale_log2 = scale * 1.4426950408889634f;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -573,11 +553,11 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
         decode_layout(p, decode_tc_heads(p.G, d), kTcMaxCtas, weight != nullptr, w);
         e = launch_decode_tc(p, st);
     } else {
-        p.C = 2 * sms < kSimtMaxCtas ? 2 * sms : kSimtMaxCtas;
+        p.C = sms < kSimtMaxCtas / 2 ? sms : kSimtMaxCtas / 2;
         decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, w);
         e = simt_d_go(p, st);
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.cl) return e;
     if (in == DDT_BF16)
         return out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16>(p, sms, st)
                                : finish_go<__nv_bfloat16, float>(p, sms, st);

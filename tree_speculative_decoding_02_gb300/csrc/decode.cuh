@@ -9,10 +9,14 @@
 // unit's tiles is a segment; it leaves a partial result (per head: the reference of its
 // exponents, their sum, and the sum of the weighted value rows) in slot u + c, which no
 // other segment has: from one segment to the next either u or c grows.
+//
+// Small calls (p.cl) are bound by latency instead: a cluster of CTAs takes a unit, and joins its
+// partials behind a cluster barrier, in the same launch.
 #pragma once
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace ddt {
 
@@ -23,6 +27,8 @@ struct DecodeParams {
     int hbs, HB, HT;  // heads a block (of the kernel), blocks a kv head, heads a partial slot holds: min(G, hbs)
     int page_rows, num_pages, max_pages, cap;
     int C;            // CTAs of the split kernel
+    int cl;           // 0, or small calls: a cluster of cl CTAs a unit, which also joins (HB is 1)
+    ddt_dtype out;
     const int32_t* block_table;
     const int32_t* prefix_len;
     const void* q;
@@ -74,6 +80,23 @@ __device__ __forceinline__ DecodeWalk dec_plan(const DecodeParams& p) {
     __shared__ long long s_pre;
     __shared__ int s_b;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.cl) {  // a unit a cluster, its tiles over the CTAs of the cluster
+        const int u = blockIdx.x / p.cl, rank = blockIdx.x % p.cl;
+        DecodeWalk w;
+        w.g = u % p.Hkv;
+        w.b = u / p.Hkv % p.B;
+        w.l = u / p.Hkv / p.B;
+        w.P = p.prefix_len[w.b];
+        w.nt = dec_tiles(w.P, p.cap);
+        const int c = min(p.cl, w.nt);
+        w.t = rank < c ? w.nt * rank / c : 0;
+        w.left = rank < c ? w.nt * (rank + 1) / c - w.t : 0;
+        // The request's status.  What its lengths and pages raise, this unit raises too, behind
+        // its cluster's barrier.  A wait that gives up in another unit does so a second after its
+        // CTA began, and all CTAs of the grid are resident.
+        if (w.l == 0 && w.g == 0 && rank == 0 && tid == 0) p.status[w.b] = DDT_OK;
+        return w;
+    }
     const int per = (p.B + NT - 1) / NT;  // consecutive requests a thread counts
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mine = 0;
@@ -153,12 +176,150 @@ __device__ __forceinline__ void dec_next(const DecodeParams& p, DecodeWalk& w) {
         w.nt = dec_tiles(w.P, p.cap);
     } while (w.nt == 0);
 }
-__device__ __forceinline__ long long dec_unit(const DecodeParams& p, const DecodeWalk& w) {
-    return ((long long)w.l * p.B + w.b) * (p.Hkv * p.HB) + w.g;
+// the segment's slot
+__device__ __forceinline__ long long dec_slot(const DecodeParams& p, const DecodeWalk& w) {
+    return p.cl ? blockIdx.x : ((long long)w.l * p.B + w.b) * (p.Hkv * p.HB) + w.g + blockIdx.x;
+}
+
+// One head's joined softmax, by one warp.
+struct HeadJoin {
+    float ref, z, tn;  // reference, sum, the new row's score (log2 units)
+    int err;           // a status for the request, or DDT_OK
+    int ns;            // segments, from slot `first` on
+    long long first;
+};
+
+template <typename Tin, int D>
+__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, int lane) {
+    const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
+    // loads that do not wait for one another first
+    const int P = p.prefix_len[b];
+    const long long pre = p.cl ? 0 : p.pre[b], all = p.cl ? 0 : p.pre[p.B];
+    float s = 0.f;
+    if (p.k_new) {
+        const Tin* q = static_cast<const Tin*>(p.q) + ((long long)lb * p.Hq + hq) * D;
+        const Tin* k = static_cast<const Tin*>(p.k_new) + ((long long)lb * p.Hkv + g) * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) s = fmaf(to_f32(q[e * 32 + lane]), to_f32(k[e * 32 + lane]), s);
+    }
+    HeadJoin j;
+    j.ref = j.z = 0.f;
+    j.tn = p.k_new ? warp_sum(s) * p.scale_log2 : -INFINITY;
+    j.ns = 0;
+    j.first = 0;
+    j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
+    if (j.err) return j;
+    const int nt = dec_tiles(P, p.cap);
+    if (p.cl) {
+        j.ns = min(p.cl, nt);
+        j.first = ((long long)lb * p.Hkv + g) * p.cl;
+    } else if (nt > 0) {
+        const int HH = p.Hkv * p.HB;
+        const long long T = all * HH * p.L;
+        const long long first = l * all * HH + pre * HH + (long long)(g * p.HB + hb) * nt;
+        const int C = (int)min((long long)p.C, T), c0 = dec_owner(T, C, first);
+        j.ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
+        j.first = (long long)lb * HH + g * p.HB + hb + c0;
+    }
+    const float2* ml = p.part_ml + j.first * p.HT + h;
+    float m = j.tn, low = 0.f;
+    for (int s = lane; s < j.ns; s += 32) {
+        const float2 v = ml[(long long)s * p.HT];
+        m = fmaxf(m, v.x);
+        low = fminf(low, v.y);
+    }
+    m = warp_max(m);
+    low = -warp_max(-low);
+    if (low < 0.f) j.err = low == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG;
+    j.ref = m == -INFINITY ? 0.f : m;
+    float z = 0.f;
+    for (int s = lane; s < j.ns; s += 32) {
+        const float2 v = ml[(long long)s * p.HT];
+        z = fmaf(tc::ex2(v.x - j.ref), v.y, z);
+    }
+    j.z = warp_sum(z) + tc::ex2(j.tn - j.ref);
+    return j;
+}
+
+// A cluster's finish (p.cl): the heads of its unit over its warps, the weight sums of each CTA's
+// own rows.  All threads of all its CTAs, behind a cluster barrier; `w` as dec_plan gave it.
+template <typename Tin, int D, int NT>
+__device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWalk& w, ddt_dtype out_type, float* s_x) {
+    constexpr int E = D / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % p.cl;
+    const int lb = w.l * p.B + w.b, g = w.g;
+    for (int h = rank + p.cl * warp; h < p.G; h += p.cl * (NT / 32)) {
+        const int hq = g * p.G + h;
+        const HeadJoin j = head_join<Tin, D>(p, lb, hq, lane);
+        const long long at = ((long long)lb * p.Hq + hq) * D;
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        if (j.err) {
+            if (lane == 0) atomicMax(p.status + w.b, j.err);
+        } else {
+            if (p.k_new) {
+                const float f = tc::ex2(j.tn - j.ref);
+                const Tin* v = static_cast<const Tin*>(p.v_new) + ((long long)lb * p.Hkv + g) * D;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = f * to_f32(v[e * 32 + lane]);
+            }
+            const float2* ml = p.part_ml + j.first * p.HT + h;
+            const float* po = p.part_o + (j.first * p.HT + h) * D;
+#pragma unroll 8
+            for (int s = 0; s < j.ns; ++s) {
+                const float f = tc::ex2(ml[(long long)s * p.HT].x - j.ref);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(f, po[(long long)s * p.HT * D + e * 32 + lane], acc[e]);
+            }
+            const float inv = j.z > 0.f ? 1.f / j.z : j.z;  // no rows at all: 0; NaN stays
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= inv;
+        }
+        if (out_type == DDT_BF16) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) static_cast<__nv_bfloat16*>(p.o)[at + e * 32 + lane] = from_f32<__nv_bfloat16>(acc[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) static_cast<float*>(p.o)[at + e * 32 + lane] = acc[e];
+        }
+    }
+    if (!p.weight) return;
+    float* s_ref = s_x;
+    float* s_inv = s_ref + p.G;
+    float* s_tn = s_inv + p.G;
+    int bad = 0;
+    for (int h = warp; h < p.G; h += NT / 32) {
+        const HeadJoin j = head_join<Tin, D>(p, lb, g * p.G + h, lane);
+        bad |= j.err;
+        if (lane == 0) {
+            s_ref[h] = j.ref;
+            s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
+            s_tn[h] = j.tn;
+        }
+    }
+    if (__syncthreads_or(bad)) return;
+    const float* sc = p.score + ((long long)lb * p.Hq + g * p.G) * p.cap;
+    float* wt = p.weight + ((long long)lb * p.Hkv + g) * p.cap;
+    const int end = min(w.P, (w.t + (int)w.left) * kDecTile);
+    if (w.left > 0)
+        for (int r = w.t * kDecTile + tid; r < end; r += NT) {
+            float sum = 0.f;
+#pragma unroll 4
+            for (int h = 0; h < p.G; ++h) sum = fmaf(tc::ex2(sc[(long long)h * p.cap + r] - s_ref[h]), s_inv[h], sum);
+            wt[r] += sum;
+        }
+    if (p.k_new && w.P < p.cap && rank == 0 && tid == 0) {  // the new token's own row
+        float sum = 0.f;
+        for (int h = 0; h < p.G; ++h) sum = fmaf(tc::ex2(s_tn[h] - s_ref[h]), s_inv[h], sum);
+        wt[w.P] += sum;
+    }
 }
 
 bool decode_tc_supported(int d, ddt_dtype in);
 int decode_tc_heads(int G, int d);
 cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
+cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
+                                 cudaStream_t st);
 
 }  // namespace ddt

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
         tc::tmem_alloc(tmem_slot, Cfg::kTmemCols);
         tc::tmem_relinquish();
     }
-    DecodeWalk w = dec_plan<kTcThreads>(p);
+    const DecodeWalk mine = dec_plan<kTcThreads>(p);
+    DecodeWalk w = mine;
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
             if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
             ok = __all_sync(kFull, ok);
             tc::named_bar(1, 128);
-            const long long slot = dec_unit(p, w) + blockIdx.x;
+            const long long slot = dec_slot(p, w);
             if (r < nh) {
                 const float z = (sm_l[r] + sm_l[HP + r]) + (sm_l[2 * HP + r] + sm_l[3 * HP + r]);
                 p.part_ml[slot * p.HT + r] = make_float2(ref, !ok ? kSegTimeout : (bad ? kSegBadPage : z));
@@ -430,6 +431,10 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
     if (warp == 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, Cfg::kTmemCols);
+    }
+    if (p.cl) {
+        if (p.cl > 1) tc::cluster_sync();
+        dec_finish<__nv_bfloat16, D, kTcThreads>(p, mine, p.out, reinterpret_cast<float*>(ring));
     }
 }
 
@@ -459,9 +464,9 @@ cudaError_t tc_go(DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, 
     constexpr int smem = DecCfg<D, HP>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    p.C *= DecCfg<D, HP>::kCtas;
-    k_decode_tc<D, HP><<<counted(p.C), kTcThreads, smem, st>>>(p, a, maps[0], maps[1], maps[2]);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    cudaLaunchConfig_t cfg = decode_config(p, false, DecCfg<D, HP>::kCtas, kTcThreads, smem, at, st);
+    return cudaLaunchKernelEx(&cfg, k_decode_tc<D, HP>, p, a, maps[0], maps[1], maps[2]);
 }
 
 }  // namespace
