@@ -104,6 +104,31 @@ def test_long_cache():
     _check(c, _run(c, 40000, 8, 1024), 40000, 8, 1024)
 
 
+# one block a unit, or a cluster of 2, 4 or 8 with a slice of the rows each: chosen by the table's
+# rows and the number of units
+@pytest.mark.parametrize("kind", ["random", "equal", "zero", "nan", "close"])
+@pytest.mark.parametrize("B,Hkv,lens,cap_rows,keep,n_recent",
+                         [(1, 1, [33000], 33024, 20000, 0), (20, 2, [17000 - 800 * i for i in range(20)], 17024, 4000, 9), (1, 4, [16500], 16640, 16499, 100), (2, 3, [9000, 17000], 17024, 33, 32),
+                          (12, 2, [8200 - 300 * i for i in range(12)], 8256, 5003, 7), (1, 2, [4100], 20032, 4090, 64)])
+def test_a_unit_in_slices(kind, B, Hkv, lens, cap_rows, keep, n_recent):
+    c = _case(35, 1, B, Hkv, 8, lens, 64, BF, cap_rows=cap_rows, placed=[n // 3 for n in lens])
+    w, g = c["w"], synth.gen(35, 81)
+    if kind == "equal":
+        w.fill_(0.37)
+    elif kind == "zero":
+        w.zero_()
+    elif kind == "nan":
+        w[torch.rand(w.shape, generator=g) < 0.7] = float("nan")
+    elif kind == "close":
+        w.view(torch.int32).copy_(torch.randint(0, 40, w.shape, generator=g).to(torch.int32) + 0x3f800000)
+    _check(c, _run(c, keep, 1, n_recent), keep, 1, n_recent)
+
+
+def test_slices_beyond_shared_memory():
+    c = _case(36, 1, 1, 1, 8, [400003], 256, BF, placed=[100000])
+    _check(c, _run(c, 150001, 4, 1000), 150001, 4, 1000)
+
+
 def test_second_eviction_and_the_steady_state():
     """Evict, append rows, evict again (the appended ones' positions follow from seq_len)."""
     c = _case(34, 1, 2, 2, 64, [600, 300], 16, BF, cap_rows=640)

@@ -11,17 +11,22 @@
 //   k_evict_claim   grid B: lengths and block table checked, pages that are used twice found.
 //   k_evict_select  grid L B Hkv: the keep-th largest key by three histogram passes (11, 11
 //                   and 10 bits), then one pass in index order for the holes and the rows
-//                   that fill them; sums and positions follow at once.
+//                   that fill them; sums and positions follow at once.  Long caches of few
+//                   units: a cluster of CTAs a unit, each with a slice of its rows, their
+//                   histograms and counts summed over the cluster's shared memory.
 //   k_evict_move    grid (L B Hkv, y): the K and V rows, 16 bytes a thread; the first layer's
 //                   first head writes the request's lengths and status.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace ddt {
 
 namespace {
 constexpr int kBins = 2048;             // bins of a histogram pass (the last one uses 1024)
 constexpr int kSelCache = 45 * 1024;    // rows whose keys fit in shared memory
+constexpr int kUncut = 16384;           // rows that one CTA takes in any case
+constexpr int kSlice = 4096;            // rows a CTA of a cluster has at least
 constexpr int kClaimThreads = 512;
 constexpr int kWindow = 1 << 20;        // pages a bitmap in shared memory covers
 constexpr int kEvict = -1;  // state of a request that is over its budget
@@ -29,6 +34,7 @@ constexpr int kEvict = -1;  // state of a request that is over its budget
 struct EvictParams {
     int L, B, Hkv, page_rows, num_pages, max_pages, cap, keep, n_sink, n_recent;
     int pieces;  // 16-byte pieces of a cached row
+    int cl;      // k_evict_select's CTAs a unit
     int most;    // moves the workspace holds a unit
     const int32_t* block_table;
     const int32_t* seq_len;
@@ -126,16 +132,30 @@ __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
     return incl - v + (warp ? before : 0);
 }
 
-// CACHED: the unit's keys are kept in shared memory after the first pass.  The histogram
+// `x` of the same variable in CTA `rank` of the cluster
+__device__ __forceinline__ int cluster_read(const int* x, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(tc::mapa_shared(tc::smem_u32(x), (uint32_t)rank)) : "memory");
+    return v;
+}
+
+// CACHED: the slice's keys are kept in shared memory after the first pass.  The histogram
 // passes take four consecutive rows a thread.
 template <int NT, bool CACHED>
 __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const EvictParams p) {
     extern __shared__ __align__(16) uint32_t s_key[];
-    __shared__ int s_hist[kBins];
+    constexpr bool kClusters = NT == 1024;  // p.cl may be above 1
+    __shared__ int s_hist[kClusters ? 2 : 1][kBins];  // while other CTAs read one, the next pass fills the other
     __shared__ uint4 s_bits[NT];
     __shared__ int s_w[2][32];
-    __shared__ int s_bin, s_rest, s_count, s_zeros, s_safe;
-    const long long u = blockIdx.x;
+    __shared__ int s_bin, s_rest, s_count, s_all[2];
+    __shared__ int s_same[2], s_cnt[4];  // of this CTA's rows: keys of 0 and protected ones; see the lists
+    const int cl = kClusters ? p.cl : 1, rank = kClusters ? blockIdx.x % cl : 0;
+    const long long u = kClusters ? blockIdx.x / cl : blockIdx.x;
+    auto sync = [&]() {
+        if (kClusters && cl > 1) tc::cluster_sync();
+        else __syncthreads();
+    };
     const int b = (int)(u / p.Hkv % p.B);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moves may be set up
@@ -145,14 +165,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     const bool cut = P > K && P <= p.cap && np >= 0 && np <= P && sq >= P;
     if (!cut) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid == 0) p.n_move[u] = 0;
+        if (tid == 0) p.n_move[u] = 0;  // (by every CTA of a cluster)
         return;
     }
+    // this CTA's rows
+    const int per = cl == 1 ? P : ((P + cl - 1) / cl + 31) & ~31, lo = min(rank * per, P), hi = min(lo + per, P);
     float* wt = p.weight + u * p.cap;
     int32_t* rp = p.row_pos + u * p.cap;
     const int32_t* table = p.block_table + (long long)b * p.max_pages;
-    for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
-    if (tid == 0) s_zeros = s_safe = 0;
+    for (int i = tid; i < kBins; i += NT) s_hist[0][i] = 0;
+    if (tid < 2) s_same[tid] = 0;
+    if (tid < 4) s_cnt[tid] = 0;
     __syncthreads();
     auto pos_of = [&](int i) { return i < np ? rp[i] : sq - P + i; };
     // the keys of rows i .. i + 3 (rows >= P: any)
@@ -165,7 +188,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
 #pragma unroll
         for (int q = 0; q < 4; ++q) key[q] = evict_key(p, ww[q], i + q < np ? rr[q] : sq - P + i + q, sq);
     };
-    auto key_of = [&](int i) { return CACHED ? s_key[i] : evict_key(p, wt[i], pos_of(i), sq); };
+    auto key_of = [&](int i) { return CACHED ? s_key[i - lo] : evict_key(p, wt[i], pos_of(i), sq); };
     // ---- the K-th largest key: its bits from the highest down.  Kept are the rows above
     //      `limit` and the first `rest` that equal it.
     uint32_t limit = 0;
@@ -175,41 +198,50 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     for (int pass = 0; pass < 3; ++pass) {
         const int sh = pass == 0 ? 21 : (pass == 1 ? 10 : 0), up = pass == 1 ? 21 : 10;
         const uint32_t mask = pass == 2 ? 1023 : 2047;
+        int* hist = s_hist[kClusters ? pass & 1 : 0];
         int zeros = 0, safe = 0;  // the two keys that many rows share: counted in registers
 #pragma unroll 2
-        for (int i = tid * 4; i < P; i += NT * 4) {
+        for (int i = lo + tid * 4; i < hi; i += NT * 4) {
             uint32_t key[4];
             if (CACHED && pass > 0) {
-                const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+                const uint4 k = *reinterpret_cast<const uint4*>(s_key + i - lo);
                 key[0] = k.x;
                 key[1] = k.y;
                 key[2] = k.z;
                 key[3] = k.w;
             } else {
                 keys4(i, key);
-                if (CACHED) *reinterpret_cast<uint4*>(s_key + i) = make_uint4(key[0], key[1], key[2], key[3]);
+                if (CACHED) *reinterpret_cast<uint4*>(s_key + i - lo) = make_uint4(key[0], key[1], key[2], key[3]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (i + q >= P || (pass > 0 && (key[q] >> up) != limit)) continue;
                 if (key[q] == 0x80000000u) ++zeros;
                 else if (key[q] == 0xffffffffu) ++safe;
-                else atomicAdd(&s_hist[(key[q] >> sh) & mask], 1);
+                else atomicAdd(&hist[(key[q] >> sh) & mask], 1);
             }
         }
         zeros = __reduce_add_sync(kFull, zeros);
         safe = __reduce_add_sync(kFull, safe);
         if (lane == 0) {
             if (zeros) {
-                atomicAdd(&s_hist[(0x80000000u >> sh) & mask], zeros);
-                if (pass == 0) atomicAdd(&s_zeros, zeros);
+                atomicAdd(&hist[(0x80000000u >> sh) & mask], zeros);
+                if (pass == 0) atomicAdd(&s_same[0], zeros);
             }
             if (safe) {
-                atomicAdd(&s_hist[(0xffffffffu >> sh) & mask], safe);
-                if (pass == 0) atomicAdd(&s_safe, safe);
+                atomicAdd(&hist[(0xffffffffu >> sh) & mask], safe);
+                if (pass == 0) atomicAdd(&s_same[1], safe);
             }
         }
-        __syncthreads();
+        sync();
+        if (pass == 0 && tid < 2) {
+            int n = s_same[tid];
+            if (cl > 1) {
+                n = 0;
+                for (int r = 0; r < cl; ++r) n += cluster_read(&s_same[tid], r);
+            }
+            s_all[tid] = n;
+        }
         // warp i has the i-th run of bins from the top, and only the warp whose run holds the
         // K-th largest looks closer
         constexpr int kPer = kBins / NT;
@@ -217,8 +249,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
         int c[kPer], sum = 0;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
-            c[q] = s_hist[top - 32 * q];
-            s_hist[top - 32 * q] = 0;  // for the next pass
+            c[q] = cl == 1 ? hist[top - 32 * q] : 0;
+            if (cl > 1)
+#pragma unroll 4
+                for (int r = 0; r < cl; ++r) c[q] += cluster_read(hist + top - 32 * q, r);
+            s_hist[kClusters ? (pass & 1) ^ 1 : 0][top - 32 * q] = 0;  // for the next pass
             sum += c[q];
         }
         sum = __reduce_add_sync(kFull, sum);
@@ -256,14 +291,51 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
             rest = 0;
             break;
         }
-        if (pass == 0 && limit == 0x80000000u >> 21 && s_count == s_zeros) {
+        if (pass == 0 && limit == 0x80000000u >> 21 && s_count == s_all[0]) {
             limit = 0x80000000u;
             break;
         }
-        if (pass == 0 && limit == 0xffffffffu >> 21 && s_count == s_safe) {
+        if (pass == 0 && limit == 0xffffffffu >> 21 && s_count == s_all[1]) {
             limit = 0xffffffffu;
             break;
         }
+    }
+    if (kClusters && cl > 1) {
+        // what the lists of the CTAs before this one will hold: above the limit below K and from K on,
+        // and equal to it
+        int n[4] = {0, 0, 0, 0};
+        for (int i = lo + tid; i < hi; i += NT) {
+            const uint32_t key = key_of(i);
+            n[0] += key > limit && i < K;
+            n[1] += key > limit && i >= K;
+            n[2] += key == limit && i < K;
+            n[3] += key == limit && i >= K;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            n[q] = __reduce_add_sync(kFull, n[q]);
+            if (lane == 0 && n[q]) atomicAdd(&s_cnt[q], n[q]);
+        }
+        sync();
+    }
+    int eqs = 0, holes = 0, movers = 0, all_holes = 0;
+    if (kClusters && cl > 1) {
+        int eq = 0;
+        for (int r = 0; r < cl; ++r) {
+            if (r == rank) {
+                eqs = eq;
+                holes = all_holes;
+            }
+            const int first = min(r * per, P), below = max(min(min(first + per, P), K) - first, 0);
+            int n[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) n[q] = cluster_read(&s_cnt[q], r);
+            const int left = tie ? max(rest - eq, 0) : 0, low = min(left, n[2]), high = min(left - low, n[3]);
+            all_holes += below - n[0] - low;
+            if (r < rank) movers += n[1] + high;
+            eq += n[2] + n[3];
+        }
+        sync();  // no CTA's shared memory is read by others from here on
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.state[b] != kEvict) {
@@ -275,14 +347,13 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     //      counts, and a warp a word for the lists.
     int32_t* src = p.src + u * p.most;
     int32_t* dst = p.dst + u * p.most;
-    int eqs = 0, holes = 0, movers = 0;
-    for (int c0 = 0; c0 < P; c0 += 32 * NT) {
-        const int words = min(NT, (P - c0 + 31) / 32);
+    for (int c0 = lo; c0 < hi; c0 += 32 * NT) {
+        const int words = min(NT, (hi - c0 + 31) / 32);
 #pragma unroll 4
         for (int w = warp; w < words; w += NT / 32) {
             const int i = c0 + w * 32 + lane;
-            const uint32_t key = i < P ? key_of(i) : 0u;  // no limit is below 0
-            const uint32_t gt = __ballot_sync(kFull, key > limit), eq = __ballot_sync(kFull, i < P && key == limit);
+            const uint32_t key = i < hi ? key_of(i) : 0u;  // no limit is below 0
+            const uint32_t gt = __ballot_sync(kFull, key > limit), eq = __ballot_sync(kFull, i < hi && key == limit);
             if (lane == 0) s_bits[w] = make_uint4(gt, eq, 0u, 0u);
         }
         __syncthreads();
@@ -298,7 +369,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
             kept |= eq;
         }
         // the word's rows that exist, and those below K
-        const uint32_t live = P - i >= 32 ? ~0u : (P <= i ? 0u : (1u << (P - i)) - 1u);
+        const uint32_t live = hi - i >= 32 ? ~0u : (hi <= i ? 0u : (1u << (hi - i)) - 1u);
         const uint32_t low = K - i >= 32 ? ~0u : (K <= i ? 0u : (1u << (K - i)) - 1u);
         const uint32_t hole = ~kept & live & low, mover = kept & ~low;
         const int at = block_scan<NT>(__popc(hole) + (__popc(mover) << 16), s_w[1], total);
@@ -316,10 +387,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
         movers += (int)((uint32_t)total >> 16);
         __syncthreads();
     }
-    for (int i = np + tid; i < K; i += NT) rp[i] = sq - P + i;
-    if (tid == 0) p.n_move[u] = holes;
-    __syncthreads();
-    for (int j0 = tid; j0 < holes; j0 += 4 * NT) {  // four moves' loads are in flight
+    for (int i = np + rank * NT + tid; i < K; i += NT * cl) rp[i] = sq - P + i;
+    if (cl > 1) holes = all_holes;
+    if (rank == 0 && tid == 0) p.n_move[u] = holes;
+    sync();
+    for (int j0 = rank * 4 * NT + tid; j0 < holes; j0 += 4 * NT * cl) {  // four moves' loads are in flight
         int s[4], d[4], pos[4], ps[4], pd[4];
         float w[4];
 #pragma unroll
@@ -347,10 +419,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
             dst[j] = pd[q];
         }
     }
-    __syncthreads();
+    sync();
     // rows K .. P - 1, four at a time but for the ends
     const int k4 = min((K + 3) & ~3, P), p4 = max(P & ~3, k4);
-    for (int i = k4 + tid * 4; i < p4; i += NT * 4) {
+    for (int i = k4 + (rank * NT + tid) * 4; i < p4; i += NT * cl * 4) {
         *reinterpret_cast<float4*>(wt + i) = make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<int4*>(rp + i) = make_int4(-1, -1, -1, -1);
     }
@@ -435,17 +507,20 @@ size_t evict_ws_bytes(int L, int B, int Hkv, const AttnPaging& pg) {
 
 // a launch that may be set up while the kernel before it ends
 static cudaError_t launch_behind(void (*kernel)(EvictParams), dim3 grid, int threads, int smem, const EvictParams& p,
-                                 cudaStream_t st) {
+                                 cudaStream_t st, int cluster = 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = counted(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -453,7 +528,7 @@ template <int NT>
 static cudaError_t select_go(const EvictParams& p, unsigned units, int keys, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(k_evict_select<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
-    return e != cudaSuccess ? e : launch_behind(k_evict_select<NT, true>, dim3(units), NT, keys, p, st);
+    return e != cudaSuccess ? e : launch_behind(k_evict_select<NT, true>, dim3(units * p.cl), NT, keys, p, st, p.cl);
 }
 
 cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging& pg, int keep, int n_sink,
@@ -489,11 +564,20 @@ cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging&
     if (e != cudaSuccess) return e;
     k_evict_claim<<<counted(B), kClaimThreads, ((pg.num_pages < kWindow ? pg.num_pages : kWindow) + 31) / 32 * 4, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // few units or long caches: many threads a unit, for its latency; else small blocks, so
-    // that several units share an SM and hide each other's barriers
-    const bool wide = units <= 2u * sms || p.cap > 8192, cached = p.cap <= kSelCache;
-    const int keys = cached ? (p.cap + 3) / 4 * 16 : 0;
-    if (!cached) e = launch_behind(k_evict_select<1024, false>, dim3(units), 1024, 0, p, st);
+    // Many threads a unit, for its latency, if there is an SM for every unit or a unit is long;
+    // else small blocks, so that several units share an SM and hide each other's barriers.  With
+    // 1024 and 256 threads: 64 units of 4000 rows 10.6 and 13.4 us, of 8000 13.3 and 19.3; but 256
+    // units of 4000 rows 19.0 and 15.2, of 8000 24.1 and 24.2, of 16000 33 and 42.
+    const bool wide = units <= (unsigned)sms || p.cap > 8192;
+    // Clusters where SMs would idle.  Of 1, 2, 4, 8 CTAs a unit: 4 units of 16000 rows 16.1, 18.3, -, -;
+    // of 32000 28.4, 24.0, 21.7, 23.9; of 131000 135, -, -, 32 us.  16 clusters of 8 are not all
+    // resident at once (32000 rows: 43.8 us, in clusters of 4 22.2).
+    p.cl = 1;
+    while (p.cl < 8 && p.cap > kUncut && units * 2 * p.cl <= (unsigned)(p.cl == 4 ? sms * 3 / 4 : sms) &&
+           p.cap >= kSlice * 2 * p.cl)
+        p.cl *= 2;
+    const int slice = p.cl == 1 ? p.cap : ((p.cap + p.cl - 1) / p.cl + 31) & ~31, keys = (slice + 3) / 4 * 16;
+    if (slice > kSelCache) e = launch_behind(k_evict_select<1024, false>, dim3(units * p.cl), 1024, 0, p, st, p.cl);
     else if (wide) e = select_go<1024>(p, units, keys, st);
     else e = select_go<256>(p, units, keys, st);
     if (e != cudaSuccess) return e;
