@@ -14,7 +14,7 @@
 //   warp 0      producer: block-table entries, TMA of K and V tiles (128 rows, 128-byte
 //               swizzle, a box a page slice, a lane a box) into one ring, Q by TMA
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
-//   warps 2-5   softmax: a thread a cached row.  The exponents' reference of a head is the
+//   warps 2-5, 6-9 ..  softmax, eight heads a warpgroup: a thread a cached row.  The exponents' reference of a head is the
 //               maximum of the segment's first tile, and moves (with O rescaled) only when a
 //               score is 2^8 above it: one vote a tile instead of its maxima.  At a segment's
 //               end the same warps write its partial.
@@ -35,11 +35,12 @@ namespace ddt {
 
 namespace {
 
-constexpr int kTcThreads = 192;
 constexpr float kTau = 8.f;  // rescale O only when a head's maximum grows by more than 2^kTau
 
 template <int D, int HP>
 struct DecCfg {
+    static constexpr int kGroups = HP / 8;                 // softmax warpgroups
+    static constexpr int kThreads = 64 + 128 * kGroups;
     static constexpr int kBlocks = D / 64;                 // 128-byte swizzle blocks of a row
     static constexpr int kStageBytes = kDecTile * D * 2;   // a K or V tile
     static constexpr int kCtas = HP == 8 && D <= 128 ? 2 : 1;  // an SM
@@ -89,19 +90,22 @@ __device__ __forceinline__ bool bar_any(int id, bool x) {
     return r != 0;
 }
 
-// 16 consecutive 32-bit columns of this thread's lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+// 8 consecutive 32-bit columns of this thread's lane
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 }  // namespace
 
 template <int D, int HP>
-__global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
+__global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
     k_decode_tc(const DecodeParams p, const DecTcArgs a, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q) {
     using Cfg = DecCfg<D, HP>;
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
     uint64_t* q_full = empty + kStages;  // [2] a segment's queries landed
     uint64_t* q_free = q_full + 2;       // [2] its last Q K^T is done
     uint64_t* s_full = q_free + 2;       // [2] S of a tile in tensor memory
-    uint64_t* p_full = s_full + 2;       // [2] P of a tile in shared memory (4 warps)
+    uint64_t* p_full = s_full + 2;       // [2] P of a tile in shared memory (the softmax warps)
     uint64_t* p_free = p_full + 2;       // [2] its P V is done
     uint64_t* drain = p_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
             tc::mbar_init(q_full + i, 1);
             tc::mbar_init(q_free + i, 1);
             tc::mbar_init(s_full + i, 1);
-            tc::mbar_init(p_full + i, 4);
+            tc::mbar_init(p_full + i, 4 * Cfg::kGroups);
             tc::mbar_init(p_free + i, 1);
         }
         tc::mbar_init(drain, 1);
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
         tc::tmem_alloc(tmem_slot, Cfg::kTmemCols);
         tc::tmem_relinquish();
     }
-    const DecodeWalk mine = dec_plan<kTcThreads>(p);
+    const DecodeWalk mine = dec_plan<Cfg::kThreads>(p);
     DecodeWalk w = mine;
     tc::tc_fence_before();
     __syncthreads();
@@ -274,13 +278,14 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
         // -------------------------------------------------- softmax, and the segments' partials
         const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
         const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
+        const int grp = (warp - 2) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
         int j = 0;
         bool ok = true;
         for (; w.left > 0; dec_next(p, w)) {
-            const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0), n_seg = dec_seg_tiles(w);
-            float m[HP], l[HP];
+            const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
+            float m[8], l[8];
 #pragma unroll
-            for (int h = 0; h < HP; ++h) {
+            for (int h = 0; h < 8; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.f;
             }
@@ -290,45 +295,44 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                 // a warp that gave up still takes part in the barriers
                 if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
                 ok = __all_sync(kFull, ok);
-                float t[HP];
+                float t[8];
                 bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
-                    uint32_t sr[NQ];
-#pragma unroll
-                    for (int c = 0; c < NQ; c += 16) tmem_ld16(tmem + lane_base + (j & 1) * NQ + c, sr + c);
+                    uint32_t sr[8];
+                    tmem_ld8(tmem + lane_base + (j & 1) * NQ + hg, sr);
                     tc::tmem_wait_ld();
                     bad |= bad_tile[j & 7];
 #pragma unroll
-                    for (int h = 0; h < HP; ++h) {
+                    for (int h = 0; h < 8; ++h) {
                         t[h] = r < n ? __uint_as_float(sr[h]) * p.scale_log2 : -INFINITY;
                         if (h < nh) above |= t[h] > m[h] + kTau;
                     }
                     if (p.score && r < n) {
                         float* sc = p.score + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * p.cap + y + r;
 #pragma unroll
-                        for (int h = 0; h < HP; ++h)
+                        for (int h = 0; h < 8; ++h)
                             if (h < nh) sc[(long long)h * p.cap] = t[h];
                     }
                 }
-                if (bar_any(1, above)) {
+                if (bar_any(bar, above)) {
                     // the segment's first tile, or a growing maximum: new references, the tile's
                     // maxima, for the heads that need them
-                    float* x = xm + (j & 1) * 4 * HP;
+                    float* x = xm + (j & 1) * 4 * HP + hg;
                     float mine = -INFINITY;
                     if (ok)
 #pragma unroll
-                        for (int h = 0; h < HP; ++h)
+                        for (int h = 0; h < 8; ++h)
                             if (h < nh) {
                                 const float v = redux_max(t[h]);
                                 if (lane == h) mine = v;
                             }
-                    if (lane < HP) x[ws * HP + lane] = mine;
-                    tc::named_bar(1, 128);
+                    if (lane < 8) x[ws * HP + lane] = mine;
+                    tc::named_bar(bar, 128);
                     if (ok) {
-                        float f[HP];
+                        float f[8];
 #pragma unroll
-                        for (int h = 0; h < HP; ++h) {
+                        for (int h = 0; h < 8; ++h) {
                             const float mt = fmaxf(fmaxf(x[h], x[HP + h]), fmaxf(x[2 * HP + h], x[3 * HP + h]));
                             f[h] = 1.f;
                             if (mt > m[h] + kTau) {
@@ -342,15 +346,14 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                             if (ok) {
                                 tc::tc_fence_after();
 #pragma unroll
-                                for (int c = 0; c < kMB * NP; c += 16) {
-                                    uint32_t o[16];
+                                for (int c = hg; c < kMB * NP; c += HP) {
+                                    uint32_t o[8];
                                     const uint32_t at = tmem + lane_base + Cfg::kOCol + c;
-                                    tmem_ld16(at, o);
+                                    tmem_ld8(at, o);
                                     tc::tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(c + e) % HP]);
-                                    tc::tmem_st16(at, o);
+                                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+                                    tmem_st8(at, o);
                                 }
                                 tc::tmem_wait_st();
                             }
@@ -363,15 +366,15 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                 if (!ok) continue;
                 unsigned char* pb = sP + (j & 1) * Cfg::kPBytes + (r >> 6) * (NP * 128);
 #pragma unroll
-                for (int h = 0; h < HP; ++h)
+                for (int h = 0; h < 8; ++h)
                     if (h < nh) {
                         const float e = tc::ex2(t[h] - m[h]);
                         l[h] += e;
                         const uint32_t hi = __float_as_uint(e) & 0xffff0000u;
                         const __nv_bfloat16 lo = __float2bfloat16_rn(e - __uint_as_float(hi));
                         const uint32_t col = ((uint32_t)(r & 63) * 2) ^ ((uint32_t)(h & 7) << 4);
-                        *reinterpret_cast<uint16_t*>(pb + h * 128 + col) = (uint16_t)(hi >> 16);
-                        *reinterpret_cast<__nv_bfloat16*>(pb + (HP + h) * 128 + col) = lo;
+                        *reinterpret_cast<uint16_t*>(pb + (hg + h) * 128 + col) = (uint16_t)(hi >> 16);
+                        *reinterpret_cast<__nv_bfloat16*>(pb + (HP + hg + h) * 128 + col) = lo;
                     }
                 if (n < kDecTile) {
                     // V rows past the prefix may hold anything, even NaN, and a zero weight
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
                     if (!ok) continue;
                     unsigned char* v = ring + st * Cfg::kStageBytes;
                     const int per = (kDecTile - n) * 8;
-                    for (int e = r; e < per * Cfg::kBlocks; e += 128)
+                    for (int e = grp * 128 + r; e < per * Cfg::kBlocks; e += 128 * Cfg::kGroups)
                         *reinterpret_cast<uint4*>(v + (e / per) * (kDecTile * 128) + n * 128 + (e % per) * 16) =
                             make_uint4(0, 0, 0, 0);
                 }
@@ -393,34 +396,35 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
             // ---- the partial: sums through shared memory, O once the last P V is done
             float sum = 0.f, ref = 0.f;
 #pragma unroll
-            for (int h = 0; h < HP; ++h)
+            for (int h = 0; h < 8; ++h)
                 if (h < nh) {
                     const float x = warp_sum(l[h]);
                     if (lane == h) sum = x;
                     if (r == h) ref = m[h];
                 }
-            if (lane < HP) sm_l[ws * HP + lane] = sum;
+            if (lane < 8) sm_l[ws * HP + hg + lane] = sum;
             if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
             ok = __all_sync(kFull, ok);
-            tc::named_bar(1, 128);
+            tc::named_bar(bar, 128);
             const long long slot = dec_slot(p, w);
             if (r < nh) {
-                const float z = (sm_l[r] + sm_l[HP + r]) + (sm_l[2 * HP + r] + sm_l[3 * HP + r]);
-                p.part_ml[slot * p.HT + r] = make_float2(ref, !ok ? kSegTimeout : (bad ? kSegBadPage : z));
+                const float* x = sm_l + hg + r;
+                const float z = (x[0] + x[HP]) + (x[2 * HP] + x[3 * HP]);
+                p.part_ml[slot * p.HT + hg + r] = make_float2(ref, !ok ? kSegTimeout : (bad ? kSegBadPage : z));
             }
             if (!ok) continue;
             tc::tc_fence_after();
 #pragma unroll
             for (int mb = 0; mb < kMB; ++mb) {
-                uint32_t o[NP];
-#pragma unroll
-                for (int c = 0; c < NP; c += 16) tmem_ld16(tmem + lane_base + Cfg::kOCol + mb * NP + c, o + c);
+                uint32_t o[16];
+                tmem_ld8(tmem + lane_base + Cfg::kOCol + mb * NP + hg, o);
+                tmem_ld8(tmem + lane_base + Cfg::kOCol + mb * NP + HP + hg, o + 8);
                 tc::tmem_wait_ld();
                 if (D >= 128 || r < D) {
-                    float* out = p.part_o + slot * p.HT * D + mb * 128 + r;
+                    float* out = p.part_o + (slot * p.HT + hg) * D + mb * 128 + r;
 #pragma unroll
-                    for (int h = 0; h < HP; ++h)
-                        if (h < nh) out[h * D] = __uint_as_float(o[h]) + __uint_as_float(o[HP + h]);
+                    for (int h = 0; h < 8; ++h)
+                        if (h < nh) out[h * D] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
                 }
             }
         }
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kTcThreads, DecCfg<D, HP>::kCtas)
     }
     if (p.cl) {
         if (p.cl > 1) tc::cluster_sync();
-        dec_finish<__nv_bfloat16, D, kTcThreads>(p, mine, p.out, reinterpret_cast<float*>(ring));
+        dec_finish<__nv_bfloat16, D, Cfg::kThreads>(p, mine, p.out, reinterpret_cast<float*>(ring));
     }
 }
 
@@ -465,7 +469,7 @@ cudaError_t tc_go(DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, 
     cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    cudaLaunchConfig_t cfg = decode_config(p, false, DecCfg<D, HP>::kCtas, kTcThreads, smem, at, st);
+    cudaLaunchConfig_t cfg = decode_config(p, false, DecCfg<D, HP>::kCtas, DecCfg<D, HP>::kThreads, smem, at, st);
     return cudaLaunchKernelEx(&cfg, k_decode_tc<D, HP>, p, a, maps[0], maps[1], maps[2]);
 }
 
