@@ -442,7 +442,7 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
  *     (and row prefix_len[b], the new token's once it is appended, if the capacity has it)
  *     gets the sum over the kv head's query heads of its softmax weights ADDED to its
  *     entry; the other entries are left as they are.  Start it at zero.
- *   o [L][B][Hq][d] (out_dtype).
+ *   o [L][B][Hq][d] (out_dtype), apart from q.
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, max_pages * page_size],
  *     DDT_ERR_INVALID_ARG if a block-table entry that the prefix needs is outside
  *     [0, num_pages); the request's output rows are then zero and its sums unchanged.
@@ -481,6 +481,7 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
  *   n_placed [B], prefix_len [B]: become keep.  seq_len [B]: tokens of the sequence that
  *     have been cached, evicted ones included (advance it where prefix_len advances, and
  *     give it to ddt_build_tree as the base of positions); read only.
+ *     The three are arrays of their own.
  * Requests with prefix_len[b] <= keep are left as they are (status DDT_OK).  Pages past
  * ceil(keep / page_size) of a cut request hold nothing any more.
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, cap]; DDT_ERR_INVALID_ARG

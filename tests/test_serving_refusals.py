@@ -90,3 +90,17 @@ def test_logprobs(lib):
     assert lib.ddt_launch_count() == before
     assert lib.ddt_token_logprobs_workspace(0, 3, 100, 4) == 0
     assert lib.ddt_token_logprobs_workspace(2, 3, 100, 4) > lib.ddt_token_logprobs_workspace(2, 3, 100, 0) > 0
+
+
+def test_buffers_that_overlap(lib):
+    """o over q, and the three lengths of an eviction in one array (seq_len would be cut with prefix_len)."""
+    before = lib.ddt_launch_count()
+    at = lambda x: ctypes.c_void_p(x)  # noqa: E731
+    q = 4096                                               # 2 * 8 * 64 bf16: 2048 bytes
+    for o in (q, q + 2032, q - 2032):
+        assert _decode(lib, q=at(q), o=at(o)) == INVALID
+    assert _decode(lib, q=at(q), o=at(q - 2048), ot=0) == INVALID
+    for kw in (dict(seq=P, plen=P, np=at(512)), dict(seq=at(512), plen=P, np=P), dict(seq=P, plen=at(512), np=P),
+               dict(seq=P, plen=at(260), np=at(512))):
+        assert _evict(lib, **kw) == INVALID, kw
+    assert lib.ddt_launch_count() == before

@@ -396,6 +396,12 @@ static bool paging_sizes_ok(int page_size, int num_pages, int max_pages) {
     return page_rows_ok(page_size) && (long)page_size * max_pages <= (1L << 30) && num_pages >= 1;
 }
 
+// buffers that a call reads after it has begun to write the other
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // the largest grid and plane counts the kernels index with 32 bits
 static bool decode_sizes_ok(int n_layers, int B, int Hq, int Hkv, int num_pages) {
     const long most = 0x7fffffffL;
@@ -430,6 +436,8 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
         !aligned16(o) || !aligned16(attn_weight))
         return DDT_ERR_INVALID_ARG;
+    const size_t n_q = (size_t)n_layers * B * Hq * d;
+    if (overlap(o, n_q * (out_dtype == DDT_BF16 ? 2 : 4), q, n_q * (in_dtype == DDT_BF16 ? 2 : 4))) return DDT_ERR_INVALID_ARG;
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
     return from_cuda(launch_decode(n_layers, B, Hq, Hkv, d, pg, in_dtype, out_dtype, q, k_new, v_new, k_pages, v_pages,
                                    prefix_len, scale, o, attn_weight, status, workspace,
@@ -460,6 +468,9 @@ ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, i
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
     if (ws_bytes < evict_ws_bytes(n_layers, B, Hkv, pg) || !aligned16(workspace) || !aligned16(k_pages) ||
         !aligned16(v_pages) || !aligned16(attn_weight) || !aligned16(row_pos))
+        return DDT_ERR_INVALID_ARG;
+    const size_t n_b = (size_t)B * sizeof(int32_t);
+    if (overlap(seq_len, n_b, prefix_len, n_b) || overlap(seq_len, n_b, n_placed, n_b) || overlap(prefix_len, n_b, n_placed, n_b))
         return DDT_ERR_INVALID_ARG;
     return from_cuda(launch_evict(n_layers, B, Hkv, (int)row_bytes, pg, keep, n_sink, n_recent, k_pages, v_pages, seq_len,
                                   attn_weight, row_pos, prefix_len, n_placed, status, workspace,

@@ -616,7 +616,7 @@ def decode_attn_paged_workspace(q, k_pages, block_table, *, weights=False):
     lib = _gpu()
     L, B, Hq, d = q.shape
     need = lib.ddt_decode_attn_paged_workspace(L, B, Hq, k_pages.shape[2], d, k_pages.shape[3], block_table.shape[1],
-                                               _DT[q.dtype], int(weights))
+                                               _code(q.dtype, "q"), int(weights))
     return _ws(need, q.device)
 
 
