@@ -26,6 +26,13 @@ constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtMaxCtas = 512;
 }  // namespace
 
+// Bound by the CUDA cores and shared memory from 4 heads a kv head on, by HBM below: a row costs
+// 4 G d flop, and every K element is read from shared memory once for all heads of the block.
+// 16 requests of 6000 rows: 32 heads over 8 kv heads of 128 168 us (5.2 TB/s), 24 over 4 of 256
+// 234 us (3.7 TB/s); before the ring, with each row's copies behind its own page lookup, 265 and
+// 305 us.  A block is 4, 8 or 16 heads, the smallest that holds the group: sums for more do not
+// fit in the registers of two CTAs an SM.
+//
 // Tiles of 32 KB of K and V (R rows), three on their way by cp.async; two barriers a tile.
 //   scores   D / 16 lanes a row, 16 channels a lane, all heads; the sums over the lanes scatter
 //            the heads over them, so a lane ends up with the scores (and the exponentials) of
@@ -291,8 +298,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
     }
 }
 
-// Blocks below n_join: WPH warps a head (1, or 8 where a head has many segments), O of the
-// head.  The others: the weight sums of some rows of one (layer, request, kv head).
+// Blocks below n_join: WPH warps a head, O of the head.  The others: the weight sums of some rows
+// of one (layer, request, kv head); with them the kernel is bound by HBM (4 bytes a head and row,
+// written by the split and read here: about 20 us of 415 for 500000 rows of 24 heads), else by
+// the latency of the join.
 template <typename Tin, typename Tout, int D, int WPH>
 __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, unsigned n_join, int chunks) {
     constexpr int E = D / 32;
@@ -489,8 +498,8 @@ template <typename Tin, typename Tout, int D, int WPH>
 static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st) {
     const size_t heads = (size_t)p.L * p.B * p.Hq;
     const unsigned n_join = (unsigned)(WPH == 1 ? (heads + 7) / 8 : heads), units = (unsigned)p.L * p.B * p.Hkv;
-    // 2048 rows a block, so that long requests get more of them; not too many for units that may
-    // be short
+    // 2048 rows a block, so that long requests get more of them (131071 rows: the call takes 103 us,
+    // 109 with 8192); not too many for units that may be short
     const unsigned most = (p.cap + 2047) / 2048, room = 24u * sms / units + 1;
     const int chunks = (int)(most < room ? most : room);
     cudaLaunchConfig_t cfg{};
@@ -508,7 +517,9 @@ static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st
 }
 template <typename Tin, typename Tout>
 static cudaError_t finish_go(const DecodeParams& p, int sms, cudaStream_t st) {
-    // segments a head: C / (units) + 1 or so
+    // Eight warps a head where it has a dozen segments (C / units) or more: whole calls with 8 and
+    // with 1, one request of 131071 rows, 8 heads over one of 128 (304 segments) 21.2 and 44.1 us, 32
+    // over 8 (39) 85.0 and 88.6; but 2 x 96 short requests of 16 heads (1 or 2) 182 and 166.
     const bool many = p.C >= 12L * p.L * p.B * p.Hkv * p.HB;
     switch (p.d) {
         case 64: return many ? finish_launch<Tin, Tout, 64, 8>(p, sms, st) : finish_launch<Tin, Tout, 64, 1>(p, sms, st);

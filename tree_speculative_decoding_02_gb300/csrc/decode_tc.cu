@@ -18,9 +18,17 @@
 //               maximum of the segment's first tile, and moves (with O rescaled) only when a
 //               score is 2^8 above it: one vote a tile instead of its maxima.  At a segment's
 //               end the same warps write its partial.
-// Up to eight heads and head sizes 64 and 128: two CTAs an SM, each with half the ring, so
-// that one's softmax chain (about 2000 cycles a tile, as long as an SM's share of HBM takes
-// for 32 KB) hides behind the other's.
+// A block of heads is 8, 16 or 32 of them: the smallest that holds the group, so the cache is
+// read once for up to 32 heads (16 for head size 256).  Eight heads a warpgroup, because the
+// chain from S to P of a tile (about 2000 cycles, as long as an SM's share of HBM takes for
+// 32 KB) grows with a thread's heads: 32 heads of 64, 16 requests of 6000 rows, 41.8 us with
+// four warpgroups and 62.5 with one.  For up to eight heads and head sizes 64 and 128 the
+// second warpgroup is that of a second CTA on the SM, with half the ring: 2 x 96 requests of
+// up to 2500 rows, 16 heads of 64, 156 us, and 215 with one CTA.
+//
+// Bound by HBM: 32 requests of 1K to 32K rows, 24 heads over 4 kv heads of 256, with weights
+// (2.49 GB): 394 us, 6.3 TB/s; one of 131071 rows, 32 heads over 8 of 128 (545 MB): 89 us, 6.1
+// TB/s; the 2 x 96 above (937 MB) 6.0 TB/s.  On the CUDA cores the first took 2.2 ms.
 // Every wait is bounded; after one gives up the CTA drains its copies and MMAs, and its
 // unfinished segments say so to the join.
 #include <cuda.h>
