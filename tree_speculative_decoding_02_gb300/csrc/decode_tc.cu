@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
         // -------------------------------------------------- softmax, and the segments' partials
         const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
         const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
-        const int grp = (warp - 2) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
+        const int grp = Cfg::kGroups == 1 ? 0 : (warp - 2) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
         int j = 0;
         bool ok = true;
         for (; w.left > 0; dec_next(p, w)) {
