@@ -20,9 +20,9 @@
 //           two finish their rows (a chain of reads that depend on one another).
 //
 // Bound by HBM without alternatives: 2000 rows of 151936 bf16 logits (608 MB) 106 us, 5.7 TB/s;
-// with 20 alternatives 124 us, the rest being the finishing of a row by warps that do not
+// with 20 alternatives 120 us, the rest being the finishing of a row by warps that do not
 // stream.  Measured and dropped: finishing in a kernel of its own 135 us, by warps of the CTA
-// that do nothing else 150 to 174, eight warps and three CTAs an SM the same 124.  Small calls
+// that do nothing else 150 to 174, eight warps and three CTAs an SM as much as this.  Small calls
 // are bound by latency: one request's walk 9.8 us, 300 rows 20 us.
 #include <limits.h>
 #include <math.h>
@@ -38,7 +38,7 @@ constexpr int kLpWarps = 4;
 constexpr int kLpThreads = kLpWarps * 32;
 constexpr int kLpCtas = 6;      // CTAs an SM
 constexpr int kLpStages = 2;    // units on their way a warp
-constexpr int kLpClusters = 2 * 256 * kLpCtas;  // CTAs of a call with several a row, at most
+constexpr int kLpClusters = 256 * kLpCtas;  // CTAs of a call with several a row, at most
 constexpr int kLpLists = 256;   // (unit, thread) pairs read again
 constexpr int kLpCand = 512;    // entries ranked
 constexpr float kLpLow = -200.f;  // 2^w is 0 from here down
@@ -74,16 +74,14 @@ static inline int lp_units(int V, size_t esz) {
 }
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// shares: those of a CTA a row, or of kLpClusters CTAs where rows have several
-static size_t lp_part_bytes(size_t rows) {
-    return (rows > kLpClusters ? rows : kLpClusters) * kLpThreads * sizeof(LpPartial);
-}
+// the shares of rows with several CTAs
+static constexpr size_t kLpPartBytes = (size_t)kLpClusters * kLpThreads * sizeof(LpPartial);
 
 // workspace: shares, the threads' largest entries of every unit.  fp32 rows have twice the
 // units of bf16 rows: the size covers both.
 size_t logprobs_ws_bytes(int B, int A, int V, int top_n) {
     const size_t rows = (size_t)B * A;
-    return lp_part_bytes(rows) + (top_n > 0 ? al256(rows * lp_units(V, 4) * 32 * sizeof(float)) : 0);
+    return kLpPartBytes + (top_n > 0 ? al256(rows * lp_units(V, 4) * 32 * sizeof(float)) : 0);
 }
 
 // The word at entry e of the row; entries outside [0, V) are -inf.
@@ -374,10 +372,11 @@ __device__ __noinline__ void lp_top_slow(const T* __restrict__ row, const T* LM,
     bi = top.id;
 }
 
-// One row's results from its n_t shares (a multiple of 32), by the whole block.
+// One row's results from its n_t shares, by the whole block: `own`, the thread's, or those at P
+// (of several CTAs).
 template <typename T>
 __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T* __restrict__ row, const T* LM,
-                                          const float4* P, int n_t, int i) {
+                                          const float4& own, const float4* P, int n_t, int i) {
     constexpr int VE = LpUnit<T>::VE, NT = kLpThreads, kWarps = kLpWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int V = p.V, nunits = p.nunits, top_n = p.top_n, lead = LpUnit<T>::lead(row);
@@ -387,11 +386,11 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
     float m = -INFINITY, best = -INFINITY;
     int id = lane;
     for (int u = tid; u < n_t; u += NT) {
-        const float4 x = P[u];
+        const float4 x = P ? P[u] : own;
         m = fmaxf(m, x.x);
         best = fmaxf(best, x.w);
     }
-    if (top_n && warp * 32 < n_t) warp_sort_best_first(best, id);
+    if (top_n) warp_sort_best_first(best, id);
     m = redux_max(m);
     S.sorted[tid] = best;
     if (lane == 0) S.m[warp] = m;
@@ -402,7 +401,7 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
     // ---- Z and sum 2^w w (a NaN sum stays NaN)
     float z = 0.f, t = 0.f;
     for (int u = tid; u < n_t; u += NT) {
-        const float4 x = P[u];
+        const float4 x = P ? P[u] : own;
         if (x.y == 0.f) continue;
         const float d = fmaxf((x.x - m) * p.s2, kLpLow), f = tc::ex2(d);
         z = fmaf(f, x.y, z);
@@ -420,9 +419,9 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
     float tau = -INFINITY;
     if (top_n) {
         best = S.sorted[lane];
-        for (int w = 1; w < kWarps && w * 32 < n_t; ++w) warp_merge_best_first(best, id, S.sorted[w * 32 + lane], lane);
+        for (int w = 1; w < kWarps; ++w) warp_merge_best_first(best, id, S.sorted[w * 32 + lane], lane);
         tau = __shfl_sync(kFull, best, top_n - 1);
-#pragma unroll 2
+#pragma unroll 4
         for (int x = tid * VE; x < nunits * 32; x += NT * VE) {
             const uint4 v = *reinterpret_cast<const uint4*>(LM + x);
 #pragma unroll
@@ -457,7 +456,7 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
     // ---- their entries that reach it, ranked by one warp
     const int nl = S.nl;
     if (nl <= kLpLists) {
-#pragma unroll 2
+#pragma unroll 4
         for (int x = tid; x < nl * 8; x += NT) {
             const int l = S.list[x >> 3];
             const int e = LpUnit<T>::entry(l >> 5, x & 7, l & 31, lead);
@@ -532,17 +531,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_token_logprobs(const T*
         if (p.top_n) LM[u * 32 + lane] = from_f32<T>(mt);
         stage = stage + 1 == kLpStages ? 0 : stage + 1;
     }
-    float4* P = p.part + (long long)i * n_w * 32;
-    P[wid * 32 + lane] = lp_share(run, p.s2);
-    // the shares of all CTAs are visible to the cluster's first one
-    if (cl > 1) {
+    const float4 own = lp_share(run, p.s2);
+    float4* P = nullptr;
+    if (cl > 1) {  // the shares of all CTAs become visible to the cluster's first one
+        P = p.part + (long long)i * n_w * 32;
+        P[wid * 32 + lane] = own;
         tc::cluster_sync();
         if (rank) return;
     } else {
         __syncthreads();
     }
     // every copy has landed and been read: the ring becomes the scratch
-    lp_finish<T>(p, *reinterpret_cast<LpScratch*>(s_ring), row, LM, P, n_w * 32, i);
+    lp_finish<T>(p, *reinterpret_cast<LpScratch*>(s_ring), row, LM, own, P, n_w * 32, i);
 }
 
 template <typename T>
@@ -554,17 +554,18 @@ static cudaError_t lp_go(int B, int N, int V, int A, int top_n, float temperatur
     const LpArgs a{rows,  N,     V,       A,       nunits,    top_n,       (float)(1.4426950408889634 / (double)temperature),
                    (float)(1.0 / (double)temperature), node, token, reinterpret_cast<float4*>(w), logprob, entropy,
                    top_token, top_logprob, status};
-    T* lane_max = reinterpret_cast<T*>(w + lp_part_bytes(rows));
+    T* lane_max = reinterpret_cast<T*>(w + kLpPartBytes);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (sms > 256) sms = 256;
     constexpr int ring = kLpWarps * kLpStages * 4096;
     static_assert(kLpCtas * (ring + 1024) <= 228 * 1024 && sizeof(LpScratch) <= ring, "shared memory of an SM");
-    // As many CTAs a row as are resident together; of a walk's entries half or more are padding.
-    // Twice as many CTAs or half: 200 rows 22.7 and 17.5 us (two waves); 512 entries of walks, 2 rows
-    // a walk 14.1, 15.9, 18.7 us for 4, 2 and 1 a row, 8 rows 19.8, 22.0, 19.6.
+    // As many CTAs a row as are resident together.  Twice as many: 200 rows 22.7 instead of 17.5 us,
+    // 450 rows 36.8 instead of 34.7.  (Walks pad their entries; two CTAs a row for 32 walks of up to 16
+    // take 15.9 instead of 18.7 us if 2 are rows, but 22.0 instead of 19.6 if 8 are, 42 instead of 33
+    // if all are.)
     int cl = 1;
-    while (cl < 8 && rows * 2LL * cl <= (node ? 2LL : 1LL) * kLpCtas * sms && cl * kLpWarps < nunits) cl *= 2;
+    while (cl < 8 && rows * 2LL * cl <= (long long)kLpCtas * sms && cl * kLpWarps < nunits) cl *= 2;
     const cudaError_t e = cudaFuncSetAttribute(k_token_logprobs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
