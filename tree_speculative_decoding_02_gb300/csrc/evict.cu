@@ -11,11 +11,11 @@
 //   k_evict_claim   grid B: lengths and block table checked, pages that are used twice found.
 //   k_evict_select  grid L B Hkv: the keep-th largest key by three histogram passes (11, 11
 //                   and 10 bits), then one pass in index order for the holes and the rows
-//                   that fill them; sums and positions follow at once.  Long caches of few
+//                   that fill them; their sums and positions follow at once.  Long caches of few
 //                   units: a cluster of CTAs a unit, each with a slice of its rows, their
 //                   histograms and counts summed over the cluster's shared memory.
-//   k_evict_move    grid (L B Hkv, y): the K and V rows, 16 bytes a thread; the first layer's
-//                   first head writes the request's lengths and status.
+//   k_evict_move    grid (L B Hkv, y): the K and V rows, 16 bytes a thread, and the entries behind
+//                   the budget; the first layer's first head writes the request's lengths and status.
 //
 // The moves are bound by HBM: 702 MB of 16 requests of up to 32768 rows cut to 8192 take 120 us
 // beside their selection's 27 (K and V rows of 512 bytes from random places; four rows' loads in
@@ -37,7 +37,6 @@ constexpr int kUncut = 16384;           // rows that one CTA takes in any case
 constexpr int kSlice = 4096;            // rows a CTA of a cluster has at least
 constexpr int kClaimThreads = 512;
 constexpr int kWindow = 1 << 20;        // pages a bitmap in shared memory covers
-constexpr int kEvict = -1;  // state of a request that is over its budget
 
 struct EvictParams {
     int L, B, Hkv, page_rows, num_pages, max_pages, cap, keep, n_sink, n_recent;
@@ -54,7 +53,7 @@ struct EvictParams {
     int32_t* n_placed;
     int32_t* status;
     // workspace
-    int32_t* state;   // [B] kEvict, DDT_OK (within the budget), or an error
+    int32_t* state;   // [B] -P (over its budget), DDT_OK (within it), or an error
     int32_t* n_move;  // [U]
     int32_t* src;     // [U][most]
     int32_t* dst;     // [U][most]
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kClaimThreads) k_evict_claim(const EvictParams
     }
     bad = __syncthreads_or(bad);
     twice = __syncthreads_or(twice);
-    if (tid == 0) p.state[b] = st != DDT_OK ? st : (bad || twice ? (int)DDT_ERR_INVALID_ARG : (cut ? kEvict : (int)DDT_OK));
+    if (tid == 0) p.state[b] = st != DDT_OK ? st : (bad || twice ? (int)DDT_ERR_INVALID_ARG : (cut ? -P : (int)DDT_OK));
 }
 
 // The order of the rows as an unsigned key: 0 for NaN, then the sums from the smallest to
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
         sync();  // no CTA's shared memory is read by others from here on
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (p.state[b] != kEvict) {
+    if (p.state[b] >= 0) {
         if (tid == 0) p.n_move[u] = 0;
         return;
     }
@@ -427,20 +426,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
             dst[j] = pd[q];
         }
     }
-    sync();
-    // rows K .. P - 1, four at a time but for the ends
-    const int k4 = min((K + 3) & ~3, P), p4 = max(P & ~3, k4);
-    for (int i = k4 + (rank * NT + tid) * 4; i < p4; i += NT * cl * 4) {
-        *reinterpret_cast<float4*>(wt + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<int4*>(rp + i) = make_int4(-1, -1, -1, -1);
-    }
-    if (tid < 8) {
-        const int i = tid < 4 ? K + tid : p4 + tid - 4;
-        if (i < (tid < 4 ? k4 : P)) {
-            wt[i] = 0.f;
-            rp[i] = -1;
-        }
-    }
 }
 
 // A block moves 256 / pieces rows at a time, a thread 16 bytes of K and of V; the next
@@ -449,13 +434,29 @@ __global__ void __launch_bounds__(256, 8) k_evict_move(const EvictParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long u = blockIdx.x;
     const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv % p.B), l = (int)(u / p.Hkv / p.B);
-    if (l == 0 && g == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-        const int st = p.state[b];
-        if (st == kEvict) {
-            p.prefix_len[b] = p.keep;
-            p.n_placed[b] = p.keep;
+    const int st = p.state[b], tid = threadIdx.x, K = p.keep;
+    if (l == 0 && g == 0 && blockIdx.y == 0 && tid == 0) {
+        if (st < 0) {
+            p.prefix_len[b] = K;
+            p.n_placed[b] = K;
         }
-        p.status[b] = st != kEvict ? st : (int)DDT_OK;
+        p.status[b] = max(st, (int)DDT_OK);
+    }
+    if (st < 0) {  // sums and positions of rows K .. P - 1, four at a time but for the ends
+        const int P = -st, k4 = min((K + 3) & ~3, P), p4 = max(P & ~3, k4);
+        float* wt = p.weight + u * p.cap;
+        int32_t* rp = p.row_pos + u * p.cap;
+        for (int i = k4 + (blockIdx.y * 256 + tid) * 4; i < p4; i += gridDim.y * 1024) {
+            *reinterpret_cast<float4*>(wt + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<int4*>(rp + i) = make_int4(-1, -1, -1, -1);
+        }
+        if (blockIdx.y == 0 && tid < 8) {
+            const int i = tid < 4 ? K + tid : p4 + tid - 4;
+            if (i < (tid < 4 ? k4 : P)) {
+                wt[i] = 0.f;
+                rp[i] = -1;
+            }
+        }
     }
     const int n = p.n_move[u];
     const int32_t* src = p.src + u * p.most;
