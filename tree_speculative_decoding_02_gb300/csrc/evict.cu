@@ -17,13 +17,13 @@
 //   k_evict_move    grid (L B Hkv, y): the K and V rows, 16 bytes a thread, and the entries behind
 //                   the budget; the first layer's first head writes the request's lengths and status.
 //
-// The moves are bound by HBM: 702 MB of 16 requests of up to 32768 rows cut to 8192 take 120 us
-// beside their selection's 27 (K and V rows of 512 bytes from random places; four rows' loads in
-// flight a thread cost half the warps and took 166).  The selection is bound by latency: three
+// The moves are bound by HBM: 702 MB of 16 requests of up to 32768 rows cut to 8192 take 105 us
+// beside their selection's 24 (K and V rows of 512 bytes from random places, 5.7 TB/s; two
+// rows' loads in flight a thread and five blocks an SM take as long).  The selection is bound by latency: three
 // passes and a few barriers each, 8.5 us for a unit of 2000 rows, 23 us for 1024 units of 4200
 // on all SMs (its floor, 8 bytes a row, is 5 us), so it begins beside the checks and the moves
 // are set up behind it.  Whole calls: 19.5 us (4 units of 2001 rows), 40 us (the 1024 units, 100
-// rows over the budget each) and 154 us (the 16 requests).
+// rows over the budget each) and 133 us (the 16 requests).
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -591,8 +591,15 @@ cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging&
     else e = select_go<256>(p, units, keys, st);
     if (e != cudaSuccess) return e;
     const int rows = 256 / (p.pieces < 256 ? p.pieces : 256);  // a block's
-    const unsigned most = (unsigned)((p.most + rows - 1) / rows), want = 8u * sms / units + 1;
-    return launch_behind(k_evict_move, dim3(units, most < 1 ? 1 : (most < want ? most : want)), 256, 0, p, st);
+    // Blocks a unit: one for every eight rounds that a full table could need, so that units of all
+    // lengths end together, but one place of every SM at least and eight times as many at most.
+    // With one place: 16 requests of 3000 to 32768 rows cut to 8192 152 us, with eight 133; but 256
+    // units cut from 1000 to 500 rows 20.5 and 25.4.
+    const long moves = keep < p.cap - keep ? keep : (p.cap > keep ? p.cap - keep : 1);
+    const long rounds = (moves + rows - 1) / rows, one = 8L * sms / units + 1, all = 64L * sms / units + 1;
+    long y = (rounds + 7) / 8;
+    y = y < one ? one : (y > all ? all : y);
+    return launch_behind(k_evict_move, dim3(units, (unsigned)(y < rounds ? y : rounds)), 256, 0, p, st);
 }
 
 }  // namespace ddt
