@@ -19,10 +19,14 @@
 //           an entry that reaches it are read again.  Six CTAs an SM: most stream while one or
 //           two finish their rows (a chain of reads that depend on one another).
 //
-// Bound by HBM without alternatives: 2000 rows of 151936 bf16 logits (608 MB) 106 us, 5.7 TB/s;
-// with 20 alternatives 120 us, the rest being the finishing of a row by warps that do not
-// stream.  Measured and dropped: finishing in a kernel of its own 135 us, by warps of the CTA
-// that do nothing else 150 to 174, eight warps and three CTAs an SM as much as this.  Small calls
+// Bound by HBM without alternatives: 1800 rows of 151936 bf16 logits (547 MB, two rounds of the
+// resident CTAs) 87 us, 6.3 TB/s; with 20 alternatives 101 us, the rest being the finishing of a
+// row by warps that do not stream, half of it the words read again.  2000 rows: 96 and 110 us, the
+// third round being short of CTAs.  Measured and dropped: finishing in a kernel of its own 135 us, by warps of the CTA
+// that do nothing else 150 to 174; resident CTAs that fetch the next row's first units before they
+// finish one 3 % slower (all rows end at once); a lane's words in one 128-byte line the same; the
+// bound by counting instead of sorting 10 % slower at 32000 entries a row; eight warps and three
+// CTAs an SM as much as this.  Small calls
 // are bound by latency: one request's walk 9.8 us, 300 rows 20 us.
 #include <limits.h>
 #include <math.h>
@@ -249,6 +253,7 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 
 struct LpArgs {
     int rows, N, V, A, nunits, top_n;
+    bool near;  // the units' largest entries behind the ring, not in the workspace
     float s2, inv_t;
     const int32_t* node;
     const int32_t* token;
@@ -475,30 +480,35 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
         }
     }
     __syncthreads();
-    if (warp) return;
-    const VId none = vid_empty();
     const int nc = S.nc;
-    float bv = none.v;
-    int bi = none.id;
     if (nl <= kLpLists && nc <= kLpCand) {
-        for (int x = 0; x < nc; x += 32) {
-            float cv = x + lane < nc ? S.cv[x + lane] : none.v;
-            int ci = x + lane < nc ? S.ci[x + lane] : none.id;
-            warp_sort_best_first(cv, ci);
-            warp_merge_best_first(bv, bi, cv, ci);
+        for (int x = tid; x < nc; x += NT) {
+            const float v = S.cv[x];
+            const int id = S.ci[x];
+            int r = 0;
+            for (int y = 0; y < nc; ++y) {
+                const float o = S.cv[y];
+                r += o > v || (o == v && S.ci[y] < id);
+            }
+            if (r < top_n) {
+                tt[r] = id;
+                tl[r] = (v - m) * p.inv_t - lz * LN2;
+            }
         }
-    } else {
+    } else if (warp == 0) {
+        float bv;
+        int bi;
         lp_top_slow<T>(row, LM, V, nunits, top_n, lane, bv, bi);
-    }
-    if (lane < top_n) {
-        tt[lane] = bi;
-        tl[lane] = (bv - m) * p.inv_t - lz * LN2;
+        if (lane < top_n) {
+            tt[lane] = bi;
+            tl[lane] = (bv - m) * p.inv_t - lz * LN2;
+        }
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_token_logprobs(const T* __restrict__ logits, T* lane_max, const LpArgs p) {
-    extern __shared__ __align__(16) uint4 s_ring[];  // [kLpWarps][kLpStages][256]
+    extern __shared__ __align__(16) uint4 s_ring[];  // [kLpWarps][kLpStages][256], largest entries (near)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int cl, rank;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_token_logprobs(const T*
     const T* row = lp_row(p, logits, i);
     const int V = p.V, nunits = p.nunits, wid = rank * kLpWarps + warp, n_w = cl * kLpWarps;
     uint4* ring = s_ring + warp * kLpStages * 256;
-    T* LM = lane_max + (long long)i * nunits * 32;
+    T* LM = p.near ? reinterpret_cast<T*>(s_ring + kLpWarps * kLpStages * 256) : lane_max + (long long)i * nunits * 32;
     int fu = wid, stage = 0;
     auto fetch = [&](int s) {
         if (fu < nunits) lp_fetch<T>(ring + s * 256, row, fu, lane, V);
@@ -551,7 +561,7 @@ static cudaError_t lp_go(int B, int N, int V, int A, int top_n, float temperatur
                          int32_t* top_token, float* top_logprob, int32_t* status, void* ws, cudaStream_t st) {
     const int nunits = lp_units(V, sizeof(T)), rows = B * A;
     unsigned char* w = static_cast<unsigned char*>(ws);
-    const LpArgs a{rows,  N,     V,       A,       nunits,    top_n,       (float)(1.4426950408889634 / (double)temperature),
+    LpArgs a{rows,  N,     V,       A,       nunits,    top_n,       false, (float)(1.4426950408889634 / (double)temperature),
                    (float)(1.0 / (double)temperature), node, token, reinterpret_cast<float4*>(w), logprob, entropy,
                    top_token, top_logprob, status};
     T* lane_max = reinterpret_cast<T*>(w + kLpPartBytes);
@@ -559,19 +569,24 @@ static cudaError_t lp_go(int B, int N, int V, int A, int top_n, float temperatur
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (sms > 256) sms = 256;
     constexpr int ring = kLpWarps * kLpStages * 4096;
-    static_assert(kLpCtas * (ring + 1024) <= 228 * 1024 && sizeof(LpScratch) <= ring, "shared memory of an SM");
+    constexpr int room = 228 * 1024 / kLpCtas - 1024 - ring;  // a CTA
+    static_assert(room >= 0 && sizeof(LpScratch) <= ring, "shared memory of an SM");
     // As many CTAs a row as are resident together.  Twice as many: 200 rows 22.7 instead of 17.5 us,
     // 450 rows 36.8 instead of 34.7.  (Walks pad their entries; two CTAs a row for 32 walks of up to 16
     // take 15.9 instead of 18.7 us if 2 are rows, but 22.0 instead of 19.6 if 8 are, 42 instead of 33
     // if all are.)
     int cl = 1;
     while (cl < 8 && rows * 2LL * cl <= (long long)kLpCtas * sms && cl * kLpWarps < nunits) cl *= 2;
-    const cudaError_t e = cudaFuncSetAttribute(k_token_logprobs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    // the units' largest entries stay in shared memory where a row has one CTA and they leave its
+    // six a place: 2000 rows of 151936 110 us, through the workspace 117 (its writes disturb the reads)
+    const int maxima = top_n ? nunits * 32 * (int)sizeof(T) : 0;
+    a.near = cl == 1 && maxima <= room;
+    const cudaError_t e = cudaFuncSetAttribute(k_token_logprobs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + room);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(counted((unsigned)rows * cl));
     cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = ring;
+    cfg.dynamicSmemBytes = ring + (a.near ? maxima : 0);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
