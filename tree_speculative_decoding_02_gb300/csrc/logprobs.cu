@@ -22,12 +22,12 @@
 // Bound by HBM without alternatives: 1800 rows of 151936 bf16 logits (547 MB, two rounds of the
 // resident CTAs) 87 us, 6.3 TB/s; with 20 alternatives 101 us, the rest being the finishing of a
 // row by warps that do not stream, half of it the words read again.  2000 rows: 96 and 110 us, the
-// third round being short of CTAs.  Measured and dropped: finishing in a kernel of its own 135 us, by warps of the CTA
-// that do nothing else 150 to 174; resident CTAs that fetch the next row's first units before they
-// finish one 3 % slower (all rows end at once); a lane's words in one 128-byte line the same; the
-// bound by counting instead of sorting 10 % slower at 32000 entries a row; eight warps and three
-// CTAs an SM as much as this.  Small calls
-// are bound by latency: one request's walk 9.8 us, 300 rows 20 us.
+// third round being short of CTAs.  Small calls are bound by latency: one request's walk 9.5 us, 300
+// rows 20 us.  Measured and dropped: finishing in a kernel of its own 135 us, by warps of the CTA that
+// do nothing else 150 to 174; resident CTAs that fetch the next row's first units before they finish
+// one 3 % slower (all rows end at once); a lane's words in one 128-byte line the same; the bound by
+// counting instead of sorting 10 % slower at 32000 entries a row; eight warps and three CTAs an SM
+// as much as this.
 #include <limits.h>
 #include <math.h>
 
