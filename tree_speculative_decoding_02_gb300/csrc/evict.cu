@@ -158,12 +158,13 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
     __shared__ int s_bin, s_rest, s_count, s_all[2];
     __shared__ int s_same[2], s_cnt[4];  // of this CTA's rows: keys of 0 and protected ones; see the lists
     const int cl = kClusters ? p.cl : 1, rank = kClusters ? blockIdx.x % cl : 0;
-    const long long u = kClusters ? blockIdx.x / cl : blockIdx.x;
+    const unsigned unit = kClusters ? blockIdx.x / (unsigned)cl : blockIdx.x;
+    const long long u = unit;
     auto sync = [&]() {
         if (kClusters && cl > 1) tc::cluster_sync();
         else __syncthreads();
     };
-    const int b = (int)(u / p.Hkv % p.B);
+    const int b = (int)(unit / (unsigned)p.Hkv % (unsigned)p.B);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moves may be set up
     const int P = p.prefix_len[b], np = p.n_placed[b], sq = p.seq_len[b], K = p.keep;
@@ -433,7 +434,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 1) k_evict_select(const Ev
 __global__ void __launch_bounds__(256, 8) k_evict_move(const EvictParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long u = blockIdx.x;
-    const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv % p.B), l = (int)(u / p.Hkv / p.B);
+    const unsigned lb = blockIdx.x / (unsigned)p.Hkv;  // (64-bit divisions would be most of the instructions)
+    const int g = (int)(blockIdx.x - lb * p.Hkv), l = (int)(lb / (unsigned)p.B), b = (int)(lb - (unsigned)l * p.B);
     const int st = p.state[b], tid = threadIdx.x, K = p.keep;
     if (l == 0 && g == 0 && blockIdx.y == 0 && tid == 0) {
         if (st < 0) {
