@@ -192,6 +192,31 @@ def test_equals_the_tree_call_on_a_root():
     assert (t["o"][:, :, 0] - r["o"]).abs().max() <= 2e-3 * r["o"].abs().max()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_launches_captured_follow_the_lengths(dtype):
+    lens = [4900, 40, 0]
+    c = _case(25, 1, 3, 8, 2, 64, lens, 16, dtype, cap_rows=5000)
+    c["k"], c["v"] = c["k"].nan_to_num(0.25), c["v"].nan_to_num(0.25)
+    d = {k: _dev(c[k]) for k in ("q", "k_new", "v_new", "k", "v", "table")}
+    P = torch.tensor(lens, dtype=torch.int32).cuda()
+    w = torch.zeros((1, 3, 2, c["table"].shape[1] * 16), device="cuda")
+    ws = ddt.decode_attn_paged_workspace(d["q"], d["k"], d["table"], weights=True)
+    out = torch.empty((1, 3, 8, 64), dtype=F32, device="cuda")
+    st = torch.empty(3, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ddt.ddt_decode_attn_paged(d["q"], d["k_new"], d["v_new"], d["k"], d["v"], d["table"], P, scale=c["scale"],
+                                  attn_weight=w, out=out, status=st, workspace=ws)
+    for lens in ([4900, 40, 0], [1, 5000, 2600], [0, 0, 0]):
+        P.copy_(torch.tensor(lens, dtype=torch.int32))
+        w.zero_()
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        c["lens"] = lens
+        _check(c, {"o": out, "status": st}, w)
+
+
 # One launch (a cluster of 1, 2, 4 or 8 blocks a unit joins its own partials) or two (the table's
 # rows are too many for that): either is chosen by the table's capacity, not by the lengths.
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -124,6 +124,35 @@ def test_a_unit_in_slices(kind, B, Hkv, lens, cap_rows, keep, n_recent):
     _check(c, _run(c, keep, 1, n_recent), keep, 1, n_recent)
 
 
+def test_slices_captured_and_refused():
+    """Clusters of eight: refused requests between others, and a replay on the same state."""
+    c = _case(38, 1, 4, 2, 8, [33000, 20000, 16000, 17000], 64, BF, cap_rows=33024)
+    c["table"][1, 5] = c["table"][1, 6]
+    c["lens"][2] = 33025
+    keep = 9001
+    eager = _run(c, keep, 3, 500)
+    assert eager["status"].cpu().tolist() == [0, 1, 3, 0]
+    _check(c, eager, keep, 3, 500, skip=[1, 2])
+    d = dict(k=c["k"].cuda(), v=c["v"].cuda(), table=c["table"].cuda(), P=torch.as_tensor(c["lens"]).cuda(),
+             placed=torch.as_tensor(c["placed"]).cuda(), seq=torch.as_tensor(c["seq"]).cuda(), w=c["w"].cuda(),
+             pos=c["pos"].cuda())
+    start = {k: x.clone() for k, x in d.items()}
+    st = torch.empty(4, dtype=torch.int32, device="cuda")
+    ws = ddt.evict_paged_workspace(d["k"], d["table"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ddt.ddt_evict_paged(d["k"], d["v"], d["table"], d["P"], d["placed"], d["seq"], d["w"], d["pos"], keep=keep,
+                            n_sink=3, n_recent=500, status=st, workspace=ws)
+    for _ in range(2):
+        for k, x in start.items():
+            d[k].copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in ("k", "v", "P", "placed", "pos", "w"):
+            assert (_bits(d[k]) == _bits(eager[k])).all() if d[k].is_floating_point() else torch.equal(d[k], eager[k]), k
+        assert torch.equal(st, eager["status"])
+
+
 def test_slices_beyond_shared_memory():
     c = _case(36, 1, 1, 1, 8, [400003], 256, BF, placed=[100000])
     _check(c, _run(c, 150001, 4, 1000), 150001, 4, 1000)

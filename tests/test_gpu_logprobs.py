@@ -47,6 +47,16 @@ def _check(r, logits, token, node=None, top_n=0, T=1.0):
     assert (r["status"] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,V,top_n", [(BF, 20001, 7), (BF, 20001, 0), (F32, 20000, 32), (F32, 45001, 3), (BF, 9000, 32)])
+def test_more_rows_than_fit_at_once(dtype, V, top_n):
+    """One block a row, its units' largest entries in shared memory or (45001 fp32 entries) not."""
+    logits = _logits(49, 1, 470, V, dtype)
+    logits[0, 3, 100:] = float("-inf")                                   # a masked row
+    logits[0, 4, ::2] = logits[0, 4].max()                               # many ties
+    token = torch.randint(0, V, (1, 470), generator=synth.gen(49, 91)).to(torch.int32)
+    _check(_run(logits, token, top_n=top_n), logits, token, top_n=top_n)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V", [1, 7, 8, 33, 1000, 2047, 2048, 2049, 20001, 151936])
 def test_every_row_scored(dtype, V):

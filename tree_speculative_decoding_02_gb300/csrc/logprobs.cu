@@ -252,7 +252,7 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 }
 
 struct LpArgs {
-    int rows, N, V, A, nunits, top_n;
+    int N, V, A, nunits, top_n;
     bool near;  // the units' largest entries behind the ring, not in the workspace
     float s2, inv_t;
     const int32_t* node;
@@ -458,7 +458,7 @@ __device__ __forceinline__ void lp_finish(const LpArgs& p, LpScratch& S, const T
         tl[tid] = NAN;
     }
     if (bad || top_n == 0) return;  // the same for the whole block
-    // ---- their entries that reach it, ranked by one warp
+    // ---- their entries that reach it, each ranked by counting the better ones
     const int nl = S.nl;
     if (nl <= kLpLists) {
 #pragma unroll 4
@@ -561,9 +561,9 @@ static cudaError_t lp_go(int B, int N, int V, int A, int top_n, float temperatur
                          int32_t* top_token, float* top_logprob, int32_t* status, void* ws, cudaStream_t st) {
     const int nunits = lp_units(V, sizeof(T)), rows = B * A;
     unsigned char* w = static_cast<unsigned char*>(ws);
-    LpArgs a{rows,  N,     V,       A,       nunits,    top_n,       false, (float)(1.4426950408889634 / (double)temperature),
-                   (float)(1.0 / (double)temperature), node, token, reinterpret_cast<float4*>(w), logprob, entropy,
-                   top_token, top_logprob, status};
+    LpArgs a{N, V, A, nunits, top_n, false, (float)(1.4426950408889634 / (double)temperature),
+             (float)(1.0 / (double)temperature), node, token, reinterpret_cast<float4*>(w), logprob, entropy,
+             top_token, top_logprob, status};
     T* lane_max = reinterpret_cast<T*>(w + kLpPartBytes);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
