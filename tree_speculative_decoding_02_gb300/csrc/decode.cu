@@ -26,8 +26,8 @@ constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtMaxCtas = 512;
 }  // namespace
 
-// Bound by the CUDA cores and shared memory from 4 heads a kv head on, by HBM below: a row costs
-// 4 G d flop, and every K element is read from shared memory once for all heads of the block.
+// Bound by HBM up to 4 heads a kv head, by the CUDA cores and shared memory above: a row costs 4 G d
+// flop, and every K element is read from shared memory once for all heads of the block.
 // 16 requests of 6000 rows: 32 heads over 8 kv heads of 128 168 us (5.2 TB/s), 24 over 4 of 256
 // 234 us (3.7 TB/s); before the ring, with each row's copies behind its own page lookup, 265 and
 // 305 us.  A block is 4, 8 or 16 heads, the smallest that holds the group: sums for more do not
@@ -450,7 +450,7 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
 }
 
 // The grid of a split kernel with `ctas` CTAs an SM.  A call is small if the tiles that its units
-// can have are no more than four (fp32, whose tiles take four times as long: one) for every CTA
+// can have are no more than four (fp32, whose tiles take longer: one) for every CTA
 // of a cluster a unit, all of them resident: the split over more CTAs would then gain less than
 // the second kernel costs.  Replayed from a graph, as a cluster and as two kernels: one request of
 // 1000 rows, 24 heads of 256, 9.7 and 11.7 us; of 4000 rows, 32 heads of 128, 12.4 and 14.5;
