@@ -292,9 +292,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
         }
     }
     if (p.cl) {
+        DecNew<float, D> mine_new;
+        mine_new.load(p, mine, dec_first_head(p), lane);
         if (p.cl > 1) tc::cluster_sync();
         else __syncthreads();
-        dec_finish<float, D, kSimtThreads>(p, mine, p.out, s_q);
+        dec_finish<float, D, kSimtThreads>(p, mine, mine_new, s_q);
     }
 }
 

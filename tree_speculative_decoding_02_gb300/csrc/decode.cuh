@@ -242,41 +242,78 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int
 }
 
 // A cluster's finish (p.cl): the heads of its unit over its warps, the weight sums of each CTA's
-// own rows.  All threads of all its CTAs, behind a cluster barrier; `w` as dec_plan gave it.
-template <typename Tin, int D, int NT>
-__device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWalk& w, ddt_dtype out_type, float* s_x) {
-    constexpr int E = D / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % p.cl;
-    const int lb = w.l * p.B + w.b, g = w.g;
-    for (int h = rank + p.cl * warp; h < p.G; h += p.cl * (NT / 32)) {
-        const int hq = g * p.G + h;
-        const HeadJoin j = head_join<Tin, D>(p, lb, hq, lane);
-        const long long at = ((long long)lb * p.Hq + hq) * D;
-        float acc[E];
+// own rows.  All threads of all its CTAs, behind a cluster barrier; `w` as dec_plan gave it.  What
+// needs no partials (the new row's part of a warp's first head) comes before the barrier.
+template <typename Tin, int D>
+struct DecNew {
+    float tn, v[D / 32];
+    __device__ __forceinline__ void load(const DecodeParams& p, const DecodeWalk& w, int h, int lane) {
+        tn = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (j.err) {
-            if (lane == 0) atomicMax(p.status + w.b, j.err);
-        } else {
-            if (p.k_new) {
-                const float f = tc::ex2(j.tn - j.ref);
-                const Tin* v = static_cast<const Tin*>(p.v_new) + ((long long)lb * p.Hkv + g) * D;
+        for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
+        if (!p.k_new || h >= p.G) return;
+        const long long lb = (long long)w.l * p.B + w.b;
+        const Tin* q = static_cast<const Tin*>(p.q) + (lb * p.Hq + w.g * p.G + h) * D + lane;
+        const Tin* k = static_cast<const Tin*>(p.k_new) + (lb * p.Hkv + w.g) * D + lane;
+        const Tin* vn = static_cast<const Tin*>(p.v_new) + (lb * p.Hkv + w.g) * D + lane;
+        float s = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = f * to_f32(v[e * 32 + lane]);
-            }
-            const float2* ml = p.part_ml + j.first * p.HT + h;
-            const float* po = p.part_o + (j.first * p.HT + h) * D;
-#pragma unroll 8
-            for (int s = 0; s < j.ns; ++s) {
-                const float f = tc::ex2(ml[(long long)s * p.HT].x - j.ref);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(f, po[(long long)s * p.HT * D + e * 32 + lane], acc[e]);
-            }
-            const float inv = j.z > 0.f ? 1.f / j.z : j.z;  // no rows at all: 0; NaN stays
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= inv;
+        for (int e = 0; e < D / 32; ++e) {
+            s = fmaf(to_f32(q[e * 32]), to_f32(k[e * 32]), s);
+            v[e] = to_f32(vn[e * 32]);
         }
-        if (out_type == DDT_BF16) {
+        tn = warp_sum(s) * p.scale_log2;
+    }
+};
+__device__ __forceinline__ int dec_first_head(const DecodeParams& p) {
+    return (int)(blockIdx.x % p.cl) + p.cl * (int)(threadIdx.x >> 5);
+}
+
+template <typename Tin, int D, int NT>
+__device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWalk& w, DecNew<Tin, D> x, float* s_x) {
+    constexpr int E = D / 32, kCh = E == 8 ? 4 : 8;  // segments whose O is in flight
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % p.cl;
+    const int lb = w.l * p.B + w.b, g = w.g, ns = min(p.cl, w.nt);
+    const long long first = ((long long)lb * p.Hkv + g) * p.cl;  // slot
+    for (int h = dec_first_head(p); h < p.G; h += p.cl * (NT / 32)) {
+        if (h >= p.cl * (NT / 32)) x.load(p, w, h, lane);
+        const float* po = p.part_o + (first * p.HT + h) * D + lane;
+        const float2 ml = lane < ns ? p.part_ml[(first + lane) * p.HT + h] : make_float2(-INFINITY, 0.f);
+        float o[kCh][E], acc[E];
+#pragma unroll
+        for (int s = 0; s < kCh; ++s)
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[s][e] = s < ns ? po[(long long)s * p.HT * D + e * 32] : 0.f;
+        const float m = fmaxf(warp_max(ml.x), x.tn), ref = m == -INFINITY ? 0.f : m, low = -warp_max(-fminf(ml.y, 0.f));
+        const float f = lane < ns ? tc::ex2(ml.x - ref) : 0.f, fn = tc::ex2(x.tn - ref);
+        const float z = warp_sum(f * ml.y) + fn;
+        const int err = (w.P < 0 || w.P > p.cap) ? DDT_ERR_CAPACITY
+                                                 : (low < 0.f ? (low == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG) : DDT_OK);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fn * x.v[e];
+#pragma unroll
+        for (int s0 = 0; s0 < 8; s0 += kCh) {
+            if (s0 >= ns) break;
+            if (s0) {
+#pragma unroll
+                for (int s = 0; s < kCh; ++s)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[s][e] = s0 + s < ns ? po[(long long)(s0 + s) * p.HT * D + e * 32] : 0.f;
+            }
+#pragma unroll
+            for (int s = 0; s < kCh; ++s) {
+                const float fs = __shfl_sync(kFull, f, s0 + s);
+                if (s0 + s < ns)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(fs, o[s][e], acc[e]);
+            }
+        }
+        const float inv = z > 0.f ? 1.f / z : z;  // no rows at all: 0; NaN stays
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = err ? 0.f : acc[e] * inv;
+        if (err && lane == 0) atomicMax(p.status + w.b, err);
+        const long long at = ((long long)lb * p.Hq + g * p.G + h) * D;
+        if (p.out == DDT_BF16) {
 #pragma unroll
             for (int e = 0; e < E; ++e) static_cast<__nv_bfloat16*>(p.o)[at + e * 32 + lane] = from_f32<__nv_bfloat16>(acc[e]);
         } else {

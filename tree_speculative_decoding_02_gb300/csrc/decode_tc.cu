@@ -439,6 +439,8 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
     }
 
     tc::tc_fence_before();
+    DecNew<__nv_bfloat16, D> mine_new;
+    if (p.cl) mine_new.load(p, mine, dec_first_head(p), lane);
     __syncthreads();
     if (warp == 1) {
         tc::tc_fence_after();
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
     }
     if (p.cl) {
         if (p.cl > 1) tc::cluster_sync();
-        dec_finish<__nv_bfloat16, D, Cfg::kThreads>(p, mine, p.out, reinterpret_cast<float*>(ring));
+        dec_finish<__nv_bfloat16, D, Cfg::kThreads>(p, mine, mine_new, reinterpret_cast<float*>(ring));
     }
 }
 
