@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
     }
     if (p.cl) {
         DecNew<float, D> mine_new;
-        mine_new.load(p, mine, dec_first_head(p), lane);
+        mine_new.load(p, (long long)mine.l * p.B + mine.b, mine.g, dec_first_head(p), lane);
         if (p.cl > 1) tc::cluster_sync();
         else __syncthreads();
         dec_finish<float, D, kSimtThreads>(p, mine, mine_new, s_q);
@@ -309,12 +309,16 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
     constexpr int E = D / 32;
     extern __shared__ float s_x[];  // [8][D] sums of the warps of a head, or 3 floats a head of a group
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the partials are there from here on
+    DecNew<Tin, D> mine;
+    // launched ahead: the partials are there from here on (the call's inputs were before)
+    auto partials = [&]() { asm volatile("griddepcontrol.wait;" ::: "memory"); };
     if (blockIdx.x < n_join) {
         const unsigned x = WPH == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
         const int lb = (int)(x / p.Hq), hq = (int)(x - (unsigned)lb * p.Hq);
+        if (lb < p.L * p.B) mine.load(p, lb, hq / p.G, hq % p.G, lane);
+        partials();
         if (lb >= p.L * p.B) return;  // (WPH 1: whole warps, no barrier follows)
-        const HeadJoin j = head_join<Tin, D>(p, lb, hq, lane);
+        const HeadJoin j = head_join(p, lb, hq, mine.tn, lane);
         Tout* out = static_cast<Tout*>(p.o) + (long long)x * D;
         if (j.err) {
             if (WPH == 1 || warp == 0) {
@@ -324,16 +328,11 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
             }
             return;  // (WPH 8: all warps)
         }
-        const int g = hq / p.G, h = (hq % p.G) % p.hbs;
+        const int h = (hq % p.G) % p.hbs;
+        const float w = WPH == 1 || warp == 0 ? tc::ex2(mine.tn - j.ref) : 0.f;
         float acc[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (p.k_new && (WPH == 1 || warp == 0)) {
-            const float w = tc::ex2(j.tn - j.ref);
-            const Tin* v = static_cast<const Tin*>(p.v_new) + ((long long)lb * p.Hkv + g) * D;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = w * to_f32(v[e * 32 + lane]);
-        }
+        for (int e = 0; e < E; ++e) acc[e] = w * mine.v[e];
         const float2* ml = p.part_ml + j.first * p.HT + h;
         const float* po = p.part_o + (j.first * p.HT + h) * D;
 #pragma unroll 4
@@ -364,17 +363,20 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
     float* s_ref = s_x;
     float* s_inv = s_ref + p.G;
     float* s_tn = s_inv + p.G;
+    mine.load(p, lb, g, warp, lane);
     const int P = p.prefix_len[lb % p.B];
+    partials();
     // blocks behind the unit's rows (the first also has the new token's)
     if (part && part * 1024LL >= P) return;
     int bad = 0;
     for (int h = warp; h < p.G; h += 8) {
-        const HeadJoin j = head_join<Tin, D>(p, lb, g * p.G + h, lane);
+        if (h >= 8) mine.load(p, lb, g, h, lane);
+        const HeadJoin j = head_join(p, lb, g * p.G + h, mine.tn, lane);
         bad |= j.err;
         if (lane == 0) {
             s_ref[h] = j.ref;
             s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
-            s_tn[h] = j.tn;
+            s_tn[h] = mine.tn;
         }
     }
     if (__syncthreads_or(bad)) return;

@@ -181,30 +181,42 @@ __device__ __forceinline__ long long dec_slot(const DecodeParams& p, const Decod
     return p.cl ? blockIdx.x : ((long long)w.l * p.B + w.b) * (p.Hkv * p.HB) + w.g + blockIdx.x;
 }
 
+// The new row's part of head h of kv head g, by one warp: its score (log2 units), and its value.
+template <typename Tin, int D>
+struct DecNew {
+    float tn, v[D / 32];
+    __device__ __forceinline__ void load(const DecodeParams& p, long long lb, int g, int h, int lane) {
+        tn = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
+        if (!p.k_new || h >= p.G) return;
+        const Tin* q = static_cast<const Tin*>(p.q) + (lb * p.Hq + g * p.G + h) * D + lane;
+        const Tin* k = static_cast<const Tin*>(p.k_new) + (lb * p.Hkv + g) * D + lane;
+        const Tin* vn = static_cast<const Tin*>(p.v_new) + (lb * p.Hkv + g) * D + lane;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            s = fmaf(to_f32(q[e * 32]), to_f32(k[e * 32]), s);
+            v[e] = to_f32(vn[e * 32]);
+        }
+        tn = warp_sum(s) * p.scale_log2;
+    }
+};
 // One head's joined softmax, by one warp.
 struct HeadJoin {
-    float ref, z, tn;  // reference, sum, the new row's score (log2 units)
+    float ref, z;      // reference, sum
     int err;           // a status for the request, or DDT_OK
     int ns;            // segments, from slot `first` on
     long long first;
 };
 
-template <typename Tin, int D>
-__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, int lane) {
+__device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, float tn, int lane) {
     const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
     // loads that do not wait for one another first
     const int P = p.prefix_len[b];
     const long long pre = p.cl ? 0 : p.pre[b], all = p.cl ? 0 : p.pre[p.B];
-    float s = 0.f;
-    if (p.k_new) {
-        const Tin* q = static_cast<const Tin*>(p.q) + ((long long)lb * p.Hq + hq) * D;
-        const Tin* k = static_cast<const Tin*>(p.k_new) + ((long long)lb * p.Hkv + g) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) s = fmaf(to_f32(q[e * 32 + lane]), to_f32(k[e * 32 + lane]), s);
-    }
     HeadJoin j;
     j.ref = j.z = 0.f;
-    j.tn = p.k_new ? warp_sum(s) * p.scale_log2 : -INFINITY;
     j.ns = 0;
     j.first = 0;
     j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
@@ -222,7 +234,7 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int
         j.first = (long long)lb * HH + g * p.HB + hb + c0;
     }
     const float2* ml = p.part_ml + j.first * p.HT + h;
-    float m = j.tn, low = 0.f;
+    float m = tn, low = 0.f;
     for (int s = lane; s < j.ns; s += 32) {
         const float2 v = ml[(long long)s * p.HT];
         m = fmaxf(m, v.x);
@@ -237,34 +249,13 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int
         const float2 v = ml[(long long)s * p.HT];
         z = fmaf(tc::ex2(v.x - j.ref), v.y, z);
     }
-    j.z = warp_sum(z) + tc::ex2(j.tn - j.ref);
+    j.z = warp_sum(z) + tc::ex2(tn - j.ref);
     return j;
 }
 
 // A cluster's finish (p.cl): the heads of its unit over its warps, the weight sums of each CTA's
 // own rows.  All threads of all its CTAs, behind a cluster barrier; `w` as dec_plan gave it.  What
 // needs no partials (the new row's part of a warp's first head) comes before the barrier.
-template <typename Tin, int D>
-struct DecNew {
-    float tn, v[D / 32];
-    __device__ __forceinline__ void load(const DecodeParams& p, const DecodeWalk& w, int h, int lane) {
-        tn = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
-        if (!p.k_new || h >= p.G) return;
-        const long long lb = (long long)w.l * p.B + w.b;
-        const Tin* q = static_cast<const Tin*>(p.q) + (lb * p.Hq + w.g * p.G + h) * D + lane;
-        const Tin* k = static_cast<const Tin*>(p.k_new) + (lb * p.Hkv + w.g) * D + lane;
-        const Tin* vn = static_cast<const Tin*>(p.v_new) + (lb * p.Hkv + w.g) * D + lane;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            s = fmaf(to_f32(q[e * 32]), to_f32(k[e * 32]), s);
-            v[e] = to_f32(vn[e * 32]);
-        }
-        tn = warp_sum(s) * p.scale_log2;
-    }
-};
 __device__ __forceinline__ int dec_first_head(const DecodeParams& p) {
     return (int)(blockIdx.x % p.cl) + p.cl * (int)(threadIdx.x >> 5);
 }
@@ -276,7 +267,7 @@ __device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWa
     const int lb = w.l * p.B + w.b, g = w.g, ns = min(p.cl, w.nt);
     const long long first = ((long long)lb * p.Hkv + g) * p.cl;  // slot
     for (int h = dec_first_head(p); h < p.G; h += p.cl * (NT / 32)) {
-        if (h >= p.cl * (NT / 32)) x.load(p, w, h, lane);
+        if (h >= p.cl * (NT / 32)) x.load(p, lb, g, h, lane);
         const float* po = p.part_o + (first * p.HT + h) * D + lane;
         const float2 ml = lane < ns ? p.part_ml[(first + lane) * p.HT + h] : make_float2(-INFINITY, 0.f);
         float o[kCh][E], acc[E];
@@ -327,12 +318,13 @@ __device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWa
     float* s_tn = s_inv + p.G;
     int bad = 0;
     for (int h = warp; h < p.G; h += NT / 32) {
-        const HeadJoin j = head_join<Tin, D>(p, lb, g * p.G + h, lane);
+        x.load(p, lb, g, h, lane);
+        const HeadJoin j = head_join(p, lb, g * p.G + h, x.tn, lane);
         bad |= j.err;
         if (lane == 0) {
             s_ref[h] = j.ref;
             s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
-            s_tn[h] = j.tn;
+            s_tn[h] = x.tn;
         }
     }
     if (__syncthreads_or(bad)) return;

@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
 
     tc::tc_fence_before();
     DecNew<__nv_bfloat16, D> mine_new;
-    if (p.cl) mine_new.load(p, mine, dec_first_head(p), lane);
+    if (p.cl) mine_new.load(p, (long long)mine.l * p.B + mine.b, mine.g, dec_first_head(p), lane);
     __syncthreads();
     if (warp == 1) {
         tc::tc_fence_after();
