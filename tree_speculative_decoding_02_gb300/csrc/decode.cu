@@ -453,20 +453,27 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
                                       : decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
 }
 
-// The grid of a split kernel with `ctas` CTAs an SM.  A call is small if the tiles that its units
-// can have are no more than four (fp32, whose tiles take longer: one) for every CTA
-// of a cluster a unit, all of them resident: the split over more CTAs would then gain less than
-// the second kernel costs.  Replayed from a graph, as a cluster and as two kernels: one request of
-// 1000 rows, 24 heads of 256, 9.7 and 11.7 us; of 4000 rows, 32 heads of 128, 12.4 and 14.5;
-// fp32, one request of 1000 rows 13.6 and 15.4, two of up to 2000 rows 19.5 and 16.0.
+// The grid of a split kernel with `ctas` CTAs an SM.  A cluster a unit saves the second kernel (2.7
+// us), but a CTA of it takes nt / cl tiles of a full table where an even split over all CTAs takes
+// units nt / C (one at least), and a tile takes about 1.2 us at head size 128 and 1.6 at 256 (fp32
+// 4.7 and 12): a call is small if the excess, times the head size, is within 384 (fp32 96).
+// Replayed from a graph, as clusters and as two kernels: one request, 32 heads over 8 of 128, 1000
+// rows 7.5 and 10.0 us, 4000 rows 10.7 and 11.1, 6000 rows (4.8 tiles of excess) 13.1 and 12.8; four
+// requests of 4000 rows (0.6) 12.2 and 16.2; 24 heads over 4 of 256, one request of 4000 rows (3)
+// 13.4 and 12.0; fp32, 32 over 8 of 128, one request of 2000 rows (1) 15.1 and 13.7, four (0.3) 20.3
+// and 25.8.  Clusters of 8 stay below the number of CTAs that the GPU's clusters of SMs have room for:
+// 16 of them with a CTA an SM do not run at once (16 units of 256, 1000 rows: 15.1 and 12.1 us).
+// Over 104 shapes of up to 8 requests and 8000 rows the rule is as fast as the better of the two but for
+// one (fp32, 16 units of 256, 1000 rows: 26.7 and 22.2 us).
 cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
                                  cudaStream_t st) {
     p.C *= ctas;
     const long units = (long)p.L * p.B * p.Hkv;
     const int nt = (p.cap + kDecTile - 1) / kDecTile;
     int cl = 1;
-    while (cl < 8 && units * 2 * cl <= p.C && cl < nt) cl *= 2;
-    p.cl = p.HB == 1 && units * cl <= p.C && nt <= (fp32 ? 1 : 4) * cl ? cl : 0;
+    while (cl < 8 && units * 2 * cl <= (cl < 4 ? p.C : p.C - p.C / (ctas == 1 ? 4 : 8)) && cl < nt) cl *= 2;
+    const double tiles = (nt + cl - 1) / cl, even = (double)units * nt / p.C;
+    p.cl = p.HB == 1 && units * cl <= p.C && (tiles - (even > 1. ? even : 1.)) * p.d <= (fp32 ? 96. : 384.) ? cl : 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(counted(p.cl ? (unsigned)(units * cl) : (unsigned)p.C));
     cfg.blockDim = dim3(threads);
