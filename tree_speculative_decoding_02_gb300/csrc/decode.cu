@@ -463,8 +463,11 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
 // 13.4 and 12.0; fp32, 32 over 8 of 128, one request of 2000 rows (1) 15.1 and 13.7, four (0.3) 20.3
 // and 25.8.  Clusters of 8 stay below the number of CTAs that the GPU's clusters of SMs have room for:
 // 16 of them with a CTA an SM do not run at once (16 units of 256, 1000 rows: 15.1 and 12.1 us).
-// Over 104 shapes of up to 8 requests and 8000 rows the rule is as fast as the better of the two but for
-// one (fp32, 16 units of 256, 1000 rows: 26.7 and 22.2 us).
+// Requests may be shorter than the table, and of different lengths: the even split follows them, so
+// the tiles of a CTA are bounded too (512 channels' worth, fp32 256).  With lengths spread from an
+// eighth of the table's rows to all of them, 16 requests of up to 1000 rows, 32 heads over 8 of 128,
+// take 12.5 and 15.1 us; one of 160 shapes is slower as clusters (fp32, 16 units of 256, 1000 rows:
+// 26.7 and 22.2 us).
 cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
                                  cudaStream_t st) {
     p.C *= ctas;
@@ -473,7 +476,7 @@ cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threa
     int cl = 1;
     while (cl < 8 && units * 2 * cl <= (cl < 4 ? p.C : p.C - p.C / (ctas == 1 ? 4 : 8)) && cl < nt) cl *= 2;
     const double tiles = (nt + cl - 1) / cl, even = (double)units * nt / p.C;
-    p.cl = p.HB == 1 && units * cl <= p.C && (tiles - (even > 1. ? even : 1.)) * p.d <= (fp32 ? 96. : 384.) ? cl : 0;
+    p.cl = p.HB == 1 && units * cl <= p.C && tiles * p.d <= (fp32 ? 256. : 512.) && (tiles - (even > 1. ? even : 1.)) * p.d <= (fp32 ? 96. : 384.) ? cl : 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(counted(p.cl ? (unsigned)(units * cl) : (unsigned)p.C));
     cfg.blockDim = dim3(threads);
