@@ -1,0 +1,102 @@
+"""ddt_decode_attn_paged on scores at the edges of fp32, in one launch and in two, against a plain
+64-bit softmax."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _serving as S
+from tests.test_gpu_decode import BF, F32, _case, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _near(c, r, want, weights, size, spread, w=None, skip=()):
+    """Of request b's o: each weight is off by a relative 2.2 decode_delta after normalisation, so a
+    channel by that times sum_p w_p |v_p| (`spread`), and by its rounding to the output type."""
+    got, half = S.f64(r["o"]), S.HALF[r["o"].dtype]
+    Hq, Hkv, d = c["q"].shape[2], c["k"].shape[2], c["q"].shape[3]
+    for b, n in enumerate(c["lens"]):
+        if b in skip:
+            continue
+        delta = S.decode_delta(d, n, size[:, b].repeat(Hq // Hkv, axis=1))[..., None]
+        tol = 2.2 * delta * spread[:, b] + half * np.abs(want[:, b]) + 1e-30
+        err = np.abs(got[:, b] - want[:, b])
+        assert (err <= tol).all(), f"request {b}: {np.nanmax(err / tol):.3g} of the tolerance"
+        if w is not None:
+            m = min(weights[b].shape[2], w.shape[-1])
+            x, exact = S.f64(w)[:, b], weights[b][:, :, :m]
+            dw = S.decode_delta(d, n, size[:, b])[..., None]
+            assert (np.abs(x[:, :, :m] - exact) <= 2.5 * dw * exact + 4 * S.U * exact + 1e-30).all(), b
+            assert (x[:, :, m:] == 0).all()
+
+
+def _plain(c):
+    """o, weights, |q||k| of the finite scores, and sum w |v|; scores of -inf have weight 0, and a
+    head with no others has no rows (o and weights 0)."""
+    f = lambda t: None if t is None else S.f64(t)  # noqa: E731
+    q, kp, vp, kn, vn = f(c["q"]), f(c["k"]), f(c["v"]), f(c["k_new"]), f(c["v_new"])
+    L, B, Hq, d = q.shape
+    Hkv = kp.shape[2]
+    G = Hq // Hkv
+    o, spread, size, weights = np.zeros(q.shape), np.zeros(q.shape), np.zeros((L, B, Hkv)), []
+    for b, n in enumerate(c["lens"]):
+        K, V = S.rows_of(kp, c["table"].numpy(), b, n), S.rows_of(vp, c["table"].numpy(), b, n)
+        if kn is not None:
+            K, V = (np.concatenate([x, y[:, b][:, :, None]], axis=2) for x, y in ((K, kn), (V, vn)))
+        w = np.zeros((L, Hkv, K.shape[2]))
+        for l in range(L):
+            for g in range(Hkv):
+                h = slice(g * G, (g + 1) * G)
+                with np.errstate(invalid="ignore"):
+                    s = q[l, b, h] @ K[l, g].T * c["scale"]
+                s[s < -3e38] = -np.inf                       # past fp32
+                m = s.max(axis=1, keepdims=True, initial=-np.inf)
+                e = np.exp(s - np.where(np.isinf(m), 0.0, m))
+                p = e / np.maximum(e.sum(axis=1, keepdims=True), 1e-300)
+                o[l, b, h], spread[l, b, h] = p @ V[l, g], p @ np.abs(V[l, g])
+                w[l, g] = p.sum(axis=0)
+                a = np.abs(q[l, b, h]) @ np.abs(np.where(np.abs(K[l, g]) > 1e37, 0, K[l, g])).T
+                size[l, b, g] = (a.max(initial=0.0) + 4.0) * abs(c["scale"])   # (4: the products left out here)
+        weights.append(w)
+    return o, weights, size, spread
+
+
+def _set_rows(c, b, rows, channel, value):
+    page = c["k"].shape[3]
+    for i in rows:
+        c["k"][:, int(c["table"][b, i // page]), :, i % page, channel] = value
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (12, 1, 128), (24, 4, 256), (40, 2, 64)])
+@pytest.mark.parametrize("cap_rows", [1024, 9000])
+@pytest.mark.parametrize("kind", ["inf", "overflow"])
+def test_scores_of_minus_infinity(dtype, Hq, Hkv, d, cap_rows, kind):
+    """Cached rows whose score is -inf (a key of -inf, or a product past fp32, the latter for every
+    second head only) have weight 0, however the rows are cut: the row alone in the last tile, whole
+    first tiles, all but the new row, and all."""
+    lens = [129, 700, 300, 200, 640]
+    c = _case(26, 1, len(lens), Hq, Hkv, d, lens, 64, dtype, cap_rows=cap_rows)
+    c["q"][..., 0] = 4.0
+    c["k_new"][..., 0] = 0.5
+    low = -math.inf
+    if kind == "overflow":
+        low = -3e38
+        c["scale"] = 1.0
+        c["q"][..., 1:] *= 0.1
+        c["q"][..., ::2, 0] = 2.0 ** -126                     # 3e38 of it: 3.5
+    _set_rows(c, 0, [128], 0, low)
+    _set_rows(c, 1, range(0, 512), 0, low)
+    _set_rows(c, 2, range(300), 0, low)
+    _set_rows(c, 3, range(200), 0, low)
+    _set_rows(c, 4, range(0, 640, 2), 0, low)
+    if kind == "inf":
+        c["k_new"][:, 3, :, 0] = low
+    w = torch.zeros((1, len(lens), Hkv, c["table"].shape[1] * 64), device="cuda")
+    r = _run(c, weight=w, out_dtype=F32)
+    assert (r["status"] == 0).all()
+    _near(c, r, *_plain(c), w)
+    if kind == "inf":
+        assert (r["o"][:, 3] == 0).all() and (w[:, 3] == 0).all()

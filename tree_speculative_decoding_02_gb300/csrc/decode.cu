@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
         const float* q = static_cast<const float*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D;
         __syncthreads();  // the previous segment is done with shared memory
         for (int e = tid; e < HBS * D; e += kSimtThreads) s_q[e] = e < nh * D ? q[e] : 0.f;
-        if (tid < HBS) s_m[tid] = -INFINITY;
+        if (tid < HBS) s_m[tid] = kNoRef;
         float acc[HBS][4], l[NV];
 #pragma unroll
         for (int h = 0; h < HBS; ++h)

@@ -51,6 +51,10 @@ struct DecodeParams {
 constexpr float kSegBadPage = -1.f;  // a block-table entry outside [0, num_pages)
 constexpr float kSegTimeout = -2.f;  // a bounded wait gave up
 
+// A segment's first reference, the lowest finite value: a head's scores may all be -inf so far, and
+// 2^(-inf - kNoRef) is 0 where 2^(-inf + inf) is NaN.
+constexpr float kNoRef = -3.402823466e38f;
+
 __host__ __device__ __forceinline__ int dec_tiles(int P, int cap) {
     return (P < 0 || P > cap) ? 0 : (P + kDecTile - 1) / kDecTile;
 }

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
             float m[8], l[8];
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
-                m[h] = -INFINITY;
+                m[h] = kNoRef;
                 l[h] = 0.f;
             }
             int bad = 0;
