@@ -435,7 +435,8 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
  * the cache: ddt_commit_paged with N = A = 1, acc_nodes 0 and acc_len 0 appends it.
  *   q [L][B][Hq][d], k_new, v_new [L][B][Hkv][d] (in_dtype); k_new and v_new may both be
  *     NULL: then only the prefix rows are attended to, and o is zero where there are none.
- *     A row whose score is -inf has weight 0; a head all of whose scores are, o of zero.
+ *     A row whose score is -inf has weight 0; a head all of whose scores are, o of zero.  A NaN
+ *     or +inf score makes its head's o, and what the head adds to attn_weight, NaN.
  *   k_pages, v_pages [L][num_pages][Hkv][page_size][d] (in_dtype), block_table
  *     [B][max_pages], page_size and capacity as in ddt_tree_attn_paged; rows past the
  *     prefix are never used, whatever they hold.  Requests may share pages.

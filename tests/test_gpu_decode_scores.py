@@ -100,3 +100,18 @@ def test_scores_of_minus_infinity(dtype, Hq, Hkv, d, cap_rows, kind):
     _near(c, r, *_plain(c), w)
     if kind == "inf":
         assert (r["o"][:, 3] == 0).all() and (w[:, 3] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap_rows", [512, 9000])
+def test_a_nan_key_makes_its_heads_and_their_sums_nan(dtype, cap_rows):
+    """By the definition every weight of a head with a NaN score is NaN; other requests are not touched."""
+    lens = [400, 400, 10]
+    c = _case(27, 1, 3, 8, 2, 64, lens, 64, dtype, cap_rows=cap_rows)
+    c["k"][:, int(c["table"][1, 3]), 0, 5, 7] = math.nan      # kv head 0 of request 1
+    w = torch.zeros((1, 3, 2, c["table"].shape[1] * 64), device="cuda")
+    r = _run(c, weight=w, out_dtype=F32)
+    o = r["o"].cpu()
+    assert o[0, 1, :4].isnan().all() and o[0, [0, 2]].isfinite().all() and o[0, 1, 4:].isfinite().all()
+    assert w[0, 1, 0, :401].isnan().all() and (w[0, 1, 0, 401:] == 0).all()
+    assert w[0, [0, 2]].isfinite().all() and w[0, 1, 1].isfinite().all()

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
         bad |= j.err;
         if (lane == 0) {
             s_ref[h] = j.ref;
-            s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
+            s_inv[h] = j.z > 0.f ? 1.f / j.z : j.z;  // (NaN stays)
             s_tn[h] = mine.tn;
         }
     }

@@ -327,7 +327,7 @@ __device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWa
         bad |= j.err;
         if (lane == 0) {
             s_ref[h] = j.ref;
-            s_inv[h] = j.z > 0.f ? 1.f / j.z : 0.f;
+            s_inv[h] = j.z > 0.f ? 1.f / j.z : j.z;  // (NaN stays)
             s_tn[h] = x.tn;
         }
     }
