@@ -444,7 +444,9 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
  *     (and row prefix_len[b], the new token's once it is appended, if the capacity has it)
  *     gets the sum over the kv head's query heads of its softmax weights ADDED to its
  *     entry; the other entries are left as they are.  Start it at zero.
- *   o [L][B][Hq][d] (out_dtype), apart from q.
+ *   o [L][B][Hq][d] (out_dtype).  o, attn_weight, status and the workspace are apart from one
+ *     another, from q, k_new, v_new, block_table and prefix_len (the call is refused
+ *     otherwise), and from the pages that the prefixes use.
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, max_pages * page_size],
  *     DDT_ERR_INVALID_ARG if a block-table entry that the prefix needs is outside
  *     [0, num_pages); the request's output rows are then zero and its sums unchanged.

@@ -1,0 +1,41 @@
+"""Buffers of the single-token calls that lie directly behind one another in one allocation are
+accepted, and the results are those of buffers of their own."""
+import pytest
+import torch
+
+from tests import _serving as S
+from tree_speculative_decoding_02_gb300 import ddt, synth
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _carve(tensors):
+    """Copies of the tensors side by side (to 16 bytes) in one allocation."""
+    n = [(t.nbytes + 15) // 16 * 16 for t in tensors]
+    base, at, out = torch.zeros(sum(n), dtype=torch.uint8, device="cuda"), 0, []
+    for t, size in zip(tensors, n):
+        v = base[at:at + t.nbytes].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        out.append(v)
+        at += size
+    return out
+
+
+@pytest.mark.parametrize("cap", [256, 9008])
+def test_decode(cap):
+    k, v, table = S.paged_cache(70, 2, 3, 4, 64, [100, 0, 77], 16, dtype=BF, cap_rows=cap)
+    g = synth.gen(70, 71)
+    q, kn, vn = (synth.normal((2, 3, 4, 64), g=g, dtype=BF) for _ in range(3))
+    w, st = torch.zeros((2, 3, 4, table.shape[1] * 16)), torch.zeros(3, dtype=I32)
+    P = torch.tensor([100, 0, 77], dtype=I32)
+    own = [t.cuda() for t in (q, kn, vn, torch.zeros_like(q), w, st, table, P)]
+    ws = ddt.decode_attn_paged_workspace(own[0], k.cuda(), table, weights=True)
+    side = _carve([*own, torch.zeros_like(ws)])
+    k, v = k.cuda(), v.cuda()
+    for x in ([*own, ws], side):
+        ddt.ddt_decode_attn_paged(x[0], x[1], x[2], k, v, x[6], x[7], scale=0.125, attn_weight=x[4], out=x[3], status=x[5],
+                                  workspace=x[8])
+    for a, b in zip(own, side):
+        assert torch.equal(a, b)

@@ -1,0 +1,45 @@
+"""Buffers that a single-token call would read, or write again, after it has begun to write them
+are refused on the host (no GPU needed: the pointers are never dereferenced)."""
+import ctypes
+import itertools
+
+import pytest
+
+from tests.test_serving_refusals import INVALID, _decode, lib, pytestmark  # noqa: F401
+
+at = ctypes.c_void_p
+
+
+def _apart(sizes):
+    """Places for buffers of these bytes, each directly behind the one before (to 16 bytes)."""
+    places, x = {}, 1 << 30
+    for name, n in sizes.items():
+        places[name] = x
+        x += (n + 15) // 16 * 16
+    return places
+
+
+def _check(call, sizes, outputs, more):
+    """Every output over every other buffer: its last 16 bytes over the other's first, the same place,
+    and its first bytes over the other's last."""
+    places = _apart(sizes)
+    for out, other in itertools.product(outputs, sizes):
+        if out == other:
+            continue
+        y, n, m = places[other], sizes[out], sizes[other]
+        for x in {y, y - (n - 1) // 16 * 16, y + (m - 1) // 16 * 16}:
+            kw = {k: at(v) for k, v in places.items()}
+            kw[out] = at(x)
+            assert call(**kw, **more) == INVALID, (out, other, x - y)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_decode(lib, G):  # noqa: F811
+    L, B, Hkv, d, page, mp = 2, 4, 2, 64, 16, 4
+    Hq = G * Hkv
+    ws = lib.ddt_decode_attn_paged_workspace(L, B, Hq, Hkv, d, page, mp, 1, 1)
+    sizes = dict(o=L * B * Hq * d * 2, w=L * B * Hkv * page * mp * 4, st=4 * B, ws=ws, q=L * B * Hq * d * 2,
+                 kn=L * B * Hkv * d * 2, vn=L * B * Hkv * d * 2, tab=4 * B * mp, plen=4 * B)
+    before = lib.ddt_launch_count()
+    _check(lambda **kw: _decode(lib, **kw), sizes, ("o", "w", "st", "ws"), dict(L=L, B=B, Hq=Hq, Hkv=Hkv, d=d, page=page, mp=mp))
+    assert lib.ddt_launch_count() == before

@@ -396,10 +396,21 @@ static bool paging_sizes_ok(int page_size, int num_pages, int max_pages) {
     return page_rows_ok(page_size) && (long)page_size * max_pages <= (1L << 30) && num_pages >= 1;
 }
 
-// buffers that a call reads after it has begun to write the other
+// Buffers that a call reads, or writes again, after it has begun to write the other.
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
+}
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+// one of the first n_out spans (what a call writes) meets another span; NULL meets none
+static bool any_overlap(const Span* s, int n, int n_out) {
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (s[i].at && s[j].at && overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes)) return true;
+    return false;
 }
 
 // the largest grid and plane counts the kernels index with 32 bits
@@ -430,14 +441,22 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
         return DDT_ERR_UNSUPPORTED;
     if (!q || !k_pages || !v_pages || !block_table || !prefix_len || !o || !status || !workspace || !k_new != !v_new)
         return DDT_ERR_INVALID_ARG;
-    if (ws_bytes < decode_ws_bytes(n_layers, B, Hq, Hkv, d, page_size * max_pages, in_dtype, attn_weight != nullptr) ||
-        !aligned16(workspace))
-        return DDT_ERR_INVALID_ARG;
+    const size_t need = decode_ws_bytes(n_layers, B, Hq, Hkv, d, page_size * max_pages, in_dtype, attn_weight != nullptr);
+    if (ws_bytes < need || !aligned16(workspace)) return DDT_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
         !aligned16(o) || !aligned16(attn_weight))
         return DDT_ERR_INVALID_ARG;
-    const size_t n_q = (size_t)n_layers * B * Hq * d;
-    if (overlap(o, n_q * (out_dtype == DDT_BF16 ? 2 : 4), q, n_q * (in_dtype == DDT_BF16 ? 2 : 4))) return DDT_ERR_INVALID_ARG;
+    const size_t n_lb = (size_t)n_layers * B, in = in_dtype == DDT_BF16 ? 2 : 4, n_new = n_lb * Hkv * d * in;
+    const Span spans[] = {{o, n_lb * Hq * d * (out_dtype == DDT_BF16 ? 2 : 4)},
+                          {attn_weight, n_lb * Hkv * page_size * max_pages * sizeof(float)},
+                          {status, B * sizeof(int32_t)},
+                          {workspace, need},
+                          {q, n_lb * Hq * d * in},
+                          {k_new, n_new},
+                          {v_new, n_new},
+                          {block_table, (size_t)B * max_pages * sizeof(int32_t)},
+                          {prefix_len, B * sizeof(int32_t)}};
+    if (any_overlap(spans, 9, 4)) return DDT_ERR_INVALID_ARG;
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
     return from_cuda(launch_decode(n_layers, B, Hq, Hkv, d, pg, in_dtype, out_dtype, q, k_new, v_new, k_pages, v_pages,
                                    prefix_len, scale, o, attn_weight, status, workspace,
