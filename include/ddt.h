@@ -485,7 +485,9 @@ ddt_status ddt_decode_attn_paged(int n_layers, int B, int Hq, int Hkv, int d, in
  *   n_placed [B], prefix_len [B]: become keep.  seq_len [B]: tokens of the sequence that
  *     have been cached, evicted ones included (advance it where prefix_len advances, and
  *     give it to ddt_build_tree as the base of positions); read only.
- *     The three are arrays of their own.
+ *   attn_weight, row_pos, prefix_len, n_placed, status and the workspace are apart from one
+ *     another, from block_table and seq_len (the call is refused otherwise), and from the pages
+ *     in use.  k_pages and v_pages are apart, or one and the same pool.
  * Requests with prefix_len[b] <= keep are left as they are (status DDT_OK).  Pages past
  * ceil(keep / page_size) of a cut request hold nothing any more.
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, cap]; DDT_ERR_INVALID_ARG

@@ -39,3 +39,23 @@ def test_decode(cap):
                                   workspace=x[8])
     for a, b in zip(own, side):
         assert torch.equal(a, b)
+
+
+def test_evict():
+    k, v, table = S.paged_cache(71, 1, 3, 2, 64, [100, 9, 90], 16, dtype=BF, cap_rows=128, poison=False)
+    w = torch.rand((1, 3, 2, table.shape[1] * 16), generator=synth.gen(71, 71))
+    P = torch.tensor([100, 9, 90], dtype=I32)
+    own = [t.cuda() for t in (w, torch.zeros_like(w, dtype=I32), P, torch.zeros_like(P), torch.full_like(P, 7), table, P)]
+    ws = ddt.evict_paged_workspace(k.cuda(), table)
+    side = _carve([*own, torch.zeros_like(ws)])
+    pools = []
+    for x in ([*own, ws], side):
+        pools.append((k.cuda(), v.cuda()))
+        ddt.ddt_evict_paged(*pools[-1], x[5], x[2], x[3], x[6], x[0], x[1], keep=50, n_recent=3, status=x[4], workspace=x[7])
+    assert own[4].tolist() == [0, 0, 0]
+    for a, b in zip([*own, *pools[0]], [*side[:7], *pools[1]]):
+        assert torch.equal(a, b)
+    x = [t.cuda() for t in (w, torch.zeros_like(w, dtype=I32), P, torch.zeros_like(P), torch.full_like(P, 7), table, P)]
+    one = k.cuda()                                              # keys that are the values too
+    ddt.ddt_evict_paged(one, one, x[5], x[2], x[3], x[6], x[0], x[1], keep=50, n_recent=3, status=x[4], workspace=ws)
+    assert torch.equal(one, pools[0][0]) and torch.equal(x[1], own[1])

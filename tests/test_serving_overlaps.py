@@ -5,7 +5,7 @@ import itertools
 
 import pytest
 
-from tests.test_serving_refusals import INVALID, _decode, lib, pytestmark  # noqa: F401
+from tests.test_serving_refusals import INVALID, _decode, _evict, lib, pytestmark  # noqa: F401
 
 at = ctypes.c_void_p
 
@@ -42,4 +42,20 @@ def test_decode(lib, G):  # noqa: F811
                  kn=L * B * Hkv * d * 2, vn=L * B * Hkv * d * 2, tab=4 * B * mp, plen=4 * B)
     before = lib.ddt_launch_count()
     _check(lambda **kw: _decode(lib, **kw), sizes, ("o", "w", "st", "ws"), dict(L=L, B=B, Hq=Hq, Hkv=Hkv, d=d, page=page, mp=mp))
+    assert lib.ddt_launch_count() == before
+
+
+def test_evict(lib):  # noqa: F811
+    L, B, Hkv, page, mp = 2, 4, 2, 16, 4
+    rows = L * B * Hkv * page * mp * 4
+    sizes = dict(w=rows, pos=rows, plen=4 * B, np=4 * B, st=4 * B, ws=lib.ddt_evict_paged_workspace(L, B, Hkv, page, 10, mp),
+                 tab=4 * B * mp, seq=4 * B)
+    before = lib.ddt_launch_count()
+    _check(lambda **kw: _evict(lib, **kw), sizes, ("w", "pos", "plen", "np", "st", "ws"),
+           dict(L=L, B=B, Hkv=Hkv, page=page, mp=mp))
+    pool = L * 10 * Hkv * page * 64 * 2
+    places = {k: at(v) for k, v in _apart({**sizes, "kp": pool, "vp": pool}).items()}
+    for x in (16, pool - 16, 16 - pool):
+        places["vp"] = at(places["kp"].value + x)
+        assert _evict(lib, **places, L=L, B=B, Hkv=Hkv, page=page, mp=mp) == INVALID, x
     assert lib.ddt_launch_count() == before

@@ -485,12 +485,16 @@ ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, i
         !status || !workspace)
         return DDT_ERR_INVALID_ARG;
     const AttnPaging pg{page_size, num_pages, max_pages, block_table};
-    if (ws_bytes < evict_ws_bytes(n_layers, B, Hkv, pg) || !aligned16(workspace) || !aligned16(k_pages) ||
-        !aligned16(v_pages) || !aligned16(attn_weight) || !aligned16(row_pos))
+    const size_t need = evict_ws_bytes(n_layers, B, Hkv, pg);
+    if (ws_bytes < need || !aligned16(workspace) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(attn_weight) ||
+        !aligned16(row_pos))
         return DDT_ERR_INVALID_ARG;
-    const size_t n_b = (size_t)B * sizeof(int32_t);
-    if (overlap(seq_len, n_b, prefix_len, n_b) || overlap(seq_len, n_b, n_placed, n_b) || overlap(prefix_len, n_b, n_placed, n_b))
-        return DDT_ERR_INVALID_ARG;
+    const size_t n_b = (size_t)B * sizeof(int32_t), n_rows = (size_t)n_layers * B * Hkv * page_size * max_pages * 4;
+    const Span spans[] = {{attn_weight, n_rows}, {row_pos, n_rows}, {prefix_len, n_b},       {n_placed, n_b},
+                          {status, n_b},         {workspace, need}, {block_table, n_b * max_pages}, {seq_len, n_b}};
+    if (any_overlap(spans, 8, 6)) return DDT_ERR_INVALID_ARG;
+    const size_t n_pool = (size_t)n_layers * num_pages * Hkv * page_size * row_bytes;
+    if (k_pages != v_pages && overlap(k_pages, n_pool, v_pages, n_pool)) return DDT_ERR_INVALID_ARG;
     return from_cuda(launch_evict(n_layers, B, Hkv, (int)row_bytes, pg, keep, n_sink, n_recent, k_pages, v_pages, seq_len,
                                   attn_weight, row_pos, prefix_len, n_placed, status, workspace,
                                   reinterpret_cast<cudaStream_t>(stream)));
