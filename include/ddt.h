@@ -525,6 +525,8 @@ ddt_status ddt_evict_paged(int n_layers, int B, int Hkv, int d, int page_size, i
  *   node < 0 marks a padding entry: logprob and entropy 0, top_token -1, top_logprob 0,
  *     status DDT_OK.  token < 0 with a row: no token is given, logprob is 0.
  *   entropy may be NULL, and top_token and top_logprob where top_n is 0.
+ *   Outputs and workspace are apart from one another, from node, token and the logits (the call
+ *     is refused otherwise).
  *   status [B][A]: DDT_ERR_NONFINITE for a row with a NaN or +inf logit or with none above
  *     -inf (outputs NaN, top_token -1); DDT_ERR_INVALID_ARG for node >= N or token >= V
  *     (outputs as for padding).

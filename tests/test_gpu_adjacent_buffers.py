@@ -59,3 +59,26 @@ def test_evict():
     one = k.cuda()                                              # keys that are the values too
     ddt.ddt_evict_paged(one, one, x[5], x[2], x[3], x[6], x[0], x[1], keep=50, n_recent=3, status=x[4], workspace=ws)
     assert torch.equal(one, pools[0][0]) and torch.equal(x[1], own[1])
+
+
+@pytest.mark.parametrize("top", [0, 5])
+def test_logprobs(top):
+    x = synth.normal((2, 5, 200), g=synth.gen(72, 71), dtype=BF)
+    node = torch.tensor([[0, 3, -1], [4, 1, 1]], dtype=I32)
+    token = torch.tensor([[9, 199, -1], [0, 5, -1]], dtype=I32)
+    names = ["logprob", "entropy", "status"] + (["top_token", "top_logprob"] if top else [])
+    like = dict(logprob=torch.zeros((2, 3)), entropy=torch.zeros((2, 3)), status=torch.zeros((2, 3), dtype=I32),
+                top_token=torch.zeros((2, 3, top), dtype=I32), top_logprob=torch.zeros((2, 3, top)))
+    own = [t.cuda() for t in (x, node, token, *(like[n] for n in names))]
+    ws = ddt.token_logprobs_workspace(own[0], own[2], top_n=top)
+    side = _carve([*own, torch.zeros_like(ws)])
+    for t in ([*own, ws], side):
+        ddt.ddt_token_logprobs(t[0], t[2], node=t[1], top_n=top, out=dict(zip(names, t[3:])), workspace=t[-1])
+    assert (own[5] == 0).all()
+    if not top:   # where no alternatives are asked for, their pointers are not looked at
+        p = [t.data_ptr() for t in side]
+        rc = ddt.load().ddt_token_logprobs(2, 5, 200, 3, 0, 1.0, 1, p[0], p[1], p[2], p[3], p[4], p[0] + 16, p[0] + 32, p[5], p[6],
+                                           ws.nbytes, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+    for a, b in zip(own, side):
+        assert torch.equal(a, b)

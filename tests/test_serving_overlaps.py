@@ -5,7 +5,7 @@ import itertools
 
 import pytest
 
-from tests.test_serving_refusals import INVALID, _decode, _evict, lib, pytestmark  # noqa: F401
+from tests.test_serving_refusals import INVALID, _decode, _evict, _logprobs, lib, pytestmark  # noqa: F401
 
 at = ctypes.c_void_p
 
@@ -58,4 +58,14 @@ def test_evict(lib):  # noqa: F811
     for x in (16, pool - 16, 16 - pool):
         places["vp"] = at(places["kp"].value + x)
         assert _evict(lib, **places, L=L, B=B, Hkv=Hkv, page=page, mp=mp) == INVALID, x
+    assert lib.ddt_launch_count() == before
+
+
+def test_logprobs(lib):  # noqa: F811
+    B, N, V, A, top = 3, 5, 200, 4, 6
+    n = 4 * B * A
+    sizes = dict(lp=n, en=n, tt=n * top, tl=n * top, st=n, ws=lib.ddt_token_logprobs_workspace(B, A, V, top), x=B * N * V * 2,
+                 node=n, tok=n)
+    before = lib.ddt_launch_count()
+    _check(lambda **kw: _logprobs(lib, **kw), sizes, ("lp", "en", "tt", "tl", "st", "ws"), dict(B=B, N=N, V=V, A=A, top=top))
     assert lib.ddt_launch_count() == before

@@ -399,7 +399,7 @@ static bool paging_sizes_ok(int page_size, int num_pages, int max_pages) {
 // Buffers that a call reads, or writes again, after it has begun to write the other.
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
+    return na && nb && x < y + nb && y < x + na;
 }
 struct Span {
     const void* at;
@@ -520,8 +520,20 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
         return DDT_ERR_UNSUPPORTED;
     if (!target_logits || !token || !logprob || !status || !workspace || (top_n > 0 && (!top_token || !top_logprob)))
         return DDT_ERR_INVALID_ARG;
-    if (ws_bytes < logprobs_ws_bytes(B, A, V, top_n) || !aligned16(workspace)) return DDT_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(target_logits) % (dtype == DDT_BF16 ? 2 : 4)) return DDT_ERR_INVALID_ARG;
+    const size_t need = logprobs_ws_bytes(B, A, V, top_n), esz = dtype == DDT_BF16 ? 2 : 4;
+    if (ws_bytes < need || !aligned16(workspace)) return DDT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(target_logits) % esz) return DDT_ERR_INVALID_ARG;
+    const size_t n_a = (size_t)B * A * 4;
+    const Span spans[] = {{logprob, n_a},
+                          {entropy, n_a},
+                          {top_token, n_a * top_n},
+                          {top_logprob, n_a * top_n},
+                          {status, n_a},
+                          {workspace, need},
+                          {target_logits, (size_t)B * N * V * esz},
+                          {node, n_a},
+                          {token, n_a}};
+    if (any_overlap(spans, 9, 6)) return DDT_ERR_INVALID_ARG;
     return from_cuda(launch_token_logprobs(B, N, V, A, top_n, temperature, dtype, target_logits, node, token, logprob,
                                            entropy, top_token, top_logprob, status, workspace,
                                            reinterpret_cast<cudaStream_t>(stream)));
