@@ -173,7 +173,12 @@ struct LpRun {
         s = t = 0.f;
     }
 };
-constexpr float kLpFar = 1e30f;  // references beyond it are taken before scaling
+// From here on differences to the reference are taken before scaling: m log2(e) / T as rounded is
+// off by up to 2^-11 below it, and its correction (lp_share) by half the square of ln 2 of that, 2^-24.
+constexpr float kLpFar = 16384.f;
+__device__ __forceinline__ bool lp_far(float ref) { return !(fabsf(ref) < kLpFar); }
+// what the terms of a near reference took too much
+__device__ __forceinline__ float lp_off(float m, float ref, float s2) { return lp_far(ref) ? 0.f : fmaf(m, s2, -ref); }
 
 // One unit's words of this thread, from shared memory (read twice: keeping them in registers
 // costs a third of the warps); returns the largest entry.
@@ -189,7 +194,9 @@ __device__ __forceinline__ float lp_add(LpRun& r, const uint4* from, float s2) {
     if ((mt - r.m) * s2 > 8.f) {  // the first unit, or an entry far above the reference
         const float ref = mt * s2;
         if (r.s != 0.f) {
-            const float d = fabsf(ref) < kLpFar && fabsf(r.ref) < kLpFar ? r.ref - ref : fmaxf((r.m - mt) * s2, kLpLow);
+            const float d = !lp_far(ref) && !lp_far(r.ref)
+                                ? r.ref - ref
+                                : fmaxf((r.m - mt) * s2 - lp_off(r.m, r.ref, s2) + lp_off(mt, ref, s2), kLpLow);
             const float f = tc::ex2(d);
             r.t = f * fmaf(d, r.s, r.t);
             r.s *= f;
@@ -217,10 +224,10 @@ __device__ __forceinline__ float lp_add(LpRun& r, const uint4* from, float s2) {
     unpack2(add2(t[0], t[1]), t0, t1);
     s0 += s1;
     t0 += t1;
-    if (__any_sync(kFull, t0 != t0 || !(fabsf(r.ref) < kLpFar))) {
-        // masked entries (0 * -inf in t), or out of fp32's range once scaled (the type's lowest
-        // value as a mask): again, term by term and with a bound
-        const bool far = !(fabsf(r.ref) < kLpFar);
+    if (__any_sync(kFull, t0 != t0 || lp_far(r.ref))) {
+        // masked entries (0 * -inf in t), or a far reference (a low temperature, logits far from
+        // zero, the type's lowest value as a mask): again, term by term and with a bound
+        const bool far = lp_far(r.ref);
         const float base = r.m == -INFINITY ? 0.f : r.m;
         s0 = t0 = 0.f;
 #pragma unroll 1
@@ -240,10 +247,9 @@ __device__ __forceinline__ float lp_add(LpRun& r, const uint4* from, float s2) {
     return mt;
 }
 
-// The share with the exact reference m: the terms took 2^-24 m s2 at most of it too much (whose
-// square is nothing).
+// The share with the exact reference m.
 __device__ __forceinline__ float4 lp_share(const LpRun& r, float s2) {
-    const float off = fabsf(r.ref) < kLpFar ? fmaf(r.m, s2, -r.ref) : 0.f, c = 1.f - 0.6931471805599453f * off;
+    const float off = lp_off(r.m, r.ref, s2), c = 1.f - 0.6931471805599453f * off;
     return make_float4(r.m, r.s * c, fmaf(-off, r.s, r.t) * c, r.mx);
 }
 
