@@ -1,5 +1,6 @@
-"""ddt_decode_attn_paged on scores at the edges of fp32, in one launch and in two, against a plain
-64-bit softmax."""
+"""ddt_decode_attn_paged on scores at the edges of fp32 (-inf, NaN), and on scores that move the
+exponents' reference many times a segment, for every head block and head size, in one launch and
+in two; against a plain 64-bit softmax."""
 import math
 
 import numpy as np
@@ -8,6 +9,7 @@ import torch
 
 from tests import _serving as S
 from tests.test_gpu_decode import BF, F32, _case, _run
+from tree_speculative_decoding_02_gb300 import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +117,58 @@ def test_a_nan_key_makes_its_heads_and_their_sums_nan(dtype, cap_rows):
     assert o[0, 1, :4].isnan().all() and o[0, [0, 2]].isfinite().all() and o[0, 1, 4:].isfinite().all()
     assert w[0, 1, 0, :401].isnan().all() and (w[0, 1, 0, 401:] == 0).all()
     assert w[0, [0, 2]].isfinite().all() and w[0, 1, 1].isfinite().all()
+
+
+def _steps(workload, G, d, n, dtype):
+    """40 requests on the same pages.  Channel 0 of the keys climbs by 9.5 (log2 of the weight, for a
+    head whose q has 1 there) from tile to tile, seven tiles and then from the start again, and the
+    values shrink by as much, so that every tile counts; heads take it whole, not at all, by half
+    (a new reference every second tile) and reversed."""
+    B = 40
+    c = _case(workload, 1, 1, G, 1, d, [n], 64, dtype, q_std=0.5)
+    g = synth.gen(workload, 72)
+    c["q"] = synth.normal((1, B, G, d), 0.5, g=g, dtype=dtype)
+    c["q"][..., 0] = torch.tensor([1.0, 0.0, 0.5, -1.0])[torch.arange(G) % 4].to(dtype)
+    c["k_new"], c["v_new"] = (synth.normal((1, B, 1, d), g=g, dtype=dtype) for _ in range(2))
+    for i in range(n):
+        page, row, level = int(c["table"][0, i // 64]), i % 64, i // 128 % 7
+        c["k"][:, page, :, row, 0] = 9.5 * level / (c["scale"] * math.log2(math.e))
+        c["v"][:, page, :, row] *= 2.0 ** (9.5 * (6 - level))
+    c["table"] = c["table"].repeat(B, 1)
+    c["lens"] = [max(0, n - 61 * b) for b in range(B)]
+    return c
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [2, 12, 24])
+@pytest.mark.parametrize("n", [1530, 6000])
+def test_the_reference_moves_many_times_a_segment(dtype, d, G, n):
+    c = _steps(28, G, d, n, dtype)
+    w = torch.zeros((1, len(c["lens"]), 1, c["table"].shape[1] * 64), device="cuda")
+    r = _run(c, weight=w, out_dtype=F32)
+    assert (r["status"] == 0).all()
+    _near(c, r, *_plain(c), w)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,G", [(64, 12), (64, 2), (128, 24)])
+def test_bad_pages_deep_in_long_segments(dtype, d, G):
+    """Segments of many more tiles than are in flight, a page that does not exist in a tile of its own
+    for every third request."""
+    c = _case(29, 1, 1, G, 1, d, [6000], 64, dtype)
+    B = 40
+    g = synth.gen(29, 72)
+    c["q"] = synth.normal((1, B, G, d), 1.5, g=g, dtype=dtype)
+    c["k_new"], c["v_new"] = (synth.normal((1, B, 1, d), g=g, dtype=dtype) for _ in range(2))
+    c["table"], c["lens"] = c["table"].repeat(B, 1), [6000 - 37 * b for b in range(B)]
+    bad = list(range(0, B, 3))
+    for b in bad:
+        c["table"][b, (7 * b) % 70] = 10 ** 6 if b % 2 else -1
+    w = torch.zeros((1, B, 1, c["table"].shape[1] * 64), device="cuda")
+    r = _run(c, weight=w, out_dtype=F32)
+    assert r["status"].cpu().tolist() == [int(b in bad) for b in range(B)]
+    assert (r["o"][:, bad] == 0).all() and (w[:, bad] == 0).all()
+    for b in bad:
+        c["table"][b] = c["table"][1]
+    _near(c, r, *_plain(c), w, skip=bad)
