@@ -2,7 +2,7 @@
 
 `Round` owns the device buffers of one synthetic workload (drafter logits, tree-row
 projections, prefix caches, GDN inputs and state, target logits), preallocates every
-output and workspace once, and `step()` enqueues build -> tree attention -> tree GDN
+output and workspace of its steps once, and `step()` enqueues build -> tree attention -> tree GDN
 -> walk -> commit with no host synchronisation.  The synthetic layers are independent,
 so each attention/GDN call covers all layers at once (a model would call per layer).
 
@@ -162,11 +162,13 @@ class Round:
             ddt.ddt_walk_accept(t["token"], t["parent"], t["n_nodes"], self.A - 1, target_logits=self.target_logits,
                                 out=self.walk, workspace=self.walk_ws, flat=bool(self.cfg.get("flat", False)))
 
-    def emitted_logprobs(self, top_n=0):
+    def emitted_logprobs(self, top_n=0, out=None, workspace=None):
         """Log probabilities of the round's emitted tokens (accepted ones and the bonus) under the
-        target, their rows' entropies and top_n alternatives; after the walk."""
+        target, their rows' entropies and top_n alternatives; after the walk.  Not a part of
+        step(): outputs and workspace that are not given (as to ddt.ddt_token_logprobs) are
+        allocated by each call."""
         return ddt.ddt_token_logprobs(self.target_logits, self.walk["emitted"], node=self.walk["acc_nodes"], top_n=top_n,
-                                      temperature=self.temperature or 1.0)
+                                      temperature=self.temperature or 1.0, out=out, workspace=workspace)
 
     def attention(self):
         """The round's attention call.  With cfg["rope"] (rotated channels) q and the tree
