@@ -26,12 +26,16 @@ constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtMaxCtas = 512;
 }  // namespace
 
-// Bound by HBM up to 4 heads a kv head, by the CUDA cores and shared memory above: a row costs 4 G d
-// flop, and every K element is read from shared memory once for all heads of the block.
-// 16 requests of 6000 rows: 32 heads over 8 kv heads of 128 168 us (5.2 TB/s), 24 over 4 of 256
-// 234 us (3.7 TB/s); before the ring, with each row's copies behind its own page lookup, 265 and
-// 305 us.  A block is 4, 8 or 16 heads, the smallest that holds the group: sums for more do not
-// fit in the registers of two CTAs an SM.
+// Up to 4 heads a kv head bound by HBM and the latency of a tile's steps: 16 requests of 4000 to 8000
+// rows (105787 in all), 32 heads over 8 kv heads of 128 (867 MB of K and V), 166 us, 5.2 TB/s.  Above,
+// bound by reads of shared memory: a lane has one row, so a piece of K is multiplied with 8 or 16
+// pieces of q from there.  24 heads over 4 of 256 (867 MB) 233 us, 3.7 TB/s; 32 over 2 of 256 (433 MB)
+// 216 us and 48 over 3 of 128 (325 MB) 170 us, 2.0 and 1.9 TB/s: half of the warps' waiting is for
+// shared memory, its data pipe is 61 % busy, the FMA pipe 23 to 26 % (the arithmetic alone, 2.6 Gflop
+// of the first and the last, would take 35 us).  Before the ring, with each row's copies behind its own
+// page lookup, the first two took 265 and 305 us.  A block is 4, 8 or 16 heads, the smallest that holds
+// the group: sums for more do not fit in the registers of two CTAs an SM (128 a thread; blocks of 8
+// heads spill 120 to 144 bytes, of 16 196 to 288: 0.2 % of the instructions at most).
 //
 // Tiles of 32 KB of K and V (R rows), three on their way by cp.async; two barriers a tile.
 //   scores   D / 16 lanes a row, 16 channels a lane, all heads; the sums over the lanes scatter

@@ -17,9 +17,10 @@
 //   k_evict_move    grid (L B Hkv, y): the K and V rows, 16 bytes a thread, and the entries behind
 //                   the budget; the first layer's first head writes the request's lengths and status.
 //
-// The moves are bound by HBM: 702 MB of 16 requests of up to 32768 rows cut to 8192 take 105 us
-// beside their selection's 24 (K and V rows of 512 bytes from random places, 5.7 TB/s; two
-// rows' loads in flight a thread and five blocks an SM take as long).  The selection is bound by latency: three
+// The moves are bound by HBM: 695 MB (336203 moves of 512-byte K and V rows from random places, and
+// the entries behind the budget) of 16 requests of up to 32768 rows cut to 8192 take 104 us, 6.7
+// TB/s, beside their selection's 24 (two rows' loads in flight a thread and five blocks an SM take
+// as long).  The selection is bound by latency: three
 // passes and a few barriers each, 8.5 us for a unit of 2000 rows, 23 us for 1024 units of 4200
 // on all SMs (its floor, 8 bytes a row, is 5 us), so it begins beside the checks and the moves
 // are set up behind it.  Whole calls: 19.5 us (4 units of 2001 rows), 40 us (the 1024 units, 100
