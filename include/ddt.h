@@ -453,7 +453,8 @@ ddt_status ddt_commit_paged(int B, int N, int A, int n_attn_layers, int Hkv, int
  *     then zero and its sums unchanged.
  * Precision: scores, exponentials (the hardware's base 2, relative error about 2^-22), sums and o
  * in fp32, rounded once to out_dtype; with bf16 caches the weights enter the product with V as
- * two bf16 parts each (2^-16 of a weight), for fp32 outputs too.
+ * two bf16 parts each (2^-16 of a weight), for fp32 outputs too, so that an infinite V entry
+ * makes its channel NaN where fp32 caches give an infinity.
  * d in {64, 128, 256}; fp32 and bf16; Hq / Hkv <= 1024; q, k_new, v_new, the pages, o and
  * attn_weight 16-byte aligned.  The same inputs give the same bits.
  * workspace: ddt_decode_attn_paged_workspace(...) bytes (want_weight: 1 with attn_weight,
