@@ -557,6 +557,127 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
                               int32_t* top_token, float* top_logprob, int32_t* status,
                               void* workspace, size_t ws_bytes, ddt_stream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * The paged prefix cache in 8 bits (no counterpart in the pages): half the bytes of a bf16
+ * cache to hold, and to read in a single-token step.
+ *
+ *   k_pages, v_pages [L][num_pages][Hkv][page_size][d] bytes, e4m3 codes (1 sign, 4 exponent,
+ *     3 mantissa bits, largest value 448, no infinities), pages and block_table as in
+ *     ddt_tree_attn_paged;
+ *   k_scale, v_scale [L][num_pages][Hkv][page_size / block] bytes: `block` consecutive rows of
+ *     a head share the scale 2^(byte - 127) (an E8M0 byte); a row's value is code * scale.
+ *     Byte 0 marks a block whose rows so far are all zero.
+ *   block: 8, 16, 32, 64 or 128, and a divisor of page_size.
+ * The byte of a block is that of the smallest e in [-100, 120] with max|x| <= 448 * 2^e over the
+ * finite channels of its rows so far: nothing saturates.  A channel above 2^-13 of its block's
+ * largest is off by at most 2^-4 of itself (half a step), a smaller one by at most 2^-17 of that
+ * largest (or 2^-110 where e is -100).  A power of two because codes are floating-point numbers: a
+ * finer scale would move the rounding steps, not narrow them.
+ *
+ * In a round over such a cache: ddt_read_paged_quant, a layer at a time, into a contiguous
+ * cache of 16 bits that ddt_tree_attn reads; after the walk ddt_append_paged_quant in the place of
+ * the commit's attention part (node = acc_nodes, count = n_emitted, advance 0), then ddt_commit
+ * without attention layers for the rest and prefix_len (or advance 1 and no ddt_commit where there
+ * are no GDN layers).  ddt_evict_paged does not take these caches.
+ * ------------------------------------------------------------------------------- */
+
+/* ddt_append_paged_quant -- rows quantised as they are written: entry j < count[b] of request b,
+ * row r = node[b][j] (r = j when node is NULL) of k and v [L][B][N][Hkv][d] (in_dtype), becomes
+ * cache row prefix_len[b] + j.
+ *   Codes are the values times 2^-e to the nearest, ties to even; an infinite or NaN channel is
+ *   stored as NaN.  A block that already holds rows keeps its scale unless a new row needs a
+ *   larger one; then its rows are rescaled in place (exact but for codes whose value falls below
+ *   2^-6, which are rounded again).  Rows and scales behind the last one written are not touched.
+ *   node [B][A] int32 or NULL (then A <= N), count [B] int32 in [0, A].
+ *   advance: nonzero adds count[b] to prefix_len[b] where status[b] is DDT_OK; 0 leaves prefix_len
+ *     as it is (the layers of a model written one call a layer: 1 with the last one).
+ *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, max_pages * page_size] or the rows
+ *     do not fit behind it, DDT_ERR_INVALID_ARG if count[b] is outside [0, A], an entry of node
+ *     outside [0, N), or an entry of block_table for a position being written outside
+ *     [0, num_pages).  Nothing of such a request is written.
+ *   Pages being written are used by one request of the call only.
+ * All buffers but node and count, which are read alone, are apart from one another (the call is refused
+ * otherwise).  d in {64, 128, 256}; A <= 1024 with node; n_layers * B <= 65535; k, v and the pages
+ * 16-byte aligned. */
+ddt_status ddt_append_paged_quant(int n_layers, int B, int N, int A, int Hkv, int d, int page_size,
+                                  int num_pages, int max_pages, int block, ddt_dtype in_dtype,
+                                  const void* k, const void* v, const int32_t* node,
+                                  const int32_t* count, const int32_t* block_table,
+                                  int32_t* prefix_len, int advance, void* k_pages, void* v_pages,
+                                  uint8_t* k_scale, uint8_t* v_scale, int32_t* status,
+                                  ddt_stream_t stream);
+
+/* ddt_read_paged_quant -- the rows read back: k_out, v_out [L][B][Hkv][Pcap][d] (out_dtype), the
+ * layout of ddt_tree_attn's caches, get the values of rows 0..prefix_len[b]-1 (exact in fp32 and
+ * in bf16, up to the largest finite value); rows behind are left as they are.
+ *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, min(Pcap, max_pages * page_size)]
+ *     (nothing of the request is written), DDT_ERR_INVALID_ARG if a block-table entry of the prefix is
+ *     outside [0, num_pages) (the rows of such pages are left as they are).
+ * Outputs are apart from one another and from the inputs.  d in {64, 128, 256};
+ * n_layers * B <= 65535; pages and outputs 16-byte aligned. */
+ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, int page_size,
+                                int num_pages, int max_pages, int block, ddt_dtype out_dtype,
+                                const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                                const uint8_t* v_scale, const int32_t* block_table,
+                                const int32_t* prefix_len, void* k_out, void* v_out,
+                                int32_t* status, ddt_stream_t stream);
+
+/* ddt_decode_attn_paged_quant -- ddt_decode_attn_paged over that cache, without the sums of the
+ * weights: q, k_new, v_new, o, prefix_len, scale, status and workspace (of
+ * ddt_decode_attn_paged_quant_workspace bytes) have the same meaning; the new token's own row enters
+ * as it is given, unquantised.  A NaN or infinite channel of q makes its head's o NaN, and a NaN of
+ * a cached row every o that the row enters.
+ * Precision: scores, exponentials (the hardware's base 2, relative error about 2^-22), sums and o in
+ * fp32, rounded once to out_dtype.  The products run on e4m3 operands with fp32 accumulators: the
+ * codes as they are, q and the weights as sums of e4m3 parts, each 16 times finer than the
+ * one before.  bf16: q in two parts (a channel exact, or off by at most 2^-21 of its head's largest),
+ * the weights in four (2^-16 of a weight, or 2^-26 of the largest where that is more); fp32: six parts
+ * of each (2^-24 of a value, or 2^-34 of the largest).
+ * The same inputs give the same bits.  o, status and the workspace are apart from one another and
+ * from the inputs (the call is refused otherwise).  d in {64, 128, 256}; Hq / Hkv <= 1024; q, k_new,
+ * v_new, the pages and o 16-byte aligned. */
+size_t ddt_decode_attn_paged_quant_workspace(int n_layers, int B, int Hq, int Hkv, int d,
+                                             ddt_dtype in_dtype);
+ddt_status ddt_decode_attn_paged_quant(int n_layers, int B, int Hq, int Hkv, int d, int page_size,
+                                       int num_pages, int max_pages, int block,
+                                       ddt_dtype in_dtype, ddt_dtype out_dtype, const void* q,
+                                       const void* k_new, const void* v_new, const void* k_pages,
+                                       const void* v_pages, const uint8_t* k_scale,
+                                       const uint8_t* v_scale, const int32_t* block_table,
+                                       const int32_t* prefix_len, float scale, void* o,
+                                       int32_t* status, void* workspace, size_t ws_bytes,
+                                       ddt_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * ddt_qk_norm_rope -- root-mean-square norms of every query and key head and the rotary embedding
+ * of ddt_rope_tree in one pass, from the rows of a projection to those that the attention
+ * calls and the cache take ([NOTES] "Where the next step is" names RoPE by branch depth; per-head
+ * norms are those of Qwen-style models, no formula there).
+ *
+ * For every layer, request b, row n < n_nodes[b] (every row when n_nodes is NULL) and head, x of d
+ * channels with the layer's weights w:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + w), then the pairs (i, i + rot_dim/2) of its
+ *   first rot_dim channels turned by position[b][n] * theta^(-2i/rot_dim) as in ddt_rope_tree.
+ *   q [L][B][N][Hq][d], k [L][B][N][Hkv][d] (dtype) with consecutive channels and any strides, in
+ *     elements, of their first four dimensions: q_stride, k_stride, HOST arrays of 4 (slices of one
+ *     projection, for instance); q_weight, k_weight [L][d] (dtype).
+ *   position [B][N] int32; n_nodes [B] int32 or NULL.  Rows past n_nodes[b] are left as they are, and
+ *     all of a request's whose n_nodes[b] is above N.
+ *   q_out [L][B][N][Hq][d], k_out [L][B][N][Hkv][d] (dtype), contiguous.  q_out may be q itself where
+ *     q is contiguous, and k_out k; otherwise outputs are apart from one another and from the
+ *     inputs (the call is refused otherwise).
+ * Precision: fp32 throughout, rounded once; an angle is off by at most 2^-23 for any position.
+ * rot_dim: 0 (no rotation) or a multiple of 16 up to d; theta > 1; eps >= 0; weight_offset 0, or 1
+ * for weights stored about zero.  d in {64, 128, 256}; buffers aligned to their elements (faster at
+ * 16 bytes, strides included).
+ * ------------------------------------------------------------------------------- */
+ddt_status ddt_qk_norm_rope(int n_layers, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                            double theta, float eps, float weight_offset, ddt_dtype dtype,
+                            const void* q, const int64_t* q_stride, const void* k,
+                            const int64_t* k_stride, const void* q_weight, const void* k_weight,
+                            const int32_t* position, const int32_t* n_nodes, void* q_out,
+                            void* k_out, ddt_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

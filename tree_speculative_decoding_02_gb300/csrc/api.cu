@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "ddt.h"
 #include "kernels.h"
@@ -537,6 +538,151 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
     return from_cuda(launch_token_logprobs(B, N, V, A, top_n, temperature, dtype, target_logits, node, token, logprob,
                                            entropy, top_token, top_logprob, status, workspace,
                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ the 8-bit paged cache
+// rows a scale: a power of two that divides a page
+static bool scale_block_ok(int block, int page_size) { return block >= 8 && block <= 128 && (block & (block - 1)) == 0 && page_size % block == 0; }
+static bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+ddt_status ddt_qk_norm_rope(int n_layers, int B, int N, int Hq, int Hkv, int d, int rot_dim, double theta, float eps,
+                            float weight_offset, ddt_dtype dtype, const void* q, const int64_t* q_stride, const void* k,
+                            const int64_t* k_stride, const void* q_weight, const void* k_weight, const int32_t* position,
+                            const int32_t* n_nodes, void* q_out, void* k_out, ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || N < 1 || Hq < 1 || Hkv < 1 || !dtype_ok(dtype) || rot_dim < 0 || rot_dim > d ||
+        !(theta > 1.0 && theta < INFINITY) || !(eps >= 0.0f && eps < INFINITY) || !(fabsf(weight_offset) < INFINITY))
+        return DDT_ERR_INVALID_ARG;
+    const long most = 0x7fffffffL;
+    if (!head_dim_ok(d) || rot_dim % 16 != 0 || n_layers > 65535 || (long)B * N > most || (long)Hq + Hkv > (1 << 16))
+        return DDT_ERR_UNSUPPORTED;
+    if (!q || !k || !q_stride || !k_stride || !q_weight || !k_weight || !position || !q_out || !k_out) return DDT_ERR_INVALID_ARG;
+    const int esz = dtype == DDT_BF16 ? 2 : 4;
+    for (const void* p : {q, k, q_weight, k_weight, (const void*)q_out, (const void*)k_out})
+        if (reinterpret_cast<uintptr_t>(p) % esz) return DDT_ERR_INVALID_ARG;
+    // the spans of the inputs; in place only over rows that lie as the output's do
+    const int64_t n[2][4] = {{n_layers, B, N, Hq}, {n_layers, B, N, Hkv}};
+    const int64_t* stride[2] = {q_stride, k_stride};
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    size_t span[2], size[2];
+    bool same[2];
+    for (int x = 0; x < 2; ++x) {
+        int64_t last = 0, dense = d;
+        same[x] = in[x] == out[x];
+        for (int i = 3; i >= 0; --i) {
+            if (n[x][i] > 1 && stride[x][i] < 0) return DDT_ERR_INVALID_ARG;
+            if (n[x][i] > 1 && stride[x][i] > (INT64_C(1) << 56) / n[x][i]) return DDT_ERR_UNSUPPORTED;
+            if (n[x][i] > 1) last += (n[x][i] - 1) * stride[x][i];
+            same[x] = same[x] && (n[x][i] == 1 || stride[x][i] == dense);
+            dense *= n[x][i];
+        }
+        span[x] = (size_t)(last + d) * esz;
+        size[x] = (size_t)dense * esz;
+    }
+    const size_t n_w = (size_t)n_layers * d * esz;
+    const Span spans[] = {{q_out, size[0]},      {k_out, size[1]},      {same[0] ? nullptr : q, span[0]},
+                          {same[1] ? nullptr : k, span[1]}, {q_weight, n_w}, {k_weight, n_w},
+                          {position, (size_t)B * N * 4}, {n_nodes, (size_t)B * 4}};
+    if (any_overlap(spans, 8, 2)) return DDT_ERR_INVALID_ARG;
+    return from_cuda(launch_qk_norm_rope(n_layers, B, N, Hq, Hkv, d, rot_dim, theta, eps, weight_offset, dtype, q, q_stride, k,
+                                         k_stride, q_weight, k_weight, position, n_nodes, q_out, k_out,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ddt_status ddt_append_paged_quant(int n_layers, int B, int N, int A, int Hkv, int d, int page_size, int num_pages,
+                                  int max_pages, int block, ddt_dtype in_dtype, const void* k, const void* v,
+                                  const int32_t* node, const int32_t* count, const int32_t* block_table,
+                                  int32_t* prefix_len, int advance, void* k_pages, void* v_pages, uint8_t* k_scale,
+                                  uint8_t* v_scale, int32_t* status, ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || N < 1 || A < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || !dtype_ok(in_dtype) ||
+        (!node && A > N))
+        return DDT_ERR_INVALID_ARG;
+    if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
+        !head_dim_ok(d) || !scale_block_ok(block, page_size) || (node && A > kMaxRows) || A > (1 << 30) ||
+        (long)n_layers * B > 65535 || Hkv > 32767)
+        return DDT_ERR_UNSUPPORTED;
+    if (!k || !v || !count || !block_table || !prefix_len || !k_pages || !v_pages || !k_scale || !v_scale || !status)
+        return DDT_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages)) return DDT_ERR_INVALID_ARG;
+    const size_t n_b = (size_t)B * 4, n_in = (size_t)n_layers * B * N * Hkv * d * (in_dtype == DDT_BF16 ? 2 : 4),
+                 n_rows = (size_t)n_layers * num_pages * Hkv * page_size;
+    const Span spans[] = {{k_pages, n_rows * d},     {v_pages, n_rows * d}, {k_scale, n_rows / block},
+                          {v_scale, n_rows / block}, {status, n_b},         {prefix_len, n_b},
+                          {k, n_in},                 {v, n_in},             {node, n_b * A},
+                          {count, n_b},              {block_table, n_b * max_pages}};
+    if (any_overlap(spans, 11, 6)) return DDT_ERR_INVALID_ARG;
+    const AttnPaging pg{page_size, num_pages, max_pages, block_table};
+    return from_cuda(launch_append_quant(n_layers, B, N, A, Hkv, d, block, pg, in_dtype, k, v, node, count, prefix_len,
+                                         advance, k_pages, v_pages, k_scale, v_scale, status,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, int page_size, int num_pages, int max_pages,
+                                int block, ddt_dtype out_dtype, const void* k_pages, const void* v_pages,
+                                const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                const int32_t* prefix_len, void* k_out, void* v_out, int32_t* status, ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || Hkv < 1 || Pcap < 1 || num_pages < 1 || max_pages < 1 || !dtype_ok(out_dtype))
+        return DDT_ERR_INVALID_ARG;
+    if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
+        !head_dim_ok(d) || !scale_block_ok(block, page_size) || Pcap > (1 << 30) || (long)n_layers * B > 65535 || Hkv > 32767)
+        return DDT_ERR_UNSUPPORTED;
+    if (!k_pages || !v_pages || !k_scale || !v_scale || !block_table || !prefix_len || !k_out || !v_out || !status)
+        return DDT_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_out) || !aligned16(v_out)) return DDT_ERR_INVALID_ARG;
+    const size_t n_b = (size_t)B * 4, n_out = (size_t)n_layers * B * Hkv * Pcap * d * (out_dtype == DDT_BF16 ? 2 : 4),
+                 n_rows = (size_t)n_layers * num_pages * Hkv * page_size;
+    const Span spans[] = {{k_out, n_out},      {v_out, n_out},            {status, n_b},
+                          {k_pages, n_rows * d}, {v_pages, n_rows * d},   {k_scale, n_rows / block},
+                          {v_scale, n_rows / block}, {block_table, n_b * max_pages}, {prefix_len, n_b}};
+    if (any_overlap(spans, 9, 3)) return DDT_ERR_INVALID_ARG;
+    const AttnPaging pg{page_size, num_pages, max_pages, block_table};
+    return from_cuda(launch_read_quant(n_layers, B, Hkv, d, block, Pcap, pg, out_dtype, k_pages, v_pages, k_scale, v_scale,
+                                       prefix_len, k_out, v_out, status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t ddt_decode_attn_paged_quant_workspace(int n_layers, int B, int Hq, int Hkv, int d, ddt_dtype in_dtype) {
+    if (n_layers < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || !dtype_ok(in_dtype)) return 0;
+    return decode_quant_ws_bytes(n_layers, B, Hq, Hkv, d, in_dtype);
+}
+
+ddt_status ddt_decode_attn_paged_quant(int n_layers, int B, int Hq, int Hkv, int d, int page_size, int num_pages,
+                                       int max_pages, int block, ddt_dtype in_dtype, ddt_dtype out_dtype, const void* q,
+                                       const void* k_new, const void* v_new, const void* k_pages, const void* v_pages,
+                                       const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                       const int32_t* prefix_len, float scale, void* o, int32_t* status, void* workspace,
+                                       size_t ws_bytes, ddt_stream_t stream) {
+    if (n_layers < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 || max_pages < 1 ||
+        !dtype_ok(in_dtype) || !dtype_ok(out_dtype))
+        return DDT_ERR_INVALID_ARG;
+    if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hq, Hkv, num_pages) ||
+        !head_dim_ok(d) || !scale_block_ok(block, page_size))
+        return DDT_ERR_UNSUPPORTED;
+    if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !prefix_len || !o || !status || !workspace ||
+        !k_new != !v_new)
+        return DDT_ERR_INVALID_ARG;
+    const size_t need = decode_quant_ws_bytes(n_layers, B, Hq, Hkv, d, in_dtype);
+    if (ws_bytes < need || !aligned16(workspace) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o))
+        return DDT_ERR_INVALID_ARG;
+    const size_t n_lb = (size_t)n_layers * B, in = in_dtype == DDT_BF16 ? 2 : 4, n_new = n_lb * Hkv * d * in,
+                 n_rows = (size_t)n_layers * num_pages * Hkv * page_size;
+    const Span spans[] = {{o, n_lb * Hq * d * (out_dtype == DDT_BF16 ? 2 : 4)},
+                          {status, B * sizeof(int32_t)},
+                          {workspace, need},
+                          {q, n_lb * Hq * d * in},
+                          {k_new, n_new},
+                          {v_new, n_new},
+                          {k_pages, n_rows * d},
+                          {v_pages, n_rows * d},
+                          {k_scale, n_rows / block},
+                          {v_scale, n_rows / block},
+                          {block_table, (size_t)B * max_pages * sizeof(int32_t)},
+                          {prefix_len, B * sizeof(int32_t)}};
+    if (any_overlap(spans, 12, 3)) return DDT_ERR_INVALID_ARG;
+    const AttnPaging pg{page_size, num_pages, max_pages, block_table};
+    return from_cuda(launch_decode_quant(n_layers, B, Hq, Hkv, d, block, pg, in_dtype, out_dtype, q, k_new, v_new, k_pages,
+                                         v_pages, k_scale, v_scale, prefix_len, scale, o, status, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
 
 // ------------------------------------------------------------------------------ host
 constexpr int kTcMaxCtas = 512;  // two an SM, for up to 256 SMs
+constexpr int kQuantMaxCtas = 512;  // three an SM, for up to 170 SMs
 static int simt_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -546,10 +547,16 @@ static cudaError_t finish_go(const DecodeParams& p, int sms, cudaStream_t st) {
     return many ? finish_launch<Tin, Tout, 256, 8>(p, sms, st) : finish_launch<Tin, Tout, 256, 1>(p, sms, st);
 }
 
-cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype in, ddt_dtype out,
-                          const void* q, const void* k_new, const void* v_new, const void* k_pages,
-                          const void* v_pages, const int32_t* prefix_len, float scale, void* o, float* weight,
-                          int32_t* status, void* ws, cudaStream_t st) {
+static cudaError_t finish_any(const DecodeParams& p, ddt_dtype in, int sms, cudaStream_t st) {
+    if (in == DDT_BF16)
+        return p.out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16>(p, sms, st)
+                                 : finish_go<__nv_bfloat16, float>(p, sms, st);
+    return p.out == DDT_BF16 ? finish_go<float, __nv_bfloat16>(p, sms, st) : finish_go<float, float>(p, sms, st);
+}
+
+static DecodeParams decode_params(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype out, const void* q,
+                                  const void* k_new, const void* v_new, const void* k_pages, const void* v_pages,
+                                  const int32_t* prefix_len, float scale, void* o, float* weight, int32_t* status) {
     DecodeParams p{};
     p.L = L;
     p.B = B;
@@ -573,8 +580,21 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
     p.status = status;
     p.out = out;
     p.scale_log2 = scale * 1.4426950408889634f;
+    return p;
+}
+
+static int sm_count() {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype in, ddt_dtype out,
+                          const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                          const void* v_pages, const int32_t* prefix_len, float scale, void* o, float* weight,
+                          int32_t* status, void* ws, cudaStream_t st) {
+    DecodeParams p = decode_params(L, B, Hq, Hkv, d, pg, out, q, k_new, v_new, k_pages, v_pages, prefix_len, scale, o, weight, status);
+    const int sms = sm_count();
     unsigned char* w = static_cast<unsigned char*>(ws);
     cudaError_t e;
     if (decode_tc_supported(d, in)) {  // bf16: persistent CTAs
@@ -586,11 +606,30 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
         decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, w);
         e = simt_d_go(p, st);
     }
-    if (e != cudaSuccess || p.cl) return e;
-    if (in == DDT_BF16)
-        return out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16>(p, sms, st)
-                               : finish_go<__nv_bfloat16, float>(p, sms, st);
-    return out == DDT_BF16 ? finish_go<float, __nv_bfloat16>(p, sms, st) : finish_go<float, float>(p, sms, st);
+    return e != cudaSuccess || p.cl ? e : finish_any(p, in, sms, st);
+}
+
+// ---- the same over a cache held in 8 bits: the split kernel is another, the join the same
+size_t decode_quant_ws_bytes(int L, int B, int Hq, int Hkv, int d, ddt_dtype in) {
+    DecodeParams p{};
+    p.L = L;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.d = d;
+    return decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, nullptr);
+}
+
+cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block, const AttnPaging& pg, ddt_dtype in,
+                                ddt_dtype out, const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                                const void* v_pages, const uint8_t* k_scale, const uint8_t* v_scale,
+                                const int32_t* prefix_len, float scale, void* o, int32_t* status, void* ws, cudaStream_t st) {
+    DecodeParams p = decode_params(L, B, Hq, Hkv, d, pg, out, q, k_new, v_new, k_pages, v_pages, prefix_len, scale, o, nullptr, status);
+    const int sms = sm_count();
+    p.C = sms < kQuantMaxCtas / 3 ? sms : kQuantMaxCtas / 3;
+    decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, static_cast<unsigned char*>(ws));
+    const cudaError_t e = launch_decode_quant_tiles(p, in, block, k_scale, v_scale, st);
+    return e != cudaSuccess || p.cl ? e : finish_any(p, in, sms, st);
 }
 
 }  // namespace ddt

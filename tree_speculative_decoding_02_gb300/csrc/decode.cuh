@@ -14,6 +14,8 @@
 // partials behind a cluster barrier, in the same launch.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -349,9 +351,53 @@ __device__ __forceinline__ void dec_finish(const DecodeParams& p, const DecodeWa
     }
 }
 
+// ---- what the tensor-core kernels share
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!tc::mbar_try(bar, parity))
+        if (clock64() - t0 > tc::kWaitCycles) return;
+}
+
+// the warp's maximum in one instruction
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// barrier of the 128 softmax threads that also tells whether any of them passed true
+__device__ __forceinline__ bool bar_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// 8 consecutive 32-bit columns of this thread's lane
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn decode_encode_fn();  // cuTensorMapEncodeTiled, or null
 bool decode_tc_supported(int d, ddt_dtype in);
 int decode_tc_heads(int G, int d);
 cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
+int decode_quant_heads(int G, ddt_dtype in);
+cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, int block, const uint8_t* ks, const uint8_t* vs,
+                                      cudaStream_t st);
 cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
                                  cudaStream_t st);
 

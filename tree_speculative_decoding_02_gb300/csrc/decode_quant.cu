@@ -1,0 +1,552 @@
+// decode_quant.cu -- k_decode_quant: ddt_decode_attn_paged_quant's pass over the cached rows, a
+// cache of e4m3 codes with a power of two for each block of rows and head.
+//
+// As for bf16 caches (decode_tc.cu) the cache is the M = 128 operand of the products and the few
+// heads are N, so no thread touches a cached element; here the codes go to the tensor cores as
+// they lie in HBM, one byte an element (kind::f8f6f4, 32 channels or rows an MMA):
+//   S^T [128 rows x heads]  = K codes [rows x d] . Q^T        (K-major)
+//   O^T [d x heads]        += V codes^T [d x rows] . P^T      (V and P as they lie, M- and N-major)
+// The other operand of such an MMA is e4m3 as well, 4 significant bits, so Q and P are sums of
+// parts in N columns of their own, each part the rounding error of those before it times 16:
+//   x = x_0 + x_1 / 16 + x_2 / 256 + ..,  x_i = e4m3(16 (x_{i-1} residue)).
+// A part takes 4 bits at least, and what lies below e4m3's normal range is made up for by the next:
+// bf16 queries (scaled by a power of two to at most 256) are whole in 2 parts, the weights get 4
+// (2^-16, as with bf16 caches); fp32 calls take 6 of each (2^-24).  With up to 8 heads the parts of
+// Q fill the MMA's smallest N, 16.
+//
+// The scales.  A block's power of two 2^a of K multiplies its rows' scores.  That of V, 2^v, goes
+// into the weights: t' = t + v (base 2), P = 2^(t' - m) with one reference m a head for all t', so
+// that P is at most 2^8 and loses nothing whatever the blocks' scales are; the softmax sum gets
+// 2^-v P = 2^(t - m).  (v counts from the scale of the segment's first row.)
+//
+//   warp 0      producer: block-table entries, TMA of K and V tiles into one ring
+//   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
+//   warp 2      queries: the parts of a segment's heads
+//   warps 3-6, 7-10 ..  softmax, eight heads a warpgroup, a thread a cached row; the row's scales are
+//               fetched a tile ahead, their page two tiles ahead
+// The split of the rows over the CTAs, the partials and the join are those of decode.cuh.
+// Every wait is bounded, as there.
+#include <cuda.h>
+#include <math.h>
+
+#include "decode.cuh"
+#include "quant.cuh"
+#include "tc.cuh"
+
+namespace ddt {
+
+namespace {
+
+constexpr float kLift = 4.f;  // a reference is this far below the score that set it: P = 2^kLift there
+constexpr float kTau = 4.f;   // and moves when a score is this much above it
+
+constexpr int pow2_at_least(int x, int y) { return x <= y ? y : pow2_at_least(x, 2 * y); }
+
+// HP: heads a block; QP, PP: parts of Q and of P
+template <int D, int HP, int QP, int PP>
+struct QuantCfg {
+    static constexpr int kGroups = HP / 8;                // softmax warpgroups
+    static constexpr int kThreads = 96 + 128 * kGroups;
+    static constexpr int kRow = D < 128 ? D : 128;        // bytes of a swizzled row
+    static constexpr int kBlocks = D / kRow;              // of a cached row
+    static constexpr int kStageBytes = kDecTile * D;      // a K or V tile
+    static constexpr int NQ = QP * HP;                    // N of Q K^T
+    static constexpr int NP = pow2_at_least(PP * HP, 32); // N of P V, and the bytes of a row of P
+    static constexpr int kCtas = QP == 6 ? (D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? 3 : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
+    static constexpr int kQBufs = kCtas == 2 && D == 256 ? 1 : 2;
+    static constexpr int kQBytes = NQ * D;
+    static constexpr int kPBytes = NP * kDecTile;
+    static constexpr int kMB = D > 128 ? D / 128 : 1;     // M blocks of P V
+    static constexpr int kOCol = 2 * NQ;                  // tensor memory: S x 2, O
+    static constexpr int kTmemCols = pow2_at_least(2 * NQ + kMB * NP, 32);
+    static constexpr int kFixed = 1024 + kQBufs * kQBytes + 2 * kPBytes + 640 + (8 + 4 * 2 + 4) * HP * 4;
+    static constexpr int kRing = (228 * 1024 / kCtas - 1024 - 256 - kFixed) / kStageBytes;
+    static constexpr int kStages = kRing > 12 ? 12 : kRing;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory");
+    static_assert(kCtas * kTmemCols <= 512, "tensor memory");
+    static_assert((4 * kStages + 22) * 4 + 64 <= 640, "barriers");
+    static_assert(NQ % 16 == 0 && NQ <= 256 && NP <= 128, "N of the products");
+    // head size 64: lanes 64-127 of O read on behind a tile, into Q and P at the end of the ring
+    static_assert(D != 64 || kQBufs * kQBytes + 2 * kPBytes >= kStageBytes, "shared memory behind the ring");
+};
+
+struct DecQuantArgs {
+    int sub;        // rows of a box: the largest of 128, 64, ... that pages are made of
+    int block;      // rows a scale
+    const uint8_t* ks;
+    const uint8_t* vs;
+};
+
+__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+
+// x and y as PARTS codes each: the code pairs, x's in the low byte
+template <int PARTS>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[PARTS]) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        c[i] = e4m3x2(x, y);
+        if (i + 1 < PARTS) {
+            const float2 v = e4m3_values(c[i]);
+            x = (x - v.x) * 16.f;
+            y = (y - v.y) * 16.f;
+        }
+    }
+}
+
+}  // namespace
+
+template <typename Tin, int D, int HP, int QP, int PP>
+__global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D, HP, QP, PP>::kCtas)
+    k_decode_quant(const DecodeParams p, const DecQuantArgs a, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+    using Cfg = QuantCfg<D, HP, QP, PP>;
+    constexpr int kStages = Cfg::kStages, NQ = Cfg::NQ, NP = Cfg::NP, kMB = Cfg::kMB, kRow = Cfg::kRow, kQBufs = Cfg::kQBufs;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* sQ = ring + kStages * Cfg::kStageBytes;  // [kQBufs]
+    unsigned char* sP = sQ + kQBufs * Cfg::kQBytes;         // [2]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sP + 2 * Cfg::kPBytes);  // [kStages] a tile landed
+    uint64_t* empty = full + kStages;                                      // [kStages] its MMAs are done
+    uint64_t* q_full = empty + kStages;  // [2] a segment's queries are there
+    uint64_t* q_free = q_full + 2;       // [2] its last Q K^T is done
+    uint64_t* s_full = q_free + 2;       // [2] S of a tile in tensor memory
+    uint64_t* p_full = s_full + 2;       // [2] P of a tile in shared memory (the softmax warps)
+    uint64_t* p_free = p_full + 2;       // [2] its P V is done
+    uint64_t* drain = p_free + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+    int* bad_tile = abort_flag + 1;                            // [8] a page of the tile does not exist
+    float* q_unit = reinterpret_cast<float*>(bad_tile + 8);    // [8][HP] log2 scores of a unit of Q K^T, by segment
+    float* xm = q_unit + 8 * HP;                               // [2][4][HP] warps' tile maxima
+    float* sm_l = xm + 2 * 4 * HP;                             // [4][HP] warps' sums of a segment
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * kStages; ++i) tc::mbar_init(full + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(q_full + i, 1);
+            tc::mbar_init(q_free + i, 1);
+            tc::mbar_init(s_full + i, 1);
+            tc::mbar_init(p_full + i, 4 * Cfg::kGroups);
+            tc::mbar_init(p_free + i, 1);
+        }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tm_k);
+        tc::prefetch_tmap(&tm_v);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, Cfg::kTmemCols);
+        tc::tmem_relinquish();
+    }
+    const DecodeWalk mine = dec_plan<Cfg::kThreads>(p);
+    DecodeWalk w = mine;
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int* abort = abort_flag;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_decode_finish may be set up
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ producer
+        const int n_box = kDecTile / a.sub;
+        int u = 0, j = 0;  // stages and tiles issued
+        bool ok = true;
+        for (; w.left > 0 && ok; dec_next(p, w)) {
+            const int g = w.g / p.HB, n_seg = dec_seg_tiles(w);
+            const int32_t* table = p.block_table + (long long)w.b * p.max_pages;
+            auto entry = [&](int t) {  // this lane's page of tile t, -1 past the prefix
+                const int pos = t * kDecTile + lane * a.sub;
+                return lane < n_box && pos < w.P ? table[pos / p.page_rows] : -1;
+            };
+            int phys = entry(w.t);
+            for (int t = w.t; t < w.t + n_seg; ++t, ++j) {
+                const int pos = t * kDecTile + lane * a.sub;
+                const bool mine = lane < n_box && pos < w.P;
+                const bool good = mine && phys >= 0 && phys < p.num_pages;
+                const int plane = (int)(((long long)w.l * p.num_pages + phys) * p.Hkv + g);
+                const int row = good ? pos % p.page_rows : 0;
+                const unsigned goods = __ballot_sync(kFull, good), bads = __ballot_sync(kFull, mine && !good);
+                if (t + 1 < w.t + n_seg) phys = entry(t + 1);
+                if (lane == 0) bad_tile[j & 7] = bads != 0;
+#pragma unroll
+                for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+                    const int st = u % kStages;
+                    ok = tc::mbar_wait(empty + st, ((u / kStages) & 1) ^ 1, abort);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    if (lane == 0) tc::mbar_expect_tx(full + st, __popc(goods) * a.sub * D);
+                    __syncwarp();
+                    if (good) {
+                        unsigned char* dst = ring + st * Cfg::kStageBytes + lane * a.sub * kRow;
+#pragma unroll
+                        for (int blk = 0; blk < Cfg::kBlocks; ++blk)
+                            tc::tma_load_3d(dst + blk * (kDecTile * kRow), kv ? &tm_v : &tm_k, full + st, blk * kRow, row, plane);
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+        // no copy may be under way when the CTA leaves
+        for (int i = max(0, u - kStages); i < u; ++i) drain_wait(full + i % kStages, (i / kStages) & 1);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = tc::idesc_e4m3(128, NQ, false, false);
+            constexpr uint32_t idesc_pv = tc::idesc_e4m3(128, NP, true, true);
+            const uint64_t kdesc = tc::desc_sw(kRow, tc::smem_u32(ring), 16, 8 * kRow);
+            const uint64_t vdesc = tc::desc_sw(kRow, tc::smem_u32(ring), kDecTile * kRow, 8 * kRow);
+            const uint64_t qdesc = tc::desc_sw(kRow, tc::smem_u32(sQ), 16, 8 * kRow);
+            const uint64_t pdesc = tc::desc_sw(NP, tc::smem_u32(sP), 16, 8 * NP);
+            int j = 0, seg = 0;
+            bool ok = true;
+            // P V of tile i; `first`: of a segment, so O starts anew (its warps have read the
+            // last segment's O before they hand over this P)
+            auto pv = [&](int i, bool first) {
+                const int st = (2 * i + 1) % kStages;
+                if (!tc::mbar_wait(full + st, ((2 * i + 1) / kStages) & 1, abort)) return false;
+                if (!tc::mbar_wait(p_full + (i & 1), (i >> 1) & 1, abort)) return false;
+                tc::tc_fence_after();
+                const uint64_t vd = vdesc + (uint64_t)((st * Cfg::kStageBytes) >> 4);
+                const uint64_t pd = pdesc + (uint64_t)(((i & 1) * Cfg::kPBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kDecTile / 32; ++kk)
+#pragma unroll
+                    for (int mb = 0; mb < kMB; ++mb)
+                        tc::mma_f8_ss(tmem + Cfg::kOCol + mb * NP, vd + (uint64_t)((mb * kDecTile * kRow + kk * 32 * kRow) >> 4),
+                                      pd + (uint64_t)((kk * 32 * NP) >> 4), idesc_pv, !first || kk > 0);
+                tc::mma_commit(empty + st);
+                tc::mma_commit(p_free + (i & 1));
+                return true;
+            };
+            bool prev_first = false;
+            for (; w.left > 0 && ok; dec_next(p, w), ++seg) {
+                const int n_seg = dec_seg_tiles(w), qb = seg % kQBufs;
+                ok = tc::mbar_wait(q_full + qb, (seg / kQBufs) & 1, abort);
+                for (int i = 0; i < n_seg && ok; ++i, ++j) {
+                    const int st = (2 * j) % kStages;
+                    ok = tc::mbar_wait(full + st, ((2 * j) / kStages) & 1, abort);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t kd = kdesc + (uint64_t)((st * Cfg::kStageBytes) >> 4);
+                    const uint64_t qd = qdesc + (uint64_t)((qb * Cfg::kQBytes) >> 4);
+                    constexpr int kSteps = kRow / 32;  // of a swizzled row
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        tc::mma_f8_ss(tmem + (j & 1) * NQ,
+                                      kd + (uint64_t)(((kk / kSteps) * (kDecTile * kRow) + (kk % kSteps) * 32) >> 4),
+                                      qd + (uint64_t)(((kk / kSteps) * (NQ * kRow) + (kk % kSteps) * 32) >> 4), idesc_qk, kk > 0);
+                    tc::mma_commit(empty + st);
+                    tc::mma_commit(s_full + (j & 1));
+                    if (i == n_seg - 1) tc::mma_commit(q_free + qb);
+                    // S of tile j + 1 may overwrite that of tile j - 1 once P of j - 1 is there
+                    if (j > 0) ok = pv(j - 1, prev_first);
+                    prev_first = i == 0;
+                }
+            }
+            if (ok && j > 0) pv(j - 1, prev_first);
+            tc::mma_commit(drain);
+            drain_wait(drain, 0);
+        }
+    } else if (warp == 2) {
+        // -------------------------------------------------------------------- queries
+        constexpr int E = D / 32;  // consecutive channels a lane
+        int seg = 0;
+        for (; w.left > 0; dec_next(p, w), ++seg) {
+            const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0), qb = seg % kQBufs;
+            const Tin* q = static_cast<const Tin*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D + lane * E;
+            bool ok = true;
+            for (int hb = 0; hb < nh; hb += 8) {
+                float x[8][E];
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[h][e] = hb + h < nh ? to_f32(q[(hb + h) * D + e]) : 0.f;
+                if (hb == 0) ok = __all_sync(kFull, tc::mbar_wait(q_free + qb, ((seg / kQBufs) & 1) ^ 1, abort));
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    if (hb + h >= nh) break;
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float y = fabsf(x[h][e]);
+                        m = fmaxf(m, y < INFINITY ? y : 0.f);
+                    }
+                    m = redux_max(m);
+                    // the power of two that takes the largest channel to [128, 256)
+                    const int up = m > 0.f ? min(134 - (__float_as_int(m) >> 23), 100) : 0;
+                    const float f = __int_as_float((127 + up) << 23);
+                    if (lane == 0) q_unit[(seg & 7) * HP + hb + h] = p.scale_log2 * __int_as_float((127 - up) << 23);
+                    uint32_t c[E / 2][QP];
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) split2<QP>(finite_or_nan(x[h][e]) * f, finite_or_nan(x[h][e + 1]) * f, c[e / 2]);
+#pragma unroll
+                    for (int i = 0; i < QP; ++i) {
+                        const int ch = lane * E;
+                        unsigned char* to = sQ + qb * Cfg::kQBytes + ch / kRow * (NQ * kRow) +
+                                            tc::swizzled<kRow>((i * HP + hb + h) * kRow + ch % kRow);
+                        if constexpr (E == 8)
+                            *reinterpret_cast<uint2*>(to) = make_uint2(c[0][i] | c[1][i] << 16, c[2][i] | c[3][i] << 16);
+                        else if constexpr (E == 4)
+                            *reinterpret_cast<uint32_t*>(to) = c[0][i] | c[1][i] << 16;
+                        else
+                            *reinterpret_cast<uint16_t*>(to) = (uint16_t)c[0][i];
+                    }
+                }
+            }
+            if (!ok) break;
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(q_full + qb);
+        }
+    } else {
+        // -------------------------------------------------- softmax, and the segments' partials
+        const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
+        const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
+        const int grp = Cfg::kGroups == 1 ? 0 : (warp - 3) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
+        const int per_page = p.page_rows / a.block;
+        int j = 0, seg = 0;
+        bool ok = true;
+        for (; w.left > 0; dec_next(p, w), ++seg) {
+            const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
+            const int32_t* table = p.block_table + (long long)w.b * p.max_pages;
+            auto page_of = [&](int pos) { return pos < w.P ? table[pos / p.page_rows] : -1; };
+            auto bytes_of = [&](int pos, int phys) {  // the row's scales: K's byte, then V's
+                if (phys < 0 || phys >= p.num_pages) return 127 | 127 << 8;
+                const long long at = (((long long)w.l * p.num_pages + phys) * p.Hkv + g) * per_page + pos % p.page_rows / a.block;
+                return (int)a.ks[at] | (int)a.vs[at] << 8;
+            };
+            const int y0 = w.t * kDecTile;
+            int here = bytes_of(y0 + r, page_of(y0 + r));
+            int next_page = n_seg > 1 ? page_of(y0 + kDecTile + r) : -1;
+            int base = bytes_of(y0, page_of(y0)) >> 8;
+            if (base == 0) base = 127;
+            float m[8], l[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                m[h] = kNoRef;
+                l[h] = 0.f;
+            }
+            int bad = 0;
+            for (int i = 0; i < n_seg; ++i, ++j) {
+                const int y = y0 + i * kDecTile, n = min(kDecTile, w.P - y);
+                const int kb = here & 255, vb = here >> 8;
+                here = i + 1 < n_seg ? bytes_of(y + kDecTile + r, next_page) : 0;
+                next_page = i + 2 < n_seg ? page_of(y + 2 * kDecTile + r) : -1;
+                const int dv = vb ? max(-126, min(126, vb - base)) : 0;  // (a block of zeros: any scale)
+                const float k_unit = scale_of(kb), v_add = (float)dv, v_back = __int_as_float((127 - dv) << 23);
+                // a warp that gave up still takes part in the barriers
+                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
+                ok = __all_sync(kFull, ok);
+                float t[8];
+                bool above = false;  // a score is far above its head's reference
+                if (ok) {
+                    tc::tc_fence_after();
+                    uint32_t sr[QP][8];
+#pragma unroll
+                    for (int x = 0; x < QP; ++x) tmem_ld8(tmem + lane_base + (j & 1) * NQ + x * HP + hg, sr[x]);
+                    tc::tmem_wait_ld();
+                    bad |= bad_tile[j & 7];
+                    const float* unit = q_unit + (seg & 7) * HP + hg;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        float s = __uint_as_float(sr[QP - 1][h]);
+#pragma unroll
+                        for (int x = QP - 2; x >= 0; --x) s = fmaf(s, 0.0625f, __uint_as_float(sr[x][h]));
+                        t[h] = r < n && h < nh ? fmaf(s, k_unit * unit[h], v_add) : -INFINITY;
+                        above |= t[h] > m[h] + (kLift + kTau);
+                    }
+                }
+                if (bar_any(bar, above)) {
+                    // the segment's first tile, or a growing maximum: new references, the tile's
+                    // maxima, for the heads that need them
+                    float* x = xm + (j & 1) * 4 * HP + hg;
+                    float mine = -INFINITY;
+                    if (ok)
+#pragma unroll
+                        for (int h = 0; h < 8; ++h)
+                            if (h < nh) {
+                                const float v = redux_max(t[h]);
+                                if (lane == h) mine = v;
+                            }
+                    if (lane < 8) x[ws * HP + lane] = mine;
+                    tc::named_bar(bar, 128);
+                    if (ok) {
+                        float f[8];
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            const float mt = fmaxf(fmaxf(x[h], x[HP + h]), fmaxf(x[2 * HP + h], x[3 * HP + h])) - kLift;
+                            f[h] = 1.f;
+                            if (mt > m[h] + kTau) {
+                                f[h] = tc::ex2(m[h] - mt);
+                                l[h] *= f[h];
+                                m[h] = mt;
+                            }
+                        }
+                        if (i > 0) {  // O holds earlier tiles of the segment: once their P V are done
+                            ok = __all_sync(kFull, tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort));
+                            if (ok) {
+                                tc::tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < kMB * PP; ++c) {
+                                    uint32_t o[8];
+                                    const uint32_t at = tmem + lane_base + Cfg::kOCol + (c / PP) * NP + (c % PP) * HP + hg;
+                                    tmem_ld8(at, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+                                    tmem_st8(at, o);
+                                }
+                                tc::tmem_wait_st();
+                            }
+                        }
+                    }
+                }
+                if (!ok) continue;
+                // the P buffer is free once P V of tile j - 2 is done
+                ok = __all_sync(kFull, tc::mbar_wait(p_free + (j & 1), ((j >> 1) & 1) ^ 1, abort));
+                if (!ok) continue;
+                uint32_t c[4][PP];
+#pragma unroll
+                for (int h = 0; h < 8; h += 2) {
+                    const float e0 = tc::ex2(t[h] - m[h]), e1 = tc::ex2(t[h + 1] - m[h + 1]);
+                    l[h] = fmaf(e0, v_back, l[h]);
+                    l[h + 1] = fmaf(e1, v_back, l[h + 1]);
+                    split2<PP>(e0, e1, c[h / 2]);
+                }
+                unsigned char* pb = sP + (j & 1) * Cfg::kPBytes;
+#pragma unroll
+                for (int x = 0; x < PP; ++x) {
+                    const uint2 v = make_uint2(c[0][x] | c[1][x] << 16, c[2][x] | c[3][x] << 16);
+                    if (HP > 8 || x + 1 == PP) {
+                        if (HP > 8 || x % 2 == 0) *reinterpret_cast<uint2*>(pb + tc::swizzled<NP>(r * NP + x * HP + hg)) = v;
+                    } else if (x % 2 == 0) {
+                        *reinterpret_cast<uint4*>(pb + tc::swizzled<NP>(r * NP + x * HP)) =
+                            make_uint4(v.x, v.y, c[0][x + 1] | c[1][x + 1] << 16, c[2][x + 1] | c[3][x + 1] << 16);
+                    }
+                }
+                if (n < kDecTile) {
+                    // V rows past the prefix may hold anything, even NaN, and a zero weight
+                    // does not cancel NaN: zero them before the MMA reads them
+                    const int st = (2 * j + 1) % kStages;
+                    ok = __all_sync(kFull, tc::mbar_wait(full + st, ((2 * j + 1) / kStages) & 1, abort));
+                    if (!ok) continue;
+                    unsigned char* v = ring + st * Cfg::kStageBytes;
+                    const int per = (kDecTile - n) * (kRow / 16);
+                    for (int e = grp * 128 + r; e < per * Cfg::kBlocks; e += 128 * Cfg::kGroups)
+                        *reinterpret_cast<uint4*>(v + (e / per) * (kDecTile * kRow) + n * kRow + (e % per) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(p_full + (j & 1));
+            }
+            // ---- the partial: sums through shared memory, O once the last P V is done
+            float sum = 0.f, ref = 0.f;
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+                if (h < nh) {
+                    const float x = warp_sum(l[h]);
+                    if (lane == h) sum = x;
+                    if (r == h) ref = m[h];
+                }
+            if (lane < 8) sm_l[ws * HP + hg + lane] = sum;
+            if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
+            ok = __all_sync(kFull, ok);
+            tc::named_bar(bar, 128);
+            const long long slot = dec_slot(p, w);
+            if (r < nh) {
+                const float* x = sm_l + hg + r;
+                const float z = (x[0] + x[HP]) + (x[2 * HP] + x[3 * HP]);
+                p.part_ml[slot * p.HT + hg + r] = make_float2(ref, !ok ? kSegTimeout : (bad ? kSegBadPage : z));
+            }
+            if (!ok) continue;
+            tc::tc_fence_after();
+            const float v_unit = scale_of(base);
+#pragma unroll
+            for (int mb = 0; mb < kMB; ++mb) {
+                uint32_t o[PP][8];
+#pragma unroll
+                for (int x = 0; x < PP; ++x) tmem_ld8(tmem + lane_base + Cfg::kOCol + mb * NP + x * HP + hg, o[x]);
+                tc::tmem_wait_ld();
+                if (D >= 128 || r < D) {
+                    float* out = p.part_o + (slot * p.HT + hg) * D + mb * 128 + r;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        if (h < nh) {
+                            float s = __uint_as_float(o[PP - 1][h]);
+#pragma unroll
+                            for (int x = PP - 2; x >= 0; --x) s = fmaf(s, 0.0625f, __uint_as_float(o[x][h]));
+                            out[h * D] = s * v_unit;
+                        }
+                }
+            }
+        }
+    }
+
+    tc::tc_fence_before();
+    DecNew<Tin, D> mine_new;
+    if (p.cl) mine_new.load(p, (long long)mine.l * p.B + mine.b, mine.g, dec_first_head(p), lane);
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, Cfg::kTmemCols);
+    }
+    if (p.cl) {
+        if (p.cl > 1) tc::cluster_sync();
+        dec_finish<Tin, D, Cfg::kThreads>(p, mine, mine_new, reinterpret_cast<float*>(ring));
+    }
+}
+
+// ------------------------------------------------------------------------------ host
+namespace {
+
+template <typename Tin, int D, int HP, int QP, int PP>
+cudaError_t quant_go(DecodeParams& p, const DecQuantArgs& a, const CUtensorMap* maps, cudaStream_t st) {
+    using Cfg = QuantCfg<D, HP, QP, PP>;
+    const auto kernel = k_decode_quant<Tin, D, HP, QP, PP>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    cudaLaunchConfig_t cfg = decode_config(p, false, Cfg::kCtas, Cfg::kThreads, Cfg::kSmem, at, st);
+    return cudaLaunchKernelEx(&cfg, kernel, p, a, maps[0], maps[1]);
+}
+
+template <int D>
+cudaError_t quant_d_go(DecodeParams& p, ddt_dtype in, const DecQuantArgs& a, const CUtensorMap* maps, cudaStream_t st) {
+    if (in == DDT_F32) return quant_go<float, D, 8, 6, 6>(p, a, maps, st);
+    return p.hbs == 8    ? quant_go<__nv_bfloat16, D, 8, 2, 4>(p, a, maps, st)
+           : p.hbs == 16 ? quant_go<__nv_bfloat16, D, 16, 2, 4>(p, a, maps, st)
+                         : quant_go<__nv_bfloat16, D, 32, 2, 4>(p, a, maps, st);
+}
+
+}  // namespace
+
+// heads a block: the smallest of 8, 16 and 32 that holds the group; 8 where the parts are six
+int decode_quant_heads(int G, ddt_dtype in) { return G <= 8 || in == DDT_F32 ? 8 : (G <= 16 ? 16 : 32); }
+
+// p.C: SMs on entry, CTAs on return
+cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, int block, const uint8_t* ks, const uint8_t* vs, cudaStream_t st) {
+    EncodeTiledFn enc = decode_encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    DecQuantArgs a{p.page_rows % 128 == 0 ? 128 : (p.page_rows < 64 ? p.page_rows : 64), block, ks, vs};
+    CUtensorMap maps[2];
+    const int row = p.d < 128 ? p.d : 128;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.page_rows, (cuuint64_t)p.L * p.num_pages * p.Hkv};
+    const cuuint64_t str[2] = {(cuuint64_t)p.d, (cuuint64_t)p.page_rows * p.d};
+    const cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)a.sub, 1}, es[3] = {1, 1, 1};
+    const void* base[2] = {p.k_pages, p.v_pages};
+    for (int i = 0; i < 2; ++i)
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base[i]), dims, str, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    return p.d == 64 ? quant_d_go<64>(p, in, a, maps, st) : (p.d == 128 ? quant_d_go<128>(p, in, a, maps, st) : quant_d_go<256>(p, in, a, maps, st));
+}
+
+}  // namespace ddt

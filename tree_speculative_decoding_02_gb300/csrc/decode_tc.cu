@@ -74,42 +74,6 @@ struct DecTcArgs {
     int sub;  // rows of a box: the largest of 128, 64, ... that pages are made of
 };
 
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!tc::mbar_try(bar, parity))
-        if (clock64() - t0 > tc::kWaitCycles) return;
-}
-
-// the warp's maximum in one instruction
-__device__ __forceinline__ float redux_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// barrier of the 128 softmax threads that also tells whether any of them passed true
-__device__ __forceinline__ bool bar_any(int id, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(id)
-        : "memory");
-    return r != 0;
-}
-
-// 8 consecutive 32-bit columns of this thread's lane
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 }  // namespace
 
 template <int D, int HP>
@@ -453,13 +417,7 @@ __global__ void __launch_bounds__(DecCfg<D, HP>::kThreads, DecCfg<D, HP>::kCtas)
 }
 
 // ------------------------------------------------------------------------------ host
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
+EncodeTiledFn decode_encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -472,6 +430,8 @@ EncodeTiledFn encode_fn() {
     });
     return fn;
 }
+
+namespace {
 
 template <int D, int HP>
 cudaError_t tc_go(DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, cudaStream_t st) {
@@ -493,7 +453,7 @@ int decode_tc_heads(int G, int d) { return G <= 8 ? 8 : (G <= 16 || d == 256 ? 1
 
 // p.C: SMs on entry, CTAs on return
 cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st) {
-    EncodeTiledFn enc = encode_fn();
+    EncodeTiledFn enc = decode_encode_fn();
     if (!enc) return cudaErrorNotSupported;
     DecTcArgs a;
     a.sub = p.page_rows % 128 == 0 ? 128 : (p.page_rows < 64 ? p.page_rows : 64);

@@ -79,6 +79,25 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
                           const void* q, const void* k_new, const void* v_new, const void* k_pages,
                           const void* v_pages, const int32_t* prefix_len, float scale, void* o, float* weight,
                           int32_t* status, void* ws, cudaStream_t st);
+// the 8-bit paged cache: k_scale, v_scale [L][num_pages][Hkv][page_rows / block]
+cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int block, const AttnPaging& pg, ddt_dtype in,
+                                const void* k, const void* v, const int32_t* node, const int32_t* count,
+                                int32_t* prefix_len, int advance, void* k_pages, void* v_pages, uint8_t* k_scale,
+                                uint8_t* v_scale, int32_t* status, cudaStream_t st);
+cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int block, int Pcap, const AttnPaging& pg, ddt_dtype out,
+                              const void* k_pages, const void* v_pages, const uint8_t* k_scale, const uint8_t* v_scale,
+                              const int32_t* prefix_len, void* k_out, void* v_out, int32_t* status, cudaStream_t st);
+size_t decode_quant_ws_bytes(int L, int B, int Hq, int Hkv, int d, ddt_dtype in);
+cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block, const AttnPaging& pg, ddt_dtype in,
+                                ddt_dtype out, const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                                const void* v_pages, const uint8_t* k_scale, const uint8_t* v_scale,
+                                const int32_t* prefix_len, float scale, void* o, int32_t* status, void* ws,
+                                cudaStream_t st);
+cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int rot, double theta, float eps, float offset,
+                                ddt_dtype dtype, const void* q, const int64_t* q_stride, const void* k,
+                                const int64_t* k_stride, const void* q_weight, const void* k_weight,
+                                const int32_t* position, const int32_t* n_nodes, void* q_out, void* k_out,
+                                cudaStream_t st);
 size_t evict_ws_bytes(int L, int B, int Hkv, const AttnPaging& pg);
 cudaError_t launch_evict(int L, int B, int Hkv, int row_bytes, const AttnPaging& pg, int keep, int n_sink,
                          int n_recent, void* k_pages, void* v_pages, const int32_t* seq_len, float* weight,

@@ -1,0 +1,68 @@
+// quant.cuh -- the 8-bit cache's format: e4m3 codes and the byte of a block's power of two; and
+// what the tensor cores take of it.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "tc.cuh"
+
+namespace ddt {
+
+// 2^(byte - 127); 0 for byte 0
+__device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
+
+// the byte of the smallest e in [-100, 120] with m <= 448 * 2^e (448 = 1.75 * 2^8); 0 for m = 0
+__device__ __forceinline__ int scale_byte(float m) {
+    const int bits = __float_as_int(m), e = (bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+    return m > 0.f ? min(max(e, -100), 120) + 127 : 0;
+}
+
+// two codes, `lo` in the low byte: to nearest, ties to even, past 448 to 448, NaN to NaN
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two codes' values (every e4m3 value is an fp16 value)
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ void values8(uint2 c, float* v) {
+    const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = e4m3_values(w[i]);
+        v[2 * i] = x.x;
+        v[2 * i + 1] = x.y;
+    }
+}
+
+namespace tc {
+
+// Matrix descriptor as desc_sw128, for swizzled rows of 128, 64 or 32 bytes (modes 2, 4 and 6).
+__device__ __forceinline__ uint64_t desc_sw(int row_bytes, uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    const uint64_t mode = row_bytes == 128 ? 2 : (row_bytes == 64 ? 4 : 6);
+    return (desc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | mode << 61;
+}
+// The byte of a tile of such rows that holds its byte `off`: bits 7.. of an address turn over bits 4..
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t swizzled(uint32_t off) {
+    return off ^ (off >> 3 & (ROW_BYTES - 1u) & 0x70u);
+}
+// kind::f8f6f4 with e4m3 A and B (format 0) and an fp32 accumulator; an MMA takes 32 bytes of K
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) { return idesc_f16(M, N, a_mn, b_mn); }
+// D[tmem] (+)= A[smem desc] * B[smem desc]  (kind::f8f6f4, one CTA)
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+}  // namespace tc
+}  // namespace ddt

@@ -60,6 +60,11 @@ _SIGS = {
     "ddt_evict_paged": ([_c_int] * 7 + [_c_p] + [_c_int] * 4 + [_c_p] * 9 + [_c_size, _c_p], _c_int),
     "ddt_token_logprobs_workspace": ([_c_int] * 4, _c_size),
     "ddt_token_logprobs": ([_c_int] * 5 + [_c_float, _c_int] + [_c_p] * 9 + [_c_size, _c_p], _c_int),
+    "ddt_append_paged_quant": ([_c_int] * 11 + [_c_p] * 6 + [_c_int] + [_c_p] * 6, _c_int),
+    "ddt_read_paged_quant": ([_c_int] * 10 + [_c_p] * 10, _c_int),
+    "ddt_decode_attn_paged_quant_workspace": ([_c_int] * 6, _c_size),
+    "ddt_decode_attn_paged_quant": ([_c_int] * 11 + [_c_p] * 9 + [_c_float] + [_c_p] * 3 + [_c_size, _c_p], _c_int),
+    "ddt_qk_norm_rope": ([_c_int] * 7 + [ctypes.c_double, _c_float, _c_float, _c_int] + [_c_p] * 11, _c_int),
     "ddt_commit": ([_c_int] * 7 + [_c_int] + [_c_p] * 4 + [_c_int] * 6 + [_c_int] + [_c_p] * 13, _c_int),
 }
 EXPORTS = tuple(_SIGS)
@@ -752,3 +757,168 @@ def ddt_token_logprobs(target_logits, token, *, node=None, top_n: int = 0, tempe
     if rc:
         _check(rc, "ddt_token_logprobs")
     return res
+
+
+# ------------------------------------------------------------------ the 8-bit paged cache
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _quant_cache(k_pages, v_pages, k_scale, v_scale, dev):
+    """The sizes (L, num_pages, Hkv, page_size, d), rows a scale, and addresses of an 8-bit cache."""
+    L, num_pages, Hkv, page, d = shape = k_pages.shape
+    if k_pages.dtype not in _CODES:
+        raise DDTError(f"k_pages has dtype {k_pages.dtype}, expected one of {list(_CODES)}")
+    scales = (L, num_pages, Hkv, k_scale.shape[3] if k_scale.dim() == 4 else 0)
+    if not scales[3] or page % scales[3]:
+        raise DDTError(f"k_scale has shape {tuple(k_scale.shape)}, expected {(L, num_pages, Hkv)} and a divisor of {page}")
+    at = (_at(k_pages, dev, shape, k_pages.dtype, "k_pages"), _at(v_pages, dev, shape, k_pages.dtype, "v_pages"),
+          _at(k_scale, dev, scales, torch.uint8, "k_scale"), _at(v_scale, dev, scales, torch.uint8, "v_scale"))
+    return shape, page // scales[3], at
+
+
+def quant_cache(L, num_pages, Hkv, page_size, d, *, block: int, device="cuda"):
+    """An empty 8-bit cache: (k_pages, v_pages, k_scale, v_scale), float8_e4m3fn codes and uint8 scale bytes."""
+    pages = [torch.zeros((L, num_pages, Hkv, page_size, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    return (*pages, *(torch.zeros((L, num_pages, Hkv, page_size // block), dtype=torch.uint8, device=device)
+                      for _ in range(2)))
+
+
+def ddt_append_paged_quant(k, v, k_pages, v_pages, k_scale, v_scale, block_table, prefix_len, count, *, node=None,
+                           advance: bool = True, status=None):
+    """Rows quantised into the 8-bit cache: k/v [L][B][N][Hkv][d]; k/v_pages [L][num_pages][Hkv][page_size][d]
+    float8_e4m3fn (or uint8) codes; k/v_scale [L][num_pages][Hkv][page_size / block] uint8, in place.  Entry
+    j < count[b] is row node[b][j] (row j without node) and becomes cache row prefix_len[b] + j; advance adds
+    count to prefix_len.  After a walk: node=acc_nodes, count=n_emitted."""
+    lib = _lib or _gpu()
+    L, B, N, Hkv, d = rows = k.shape
+    dev, dt = _here(k, "k"), k.dtype
+    code = _code(dt, "k")
+    pk, pv = _at(k, dev, rows, dt, "k"), _at(v, dev, rows, dt, "v")
+    (L2, num_pages, Hkv2, page, d2), block, at = _quant_cache(k_pages, v_pages, k_scale, v_scale, dev)
+    if (L2, Hkv2, d2) != (L, Hkv, d):
+        raise DDTError(f"k has layers, heads and head size {(L, Hkv, d)}, the cache {(L2, Hkv2, d2)}")
+    max_pages = block_table.shape[1]
+    each = (B,)
+    pn, A = None, N
+    if node is not None:
+        A = node.shape[1]
+        pn = _at(node, dev, (B, A), _I32, "node")
+    pc = _at(count, dev, each, _I32, "count")
+    ptab = _at(block_table, dev, (B, max_pages), _I32, "block_table")
+    plen = _at(prefix_len, dev, each, _I32, "prefix_len")
+    if status is None:
+        status = torch.empty(each, dtype=_I32, device=k.device)
+    pst = _at(status, dev, each, _I32, "status")
+    rc = lib.ddt_append_paged_quant(L, B, N, A, Hkv, d, page, num_pages, max_pages, block, code, pk, pv, pn, pc, ptab, plen,
+                                    int(advance), *at, pst, _raw_stream(dev))
+    if rc:
+        _check(rc, "ddt_append_paged_quant")
+    return {"status": status}
+
+
+def ddt_read_paged_quant(k_pages, v_pages, k_scale, v_scale, block_table, prefix_len, k_out, v_out, *, status=None):
+    """The 8-bit cache's rows 0..prefix_len[b]-1 as values: k/v_out [L][B][Hkv][Pcap][d] bf16 or fp32, the caches
+    that ddt_tree_attn takes."""
+    lib = _lib or _gpu()
+    dev = _here(k_pages, "k_pages")
+    (L, num_pages, Hkv, page, d), block, at = _quant_cache(k_pages, v_pages, k_scale, v_scale, dev)
+    B, max_pages = block_table.shape
+    Pcap = k_out.shape[3] if k_out.dim() == 5 else 0
+    out, dt = (L, B, Hkv, Pcap, d), k_out.dtype
+    code = _code(dt, "k_out")
+    pk, pv = _at(k_out, dev, out, dt, "k_out"), _at(v_out, dev, out, dt, "v_out")
+    each = (B,)
+    ptab = _at(block_table, dev, (B, max_pages), _I32, "block_table")
+    plen = _at(prefix_len, dev, each, _I32, "prefix_len")
+    if status is None:
+        status = torch.empty(each, dtype=_I32, device=k_pages.device)
+    pst = _at(status, dev, each, _I32, "status")
+    rc = lib.ddt_read_paged_quant(L, B, Hkv, d, Pcap, page, num_pages, max_pages, block, code, *at, ptab, plen, pk, pv, pst,
+                                  _raw_stream(dev))
+    if rc:
+        _check(rc, "ddt_read_paged_quant")
+    return {"status": status}
+
+
+def decode_attn_paged_quant_workspace(q, k_pages, block_table):
+    """A workspace for ddt_decode_attn_paged_quant calls of these shapes (one call at a time may use it)."""
+    lib = _gpu()
+    L, B, Hq, d = q.shape
+    return _ws(lib.ddt_decode_attn_paged_quant_workspace(L, B, Hq, k_pages.shape[2], d, _code(q.dtype, "q")), q.device)
+
+
+def ddt_decode_attn_paged_quant(q, k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, prefix_len, *,
+                                scale: float, out_dtype=None, out=None, status=None, workspace=None):
+    """ddt_decode_attn_paged over the 8-bit cache, without the sums of the weights: one new token a request, q
+    [L][B][Hq][d]; k/v_new [L][B][Hkv][d] (its own row, or both None)."""
+    lib = _lib or _gpu()
+    L, B, Hq, d = heads = q.shape
+    dev, dt = _here(q, "q"), q.dtype
+    in_code = _code(dt, "q")
+    pq = _at(q, dev, heads, dt, "q")
+    (L2, num_pages, Hkv, page, d2), block, at = _quant_cache(k_pages, v_pages, k_scale, v_scale, dev)
+    if (L2, d2) != (L, d):
+        raise DDTError(f"q has layers and head size {(L, d)}, the cache {(L2, d2)}")
+    max_pages = block_table.shape[1]
+    pk = pv = None
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise DDTError("k_new and v_new are given together or not at all")
+        pk = _at(k_new, dev, (L, B, Hkv, d), dt, "k_new")
+        pv = _at(v_new, dev, (L, B, Hkv, d), dt, "v_new")
+    ptab = _at(block_table, dev, (B, max_pages), _I32, "block_table")
+    each = (B,)
+    plen = _at(prefix_len, dev, each, _I32, "prefix_len")
+    if out is None:
+        out = torch.empty(heads, dtype=out_dtype or dt, device=q.device)
+    out_dtype = out_dtype or out.dtype
+    out_code = in_code if out_dtype is dt else _code(out_dtype, "out")
+    po = _at(out, dev, heads, out_dtype, "out")
+    if status is None:
+        status = torch.empty(each, dtype=_I32, device=q.device)
+    pst = _at(status, dev, each, _I32, "status")
+    if workspace is None:
+        workspace = decode_attn_paged_quant_workspace(q, k_pages, block_table)
+    pws, ws_bytes = _ws_at(dev, workspace)
+    rc = lib.ddt_decode_attn_paged_quant(L, B, Hq, Hkv, d, page, num_pages, max_pages, block, in_code, out_code, pq, pk, pv, *at,
+                                         ptab, plen, float(scale), po, pst, pws, ws_bytes, _raw_stream(dev))
+    if rc:
+        _check(rc, "ddt_decode_attn_paged_quant")
+    return {"o": out, "status": status}
+
+
+# ------------------------------------------------------------- norms and rotation of heads
+_Strides = ctypes.c_int64 * 4
+
+
+def ddt_qk_norm_rope(q, k, q_weight, k_weight, position, *, n_nodes=None, rot_dim=None, theta=10000.0, eps=1e-6,
+                     weight_offset=0.0, q_out=None, k_out=None):
+    """Root-mean-square norms of every head and rotation by position (rot_dim channels, all by default; 0: none) in
+    one pass: q [L][B][N][Hq][d], k [L][B][N][Hkv][d] with contiguous channels and any other strides, weights [L][d],
+    position [B][N] int32, n_nodes [B] int32 or None (all rows).  Returns (q_out, k_out), contiguous; they may be q
+    and k themselves."""
+    lib = _lib or _gpu()
+    L, B, N, Hq, d = q.shape
+    Hkv = k.shape[3]
+    dev, dt = _here(q, "q"), q.dtype
+    code = _code(dt, "q")
+    qs, ks = q.stride(), k.stride()
+    if k.dtype != dt or tuple(k.shape) != (L, B, N, Hkv, d) or k.get_device() != dev or qs[4] != 1 or ks[4] != 1:
+        raise DDTError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be {dt} on cuda:{dev} with contiguous channels")
+    pw, kw = _at(q_weight, dev, (L, d), dt, "q_weight"), _at(k_weight, dev, (L, d), dt, "k_weight")
+    ppos = _at(position, dev, (B, N), _I32, "position")
+    pn = None if n_nodes is None else _at(n_nodes, dev, (B,), _I32, "n_nodes")
+    # rows past n_nodes are not written: zeros where the caller gives no output
+    new = torch.empty if n_nodes is None else torch.zeros
+    if q_out is None:
+        q_out = new((L, B, N, Hq, d), dtype=dt, device=q.device)
+    if k_out is None:
+        k_out = new((L, B, N, Hkv, d), dtype=dt, device=q.device)
+    po, pk = _at(q_out, dev, (L, B, N, Hq, d), dt, "q_out"), _at(k_out, dev, (L, B, N, Hkv, d), dt, "k_out")
+    rc = lib.ddt_qk_norm_rope(L, B, N, Hq, Hkv, d, d if rot_dim is None else int(rot_dim), float(theta), float(eps),
+                              float(weight_offset), code, q.data_ptr(), _Strides(*qs[:4]), k.data_ptr(), _Strides(*ks[:4]),
+                              pw, kw, ppos, pn, po, pk, _raw_stream(dev))
+    if rc:
+        _check(rc, "ddt_qk_norm_rope")
+    return q_out, k_out
