@@ -22,8 +22,8 @@
 //   warp 0      producer: block-table entries, TMA of K and V tiles into one ring
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
 //   warp 2      queries: the parts of a segment's heads
-//   warps 3-6, 7-10 ..  softmax, eight heads a warpgroup, a thread a cached row; the row's scales are
-//               fetched a tile ahead, their page two tiles ahead
+//   warp 3      scales: the bytes of a tile's blocks, two tiles ahead of the softmax
+//   warps 4-7, 8-11 ..  softmax, eight heads a warpgroup, a thread a cached row
 // The split of the rows over the CTAs, the partials and the join are those of decode.cuh.
 // Every wait is bounded, as there.
 #include <cuda.h>
@@ -46,7 +46,7 @@ constexpr int pow2_at_least(int x, int y) { return x <= y ? y : pow2_at_least(x,
 template <int D, int HP, int QP, int PP>
 struct QuantCfg {
     static constexpr int kGroups = HP / 8;                // softmax warpgroups
-    static constexpr int kThreads = 96 + 128 * kGroups;
+    static constexpr int kThreads = 128 + 128 * kGroups;
     static constexpr int kRow = D < 128 ? D : 128;        // bytes of a swizzled row
     static constexpr int kBlocks = D / kRow;              // of a cached row
     static constexpr int kStageBytes = kDecTile * D;      // a K or V tile
@@ -65,7 +65,10 @@ struct QuantCfg {
     static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory");
     static_assert(kCtas * kTmemCols <= 512, "tensor memory");
-    static_assert((4 * kStages + 22) * 4 + 64 <= 640, "barriers");
+    static_assert((2 * kStages + 15) * 8 + 40 + 4 * 64 <= 640, "barriers and scales");
+    // bad_tile and q_unit are kept for 8 tiles (segments): the producer is up to 6 tiles ahead of the products, they two of
+    // the softmax
+    static_assert(kStages <= 12, "rings of 8");
     static_assert(NQ % 16 == 0 && NQ <= 256 && NP <= 128, "N of the products");
     // head size 64: lanes 64-127 of O read on behind a tile, into Q and P at the end of the ring
     static_assert(D != 64 || kQBufs * kQBytes + 2 * kPBytes >= kStageBytes, "shared memory behind the ring");
@@ -113,11 +116,13 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
     uint64_t* s_full = q_free + 2;       // [2] S of a tile in tensor memory
     uint64_t* p_full = s_full + 2;       // [2] P of a tile in shared memory (the softmax warps)
     uint64_t* p_free = p_full + 2;       // [2] its P V is done
-    uint64_t* drain = p_free + 2;
+    uint64_t* x_full = p_free + 2;       // [4] a tile's scales are there
+    uint64_t* drain = x_full + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     int* bad_tile = abort_flag + 1;                            // [8] a page of the tile does not exist
-    float* q_unit = reinterpret_cast<float*>(bad_tile + 8);    // [8][HP] log2 scores of a unit of Q K^T, by segment
+    int* scales = bad_tile + 8;                                // [4][16] a tile's scales by block: K's byte, V's << 8
+    float* q_unit = reinterpret_cast<float*>(scales + 4 * 16);  // [8][HP] log2 scores of a unit of Q K^T, by segment
     float* xm = q_unit + 8 * HP;                               // [2][4][HP] warps' tile maxima
     float* sm_l = xm + 2 * 4 * HP;                             // [4][HP] warps' sums of a segment
 
@@ -131,6 +136,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
             tc::mbar_init(p_full + i, 4 * Cfg::kGroups);
             tc::mbar_init(p_free + i, 1);
         }
+        for (int i = 0; i < 4; ++i) tc::mbar_init(x_full + i, 1);
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
@@ -303,28 +309,44 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_full + qb);
         }
+    } else if (warp == 3) {
+        // --------------------------------------------------------------------- scales
+        const int n_blk = kDecTile / a.block, per_page = p.page_rows / a.block;
+        int j = 0;
+        bool ok = true;
+        for (; w.left > 0 && ok; dec_next(p, w)) {
+            const int g = w.g / p.HB, n_seg = dec_seg_tiles(w);
+            const int32_t* table = p.block_table + (long long)w.b * p.max_pages;
+            auto entry = [&](int t) {  // the page of this lane's block of tile t, -1 past the prefix
+                const int pos = t * kDecTile + lane * a.block;
+                return lane < n_blk && pos < w.P ? table[pos / p.page_rows] : -1;
+            };
+            int phys = entry(w.t);
+            for (int t = w.t; t < w.t + n_seg; ++t, ++j) {
+                const bool good = phys >= 0 && phys < p.num_pages;
+                const int in = (t * kDecTile + lane * a.block) % p.page_rows / a.block;
+                const long long at = good ? (((long long)w.l * p.num_pages + phys) * p.Hkv + g) * per_page + in : 0;
+                const uint32_t kb = a.ks[at], vb = a.vs[at];
+                if (t + 1 < w.t + n_seg) phys = entry(t + 1);
+                // at most two tiles ahead of the softmax, so no slot of four is written that it still reads
+                if (j >= 2) ok = __all_sync(kFull, tc::mbar_wait(p_full + (j & 1), ((j - 2) >> 1) & 1, abort));
+                if (!ok) break;
+                if (lane < n_blk) scales[(j & 3) * 16 + lane] = (int)(kb | vb << 8);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(x_full + (j & 3));
+            }
+        }
     } else {
         // -------------------------------------------------- softmax, and the segments' partials
         const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
         const uint32_t lane_base = (uint32_t)(32 * ws) << 16;
-        const int grp = Cfg::kGroups == 1 ? 0 : (warp - 3) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
-        const int per_page = p.page_rows / a.block;
+        const int grp = Cfg::kGroups == 1 ? 0 : (warp - 4) >> 2, hg = grp * 8, bar = 1 + grp;  // heads hg .. hg + 7 of the block
+        const int my_block = r / a.block;
         int j = 0, seg = 0;
         bool ok = true;
         for (; w.left > 0; dec_next(p, w), ++seg) {
-            const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
-            const int32_t* table = p.block_table + (long long)w.b * p.max_pages;
-            auto page_of = [&](int pos) { return pos < w.P ? table[pos / p.page_rows] : -1; };
-            auto bytes_of = [&](int pos, int phys) {  // the row's scales: K's byte, then V's
-                if (phys < 0 || phys >= p.num_pages) return 127 | 127 << 8;
-                const long long at = (((long long)w.l * p.num_pages + phys) * p.Hkv + g) * per_page + pos % p.page_rows / a.block;
-                return (int)a.ks[at] | (int)a.vs[at] << 8;
-            };
-            const int y0 = w.t * kDecTile;
-            int here = bytes_of(y0 + r, page_of(y0 + r));
-            int next_page = n_seg > 1 ? page_of(y0 + kDecTile + r) : -1;
-            int base = bytes_of(y0, page_of(y0)) >> 8;
-            if (base == 0) base = 127;
+            const int h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
+            int base = 127;  // V's scale of the segment's first row
             float m[8], l[8];
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
@@ -333,19 +355,19 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
             }
             int bad = 0;
             for (int i = 0; i < n_seg; ++i, ++j) {
-                const int y = y0 + i * kDecTile, n = min(kDecTile, w.P - y);
-                const int kb = here & 255, vb = here >> 8;
-                here = i + 1 < n_seg ? bytes_of(y + kDecTile + r, next_page) : 0;
-                next_page = i + 2 < n_seg ? page_of(y + 2 * kDecTile + r) : -1;
-                const int dv = vb ? max(-126, min(126, vb - base)) : 0;  // (a block of zeros: any scale)
-                const float k_unit = scale_of(kb), v_add = (float)dv, v_back = __int_as_float((127 - dv) << 23);
+                const int n = min(kDecTile, w.P - (w.t + i) * kDecTile);
                 // a warp that gave up still takes part in the barriers
-                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
+                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort) && tc::mbar_wait(x_full + (j & 3), (j >> 2) & 1, abort);
                 ok = __all_sync(kFull, ok);
-                float t[8];
+                float t[8], v_back = 1.f;
                 bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
+                    const int x = scales[(j & 3) * 16 + my_block], vb = x >> 8;
+                    if (i == 0 && scales[(j & 3) * 16] >> 8) base = scales[(j & 3) * 16] >> 8;
+                    const int dv = vb ? max(-126, min(126, vb - base)) : 0;  // (a block of zeros: any scale)
+                    const float k_unit = scale_of(x & 255), v_add = (float)dv;
+                    v_back = __int_as_float((127 - dv) << 23);
                     uint32_t sr[QP][8];
 #pragma unroll
                     for (int x = 0; x < QP; ++x) tmem_ld8(tmem + lane_base + (j & 1) * NQ + x * HP + hg, sr[x]);

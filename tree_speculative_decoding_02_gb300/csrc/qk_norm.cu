@@ -43,27 +43,35 @@ struct NormArgs {
     void* ko;
 };
 
+// 8 channels as they lie in memory (which may be what is written later: not the read-only path)
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_run(const T* p, float (&v)[8]) {
-    if (VEC) {
-        if (sizeof(T) == 2) {
-            const uint4 u = *reinterpret_cast<const uint4*>(p);  // (may be what is written: not the read-only path)
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Run {
+    static constexpr int W = 8 * (int)sizeof(T) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if (VEC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < W; i += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
             }
         } else {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+            for (int i = 0; i < 8; ++i) {
+                if (sizeof(T) == 4) {
+                    w[i % W] = reinterpret_cast<const uint32_t*>(p)[i];
+                } else {
+                    const uint32_t h = reinterpret_cast<const uint16_t*>(p)[i];
+                    w[i / 2] = i % 2 ? w[i / 2] | h << 16 : h;
+                }
+            }
+        }
     }
-}
+    __device__ __forceinline__ float operator[](int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(w[i % W]);
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_run(T* p, const float (&v)[8]) {
@@ -92,20 +100,37 @@ template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
     constexpr int LPR = D / 16, kRows = kThreads / LPR;  // lanes a row, rows at a time
     __shared__ float2 s_cs[kMaxTokens * D / 2];
-    __shared__ int s_live[kMaxTokens];
     const int tid = threadIdx.x, half = a.rot / 2, heads = a.Hq + a.Hkv;
     const long long rows = (long long)a.B * a.N, first = (long long)blockIdx.x * a.tokens;
-    const int l = blockIdx.y, nt = (int)min((long long)a.tokens, rows - first);
+    const int l = blockIdx.y, nt = (int)min((long long)a.tokens, rows - first), items = nt * heads;
     const int c = tid % LPR;
     // this lane's two runs: of the rotated channels the halves of its pairs, of the others neighbours
     const bool turned = 16 * c < a.rot;
     const int lo = turned ? 8 * c : 16 * c, hi = turned ? half + 8 * c : 16 * c + 8;
+    const unsigned mask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);  // the lanes of a row, which agree throughout
 
-    if (tid < nt) {
-        const int b = (int)((first + tid) / a.N), n = (int)((first + tid) % a.N);
-        const int nn = a.n_nodes ? a.n_nodes[b] : a.N;
-        s_live[tid] = n < nn && nn <= a.N;
-    }
+    // rows it and it + kRows: both are on their way before the first is worked on
+    Run<T, VEC> u[2], v[2];
+    bool live[2];
+    auto fetch = [&](int it, int s) {
+        live[s] = false;
+        if (it >= items) return;
+        const int t = it / heads, h = it - t * heads;
+        const long long tok = first + t;
+        const int b = (int)(tok / a.N), n = (int)(tok - (long long)b * a.N);
+        if (a.n_nodes) {
+            const int nn = a.n_nodes[b];
+            if (n >= nn || nn > a.N) return;
+        }
+        live[s] = true;
+        const T* x = h < a.Hq ? static_cast<const T*>(a.q) + l * a.qs[0] + b * a.qs[1] + n * a.qs[2] + h * a.qs[3]
+                              : static_cast<const T*>(a.k) + l * a.ks[0] + b * a.ks[1] + n * a.ks[2] + (h - a.Hq) * a.ks[3];
+        u[s].load(x + lo);
+        v[s].load(x + hi);
+    };
+    const int it0 = tid / LPR;
+    fetch(it0, 0);
+    fetch(it0 + kRows, 1);
     for (int e = tid; e < nt * half; e += kThreads) {
         const int t = e / half, i = e - t * half;
         const unsigned long long turn = (unsigned long long)(long long)a.position[first + t] * fr.f[i];
@@ -114,48 +139,47 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
         s_cs[e] = make_float2(co, s);
     }
     __syncthreads();
-    const int items = nt * heads;
-    const unsigned mask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);  // the lanes of a row, which agree throughout
-    for (int it = tid / LPR; it < items; it += kRows) {
-        const int t = it / heads, h = it - t * heads;
-        const bool live = s_live[t];
-        const long long tok = first + t;
-        const int b = (int)(tok / a.N), n = (int)(tok - (long long)b * a.N);
-        const bool isq = h < a.Hq;
-        const T* x = isq ? static_cast<const T*>(a.q) + l * a.qs[0] + b * a.qs[1] + n * a.qs[2] + h * a.qs[3]
-                         : static_cast<const T*>(a.k) + l * a.ks[0] + b * a.ks[1] + n * a.ks[2] + (h - a.Hq) * a.ks[3];
-        T* y = isq ? static_cast<T*>(a.qo) + ((l * rows + tok) * a.Hq + h) * D
-                   : static_cast<T*>(a.ko) + ((l * rows + tok) * a.Hkv + (h - a.Hq)) * D;
-        const T* w = static_cast<const T*>(isq ? a.qw : a.kw) + (long long)l * D;
-        if (!live) continue;
-        float u[8], v[8], wu[8], wv[8];
-        load_run<T, VEC>(x + lo, u);
-        load_run<T, VEC>(x + hi, v);
-        load_run<T, VEC>(w + lo, wu);
-        load_run<T, VEC>(w + hi, wv);
-        float ss = 0.f;
+    for (int it = it0; it < items; it += 2 * kRows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+        for (int s = 0; s < 2; ++s) {
+            if (!live[s]) continue;
+            const int i0 = it + s * kRows, t = i0 / heads, h = i0 - t * heads;
+            const bool isq = h < a.Hq;
+            T* y = isq ? static_cast<T*>(a.qo) + ((l * rows + first + t) * a.Hq + h) * D
+                       : static_cast<T*>(a.ko) + ((l * rows + first + t) * a.Hkv + (h - a.Hq)) * D;
+            const T* w = static_cast<const T*>(isq ? a.qw : a.kw) + (long long)l * D;
+            Run<T, VEC> wu, wv;
+            wu.load(w + lo);
+            wv.load(w + hi);
+            float ss = 0.f;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+            for (int i = 0; i < 8; ++i) ss = fmaf(u[s][i], u[s][i], fmaf(v[s][i], v[s][i], ss));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            u[i] = u[i] * r * (a.offset + wu[i]);
-            v[i] = v[i] * r * (a.offset + wv[i]);
-        }
-        if (turned) {
-            const float2* cs = s_cs + t * half + 8 * c;
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+            const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+            float p[8], q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 k = cs[i];
-                const float p = u[i];
-                u[i] = fmaf(p, k.x, -v[i] * k.y);
-                v[i] = fmaf(v[i], k.x, p * k.y);
+                p[i] = u[s][i] * r * (a.offset + wu[i]);
+                q[i] = v[s][i] * r * (a.offset + wv[i]);
             }
+            if (turned) {
+                const float4* cs = reinterpret_cast<const float4*>(s_cs + t * half + 8 * c);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 k = cs[i / 2];
+                    const float p0 = p[i], p1 = p[i + 1];
+                    p[i] = fmaf(p0, k.x, -q[i] * k.y);
+                    q[i] = fmaf(q[i], k.x, p0 * k.y);
+                    p[i + 1] = fmaf(p1, k.z, -q[i + 1] * k.w);
+                    q[i + 1] = fmaf(q[i + 1], k.z, p1 * k.w);
+                }
+            }
+            store_run<T, VEC>(y + lo, p);
+            store_run<T, VEC>(y + hi, q);
         }
-        store_run<T, VEC>(y + lo, u);
-        store_run<T, VEC>(y + hi, v);
+        fetch(it + 2 * kRows, 0);
+        fetch(it + 3 * kRows, 1);
     }
 }
 
@@ -200,9 +224,12 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
         a.ks[i] = kn[i] > 1 ? k_stride[i] : 0;
         bits |= (uintptr_t)(a.qs[i] * esz) | (uintptr_t)(a.ks[i] * esz);
     }
+    // frequency i as a product of two powers, 16 + 8 of them at most: a power takes the host some 50 ns
     NormFreq fr{};
-    for (int i = 0; i < rot / 2; ++i)
-        fr.f[i] = (unsigned long long)(powl((long double)theta, -2.0L * i / rot) * (18446744073709551616.0L / 6.283185307179586476925L));
+    double near[16], far[8];
+    for (int i = 0; i < 16 && i < rot / 2; ++i) near[i] = pow(theta, -2.0 * i / rot) * (18446744073709551616.0 / 6.283185307179586477);
+    for (int i = 0; i < 8 && 16 * i < rot / 2; ++i) far[i] = pow(theta, -32.0 * i / rot);
+    for (int i = 0; i < rot / 2; ++i) fr.f[i] = (unsigned long long)(near[i % 16] * far[i / 16]);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     a.tokens = 1;

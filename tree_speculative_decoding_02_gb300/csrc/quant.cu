@@ -27,8 +27,9 @@ struct AppendArgs {
     int L, B, N, A, Hkv, d, S;
     int page_rows, num_pages, max_pages, cap;
     int wpi, iters;   // warps an item (a block's K or V rows of one head), vectors a lane of it
-    int blocks;       // blocks that a request's rows may fall into
+    int run;          // blocks a CTA
     int advance, solo;  // solo: one CTA has all of a request
+    int checked;      // the status is there already
     const void* k;
     const void* v;
     const int32_t* node;   // or null
@@ -42,8 +43,34 @@ struct AppendArgs {
     int32_t* status;
 };
 
+// 8 channels as they lie in memory, read once
 template <typename T>
-__device__ __forceinline__ void load8_any(const T* p, float (&v)[8]) { load8_stream(p, v); }
+struct Vec8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ld_stream_u4(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (sizeof(T) == 4) {
+                    v[4 * i + k] = __uint_as_float(x[k]);
+                } else {
+                    v[2 * k] = __uint_as_float(x[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
+                }
+            }
+        }
+    }
+};
 
 // what is not finite becomes NaN, the rest is scaled
 __device__ __forceinline__ float scaled(float x, float inv) { return fmaf(x, 0.f, x) * inv; }
@@ -57,15 +84,8 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
 
 }  // namespace
 
-// grid (blocks, item groups, L * B).  A CTA takes a block of one request and layer, wpi of its warps
-// an item.  Its rows are read once into registers where a lane has up to kChunk vectors of them.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
-    __shared__ float s_max[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.z % a.B, l = blockIdx.z / a.B;
-    const int P = a.prefix_len[b], n = a.count[b];
-    // ---- the request as a whole: nothing of it is written unless all of it can be
+// All threads of a CTA: the request as a whole.  Nothing of it is written unless all of it can be.
+__device__ __forceinline__ int append_check(const AppendArgs& a, int b, int P, int n) {
     int err = P < 0 || P > a.cap ? DDT_ERR_CAPACITY : DDT_OK;
     if (!err && (n < 0 || n > a.A)) err = DDT_ERR_INVALID_ARG;
     if (!err && n > a.cap - P) err = DDT_ERR_CAPACITY;
@@ -73,92 +93,116 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
     int bad = 0;
     if (!err && n > 0) {
         const int p1 = (P + n - 1) / a.page_rows;
-        for (int p = P / a.page_rows + tid; p <= p1; p += kThreads) bad |= table[p] < 0 || table[p] >= a.num_pages;
+        for (int p = P / a.page_rows + threadIdx.x; p <= p1; p += kThreads) bad |= table[p] < 0 || table[p] >= a.num_pages;
         if (a.node)
-            for (int i = tid; i < n; i += kThreads) {
+            for (int i = threadIdx.x; i < n; i += kThreads) {
                 const int r = a.node[(long long)b * a.A + i];
                 bad |= r < 0 || r >= a.N;
             }
     }
-    if (__syncthreads_or(bad)) err = DDT_ERR_INVALID_ARG;
-    if (l == 0 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    return __syncthreads_or(bad) ? DDT_ERR_INVALID_ARG : err;
+}
+
+// grid B: the check by itself, where every CTA of the next kernel would look at many pages
+__global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
+    const int b = blockIdx.x, err = append_check(a, b, a.prefix_len[b], a.count[b]);
+    if (threadIdx.x == 0) a.status[b] = err;
+}
+
+// grid (runs of blocks, item groups, L * B).  A CTA takes a few blocks of one request and layer, one after
+// another; wpi of its warps an item.  A lane has up to kChunk vectors of the item's rows in registers, so they
+// are read once (a block of 128 rows of 256 channels twice).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
+    __shared__ float s_max[2][kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.z % a.B, l = blockIdx.z / a.B;
+    if (a.checked) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int P = a.prefix_len[b], n = a.count[b];
+    const int err = a.checked ? a.status[b] : append_check(a, b, P, n);
+    if (!a.checked && l == 0 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
         a.status[b] = err;
         if (a.solo && a.advance && !err) a.prefix_len[b] = P + n;
     }
-    const int first = P / a.S + blockIdx.x;  // this CTA's block of the request
-    if (err || n == 0 || (long long)first * a.S >= (long long)P + n) return;
-
-    const int r0 = first * a.S, lo = max(P - r0, 0), hi = min(P + n - r0, a.S);  // new rows [lo, hi) of the block
-    const int phys = table[r0 / a.page_rows];
+    if (err || n == 0) return;
+    const int32_t* table = a.table + (long long)b * a.max_pages;
     const int item = blockIdx.y * (kWarps / a.wpi) + warp / a.wpi, part = warp % a.wpi;
     const bool real = item < 2 * a.Hkv;
     const int isv = item & 1, g = min(item >> 1, a.Hkv - 1);
-    const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
-    unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + r0 % a.page_rows) * a.d;
-    unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + r0 % a.page_rows / a.S;
     const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * a.d + (long long)g * a.d;
     const long long pitch = (long long)a.Hkv * a.d;
-    const int old = real && lo > 0 ? *byte : 0;
-
     // vector e of the item: 8 channels of row e / (d / 8) of the block
-    const int vpr = a.d / 8, e0 = part * a.iters * 32 + lane;
-    float x[kChunk][8];
-    auto load = [&](int it0) {
+    const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5), e0 = part * a.iters * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
+
+    int first = P / a.S + blockIdx.x * a.run;
+    for (int turn = 0; turn < a.run && (long long)first * a.S < (long long)P + n; ++turn, ++first) {
+        const int r0 = first * a.S, lo = max(P - r0, 0), hi = min(P + n - r0, a.S);  // new rows [lo, hi) of the block
+        const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows, phys = table[lp];
+        Vec8<T> x[kChunk];
+        auto load = [&](int it0) {
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            const int e = e0 + (it0 + i) * 32, r = e / vpr;
-            const bool mine = real && it0 + i < a.iters && r >= lo && r < hi;
-            if (mine) {
-                const int j = r0 + r - P;
-                const long long row = a.node ? a.node[(long long)b * a.A + j] : j;
-                load8_any(src + row * pitch + e % vpr * 8, x[i]);
-            } else {
+            for (int i = 0; i < kChunk; ++i) {
+                const int r = (e0 + (it0 + i) * 32) >> shift;
+                if (real && it0 + i < a.iters && r >= lo && r < hi) {
+                    const int j = r0 + r - P;
+                    const long long row = a.node ? a.node[(long long)b * a.A + j] : j;
+                    x[i].load(src + row * pitch + ch);
+                } else {
+                    x[i].zero();
+                }
+            }
+        };
+        float m = 0.f;
+        for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
+            load(it0);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[i][c] = 0.f;
+            for (int i = 0; i < kChunk; ++i) {
+                float v[8];
+                x[i].get(v);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float y = fabsf(v[c]);
+                    m = fmaxf(m, y < INFINITY ? y : 0.f);
+                }
             }
         }
-    };
-    float m = 0.f;
-    for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
-        load(it0);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float y = fabsf(x[i][c]);
-                m = fmaxf(m, y < INFINITY ? y : 0.f);
-            }
-    }
-    m = warp_max(m);
-    if (a.wpi > 1) {
-        if (lane == 0) s_max[warp] = m;
-        __syncthreads();
-        for (int i = warp / a.wpi * a.wpi, k = 0; k < a.wpi; ++k) m = fmaxf(m, s_max[i + k]);
-    }
-    if (!real) return;
-    const int now = max(old, scale_byte(m));
-    if (part == 0 && lane == 0) *byte = (unsigned char)now;
-    const float inv = now ? scale_of(254 - now) : 0.f;
-    for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
-        if (a.iters > kChunk) load(it0);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            const int e = e0 + (it0 + i) * 32, r = e / vpr;
-            if (it0 + i < a.iters && r >= lo && r < hi)
-                *reinterpret_cast<uint2*>(page + (long long)r * a.d + e % vpr * 8) = codes8(x[i], inv);
+        const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
+        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
+        unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
+        const int old = real && lo > 0 ? *byte : 0;
+        m = warp_max(m);
+        if (a.wpi > 1) {
+            if (lane == 0) s_max[turn & 1][warp] = m;
+            __syncthreads();
+            for (int i = warp / a.wpi * a.wpi, k = 0; k < a.wpi; ++k) m = fmaxf(m, s_max[turn & 1][i + k]);
         }
-    }
-    if (old && now > old) {  // the rows that the block had, under its new scale
-        const float f = scale_of(max(127 + old - now, 0));
-        for (int e = part * 32 + lane; e < lo * vpr; e += a.wpi * 32) {
-            uint2* at = reinterpret_cast<uint2*>(page + (long long)e * 8);
-            const uint2 c = *at;
-            float v[8];
-            values8(c, v);
+        if (!real) continue;
+        const int now = max(old, scale_byte(m));
+        if (part == 0 && lane == 0) *byte = (unsigned char)now;
+        const float inv = now ? scale_of(254 - now) : 0.f;
+        for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
+            if (a.iters > kChunk) load(it0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= f;
-            const uint32_t w0 = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16, w1 = e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16;
-            *at = make_uint2(w0, w1);
+            for (int i = 0; i < kChunk; ++i) {
+                const int r = (e0 + (it0 + i) * 32) >> shift;
+                if (it0 + i < a.iters && r >= lo && r < hi) {
+                    float v[8];
+                    x[i].get(v);
+                    *reinterpret_cast<uint2*>(page + (long long)r * a.d + ch) = codes8(v, inv);
+                }
+            }
+        }
+        if (old && now > old) {  // the rows that the block had, under its new scale
+            const float f = scale_of(max(127 + old - now, 0));
+            for (int e = part * 32 + lane; e < lo << shift; e += a.wpi * 32) {
+                uint2* at = reinterpret_cast<uint2*>(page + (long long)e * 8);
+                const uint2 c = *at;
+                float v[8];
+                values8(c, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= f;
+                *at = make_uint2(e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16, e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16);
+            }
         }
     }
 }
@@ -202,22 +246,29 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     a.wpi = 1;
     while (a.wpi < kWarps && vectors > kChunk * a.wpi) a.wpi *= 2;
     a.iters = (vectors + a.wpi - 1) / a.wpi;
-    a.blocks = (int)(((long long)A + S - 2) / S + 1);
+    const int blocks = (int)(((long long)A + S - 2) / S + 1);  // that a request's rows may fall into
     const int per = kWarps / a.wpi, groups = (2 * Hkv + per - 1) / per;
-    a.solo = L == 1 && a.blocks == 1 && groups == 1;
-    const dim3 grid(a.blocks, groups, L * B);
-    if (in == DDT_BF16) k_append_quant<__nv_bfloat16><<<counted(grid), kThreads, 0, st>>>(a);
-    else k_append_quant<float><<<counted(grid), kThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !advance || a.solo) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(counted((unsigned)(B + 127) / 128));
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
+    a.solo = L == 1 && blocks == 1 && groups == 1;
+    a.run = blocks > 64 ? 4 : 1;
+    a.checked = (A + pg.page_rows - 1) / pg.page_rows > kThreads;
+    if (a.checked) {
+        k_append_check<<<counted(dim3(B)), kThreads, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute at{};  // set up while the kernel before ends
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = counted(dim3((blocks + a.run - 1) / a.run, groups, L * B));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
     cfg.attrs = &at;
+    cfg.numAttrs = a.checked ? 1 : 0;
+    cudaError_t e = in == DDT_BF16 ? cudaLaunchKernelEx(&cfg, k_append_quant<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, k_append_quant<float>, a);
+    if (e != cudaSuccess || !advance || a.solo) return e;
+    cfg.gridDim = dim3(counted((unsigned)(B + 127) / 128));
+    cfg.blockDim = dim3(128);
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_append_advance, B, count, (const int32_t*)status, prefix_len);
 }
@@ -237,10 +288,13 @@ struct ReadArgs {
     void* vo;
     int32_t* status;
 };
-constexpr int kReadVecs = 4;  // 16 codes each, in flight a thread
+constexpr int kReadVecs = 4;   // 16 codes each, in flight a thread
+constexpr int kReadTurns = 4;  // such steps a CTA
 }  // namespace
 
-// grid (row chunks, 2 * Hkv, L * B): kReadVecs * kThreads * 16 codes of one head's K or V a CTA
+// grid (row chunks, 2 * Hkv, L * B): kReadTurns steps of kReadVecs * kThreads * 16 codes of one head's K or V
+// a CTA.  (The grid goes by the table's rows; CTAs behind a request's own take a few hundred cycles each, which
+// larger ones make rarer.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
     const int tid = threadIdx.x, b = blockIdx.z % a.B, l = blockIdx.z / a.B, g = blockIdx.y >> 1, isv = blockIdx.y & 1;
@@ -255,48 +309,49 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
         if (tid == 0) a.status[b] = !fits ? DDT_ERR_CAPACITY : (bad ? DDT_ERR_INVALID_ARG : DDT_OK);
     }
     if (!fits) return;
-    const int vpr = a.d / 16, rows = kReadVecs * kThreads / vpr, y0 = blockIdx.x * rows;
-    if (y0 >= P) return;
+    const int vpr = a.d / 16, rows = kReadVecs * kThreads / vpr;
     const unsigned char* pages = isv ? a.vp : a.kp;
     const unsigned char* scales = isv ? a.vs : a.ks;
     T* out = static_cast<T*>(isv ? a.vo : a.ko) + (((long long)l * a.B + b) * a.Hkv + g) * (long long)a.Pcap * a.d;
-    uint4 c[kReadVecs];
-    float f[kReadVecs];
-    bool there[kReadVecs];
+    for (int y0 = blockIdx.x * kReadTurns * rows, turn = 0; turn < kReadTurns && y0 < P; ++turn, y0 += rows) {
+        uint4 c[kReadVecs];
+        float f[kReadVecs];
+        bool there[kReadVecs];
 #pragma unroll
-    for (int i = 0; i < kReadVecs; ++i) {
-        const int e = tid + i * kThreads, y = y0 + e / vpr;
-        there[i] = y < P;
-        if (!there[i]) continue;
-        const int lp = y / a.page_rows, phys = table[lp], r = y - lp * a.page_rows;
-        there[i] = phys >= 0 && phys < a.num_pages;
-        if (!there[i]) continue;
-        const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
-        c[i] = ld_stream_u4(pages + (plane * a.page_rows + r) * a.d + e % vpr * 16);
-        f[i] = scale_of(scales[plane * (a.page_rows / a.S) + r / a.S]);
-    }
+        for (int i = 0; i < kReadVecs; ++i) {
+            const int e = tid + i * kThreads, y = y0 + e / vpr;
+            there[i] = y < P;
+            if (!there[i]) continue;
+            const int lp = y / a.page_rows, phys = table[lp], r = y - lp * a.page_rows;
+            there[i] = phys >= 0 && phys < a.num_pages;
+            if (!there[i]) continue;
+            const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
+            c[i] = ld_stream_u4(pages + (plane * a.page_rows + r) * a.d + e % vpr * 16);
+            f[i] = scale_of(scales[plane * (a.page_rows / a.S) + r / a.S]);
+        }
 #pragma unroll
-    for (int i = 0; i < kReadVecs; ++i) {
-        if (!there[i]) continue;
-        const int e = tid + i * kThreads;
-        T* to = out + (long long)(y0 + e / vpr) * a.d + e % vpr * 16;
-        float v[16];
-        values8(make_uint2(c[i].x, c[i].y), v);
-        values8(make_uint2(c[i].z, c[i].w), v + 8);
+        for (int i = 0; i < kReadVecs; ++i) {
+            if (!there[i]) continue;
+            const int e = tid + i * kThreads;
+            T* to = out + (long long)(y0 + e / vpr) * a.d + e % vpr * 16;
+            float v[16];
+            values8(make_uint2(c[i].x, c[i].y), v);
+            values8(make_uint2(c[i].z, c[i].w), v + 8);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] *= f[i];
-        if (sizeof(T) == 2) {
-            uint32_t w[8];
+            for (int k = 0; k < 16; ++k) v[k] *= f[i];
+            if (sizeof(T) == 2) {
+                uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&z);
+                for (int k = 0; k < 8; ++k) {
+                    const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&z);
+                }
+                reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(to)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
-            reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(to)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
     }
 }
@@ -307,7 +362,7 @@ cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int S, int Pcap, con
     ReadArgs a{L, B, Hkv, d, S, Pcap, pg.page_rows, pg.num_pages, pg.max_pages, pg.page_rows * pg.max_pages, pg.block_table, prefix_len,
                static_cast<const unsigned char*>(kp), static_cast<const unsigned char*>(vp), ks, vs, ko, vo, status};
     const int rows = kReadVecs * kThreads / (d / 16), most = Pcap < a.cap ? Pcap : a.cap;
-    const dim3 grid((most + rows - 1) / rows, 2 * Hkv, L * B);
+    const dim3 grid((most + kReadTurns * rows - 1) / (kReadTurns * rows), 2 * Hkv, L * B);
     if (out == DDT_BF16) k_read_quant<__nv_bfloat16><<<counted(grid), kThreads, 0, st>>>(a);
     else k_read_quant<float><<<counted(grid), kThreads, 0, st>>>(a);
     return cudaGetLastError();
