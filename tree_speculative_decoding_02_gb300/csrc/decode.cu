@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
 
 // ------------------------------------------------------------------------------ host
 constexpr int kTcMaxCtas = 512;  // two an SM, for up to 256 SMs
-constexpr int kQuantMaxCtas = 512;  // three an SM, for up to 170 SMs
+constexpr int kQuantMaxCtas = 640;  // four an SM, for up to 160 SMs
 static int simt_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -626,7 +626,7 @@ cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block,
                                 const int32_t* prefix_len, float scale, void* o, int32_t* status, void* ws, cudaStream_t st) {
     DecodeParams p = decode_params(L, B, Hq, Hkv, d, pg, out, q, k_new, v_new, k_pages, v_pages, prefix_len, scale, o, nullptr, status);
     const int sms = sm_count();
-    p.C = sms < kQuantMaxCtas / 3 ? sms : kQuantMaxCtas / 3;
+    p.C = sms < kQuantMaxCtas / 4 ? sms : kQuantMaxCtas / 4;
     decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, static_cast<unsigned char*>(ws));
     const cudaError_t e = launch_decode_quant_tiles(p, in, block, k_scale, v_scale, st);
     return e != cudaSuccess || p.cl ? e : finish_any(p, in, sms, st);

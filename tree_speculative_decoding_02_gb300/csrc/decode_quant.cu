@@ -42,8 +42,8 @@ constexpr float kTau = 4.f;   // and moves when a score is this much above it
 
 constexpr int pow2_at_least(int x, int y) { return x <= y ? y : pow2_at_least(x, 2 * y); }
 
-// HP: heads a block; QP, PP: parts of Q and of P
-template <int D, int HP, int QP, int PP>
+// HP: heads a block; GH: of the eight of a warpgroup, those that there are; QP, PP: parts of Q and of P
+template <int D, int HP, int GH, int QP, int PP>
 struct QuantCfg {
     static constexpr int kGroups = HP / 8;                // softmax warpgroups
     static constexpr int kThreads = 128 + 128 * kGroups;
@@ -52,7 +52,7 @@ struct QuantCfg {
     static constexpr int kStageBytes = kDecTile * D;      // a K or V tile
     static constexpr int NQ = QP * HP;                    // N of Q K^T
     static constexpr int NP = pow2_at_least(PP * HP, 32); // N of P V, and the bytes of a row of P
-    static constexpr int kCtas = QP == 6 ? (D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? 3 : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
+    static constexpr int kCtas = QP == 6 ? (D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? (GH < 8 ? 4 : 3) : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
     static constexpr int kQBufs = kCtas == 2 && D == 256 ? 1 : 2;
     static constexpr int kQBytes = NQ * D;
     static constexpr int kPBytes = NP * kDecTile;
@@ -99,11 +99,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[PARTS]) {
 
 }  // namespace
 
-template <typename Tin, int D, int HP, int QP, int PP>
-__global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D, HP, QP, PP>::kCtas)
+template <typename Tin, int D, int HP, int GH, int QP, int PP>
+__global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCfg<D, HP, GH, QP, PP>::kCtas)
     k_decode_quant(const DecodeParams p, const DecQuantArgs a, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
-    using Cfg = QuantCfg<D, HP, QP, PP>;
+    using Cfg = QuantCfg<D, HP, GH, QP, PP>;
     constexpr int kStages = Cfg::kStages, NQ = Cfg::NQ, NP = Cfg::NP, kMB = Cfg::kMB, kRow = Cfg::kRow, kQBufs = Cfg::kQBufs;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
         for (; w.left > 0; dec_next(p, w), ++seg) {
             const int h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
             int base = 127;  // V's scale of the segment's first row
-            float m[8], l[8];
+            float m[GH], l[GH];
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
+            for (int h = 0; h < GH; ++h) {
                 m[h] = kNoRef;
                 l[h] = 0.f;
             }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                 // a warp that gave up still takes part in the barriers
                 if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort) && tc::mbar_wait(x_full + (j & 3), (j >> 2) & 1, abort);
                 ok = __all_sync(kFull, ok);
-                float t[8], v_back = 1.f;
+                float t[GH], v_back = 1.f;
                 bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                     bad |= bad_tile[j & 7];
                     const float* unit = q_unit + (seg & 7) * HP + hg;
 #pragma unroll
-                    for (int h = 0; h < 8; ++h) {
+                    for (int h = 0; h < GH; ++h) {
                         float s = __uint_as_float(sr[QP - 1][h]);
 #pragma unroll
                         for (int x = QP - 2; x >= 0; --x) s = fmaf(s, 0.0625f, __uint_as_float(sr[x][h]));
@@ -390,17 +390,16 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                     float mine = -INFINITY;
                     if (ok)
 #pragma unroll
-                        for (int h = 0; h < 8; ++h)
-                            if (h < nh) {
-                                const float v = redux_max(t[h]);
-                                if (lane == h) mine = v;
-                            }
+                        for (int h = 0; h < GH; ++h) {
+                            const float v = redux_max(t[h]);
+                            if (lane == h) mine = v;
+                        }
                     if (lane < 8) x[ws * HP + lane] = mine;
                     tc::named_bar(bar, 128);
                     if (ok) {
-                        float f[8];
+                        float f[GH];
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
+                        for (int h = 0; h < GH; ++h) {
                             const float mt = fmaxf(fmaxf(x[h], x[HP + h]), fmaxf(x[2 * HP + h], x[3 * HP + h])) - kLift;
                             f[h] = 1.f;
                             if (mt > m[h] + kTau) {
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                                     tmem_ld8(at, o);
                                     tc::tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+                                    for (int e = 0; e < GH; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
                                     tmem_st8(at, o);
                                 }
                                 tc::tmem_wait_st();
@@ -432,9 +431,9 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                 // the P buffer is free once P V of tile j - 2 is done
                 ok = __all_sync(kFull, tc::mbar_wait(p_free + (j & 1), ((j >> 1) & 1) ^ 1, abort));
                 if (!ok) continue;
-                uint32_t c[4][PP];
+                uint32_t c[4][PP] = {};
 #pragma unroll
-                for (int h = 0; h < 8; h += 2) {
+                for (int h = 0; h < GH; h += 2) {
                     const float e0 = tc::ex2(t[h] - m[h]), e1 = tc::ex2(t[h + 1] - m[h + 1]);
                     l[h] = fmaf(e0, v_back, l[h]);
                     l[h + 1] = fmaf(e1, v_back, l[h + 1]);
@@ -471,12 +470,11 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
             // ---- the partial: sums through shared memory, O once the last P V is done
             float sum = 0.f, ref = 0.f;
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-                if (h < nh) {
-                    const float x = warp_sum(l[h]);
-                    if (lane == h) sum = x;
-                    if (r == h) ref = m[h];
-                }
+            for (int h = 0; h < GH; ++h) {
+                const float x = warp_sum(l[h]);
+                if (lane == h) sum = x;
+                if (r == h) ref = m[h];
+            }
             if (lane < 8) sm_l[ws * HP + hg + lane] = sum;
             if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
             ok = __all_sync(kFull, ok);
@@ -499,7 +497,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
                 if (D >= 128 || r < D) {
                     float* out = p.part_o + (slot * p.HT + hg) * D + mb * 128 + r;
 #pragma unroll
-                    for (int h = 0; h < 8; ++h)
+                    for (int h = 0; h < GH; ++h)
                         if (h < nh) {
                             float s = __uint_as_float(o[PP - 1][h]);
 #pragma unroll
@@ -528,10 +526,10 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, QP, PP>::kThreads, QuantCfg<D,
 // ------------------------------------------------------------------------------ host
 namespace {
 
-template <typename Tin, int D, int HP, int QP, int PP>
+template <typename Tin, int D, int HP, int GH, int QP, int PP>
 cudaError_t quant_go(DecodeParams& p, const DecQuantArgs& a, const CUtensorMap* maps, cudaStream_t st) {
-    using Cfg = QuantCfg<D, HP, QP, PP>;
-    const auto kernel = k_decode_quant<Tin, D, HP, QP, PP>;
+    using Cfg = QuantCfg<D, HP, GH, QP, PP>;
+    const auto kernel = k_decode_quant<Tin, D, HP, GH, QP, PP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
@@ -541,10 +539,12 @@ cudaError_t quant_go(DecodeParams& p, const DecQuantArgs& a, const CUtensorMap* 
 
 template <int D>
 cudaError_t quant_d_go(DecodeParams& p, ddt_dtype in, const DecQuantArgs& a, const CUtensorMap* maps, cudaStream_t st) {
-    if (in == DDT_F32) return quant_go<float, D, 8, 6, 6>(p, a, maps, st);
-    return p.hbs == 8    ? quant_go<__nv_bfloat16, D, 8, 2, 4>(p, a, maps, st)
-           : p.hbs == 16 ? quant_go<__nv_bfloat16, D, 16, 2, 4>(p, a, maps, st)
-                         : quant_go<__nv_bfloat16, D, 32, 2, 4>(p, a, maps, st);
+    if (in == DDT_F32) return quant_go<float, D, 8, 8, 6, 6>(p, a, maps, st);
+    return p.G <= 2      ? quant_go<__nv_bfloat16, D, 8, 2, 2, 4>(p, a, maps, st)
+           : p.G <= 4    ? quant_go<__nv_bfloat16, D, 8, 4, 2, 4>(p, a, maps, st)
+           : p.hbs == 8  ? quant_go<__nv_bfloat16, D, 8, 8, 2, 4>(p, a, maps, st)
+           : p.hbs == 16 ? quant_go<__nv_bfloat16, D, 16, 8, 2, 4>(p, a, maps, st)
+                         : quant_go<__nv_bfloat16, D, 32, 8, 2, 4>(p, a, maps, st);
 }
 
 }  // namespace

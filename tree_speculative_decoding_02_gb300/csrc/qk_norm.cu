@@ -99,7 +99,8 @@ __device__ __forceinline__ void store_run(T* p, const float (&v)[8]) {
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
     constexpr int LPR = D / 16, kRows = kThreads / LPR;  // lanes a row, rows at a time
-    __shared__ float2 s_cs[kMaxTokens * D / 2];
+    __shared__ __align__(16) float2 s_cs[kMaxTokens * D / 2];
+    __shared__ __align__(16) float s_w[2][D];  // offset + weight: of q, of k
     const int tid = threadIdx.x, half = a.rot / 2, heads = a.Hq + a.Hkv;
     const long long rows = (long long)a.B * a.N, first = (long long)blockIdx.x * a.tokens;
     const int l = blockIdx.y, nt = (int)min((long long)a.tokens, rows - first), items = nt * heads;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
     const int lo = turned ? 8 * c : 16 * c, hi = turned ? half + 8 * c : 16 * c + 8;
     const unsigned mask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);  // the lanes of a row, which agree throughout
 
-    // rows it and it + kRows: both are on their way before the first is worked on
+    // two rows are on their way while one is worked on
     Run<T, VEC> u[2], v[2];
     bool live[2];
     auto fetch = [&](int it, int s) {
@@ -138,30 +139,36 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
         sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &co);  // half turns: 2^-31
         s_cs[e] = make_float2(co, s);
     }
+    for (int e = tid; e < 2 * D; e += kThreads)
+        s_w[e / D][e % D] = a.offset + to_f32(static_cast<const T*>(e < D ? a.qw : a.kw)[(long long)l * D + e % D]);
     __syncthreads();
     for (int it = it0; it < items; it += 2 * kRows) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if (!live[s]) continue;
             const int i0 = it + s * kRows, t = i0 / heads, h = i0 - t * heads;
+            if (!live[s]) {
+                fetch(i0 + 2 * kRows, s);
+                continue;
+            }
             const bool isq = h < a.Hq;
             T* y = isq ? static_cast<T*>(a.qo) + ((l * rows + first + t) * a.Hq + h) * D
                        : static_cast<T*>(a.ko) + ((l * rows + first + t) * a.Hkv + (h - a.Hq)) * D;
-            const T* w = static_cast<const T*>(isq ? a.qw : a.kw) + (long long)l * D;
-            Run<T, VEC> wu, wv;
-            wu.load(w + lo);
-            wv.load(w + hi);
-            float ss = 0.f;
+            float p[8], q[8], ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(u[s][i], u[s][i], fmaf(v[s][i], v[s][i], ss));
+            for (int i = 0; i < 8; ++i) {
+                p[i] = u[s][i];
+                q[i] = v[s][i];
+                ss = fmaf(p[i], p[i], fmaf(q[i], q[i], ss));
+            }
+            fetch(i0 + 2 * kRows, s);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
             const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-            float p[8], q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = u[s][i] * r * (a.offset + wu[i]);
-                q[i] = v[s][i] * r * (a.offset + wv[i]);
+            for (int i = 0; i < 8; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(s_w[!isq] + lo + i), z = *reinterpret_cast<const float4*>(s_w[!isq] + hi + i);
+                p[i] *= r * x.x; p[i + 1] *= r * x.y; p[i + 2] *= r * x.z; p[i + 3] *= r * x.w;
+                q[i] *= r * z.x; q[i + 1] *= r * z.y; q[i + 2] *= r * z.z; q[i + 3] *= r * z.w;
             }
             if (turned) {
                 const float4* cs = reinterpret_cast<const float4*>(s_cs + t * half + 8 * c);
@@ -178,8 +185,6 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
             store_run<T, VEC>(y + lo, p);
             store_run<T, VEC>(y + hi, q);
         }
-        fetch(it + 2 * kRows, 0);
-        fetch(it + 3 * kRows, 1);
     }
 }
 
@@ -233,7 +238,7 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     a.tokens = 1;
-    while (a.tokens < kMaxTokens && a.tokens * (Hq + Hkv) * (d / 16) < kThreads && (long long)L * B * N >= 16LL * sms * a.tokens) a.tokens *= 2;
+    while (a.tokens < kMaxTokens && (long long)L * B * N >= 8LL * sms * a.tokens) a.tokens *= 2;
     return dtype == DDT_BF16 ? norm_d_go<__nv_bfloat16>(L, d, a, fr, (bits & 15) == 0, st) : norm_d_go<float>(L, d, a, fr, (bits & 15) == 0, st);
 }
 

@@ -26,7 +26,7 @@ constexpr int kChunk = 8;  // vectors of 8 channels a lane has in flight
 struct AppendArgs {
     int L, B, N, A, Hkv, d, S;
     int page_rows, num_pages, max_pages, cap;
-    int wpi, iters;   // warps an item (a block's K or V rows of one head), vectors a lane of it
+    int wpi;          // warps an item (a block's K or V rows of one head)
     int run;          // blocks a CTA
     int advance, solo;  // solo: one CTA has all of a request
     int checked;      // the status is there already
@@ -55,6 +55,16 @@ struct Vec8 {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = make_uint4(0, 0, 0, 0);
     }
+    // the largest |x| as bits, of bf16 vectors in halves of 16 bits (integers order as the values do)
+    __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = sizeof(T) == 4 ? max(m, x[k] & 0x7fffffffu) : __vmaxu2(m, x[k] & 0x7fff7fffu);
+        }
+        return m;
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
@@ -72,14 +82,11 @@ struct Vec8 {
     }
 };
 
-// what is not finite becomes NaN, the rest is scaled
-__device__ __forceinline__ float scaled(float x, float inv) { return fmaf(x, 0.f, x) * inv; }
-
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(scaled(v[2 * i], inv), scaled(v[2 * i + 1], inv));
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 }  // namespace
@@ -110,8 +117,8 @@ __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
 }
 
 // grid (runs of blocks, item groups, L * B).  A CTA takes a few blocks of one request and layer, one after
-// another; wpi of its warps an item.  A lane has up to kChunk vectors of the item's rows in registers, so they
-// are read once (a block of 128 rows of 256 channels twice).
+// another; wpi of its warps an item.  Up to kChunk vectors a lane stay in registers between the maximum and the
+// codes; items of more (blocks of 128 rows of 256 channels) are read twice.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
     __shared__ float s_max[2][kWarps];
@@ -119,32 +126,38 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
     const int b = blockIdx.z % a.B, l = blockIdx.z / a.B;
     if (a.checked) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int P = a.prefix_len[b], n = a.count[b];
+    int first = P / a.S + blockIdx.x * a.run;  // block
+    // a CTA without rows: none, or none so far behind the prefix (which is for others to judge)
+    if ((blockIdx.x > 0 || blockIdx.y > 0 || l > 0) && (n <= 0 || (long long)first * a.S >= (long long)P + n)) return;
     const int err = a.checked ? a.status[b] : append_check(a, b, P, n);
     if (!a.checked && l == 0 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
         a.status[b] = err;
         if (a.solo && a.advance && !err) a.prefix_len[b] = P + n;
     }
-    if (err || n == 0) return;
+    if (err) return;
     const int32_t* table = a.table + (long long)b * a.max_pages;
     const int item = blockIdx.y * (kWarps / a.wpi) + warp / a.wpi, part = warp % a.wpi;
     const bool real = item < 2 * a.Hkv;
     const int isv = item & 1, g = min(item >> 1, a.Hkv - 1);
     const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * a.d + (long long)g * a.d;
     const long long pitch = (long long)a.Hkv * a.d;
-    // vector e of the item: 8 channels of row e / (d / 8) of the block
-    const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5), e0 = part * a.iters * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
+    // vector e of the item: 8 channels of its row e / (d / 8); a lane's are the same ones of every row
+    const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5), step = a.wpi * 32, e0 = part * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
 
-    int first = P / a.S + blockIdx.x * a.run;
     for (int turn = 0; turn < a.run && (long long)first * a.S < (long long)P + n; ++turn, ++first) {
         const int r0 = first * a.S, lo = max(P - r0, 0), hi = min(P + n - r0, a.S);  // new rows [lo, hi) of the block
         const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows, phys = table[lp];
+        const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
+        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
+        unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
+        const int old = real && lo > 0 ? *byte : 0;
+        const int count = (hi - lo) << shift;  // the item's vectors
         Vec8<T> x[kChunk];
-        auto load = [&](int it0) {
+        auto load = [&](int e) {  // vectors e, e + step, ..
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) {
-                const int r = (e0 + (it0 + i) * 32) >> shift;
-                if (real && it0 + i < a.iters && r >= lo && r < hi) {
-                    const int j = r0 + r - P;
+                if (real && e + i * step < count) {
+                    const int j = r0 + lo + ((e + i * step) >> shift) - P;
                     const long long row = a.node ? a.node[(long long)b * a.A + j] : j;
                     x[i].load(src + row * pitch + ch);
                 } else {
@@ -152,25 +165,30 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
                 }
             }
         };
-        float m = 0.f;
-        for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
-            load(it0);
+        uint32_t most = 0;
+        for (int e = e0; e < count; e += kChunk * step) {
+            load(e);
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                float v[8];
-                x[i].get(v);
+            for (int i = 0; i < kChunk; ++i) most = x[i].top(most);
+        }
+        if (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
+        most = __reduce_max_sync(kFull, most);
+        float m = __uint_as_float(most);
+        const bool finite = most < 0x7f800000u;
+        if (!finite) {  // infinities or NaN: the largest of the others
+            m = 0.f;
+            for (int e = e0; e - lane < count; e += kChunk * step) {
+                load(e);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float y = fabsf(v[c]);
-                    m = fmaxf(m, y < INFINITY ? y : 0.f);
+                for (int i = 0; i < kChunk; ++i) {
+                    float v[8];
+                    x[i].get(v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) m = fabsf(v[c]) < INFINITY ? fmaxf(m, fabsf(v[c])) : m;
                 }
             }
+            m = warp_max(m);
         }
-        const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
-        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
-        unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
-        const int old = real && lo > 0 ? *byte : 0;
-        m = warp_max(m);
         if (a.wpi > 1) {
             if (lane == 0) s_max[turn & 1][warp] = m;
             __syncthreads();
@@ -180,17 +198,18 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
         const int now = max(old, scale_byte(m));
         if (part == 0 && lane == 0) *byte = (unsigned char)now;
         const float inv = now ? scale_of(254 - now) : 0.f;
-        for (int it0 = 0; it0 < a.iters; it0 += kChunk) {
-            if (a.iters > kChunk) load(it0);
+        for (int e = e0; e < count; e += kChunk * step) {
+            if (count > kChunk * step || !finite) load(e);
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                const int r = (e0 + (it0 + i) * 32) >> shift;
-                if (it0 + i < a.iters && r >= lo && r < hi) {
+            for (int i = 0; i < kChunk; ++i)
+                if (e + i * step < count) {
                     float v[8];
                     x[i].get(v);
-                    *reinterpret_cast<uint2*>(page + (long long)r * a.d + ch) = codes8(v, inv);
+                    if (!finite)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) v[c] = fmaf(v[c], 0.f, v[c]);  // an infinity becomes NaN
+                    *reinterpret_cast<uint2*>(page + (long long)(lo + ((e + i * step) >> shift)) * a.d + ch) = codes8(v, inv);
                 }
-            }
         }
         if (old && now > old) {  // the rows that the block had, under its new scale
             const float f = scale_of(max(127 + old - now, 0));
@@ -242,10 +261,9 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     a.ks = ks;
     a.vs = vs;
     a.status = status;
-    const int vectors = S * d / 256;  // a lane of one warp has this many of an item
+    const int vectors = (S < A ? S : A) * d / 256;  // a lane of one warp has this many of an item at most
     a.wpi = 1;
     while (a.wpi < kWarps && vectors > kChunk * a.wpi) a.wpi *= 2;
-    a.iters = (vectors + a.wpi - 1) / a.wpi;
     const int blocks = (int)(((long long)A + S - 2) / S + 1);  // that a request's rows may fall into
     const int per = kWarps / a.wpi, groups = (2 * Hkv + per - 1) / per;
     a.solo = L == 1 && blocks == 1 && groups == 1;
@@ -287,14 +305,14 @@ struct ReadArgs {
     void* ko;
     void* vo;
     int32_t* status;
+    int turns;
 };
 constexpr int kReadVecs = 4;   // 16 codes each, in flight a thread
-constexpr int kReadTurns = 4;  // such steps a CTA
 }  // namespace
 
-// grid (row chunks, 2 * Hkv, L * B): kReadTurns steps of kReadVecs * kThreads * 16 codes of one head's K or V
-// a CTA.  (The grid goes by the table's rows; CTAs behind a request's own take a few hundred cycles each, which
-// larger ones make rarer.)
+// grid (row chunks, 2 * Hkv, L * B): `turns` steps of kReadVecs * kThreads * 16 codes of one head's K or V a CTA.
+// (The grid goes by the table's rows; CTAs behind a request's own take a few hundred cycles each, which larger ones
+// make rarer.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
     const int tid = threadIdx.x, b = blockIdx.z % a.B, l = blockIdx.z / a.B, g = blockIdx.y >> 1, isv = blockIdx.y & 1;
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
     const unsigned char* pages = isv ? a.vp : a.kp;
     const unsigned char* scales = isv ? a.vs : a.ks;
     T* out = static_cast<T*>(isv ? a.vo : a.ko) + (((long long)l * a.B + b) * a.Hkv + g) * (long long)a.Pcap * a.d;
-    for (int y0 = blockIdx.x * kReadTurns * rows, turn = 0; turn < kReadTurns && y0 < P; ++turn, y0 += rows) {
+    for (int y0 = blockIdx.x * a.turns * rows, turn = 0; turn < a.turns && y0 < P; ++turn, y0 += rows) {
         uint4 c[kReadVecs];
         float f[kReadVecs];
         bool there[kReadVecs];
@@ -362,7 +380,9 @@ cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int S, int Pcap, con
     ReadArgs a{L, B, Hkv, d, S, Pcap, pg.page_rows, pg.num_pages, pg.max_pages, pg.page_rows * pg.max_pages, pg.block_table, prefix_len,
                static_cast<const unsigned char*>(kp), static_cast<const unsigned char*>(vp), ks, vs, ko, vo, status};
     const int rows = kReadVecs * kThreads / (d / 16), most = Pcap < a.cap ? Pcap : a.cap;
-    const dim3 grid((most + kReadTurns * rows - 1) / (kReadTurns * rows), 2 * Hkv, L * B);
+    const long long steps = (most + rows - 1) / rows;
+    a.turns = steps * 2 * Hkv * L * B > 16384 ? 4 : 1;  // 20 or more an SM's resident CTA
+    const dim3 grid((unsigned)((steps + a.turns - 1) / a.turns), 2 * Hkv, L * B);
     if (out == DDT_BF16) k_read_quant<__nv_bfloat16><<<counted(grid), kThreads, 0, st>>>(a);
     else k_read_quant<float><<<counted(grid), kThreads, 0, st>>>(a);
     return cudaGetLastError();
