@@ -31,6 +31,7 @@ struct NormFreq {
 
 struct NormArgs {
     int B, N, Hq, Hkv, rot, tokens;  // tokens a CTA
+    int dt, dh;                      // the rows that a CTA takes at a time, as tokens and heads
     float eps, offset;
     long long qs[4], ks[4];  // strides of the inputs in elements: layer, request, row, head
     const void* q;
@@ -97,62 +98,85 @@ __device__ __forceinline__ void store_run(T* p, const float (&v)[8]) {
 }  // namespace
 
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
-    constexpr int LPR = D / 16, kRows = kThreads / LPR;  // lanes a row, rows at a time
-    __shared__ __align__(16) float2 s_cs[kMaxTokens * D / 2];
-    __shared__ __align__(16) float s_w[2][D];  // offset + weight: of q, of k
-    const int tid = threadIdx.x, half = a.rot / 2, heads = a.Hq + a.Hkv;
-    const long long rows = (long long)a.B * a.N, first = (long long)blockIdx.x * a.tokens;
-    const int l = blockIdx.y, nt = (int)min((long long)a.tokens, rows - first), items = nt * heads;
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
+    constexpr int LPR = D / 16;  // lanes a row
+    // four float4 a lane, lane after lane: a quarter warp reads 128 consecutive bytes
+    __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16] pairs (cos, sin)
+    __shared__ float4 s_w[2][4 * LPR];           // offset + weight: of q, of k
+    __shared__ long long s_at[kMaxTokens][2];    // a token's place in q and in k, or -1
+    const int tid = threadIdx.x, half = a.rot / 2, lanes = a.rot / 16, heads = a.Hq + a.Hkv;
+    const unsigned rows = (unsigned)a.B * (unsigned)a.N, first = blockIdx.x * (unsigned)a.tokens;  // (fewer than 2^31)
+    const int l = blockIdx.y, nt = (int)min((unsigned)a.tokens, rows - first);
     const int c = tid % LPR;
     // this lane's two runs: of the rotated channels the halves of its pairs, of the others neighbours
-    const bool turned = 16 * c < a.rot;
+    const bool turned = c < lanes;
     const int lo = turned ? 8 * c : 16 * c, hi = turned ? half + 8 * c : 16 * c + 8;
     const unsigned mask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);  // the lanes of a row, which agree throughout
 
-    // two rows are on their way while one is worked on
-    Run<T, VEC> u[2], v[2];
-    bool live[2];
-    auto fetch = [&](int it, int s) {
-        live[s] = false;
-        if (it >= items) return;
-        const int t = it / heads, h = it - t * heads;
-        const long long tok = first + t;
-        const int b = (int)(tok / a.N), n = (int)(tok - (long long)b * a.N);
-        if (a.n_nodes) {
-            const int nn = a.n_nodes[b];
-            if (n >= nn || nn > a.N) return;
-        }
-        live[s] = true;
-        const T* x = h < a.Hq ? static_cast<const T*>(a.q) + l * a.qs[0] + b * a.qs[1] + n * a.qs[2] + h * a.qs[3]
-                              : static_cast<const T*>(a.k) + l * a.ks[0] + b * a.ks[1] + n * a.ks[2] + (h - a.Hq) * a.ks[3];
-        u[s].load(x + lo);
-        v[s].load(x + hi);
+    if (tid < nt) {
+        const unsigned tok = first + tid, b = tok / (unsigned)a.N, n = tok - b * (unsigned)a.N;
+        const int nn = a.n_nodes ? a.n_nodes[b] : a.N;
+        const bool live = (int)n < nn && nn <= a.N;
+        s_at[tid][0] = live ? l * a.qs[0] + b * a.qs[1] + n * a.qs[2] : -1;
+        s_at[tid][1] = l * a.ks[0] + b * a.ks[1] + n * a.ks[2];
+    }
+    __syncthreads();
+    // a lane group's rows, kThreads / LPR apart: head h of token t
+    struct Item {
+        int t, h;
     };
-    const int it0 = tid / LPR;
-    fetch(it0, 0);
-    fetch(it0 + kRows, 1);
+    auto next = [&](Item x) {
+        x.t += a.dt;
+        x.h += a.dh;
+        if (x.h >= heads) {
+            x.h -= heads;
+            ++x.t;
+        }
+        return x;
+    };
+    Item now{tid / LPR / heads, tid / LPR % heads}, ahead = now;
+    Run<T, VEC> u[2], v[2];  // two rows are on their way while one is worked on
+    bool live[2];
+    auto fetch = [&](int s) {
+        live[s] = false;
+        if (ahead.t < nt) {
+            const long long at = s_at[ahead.t][0];
+            if (at >= 0) {
+                live[s] = true;
+                const T* x = ahead.h < a.Hq ? static_cast<const T*>(a.q) + at + ahead.h * a.qs[3]
+                                            : static_cast<const T*>(a.k) + s_at[ahead.t][1] + (ahead.h - a.Hq) * a.ks[3];
+                u[s].load(x + lo);
+                v[s].load(x + hi);
+            }
+        }
+        ahead = next(ahead);
+    };
+    fetch(0);
+    fetch(1);
     for (int e = tid; e < nt * half; e += kThreads) {
         const int t = e / half, i = e - t * half;
         const unsigned long long turn = (unsigned long long)(long long)a.position[first + t] * fr.f[i];
         float s, co;
         sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &co);  // half turns: 2^-31
-        s_cs[e] = make_float2(co, s);
+        reinterpret_cast<float2*>(s_cs)[((t * 4 + i % 8 / 2) * lanes + i / 8) * 2 + i % 2] = make_float2(co, s);
     }
-    for (int e = tid; e < 2 * D; e += kThreads)
-        s_w[e / D][e % D] = a.offset + to_f32(static_cast<const T*>(e < D ? a.qw : a.kw)[(long long)l * D + e % D]);
+    for (int e = tid; e < 2 * D; e += kThreads) {
+        // channel ch is the j-th of its lane: of the low run 0..7, of the high one 8..15
+        const int x = e / D, ch = e % D, k = ch < half ? ch / 8 : (ch < a.rot ? (ch - half) / 8 : ch / 16);
+        const int j = ch < half ? ch % 8 : (ch < a.rot ? 8 + (ch - half) % 8 : ch % 16);
+        reinterpret_cast<float*>(s_w[x])[(j / 4 * LPR + k) * 4 + j % 4] =
+            a.offset + to_f32(static_cast<const T*>(x ? a.kw : a.qw)[(long long)l * D + ch]);
+    }
     __syncthreads();
-    for (int it = it0; it < items; it += 2 * kRows) {
+    while (now.t < nt) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int i0 = it + s * kRows, t = i0 / heads, h = i0 - t * heads;
+            const Item at = now;
+            now = next(now);
             if (!live[s]) {
-                fetch(i0 + 2 * kRows, s);
+                fetch(s);
                 continue;
             }
-            const bool isq = h < a.Hq;
-            T* y = isq ? static_cast<T*>(a.qo) + ((l * rows + first + t) * a.Hq + h) * D
-                       : static_cast<T*>(a.ko) + ((l * rows + first + t) * a.Hkv + (h - a.Hq)) * D;
             float p[8], q[8], ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -160,21 +184,23 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
                 q[i] = v[s][i];
                 ss = fmaf(p[i], p[i], fmaf(q[i], q[i], ss));
             }
-            fetch(i0 + 2 * kRows, s);
+            fetch(s);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
             const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+            const bool isq = at.h < a.Hq;
+            const float4* w = s_w[!isq] + c;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(s_w[!isq] + lo + i), z = *reinterpret_cast<const float4*>(s_w[!isq] + hi + i);
-                p[i] *= r * x.x; p[i + 1] *= r * x.y; p[i + 2] *= r * x.z; p[i + 3] *= r * x.w;
-                q[i] *= r * z.x; q[i + 1] *= r * z.y; q[i + 2] *= r * z.z; q[i + 3] *= r * z.w;
+            for (int i = 0; i < 2; ++i) {
+                const float4 x = w[i * LPR], z = w[(2 + i) * LPR];
+                p[4 * i] *= r * x.x; p[4 * i + 1] *= r * x.y; p[4 * i + 2] *= r * x.z; p[4 * i + 3] *= r * x.w;
+                q[4 * i] *= r * z.x; q[4 * i + 1] *= r * z.y; q[4 * i + 2] *= r * z.z; q[4 * i + 3] *= r * z.w;
             }
             if (turned) {
-                const float4* cs = reinterpret_cast<const float4*>(s_cs + t * half + 8 * c);
+                const float4* cs = s_cs + at.t * 4 * lanes + c;
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    const float4 k = cs[i / 2];
+                    const float4 k = cs[i / 2 * lanes];
                     const float p0 = p[i], p1 = p[i + 1];
                     p[i] = fmaf(p0, k.x, -q[i] * k.y);
                     q[i] = fmaf(q[i], k.x, p0 * k.y);
@@ -182,6 +208,8 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const NormArgs a, con
                     q[i + 1] = fmaf(q[i + 1], k.z, p1 * k.w);
                 }
             }
+            const long long row = (long long)l * rows + first + at.t;
+            T* y = isq ? static_cast<T*>(a.qo) + (row * a.Hq + at.h) * D : static_cast<T*>(a.ko) + (row * a.Hkv + (at.h - a.Hq)) * D;
             store_run<T, VEC>(y + lo, p);
             store_run<T, VEC>(y + hi, q);
         }
@@ -238,7 +266,9 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     a.tokens = 1;
-    while (a.tokens < kMaxTokens && (long long)L * B * N >= 8LL * sms * a.tokens) a.tokens *= 2;
+    while (a.tokens < kMaxTokens && (long long)L * B * N >= 16LL * sms * a.tokens) a.tokens *= 2;
+    a.dt = kThreads / (d / 16) / (Hq + Hkv);
+    a.dh = kThreads / (d / 16) % (Hq + Hkv);
     return dtype == DDT_BF16 ? norm_d_go<__nv_bfloat16>(L, d, a, fr, (bits & 15) == 0, st) : norm_d_go<float>(L, d, a, fr, (bits & 15) == 0, st);
 }
 

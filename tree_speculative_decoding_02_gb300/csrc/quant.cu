@@ -27,7 +27,7 @@ struct AppendArgs {
     int L, B, N, A, Hkv, d, S;
     int page_rows, num_pages, max_pages, cap;
     int wpi;          // warps an item (a block's K or V rows of one head)
-    int run;          // blocks a CTA
+    int run, groups;  // blocks a CTA; CTAs that share a block's items
     int advance, solo;  // solo: one CTA has all of a request
     int checked;      // the status is there already
     const void* k;
@@ -65,29 +65,31 @@ struct Vec8 {
         }
         return m;
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (sizeof(T) == 4) {
-                    v[4 * i + k] = __uint_as_float(x[k]);
-                } else {
-                    v[2 * k] = __uint_as_float(x[k] << 16);
-                    v[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
-                }
-            }
+    __device__ __forceinline__ float get(int i) const {
+        if (sizeof(T) == 4) {
+            const uint4& x = w[i / 4 % (sizeof(T) / 2)];
+            return __uint_as_float(i % 4 == 0 ? x.x : (i % 4 == 1 ? x.y : (i % 4 == 2 ? x.z : x.w)));
         }
+        const uint32_t x = i / 2 == 0 ? w[0].x : (i / 2 == 1 ? w[0].y : (i / 2 == 2 ? w[0].z : w[0].w));
+        return __uint_as_float(i % 2 ? x & 0xffff0000u : x << 16);
+    }
+    __device__ __forceinline__ uint2 codes(float inv) const {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = e4m3x2(get(2 * i) * inv, get(2 * i + 1) * inv);
+        return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    }
+    // the same where an infinity may be among them: it becomes NaN
+    __device__ __forceinline__ uint2 codes_any(float inv) const {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = get(2 * i), y = get(2 * i + 1);
+            c[i] = e4m3x2(fmaf(x, 0.f, x) * inv, fmaf(y, 0.f, y) * inv);
+        }
+        return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
     }
 };
-
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
-}
 
 }  // namespace
 
@@ -116,53 +118,46 @@ __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
     if (threadIdx.x == 0) a.status[b] = err;
 }
 
-// grid (runs of blocks, item groups, L * B).  A CTA takes a few blocks of one request and layer, one after
+// grid (runs of blocks x item groups, 1, L * B).  A CTA takes a few blocks of one request and layer, one after
 // another; wpi of its warps an item.  Up to kChunk vectors a lane stay in registers between the maximum and the
 // codes; items of more (blocks of 128 rows of 256 channels) are read twice.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_quant(const AppendArgs a) {
     __shared__ float s_max[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.z % a.B, l = blockIdx.z / a.B;
+    const int b = blockIdx.z % a.B, l = blockIdx.z / a.B, group = blockIdx.x % a.groups;
     if (a.checked) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int P = a.prefix_len[b], n = a.count[b];
-    int first = P / a.S + blockIdx.x * a.run;  // block
+    int first = P / a.S + blockIdx.x / a.groups * a.run;  // block
     // a CTA without rows: none, or none so far behind the prefix (which is for others to judge)
-    if ((blockIdx.x > 0 || blockIdx.y > 0 || l > 0) && (n <= 0 || (long long)first * a.S >= (long long)P + n)) return;
+    if ((blockIdx.x > 0 || l > 0) && (n <= 0 || (long long)first * a.S >= (long long)P + n)) return;
     const int err = a.checked ? a.status[b] : append_check(a, b, P, n);
-    if (!a.checked && l == 0 && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    if (!a.checked && l == 0 && blockIdx.x == 0 && tid == 0) {
         a.status[b] = err;
         if (a.solo && a.advance && !err) a.prefix_len[b] = P + n;
     }
     if (err) return;
     const int32_t* table = a.table + (long long)b * a.max_pages;
-    const int item = blockIdx.y * (kWarps / a.wpi) + warp / a.wpi, part = warp % a.wpi;
+    const int item = group * (kWarps / a.wpi) + warp / a.wpi, part = warp % a.wpi;
     const bool real = item < 2 * a.Hkv;
     const int isv = item & 1, g = min(item >> 1, a.Hkv - 1);
-    const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * a.d + (long long)g * a.d;
-    const long long pitch = (long long)a.Hkv * a.d;
     // vector e of the item: 8 channels of its row e / (d / 8); a lane's are the same ones of every row
     const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5), step = a.wpi * 32, e0 = part * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
+    const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * a.d + (long long)g * a.d + ch;
+    const int pitch = a.Hkv * a.d;  // (below 2^23)
 
     for (int turn = 0; turn < a.run && (long long)first * a.S < (long long)P + n; ++turn, ++first) {
         const int r0 = first * a.S, lo = max(P - r0, 0), hi = min(P + n - r0, a.S);  // new rows [lo, hi) of the block
-        const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows, phys = table[lp];
-        const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
-        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
-        unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
-        const int old = real && lo > 0 ? *byte : 0;
-        const int count = (hi - lo) << shift;  // the item's vectors
+        const int count = real ? (hi - lo) << shift : 0;  // the item's vectors
         Vec8<T> x[kChunk];
         auto load = [&](int e) {  // vectors e, e + step, ..
+            const int j = r0 + lo - P + (e >> shift);
+            const T* at = src + (long long)j * pitch;
+            const int32_t* node = a.node + (long long)b * a.A + j;
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) {
-                if (real && e + i * step < count) {
-                    const int j = r0 + lo + ((e + i * step) >> shift) - P;
-                    const long long row = a.node ? a.node[(long long)b * a.A + j] : j;
-                    x[i].load(src + row * pitch + ch);
-                } else {
-                    x[i].zero();
-                }
+                x[i].zero();
+                if (e + i * step < count) x[i].load(a.node ? src + (long long)node[i * (step >> shift)] * pitch : at + (long long)(i * (step >> shift)) * pitch);
             }
         };
         uint32_t most = 0;
@@ -171,22 +166,25 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) most = x[i].top(most);
         }
+        const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows;
+        const long long plane = ((long long)l * a.num_pages + table[lp]) * a.Hkv + g;
+        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
+        unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
+        const int old = real && lo > 0 ? *byte : 0;
         if (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
         most = __reduce_max_sync(kFull, most);
         float m = __uint_as_float(most);
         const bool finite = most < 0x7f800000u;
         if (!finite) {  // infinities or NaN: the largest of the others
             m = 0.f;
-            for (int e = e0; e - lane < count; e += kChunk * step) {
+            for (int e = e0; e < count; e += kChunk * step) {
                 load(e);
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) {
-                    float v[8];
-                    x[i].get(v);
+                for (int i = 0; i < kChunk; ++i)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) m = fabsf(v[c]) < INFINITY ? fmaxf(m, fabsf(v[c])) : m;
-                }
+                    for (int k = 0; k < 8; ++k) m = fabsf(x[i].get(k)) < INFINITY ? fmaxf(m, fabsf(x[i].get(k))) : m;
             }
+            __syncwarp();
             m = warp_max(m);
         }
         if (a.wpi > 1) {
@@ -199,22 +197,17 @@ __global__ void __launch_bounds__(kThreads) k_append_quant(const AppendArgs a) {
         if (part == 0 && lane == 0) *byte = (unsigned char)now;
         const float inv = now ? scale_of(254 - now) : 0.f;
         for (int e = e0; e < count; e += kChunk * step) {
-            if (count > kChunk * step || !finite) load(e);
+            if (count > kChunk * step) load(e);
+            unsigned char* to = page + (lo * a.d + (e >> shift) * a.d + ch);
+            const int rows = (step >> shift) * a.d;
 #pragma unroll
             for (int i = 0; i < kChunk; ++i)
-                if (e + i * step < count) {
-                    float v[8];
-                    x[i].get(v);
-                    if (!finite)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = fmaf(v[c], 0.f, v[c]);  // an infinity becomes NaN
-                    *reinterpret_cast<uint2*>(page + (long long)(lo + ((e + i * step) >> shift)) * a.d + ch) = codes8(v, inv);
-                }
+                if (e + i * step < count) *reinterpret_cast<uint2*>(to + i * rows) = finite ? x[i].codes(inv) : x[i].codes_any(inv);
         }
         if (old && now > old) {  // the rows that the block had, under its new scale
             const float f = scale_of(max(127 + old - now, 0));
             for (int e = part * 32 + lane; e < lo << shift; e += a.wpi * 32) {
-                uint2* at = reinterpret_cast<uint2*>(page + (long long)e * 8);
+                uint2* at = reinterpret_cast<uint2*>(page + e * 8);
                 const uint2 c = *at;
                 float v[8];
                 values8(c, v);
@@ -265,8 +258,9 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     a.wpi = 1;
     while (a.wpi < kWarps && vectors > kChunk * a.wpi) a.wpi *= 2;
     const int blocks = (int)(((long long)A + S - 2) / S + 1);  // that a request's rows may fall into
-    const int per = kWarps / a.wpi, groups = (2 * Hkv + per - 1) / per;
-    a.solo = L == 1 && blocks == 1 && groups == 1;
+    const int per = kWarps / a.wpi;
+    a.groups = (2 * Hkv + per - 1) / per;
+    a.solo = L == 1 && blocks == 1 && a.groups == 1;
     a.run = blocks > 64 ? 4 : 1;
     a.checked = (A + pg.page_rows - 1) / pg.page_rows > kThreads;
     if (a.checked) {
@@ -278,7 +272,7 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = counted(dim3((blocks + a.run - 1) / a.run, groups, L * B));
+    cfg.gridDim = counted(dim3((unsigned)((long long)(blocks + a.run - 1) / a.run * a.groups), 1, L * B));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cfg.attrs = &at;
