@@ -265,8 +265,18 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
     for (int i = 0; i < rot / 2; ++i) fr.f[i] = (unsigned long long)(near[i % 16] * far[i / 16]);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    a.tokens = 1;
-    while (a.tokens < kMaxTokens && (long long)L * B * N >= 16LL * sms * a.tokens) a.tokens *= 2;
+    // tokens a CTA: the fewest steps in all, a CTA's start counted as two (rounds of the resident CTAs, and how
+    // full a CTA's last step is)
+    const int at_once = kThreads / (d / 16), resident = (dtype == DDT_BF16 ? 4 : 3) * sms;
+    long long best = 0;
+    for (int t = 1; t <= kMaxTokens; ++t) {
+        const long long ctas = ((long long)B * N + t - 1) / t * L;
+        const long long steps = (ctas + resident - 1) / resident * (2 + ((long long)t * (Hq + Hkv) + at_once - 1) / at_once);
+        if (t == 1 || steps < best) {
+            best = steps;
+            a.tokens = t;
+        }
+    }
     a.dt = kThreads / (d / 16) / (Hq + Hkv);
     a.dh = kThreads / (d / 16) % (Hq + Hkv);
     return dtype == DDT_BF16 ? norm_d_go<__nv_bfloat16>(L, d, a, fr, (bits & 15) == 0, st) : norm_d_go<float>(L, d, a, fr, (bits & 15) == 0, st);

@@ -114,6 +114,7 @@ __device__ __forceinline__ int append_check(const AppendArgs& a, int b, int P, i
 
 // grid B: the check by itself, where every CTA of the next kernel would look at many pages
 __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.x, err = append_check(a, b, a.prefix_len[b], a.count[b]);
     if (threadIdx.x == 0) a.status[b] = err;
 }
@@ -126,12 +127,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
     __shared__ float s_max[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.z % a.B, l = blockIdx.z / a.B, group = blockIdx.x % a.groups;
-    if (a.checked) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_append_advance may be set up
     const int P = a.prefix_len[b], n = a.count[b];
     int first = P / a.S + blockIdx.x / a.groups * a.run;  // block
     // a CTA without rows: none, or none so far behind the prefix (which is for others to judge)
     if ((blockIdx.x > 0 || l > 0) && (n <= 0 || (long long)first * a.S >= (long long)P + n)) return;
-    const int err = a.checked ? a.status[b] : append_check(a, b, P, n);
+    // (checked: the rows are read beside that kernel, and its verdict awaited before anything is written; the first CTA
+    // of a request awaits it in any case, so that this kernel does not end before it)
+    const bool sound = P >= 0 && P <= a.cap && n > 0 && n <= a.A && n <= a.cap - P;
+    if (a.checked && !sound) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int err = a.checked ? DDT_OK : append_check(a, b, P, n);
     if (!a.checked && l == 0 && blockIdx.x == 0 && tid == 0) {
         a.status[b] = err;
         if (a.solo && a.advance && !err) a.prefix_len[b] = P + n;
@@ -165,6 +173,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
             load(e);
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) most = x[i].top(most);
+        }
+        if (a.checked && turn == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (*static_cast<volatile int32_t*>(a.status + b) != DDT_OK) return;
         }
         const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows;
         const long long plane = ((long long)l * a.num_pages + table[lp]) * a.Hkv + g;
@@ -256,7 +268,9 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     a.status = status;
     const int vectors = (S < A ? S : A) * d / 256;  // a lane of one warp has this many of an item at most
     a.wpi = 1;
-    while (a.wpi < kWarps && vectors > kChunk * a.wpi) a.wpi *= 2;
+    // (a few rows of many requests: one warp, which reads up to 16 vectors twice, from L1 the second time)
+    const bool few = A <= 32 && (long)L * B * Hkv >= 1024;
+    while (a.wpi < kWarps && vectors > (few ? 2 : 1) * kChunk * a.wpi) a.wpi *= 2;
     const int blocks = (int)(((long long)A + S - 2) / S + 1);  // that a request's rows may fall into
     const int per = kWarps / a.wpi;
     a.groups = (2 * Hkv + per - 1) / per;
@@ -333,6 +347,8 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
         for (int i = 0; i < kReadVecs; ++i) {
             const int e = tid + i * kThreads, y = y0 + e / vpr;
             there[i] = y < P;
+            c[i] = make_uint4(0, 0, 0, 0);
+            f[i] = 0.f;
             if (!there[i]) continue;
             const int lp = y / a.page_rows, phys = table[lp], r = y - lp * a.page_rows;
             there[i] = phys >= 0 && phys < a.num_pages;
@@ -343,26 +359,52 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < kReadVecs; ++i) {
-            if (!there[i]) continue;
-            const int e = tid + i * kThreads;
-            T* to = out + (long long)(y0 + e / vpr) * a.d + e % vpr * 16;
-            float v[16];
-            values8(make_uint2(c[i].x, c[i].y), v);
-            values8(make_uint2(c[i].z, c[i].w), v + 8);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] *= f[i];
-            if (sizeof(T) == 2) {
-                uint32_t w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                    w[k] = *reinterpret_cast<const uint32_t*>(&z);
-                }
-                reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            // Lanes in twos (fp32: fours), which share a row, exchange words so that each store of theirs fills 32 (64)
+            // consecutive bytes: word w of lane x goes to lane w, as its word x.
+            constexpr int X = sizeof(T) / 2;  // 16 bytes of output a word of X, in 8 / X codes
+            uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            const int me = tid & (2 * X - 1);
+            if constexpr (X == 1) {  // words of 8 codes: (w0 w1), (w2 w3)
+                const uint32_t s0 = me ? w[0] : w[2], s1 = me ? w[1] : w[3];
+                const uint32_t r0 = __shfl_xor_sync(kFull, s0, 1), r1 = __shfl_xor_sync(kFull, s1, 1);
+                if (me) w[0] = r0, w[1] = r1;
+                else w[2] = r0, w[3] = r1;
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(to)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                for (int k = 0; k < 4; k += 2) {
+                    const uint32_t r = __shfl_xor_sync(kFull, me & 1 ? w[k] : w[k + 1], 1);
+                    if (me & 1) w[k] = r;
+                    else w[k + 1] = r;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t r = __shfl_xor_sync(kFull, me & 2 ? w[k] : w[k + 2], 2);
+                    if (me & 2) w[k] = r;
+                    else w[k + 2] = r;
+                }
+            }
+            if (!there[i]) continue;
+            const int e = tid + i * kThreads;
+            T* to = out + (long long)(y0 + e / vpr) * a.d + e % vpr * 16 - me * 16 + me * (16 / (int)sizeof(T));
+#pragma unroll
+            for (int x = 0; x < 2 * X; ++x) {
+                uint32_t z[4];
+                if constexpr (X == 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = e4m3_values(w[2 * x + k / 2] >> (k % 2 * 16) & 0xffffu);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(v.x * f[i], v.y * f[i]);
+                        z[k] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 v = e4m3_values(w[x] >> (k * 16) & 0xffffu);
+                        z[2 * k] = __float_as_uint(v.x * f[i]);
+                        z[2 * k + 1] = __float_as_uint(v.y * f[i]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(to + x * 16) = make_uint4(z[0], z[1], z[2], z[3]);
             }
         }
     }
