@@ -91,8 +91,9 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[PARTS]) {
         c[i] = e4m3x2(x, y);
         if (i + 1 < PARTS) {
             const float2 v = e4m3_values(c[i]);
-            x = (x - v.x) * 16.f;
-            y = (y - v.y) * 16.f;
+            const float2 z = f2_get(fma2(f2(v.x, v.y), f2(-16.f, -16.f), f2(x, y) * f2(16.f, 16.f)));  // exact
+            x = z.x;
+            y = z.y;
         }
     }
 }
@@ -265,17 +266,16 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
             const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0), qb = seg % kQBufs;
             const Tin* q = static_cast<const Tin*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D + lane * E;
             bool ok = true;
-            for (int hb = 0; hb < nh; hb += 8) {
-                float x[8][E];
+            for (int hb = 0; hb < HP; hb += 8) {
+                float x[GH][E];
 #pragma unroll
-                for (int h = 0; h < 8; ++h)
+                for (int h = 0; h < GH; ++h)
 #pragma unroll
                     for (int e = 0; e < E; ++e) x[h][e] = hb + h < nh ? to_f32(q[(hb + h) * D + e]) : 0.f;
                 if (hb == 0) ok = __all_sync(kFull, tc::mbar_wait(q_free + qb, ((seg / kQBufs) & 1) ^ 1, abort));
                 if (!ok) break;
 #pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    if (hb + h >= nh) break;
+                for (int h = 0; h < GH; ++h) {  // (of heads that are not there: zeros)
                     float m = 0.f;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
         for (; w.left > 0; dec_next(p, w), ++seg) {
             const int h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
             int base = 127;  // V's scale of the segment's first row
-            float m[GH], l[GH];
+            F2 m[GH / 2], l[GH / 2];  // two heads each; m holds minus the reference
 #pragma unroll
-            for (int h = 0; h < GH; ++h) {
-                m[h] = kNoRef;
-                l[h] = 0.f;
+            for (int h = 0; h < GH / 2; ++h) {
+                m[h] = f2(-kNoRef, -kNoRef);
+                l[h] = f2(0.f, 0.f);
             }
             int bad = 0;
             for (int i = 0; i < n_seg; ++i, ++j) {
@@ -359,28 +359,40 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 // a warp that gave up still takes part in the barriers
                 if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort) && tc::mbar_wait(x_full + (j & 3), (j >> 2) & 1, abort);
                 ok = __all_sync(kFull, ok);
-                float t[GH], v_back = 1.f;
+                F2 t[GH / 2];
+                float v_back = 1.f;
                 bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
                     const int x = scales[(j & 3) * 16 + my_block], vb = x >> 8;
                     if (i == 0 && scales[(j & 3) * 16] >> 8) base = scales[(j & 3) * 16] >> 8;
                     const int dv = vb ? max(-126, min(126, vb - base)) : 0;  // (a block of zeros: any scale)
-                    const float k_unit = scale_of(x & 255), v_add = (float)dv;
+                    const F2 k_unit = f2(scale_of(x & 255), scale_of(x & 255));
+                    const float add = r < n ? (float)dv : -INFINITY;  // a row past the prefix: weight 0
+                    const F2 v_add = f2(add, add);
                     v_back = __int_as_float((127 - dv) << 23);
                     uint32_t sr[QP][8];
 #pragma unroll
-                    for (int x = 0; x < QP; ++x) tmem_ld8(tmem + lane_base + (j & 1) * NQ + x * HP + hg, sr[x]);
+                    for (int y = 0; y < QP; ++y) tmem_ld8(tmem + lane_base + (j & 1) * NQ + y * HP + hg, sr[y]);
                     tc::tmem_wait_ld();
                     bad |= bad_tile[j & 7];
-                    const float* unit = q_unit + (seg & 7) * HP + hg;
+                    const float2* unit = reinterpret_cast<const float2*>(q_unit + (seg & 7) * HP + hg);
 #pragma unroll
-                    for (int h = 0; h < GH; ++h) {
-                        float s = __uint_as_float(sr[QP - 1][h]);
+                    for (int h = 0; h < GH / 2; ++h) {
+                        F2 s = f2(__uint_as_float(sr[QP - 1][2 * h]), __uint_as_float(sr[QP - 1][2 * h + 1]));
 #pragma unroll
-                        for (int x = QP - 2; x >= 0; --x) s = fmaf(s, 0.0625f, __uint_as_float(sr[x][h]));
-                        t[h] = r < n && h < nh ? fmaf(s, k_unit * unit[h], v_add) : -INFINITY;
-                        above |= t[h] > m[h] + (kLift + kTau);
+                        for (int y = QP - 2; y >= 0; --y)
+                            s = fma2(s, f2(0.0625f, 0.0625f), f2(__uint_as_float(sr[y][2 * h]), __uint_as_float(sr[y][2 * h + 1])));
+                        const float2 q = unit[h];
+                        t[h] = fma2(s, k_unit * f2(q.x, q.y), v_add);
+                        const float2 d = f2_get(t[h] + m[h]);
+                        above |= d.x > kLift + kTau;
+                        above |= d.y > kLift + kTau;
+                    }
+                    if (n < kDecTile && r >= n) {  // (what lies in the rows behind the prefix may be NaN)
+                        above = false;
+#pragma unroll
+                        for (int h = 0; h < GH / 2; ++h) t[h] = v_add;
                     }
                 }
                 if (bar_any(bar, above)) {
@@ -390,23 +402,32 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                     float mine = -INFINITY;
                     if (ok)
 #pragma unroll
-                        for (int h = 0; h < GH; ++h) {
-                            const float v = redux_max(t[h]);
-                            if (lane == h) mine = v;
+                        for (int h = 0; h < GH / 2; ++h) {
+                            const float2 y = f2_get(t[h]);
+                            const float v0 = redux_max(y.x), v1 = redux_max(y.y);
+                            if (lane == 2 * h) mine = v0;
+                            if (lane == 2 * h + 1) mine = v1;
                         }
                     if (lane < 8) x[ws * HP + lane] = mine;
                     tc::named_bar(bar, 128);
                     if (ok) {
                         float f[GH];
 #pragma unroll
-                        for (int h = 0; h < GH; ++h) {
-                            const float mt = fmaxf(fmaxf(x[h], x[HP + h]), fmaxf(x[2 * HP + h], x[3 * HP + h])) - kLift;
-                            f[h] = 1.f;
-                            if (mt > m[h] + kTau) {
-                                f[h] = tc::ex2(m[h] - mt);
-                                l[h] *= f[h];
-                                m[h] = mt;
+                        for (int h = 0; h < GH / 2; ++h) {
+                            const float2 old = f2_get(m[h]);
+                            float now[2] = {old.x, old.y};
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = 2 * h + e;
+                                const float mt = fmaxf(fmaxf(x[k], x[HP + k]), fmaxf(x[2 * HP + k], x[3 * HP + k])) - kLift;
+                                f[k] = 1.f;
+                                if (mt > kTau - now[e]) {
+                                    f[k] = tc::ex2(-now[e] - mt);
+                                    now[e] = -mt;
+                                }
                             }
+                            l[h] = l[h] * f2(f[2 * h], f[2 * h + 1]);
+                            m[h] = f2(now[0], now[1]);
                         }
                         if (i > 0) {  // O holds earlier tiles of the segment: once their P V are done
                             ok = __all_sync(kFull, tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort));
@@ -433,11 +454,11 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 if (!ok) continue;
                 uint32_t c[4][PP] = {};
 #pragma unroll
-                for (int h = 0; h < GH; h += 2) {
-                    const float e0 = tc::ex2(t[h] - m[h]), e1 = tc::ex2(t[h + 1] - m[h + 1]);
-                    l[h] = fmaf(e0, v_back, l[h]);
-                    l[h + 1] = fmaf(e1, v_back, l[h + 1]);
-                    split2<PP>(e0, e1, c[h / 2]);
+                for (int h = 0; h < GH / 2; ++h) {
+                    const float2 d = f2_get(t[h] + m[h]);
+                    const float e0 = tc::ex2(d.x), e1 = tc::ex2(d.y);
+                    l[h] = fma2(f2(e0, e1), f2(v_back, v_back), l[h]);
+                    split2<PP>(e0, e1, c[h]);
                 }
                 unsigned char* pb = sP + (j & 1) * Cfg::kPBytes;
 #pragma unroll
@@ -470,10 +491,11 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
             // ---- the partial: sums through shared memory, O once the last P V is done
             float sum = 0.f, ref = 0.f;
 #pragma unroll
-            for (int h = 0; h < GH; ++h) {
-                const float x = warp_sum(l[h]);
-                if (lane == h) sum = x;
-                if (r == h) ref = m[h];
+            for (int h = 0; h < GH / 2; ++h) {
+                const float2 z = f2_get(l[h]), y = f2_get(m[h]);
+                const float x0 = warp_sum(z.x), x1 = warp_sum(z.y);
+                if (lane == 2 * h) sum = x0, ref = -y.x;
+                if (lane == 2 * h + 1) sum = x1, ref = -y.y;
             }
             if (lane < 8) sm_l[ws * HP + hg + lane] = sum;
             if (ok) ok = tc::mbar_wait(p_free + ((j - 1) & 1), ((j - 1) >> 1) & 1, abort);
