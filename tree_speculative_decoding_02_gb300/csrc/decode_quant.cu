@@ -83,17 +83,38 @@ struct DecQuantArgs {
 
 __device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
 
-// x and y as PARTS codes each: the code pairs, x's in the low byte
+// x[0..3] as PARTS codes each, a word a part.  Up to four parts: what the first one leaves is rounded to fp16, 11 bits
+// of at most 2^-4 x (2^-16 of x), which three more parts hold; more: fp32 throughout.
 template <int PARTS>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[PARTS]) {
+__device__ __forceinline__ void split4(const float (&x)[4], uint32_t (&c)[PARTS]) {
+    F2 u = f2(x[0], x[1]), v = f2(x[2], x[3]);
+    c[0] = e4m3x4(x[0], x[1], x[2], x[3]);
+    __half2 p, q;
+    e4m3x4_values(c[0], p, q);
+    if constexpr (PARTS <= 4) {
+        const float2 fp = __half22float2(p), fq = __half22float2(q);
+        const float2 ru = f2_get(u - f2(fp.x, fp.y)), rv = f2_get(v - f2(fq.x, fq.y));
+        const __half2 k16 = __float2half2_rn(16.f);
+        __half2 hu = __hmul2(__floats2half2_rn(ru.x, ru.y), k16), hv = __hmul2(__floats2half2_rn(rv.x, rv.y), k16);
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-        c[i] = e4m3x2(x, y);
-        if (i + 1 < PARTS) {
-            const float2 v = e4m3_values(c[i]);
-            const float2 z = f2_get(fma2(f2(v.x, v.y), f2(-16.f, -16.f), f2(x, y) * f2(16.f, 16.f)));  // exact
-            x = z.x;
-            y = z.y;
+        for (int i = 1; i < PARTS; ++i) {
+            c[i] = e4m3x4(hu, hv);
+            if (i + 1 < PARTS) {
+                e4m3x4_values(c[i], p, q);
+                hu = __hmul2(__hsub2(hu, p), k16);
+                hv = __hmul2(__hsub2(hv, q), k16);
+            }
+        }
+    } else {
+        const F2 k16 = f2(16.f, 16.f);
+#pragma unroll
+        for (int i = 1; i < PARTS; ++i) {
+            const float2 fp = __half22float2(p), fq = __half22float2(q);
+            u = (u - f2(fp.x, fp.y)) * k16;
+            v = (v - f2(fq.x, fq.y)) * k16;
+            const float2 a = f2_get(u), b = f2_get(v);
+            c[i] = e4m3x4(a.x, a.y, b.x, b.y);
+            if (i + 1 < PARTS) e4m3x4_values(c[i], p, q);
         }
     }
 }
@@ -235,7 +256,8 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 ok = tc::mbar_wait(q_full + qb, (seg / kQBufs) & 1, abort);
                 for (int i = 0; i < n_seg && ok; ++i, ++j) {
                     const int st = (2 * j) % kStages;
-                    ok = tc::mbar_wait(full + st, ((2 * j) / kStages) & 1, abort);
+                    // (the scales for the softmax's sake, which waits for S alone)
+                    ok = tc::mbar_wait(full + st, ((2 * j) / kStages) & 1, abort) && tc::mbar_wait(x_full + (j & 3), (j >> 2) & 1, abort);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint64_t kd = kdesc + (uint64_t)((st * Cfg::kStageBytes) >> 4);
@@ -287,18 +309,23 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                     const int up = m > 0.f ? min(134 - (__float_as_int(m) >> 23), 100) : 0;
                     const float f = __int_as_float((127 + up) << 23);
                     if (lane == 0) q_unit[(seg & 7) * HP + hb + h] = p.scale_log2 * __int_as_float((127 - up) << 23);
-                    uint32_t c[E / 2][QP];
+                    uint32_t c[(E + 3) / 4][QP];
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) split2<QP>(finite_or_nan(x[h][e]) * f, finite_or_nan(x[h][e + 1]) * f, c[e / 2]);
+                    for (int e = 0; e < E; e += 4) {
+                        float y[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) y[z] = e + z < E ? finite_or_nan(x[h][(e + z) % E]) * f : 0.f;
+                        split4<QP>(y, c[e / 4]);
+                    }
 #pragma unroll
                     for (int i = 0; i < QP; ++i) {
                         const int ch = lane * E;
                         unsigned char* to = sQ + qb * Cfg::kQBytes + ch / kRow * (NQ * kRow) +
                                             tc::swizzled<kRow>((i * HP + hb + h) * kRow + ch % kRow);
                         if constexpr (E == 8)
-                            *reinterpret_cast<uint2*>(to) = make_uint2(c[0][i] | c[1][i] << 16, c[2][i] | c[3][i] << 16);
+                            *reinterpret_cast<uint2*>(to) = make_uint2(c[0][i], c[E / 4 - 1][i]);
                         else if constexpr (E == 4)
-                            *reinterpret_cast<uint32_t*>(to) = c[0][i] | c[1][i] << 16;
+                            *reinterpret_cast<uint32_t*>(to) = c[0][i];
                         else
                             *reinterpret_cast<uint16_t*>(to) = (uint16_t)c[0][i];
                     }
@@ -357,7 +384,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
             for (int i = 0; i < n_seg; ++i, ++j) {
                 const int n = min(kDecTile, w.P - (w.t + i) * kDecTile);
                 // a warp that gave up still takes part in the barriers
-                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort) && tc::mbar_wait(x_full + (j & 3), (j >> 2) & 1, abort);
+                if (ok) ok = tc::mbar_wait(s_full + (j & 1), (j >> 1) & 1, abort);
                 ok = __all_sync(kFull, ok);
                 F2 t[GH / 2];
                 float v_back = 1.f;
@@ -449,26 +476,29 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                     }
                 }
                 if (!ok) continue;
-                // the P buffer is free once P V of tile j - 2 is done
-                ok = __all_sync(kFull, tc::mbar_wait(p_free + (j & 1), ((j >> 1) & 1) ^ 1, abort));
-                if (!ok) continue;
-                uint32_t c[4][PP] = {};
+                // (the P buffer is free: S of tile j comes after P V of tile j - 2)
+                uint32_t c[2][PP] = {};
 #pragma unroll
-                for (int h = 0; h < GH / 2; ++h) {
-                    const float2 d = f2_get(t[h] + m[h]);
-                    const float e0 = tc::ex2(d.x), e1 = tc::ex2(d.y);
-                    l[h] = fma2(f2(e0, e1), f2(v_back, v_back), l[h]);
-                    split2<PP>(e0, e1, c[h]);
+                for (int h = 0; h < GH; h += 4) {
+                    float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int y = 0; y < 4 && h + y < GH; y += 2) {
+                        const float2 d = f2_get(t[(h + y) / 2] + m[(h + y) / 2]);
+                        e[y] = tc::ex2(d.x);
+                        e[y + 1] = tc::ex2(d.y);
+                        l[(h + y) / 2] = fma2(f2(e[y], e[y + 1]), f2(v_back, v_back), l[(h + y) / 2]);
+                    }
+                    split4<PP>(e, c[h / 4]);
                 }
                 unsigned char* pb = sP + (j & 1) * Cfg::kPBytes;
 #pragma unroll
                 for (int x = 0; x < PP; ++x) {
-                    const uint2 v = make_uint2(c[0][x] | c[1][x] << 16, c[2][x] | c[3][x] << 16);
+                    const uint2 v = make_uint2(c[0][x], c[1][x]);
                     if (HP > 8 || x + 1 == PP) {
                         if (HP > 8 || x % 2 == 0) *reinterpret_cast<uint2*>(pb + tc::swizzled<NP>(r * NP + x * HP + hg)) = v;
                     } else if (x % 2 == 0) {
                         *reinterpret_cast<uint4*>(pb + tc::swizzled<NP>(r * NP + x * HP)) =
-                            make_uint4(v.x, v.y, c[0][x + 1] | c[1][x + 1] << 16, c[2][x + 1] | c[3][x + 1] << 16);
+                            make_uint4(v.x, v.y, c[0][(x + 1) % PP], c[1][(x + 1) % PP]);
                     }
                 }
                 if (n < kDecTile) {

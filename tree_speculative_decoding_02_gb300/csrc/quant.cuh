@@ -40,6 +40,28 @@ __device__ __forceinline__ void values8(uint2 c, float* v) {
     }
 }
 
+// four codes in a word, and their values as fp16
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+    uint32_t r;
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}"
+        : "=r"(r)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(__half2 x, __half2 y) {
+    uint32_t r;
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n mov.b32 %0, {a, b};\n}"
+        : "=r"(r)
+        : "r"(*reinterpret_cast<const uint32_t*>(&x)), "r"(*reinterpret_cast<const uint32_t*>(&y)));
+    return r;
+}
+__device__ __forceinline__ void e4m3x4_values(uint32_t c, __half2& x, __half2& y) {
+    uint32_t a, b;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(a), "=r"(b) : "r"(c));
+    x = *reinterpret_cast<const __half2*>(&a);
+    y = *reinterpret_cast<const __half2*>(&b);
+}
+
 // Two fp32 in a 64-bit register: one instruction for both.
 struct F2 {
     unsigned long long v;
@@ -57,6 +79,11 @@ __device__ __forceinline__ float2 f2_get(F2 a) {
 __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) {
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
