@@ -6,6 +6,11 @@ output and workspace of its steps once, and `step()` enqueues build -> tree atte
 -> walk -> commit with no host synchronisation.  The synthetic layers are independent,
 so each attention/GDN call covers all layers at once (a model would call per layer).
 
+cfg["kv_quant"] (rows a scale; with cfg["page"]) holds the prefixes in 8-bit pages: each layer's are
+read back into one layer's scratch for its tree attention, and the accepted rows are quantised as
+they are appended.  cfg["qk_norm"] takes q and the tree keys before their per-head norms, and
+normalises and (with cfg["rope"]) rotates them in one pass.
+
 All arithmetic is in libddt.so; this module only allocates and passes pointers.
 """
 from __future__ import annotations
@@ -56,12 +61,23 @@ class Round:
                                           workload=workload, dtype=dt, device=dev, poison=poison)
             self.attn_o = torch.empty((self.Lf, B, N, c["Hq"], c["d"]), dtype=attn_out_dtype or dt, device=dev)
             self.attn_status = torch.empty((B,), **i32)
-            ws = ddt.load().ddt_tree_attn_workspace(self.Lf, B, N, c["Hq"], c["Hkv"], c["d"], self.Pcap)
+            self.quant = int(c.get("kv_quant", 0))   # > 0: 8-bit pages, this many rows a scale
+            ws = ddt.load().ddt_tree_attn_workspace(1 if self.quant else self.Lf, B, N, c["Hq"], c["Hkv"], c["d"], self.Pcap)
             if c.get("rope"):
                 ws = ddt.rope_workspace_bytes(ws, B, N, int(c["rope"]))
             self.attn_ws = torch.empty(max(16, ws), dtype=torch.uint8, device=dev)
-            if self.page:
+            if self.quant:
+                if not self.page:
+                    raise ValueError("kv_quant is a form of the paged cache: give page too")
+                self._to_quantised(workload)
+            elif self.page:
                 self._to_pages(workload)
+            self.qk_norm = bool(c.get("qk_norm"))
+            if self.qk_norm:
+                gw = synth.gen(workload, 61, dev)
+                self.q_weight, self.k_weight = (1 + synth.normal((self.Lf, c["d"]), 0.2, g=gw, dtype=dt, device=dev)
+                                                for _ in range(2))
+                self.q_heads, self.k_heads = torch.zeros_like(self.attn.q), torch.zeros_like(self.attn.k_tree)
         # GDN layers (state stored [dv][dk])
         self.Lg = c.get("Lg", 0)
         if self.Lg:
@@ -99,10 +115,7 @@ class Round:
         behind a shuffled block table (two spare pages), one layer at a time."""
         a, pg = self.attn, self.page
         L, B, Hkv, Pcap, d = a.k_cache.shape
-        mp = Pcap // pg
-        num = B * mp + 2
-        g = synth.gen(workload, 60)
-        self.block_table = torch.randperm(num, generator=g)[:B * mp].reshape(B, mp).to(torch.int32).to(self.device)
+        num, mp = self._new_table(workload)
         phys = self.block_table.flatten().long()
         self.k_pages = torch.empty((L, num, Hkv, pg, d), dtype=a.k_cache.dtype, device=self.device)
         self.v_pages = torch.empty_like(self.k_pages)
@@ -110,6 +123,36 @@ class Round:
             for l in range(L):
                 dst[l, phys] = src[l].reshape(B, Hkv, mp, pg, d).transpose(1, 2).reshape(B * mp, Hkv, pg, d)
         a.k_cache = a.v_cache = None
+
+    def _new_table(self, workload):
+        """A shuffled block table (two spare pages); the number of pages and a request's share."""
+        B, mp = self.attn.k_cache.shape[1], self.Pcap // self.page
+        num = B * mp + 2
+        g = synth.gen(workload, 60)
+        self.block_table = torch.randperm(num, generator=g)[:B * mp].reshape(B, mp).to(torch.int32).to(self.device)
+        return num, mp
+
+    def _to_quantised(self, workload):
+        """Append the contiguous prefixes to an empty 8-bit paged cache, a layer at a time, and keep one layer's
+        contiguous caches as the scratch that the tree attention reads."""
+        a = self.attn
+        L, B, Hkv, Pcap, d = a.k_cache.shape
+        num, _ = self._new_table(workload)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = ddt.quant_cache(L, num, Hkv, self.page, d, block=self.quant,
+                                                                                 device=self.device)
+        rows = max(1, int(self.prefix0.max()))
+        none = torch.zeros_like(self.prefix0)
+        for l in range(L):
+            k, v = (x[l:l + 1, :, :, :rows].transpose(2, 3).contiguous() for x in (a.k_cache, a.v_cache))
+            ddt.ddt_append_paged_quant(k, v, *self._layer(l), self.block_table, none, self.prefix0, advance=False)
+        self.k_scratch, self.v_scratch = a.k_cache[:1].clone(), a.v_cache[:1].clone()
+        self.layer_status = torch.zeros((L, B), dtype=torch.int32, device=self.device)
+        self.read_status, self.append_status = (torch.zeros((B,), dtype=torch.int32, device=self.device) for _ in range(2))
+        a.k_cache = a.v_cache = None
+
+    def _layer(self, l):
+        """One layer of the 8-bit cache."""
+        return tuple(x[l:l + 1] for x in (self.k_pages, self.v_pages, self.k_scale, self.v_scale))
 
     # ------------------------------------------------------------------ the round
     def step(self, wait=None):
@@ -134,8 +177,15 @@ class Round:
             wait("walk")
         self.walk_step()
         kw = {}
+        quant = bool(self.Lf and self.quant)
+        if quant:   # its rows first: the commit below moves prefix_len (where nothing else does, the append)
+            ddt.ddt_append_paged_quant(self.k_rows(), self.attn.v_tree, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
+                                       self.block_table, self.prefix_len, self.walk["n_emitted"],
+                                       node=self.walk["acc_nodes"], advance=not self.Lg, status=self.append_status)
+            if not self.Lg:
+                return
         if self.Lf and not self.page:
-            kw.update(k_tree=self.attn.k_tree, v_tree=self.attn.v_tree, k_cache=self.attn.k_cache,
+            kw.update(k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_cache=self.attn.k_cache,
                       v_cache=self.attn.v_cache)
         if self.Lg:
             g = self.gdn
@@ -143,9 +193,9 @@ class Round:
                       Hk=c["Hk"])
         if not (self.Lf or self.Lg):
             return                     # nothing is cached: the round ends with the walk
-        if self.Lf and self.page:
+        if self.Lf and self.page and not quant:
             ddt.ddt_commit_paged(self.walk["acc_nodes"], self.walk["acc_len"], self.prefix_len, self.block_table,
-                                 k_tree=self.attn.k_tree, v_tree=self.attn.v_tree, k_pages=self.k_pages,
+                                 k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_pages=self.k_pages,
                                  v_pages=self.v_pages, out=self.commit, **kw)
         else:
             ddt.ddt_commit(self.walk["acc_nodes"], self.walk["acc_len"], self.prefix_len, out=self.commit, **kw)
@@ -179,23 +229,50 @@ class Round:
         c, a = self.cfg, self.attn
         scale = 1.0 / math.sqrt(c["d"])
         rot = int(c.get("rope", 0))
-        if rot:
+        q, k_tree = a.q, a.k_tree
+        if self.qk_norm:
+            q, k_tree = ddt.ddt_qk_norm_rope(q, k_tree, self.q_weight, self.k_weight, self.tree["position"],
+                                             n_nodes=self.tree["n_nodes"], rot_dim=rot, q_out=self.q_heads, k_out=self.k_heads)
+            rot = 0
+        elif rot:
             ddt.ddt_rope_tree(None, a.k_tree, self.tree["position"], self.tree["n_nodes"], rot_dim=rot, Hq=c["Hq"])
         common = dict(scale=scale, out_dtype=self.attn_o.dtype, out=self.attn_o, status=self.attn_status,
                       workspace=self.attn_ws)
+        if self.quant:
+            return self._attention_quantised(q, k_tree, rot, scale)
         if self.page and rot:
-            ddt.ddt_tree_attn_paged_rope(a.q, a.k_tree, a.v_tree, self.k_pages, self.v_pages, self.block_table,
+            ddt.ddt_tree_attn_paged_rope(q, k_tree, a.v_tree, self.k_pages, self.v_pages, self.block_table,
                                          self.prefix_len, self.tree["n_nodes"], self.tree["anc"], self.tree["position"],
                                          rot_dim=rot, **common)
         elif self.page:
-            ddt.ddt_tree_attn_paged(a.q, a.k_tree, a.v_tree, self.k_pages, self.v_pages, self.block_table,
+            ddt.ddt_tree_attn_paged(q, k_tree, a.v_tree, self.k_pages, self.v_pages, self.block_table,
                                     self.prefix_len, self.tree["n_nodes"], self.tree["anc"], **common)
         elif rot:
-            ddt.ddt_tree_attn_rope(a.q, a.k_tree, a.v_tree, a.k_cache, a.v_cache, self.prefix_len, self.tree["n_nodes"],
+            ddt.ddt_tree_attn_rope(q, k_tree, a.v_tree, a.k_cache, a.v_cache, self.prefix_len, self.tree["n_nodes"],
                                    self.tree["anc"], self.tree["position"], rot_dim=rot, **common)
         else:
-            ddt.ddt_tree_attn(a.q, a.k_tree, a.v_tree, a.k_cache, a.v_cache, self.prefix_len, self.tree["n_nodes"],
+            ddt.ddt_tree_attn(q, k_tree, a.v_tree, a.k_cache, a.v_cache, self.prefix_len, self.tree["n_nodes"],
                               self.tree["anc"], **common)
+
+    def _attention_quantised(self, q, k_tree, rot, scale):
+        """The tree attention of an 8-bit cache: layer by layer, over the layer's rows read back."""
+        t, v_tree = self.tree, self.attn.v_tree
+        for l in range(self.Lf):
+            at, st = slice(l, l + 1), self.layer_status[l]
+            ddt.ddt_read_paged_quant(*self._layer(l), self.block_table, self.prefix_len, self.k_scratch, self.v_scratch,
+                                     status=self.read_status)
+            common = dict(scale=scale, out_dtype=self.attn_o.dtype, out=self.attn_o[at], status=st, workspace=self.attn_ws)
+            args = (q[at], k_tree[at], v_tree[at], self.k_scratch, self.v_scratch, self.prefix_len, t["n_nodes"], t["anc"])
+            if rot:
+                ddt.ddt_tree_attn_rope(*args, t["position"], rot_dim=rot, **common)
+            else:
+                ddt.ddt_tree_attn(*args, **common)
+            torch.maximum(st, self.read_status, out=st)
+        torch.amax(self.layer_status, 0, out=self.attn_status)
+
+    def k_rows(self):
+        """The tree keys as the attention takes them and the commit copies them."""
+        return self.k_heads if self.qk_norm else self.attn.k_tree
 
     def restore_prefix(self):
         """Reset the committed prefix lengths (the commit advanced them)."""
