@@ -567,7 +567,7 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
  *   k_scale, v_scale [L][num_pages][Hkv][page_size / block] bytes: `block` consecutive rows of
  *     a head share the scale 2^(byte - 127) (an E8M0 byte); a row's value is code * scale.
  *     Byte 0 marks a block whose rows so far are all zero.
- *   block: 8, 16, 32, 64 or 128, and a divisor of page_size.
+ *   block: 8, 16, 32, 64 or 128, and a divisor of page_size.  Hkv * page_size * d < 2^31.
  * The byte of a block is that of the smallest e in [-100, 120] with max|x| <= 448 * 2^e over the
  * finite channels of its rows so far: nothing saturates.  A channel above 2^-13 of its block's
  * largest is off by at most 2^-4 of itself (half a step), a smaller one by at most 2^-17 of that

@@ -543,6 +543,8 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
 // ------------------------------------------------------------------ the 8-bit paged cache
 // rows a scale: a power of two that divides a page
 static bool scale_block_ok(int block, int page_size) { return block >= 8 && block <= 128 && (block & (block - 1)) == 0 && page_size % block == 0; }
+// (a page of all heads is indexed with 32 bits)
+static bool quant_page_ok(int Hkv, int page_size, int d) { return (long)Hkv * page_size <= 0x7fffffffL / d; }
 static bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
 ddt_status ddt_qk_norm_rope(int n_layers, int B, int N, int Hq, int Hkv, int d, int rot_dim, double theta, float eps,
@@ -598,7 +600,7 @@ ddt_status ddt_append_paged_quant(int n_layers, int B, int N, int A, int Hkv, in
         (!node && A > N))
         return DDT_ERR_INVALID_ARG;
     if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
-        !head_dim_ok(d) || !scale_block_ok(block, page_size) || (node && A > kMaxRows) || A > (1 << 30) ||
+        !head_dim_ok(d) || !scale_block_ok(block, page_size) || !quant_page_ok(Hkv, page_size, d) || (node && A > kMaxRows) || A > (1 << 30) ||
         (long)n_layers * B > 65535 || Hkv > 32767)
         return DDT_ERR_UNSUPPORTED;
     if (!k || !v || !count || !block_table || !prefix_len || !k_pages || !v_pages || !k_scale || !v_scale || !status)
@@ -624,7 +626,7 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
     if (n_layers < 1 || B < 1 || Hkv < 1 || Pcap < 1 || num_pages < 1 || max_pages < 1 || !dtype_ok(out_dtype))
         return DDT_ERR_INVALID_ARG;
     if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hkv, Hkv, num_pages) ||
-        !head_dim_ok(d) || !scale_block_ok(block, page_size) || Pcap > (1 << 30) || (long)n_layers * B > 65535 || Hkv > 32767)
+        !head_dim_ok(d) || !scale_block_ok(block, page_size) || !quant_page_ok(Hkv, page_size, d) || Pcap > (1 << 30) || (long)n_layers * B > 65535 || Hkv > 32767)
         return DDT_ERR_UNSUPPORTED;
     if (!k_pages || !v_pages || !k_scale || !v_scale || !block_table || !prefix_len || !k_out || !v_out || !status)
         return DDT_ERR_INVALID_ARG;
@@ -655,7 +657,7 @@ ddt_status ddt_decode_attn_paged_quant(int n_layers, int B, int Hq, int Hkv, int
         !dtype_ok(in_dtype) || !dtype_ok(out_dtype))
         return DDT_ERR_INVALID_ARG;
     if (!paging_sizes_ok(page_size, num_pages, max_pages) || !decode_sizes_ok(n_layers, B, Hq, Hkv, num_pages) ||
-        !head_dim_ok(d) || !scale_block_ok(block, page_size))
+        !head_dim_ok(d) || !scale_block_ok(block, page_size) || !quant_page_ok(Hkv, page_size, d))
         return DDT_ERR_UNSUPPORTED;
     if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !prefix_len || !o || !status || !workspace ||
         !k_new != !v_new)

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "quant.cuh"
 
 namespace ddt {
 
@@ -75,7 +76,14 @@ struct Run {
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_run(T* p, const float (&v)[8]) {
+__device__ __forceinline__ void store_run(T* p, const F2 (&x)[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = f2_get(x[i]);
+        v[2 * i] = y.x;
+        v[2 * i + 1] = y.y;
+    }
     if (VEC) {
         if (sizeof(T) == 2) {
             uint32_t w[4];
@@ -101,7 +109,7 @@ template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
     constexpr int LPR = D / 16;  // lanes a row
     // four float4 a lane, lane after lane: a quarter warp reads 128 consecutive bytes
-    __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16] pairs (cos, sin)
+    __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16]: two cosines, their sines
     __shared__ float4 s_w[2][4 * LPR];           // offset + weight: of q, of k
     __shared__ long long s_at[kMaxTokens][2];    // a token's place in q and in k, or -1
     const int tid = threadIdx.x, half = a.rot / 2, lanes = a.rot / 16, heads = a.Hq + a.Hkv;
@@ -158,7 +166,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
         const unsigned long long turn = (unsigned long long)(long long)a.position[first + t] * fr.f[i];
         float s, co;
         sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &co);  // half turns: 2^-31
-        reinterpret_cast<float2*>(s_cs)[((t * 4 + i % 8 / 2) * lanes + i / 8) * 2 + i % 2] = make_float2(co, s);
+        float* to = reinterpret_cast<float*>(s_cs + (t * 4 + i % 8 / 2) * lanes + i / 8) + i % 2;
+        to[0] = co;
+        to[2] = s;
     }
     for (int e = tid; e < 2 * D; e += kThreads) {
         // channel ch is the j-th of its lane: of the low run 0..7, of the high one 8..15
@@ -177,39 +187,42 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
                 fetch(s);
                 continue;
             }
-            float p[8], q[8], ss = 0.f;
+            F2 p[4], q[4], sum = f2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = u[s][i];
-                q[i] = v[s][i];
-                ss = fmaf(p[i], p[i], fmaf(q[i], q[i], ss));
+            for (int i = 0; i < 4; ++i) {
+                p[i] = f2(u[s][2 * i], u[s][2 * i + 1]);
+                q[i] = f2(v[s][2 * i], v[s][2 * i + 1]);
+                sum = fma2(p[i], p[i], fma2(q[i], q[i], sum));
             }
             fetch(s);
+            float ss = f2_get(sum).x + f2_get(sum).y;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
             const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+            const F2 rr = f2(r, r);
             const bool isq = at.h < a.Hq;
             const float4* w = s_w[!isq] + c;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float4 x = w[i * LPR], z = w[(2 + i) * LPR];
-                p[4 * i] *= r * x.x; p[4 * i + 1] *= r * x.y; p[4 * i + 2] *= r * x.z; p[4 * i + 3] *= r * x.w;
-                q[4 * i] *= r * z.x; q[4 * i + 1] *= r * z.y; q[4 * i + 2] *= r * z.z; q[4 * i + 3] *= r * z.w;
+                p[2 * i] = p[2 * i] * (rr * f2(x.x, x.y));
+                p[2 * i + 1] = p[2 * i + 1] * (rr * f2(x.z, x.w));
+                q[2 * i] = q[2 * i] * (rr * f2(z.x, z.y));
+                q[2 * i + 1] = q[2 * i + 1] * (rr * f2(z.z, z.w));
             }
             if (turned) {
                 const float4* cs = s_cs + at.t * 4 * lanes + c;
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float4 k = cs[i / 2 * lanes];
-                    const float p0 = p[i], p1 = p[i + 1];
-                    p[i] = fmaf(p0, k.x, -q[i] * k.y);
-                    q[i] = fmaf(q[i], k.x, p0 * k.y);
-                    p[i + 1] = fmaf(p1, k.z, -q[i + 1] * k.w);
-                    q[i + 1] = fmaf(q[i + 1], k.z, p1 * k.w);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 k = cs[i * lanes];
+                    const F2 co = f2(k.x, k.y), si = f2(k.z, k.w), p0 = p[i];
+                    p[i] = p0 * co - q[i] * si;
+                    q[i] = fma2(q[i], co, p0 * si);
                 }
             }
-            const long long row = (long long)l * rows + first + at.t;
-            T* y = isq ? static_cast<T*>(a.qo) + (row * a.Hq + at.h) * D : static_cast<T*>(a.ko) + (row * a.Hkv + (at.h - a.Hq)) * D;
+            // (a CTA's rows span less than 2^31 elements)
+            T* y = isq ? static_cast<T*>(a.qo) + ((long long)l * rows + first) * a.Hq * D + (at.t * a.Hq + at.h) * D
+                       : static_cast<T*>(a.ko) + ((long long)l * rows + first) * a.Hkv * D + (at.t * a.Hkv + at.h - a.Hq) * D;
             store_run<T, VEC>(y + lo, p);
             store_run<T, VEC>(y + hi, q);
         }

@@ -59,9 +59,10 @@ struct Vec8 {
     __device__ __forceinline__ uint32_t top(uint32_t m) const {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m = sizeof(T) == 4 ? max(m, x[k] & 0x7fffffffu) : __vmaxu2(m, x[k] & 0x7fff7fffu);
+            if (sizeof(T) == 4)
+                m = max(max(max(m, w[i].x & 0x7fffffffu), max(w[i].y & 0x7fffffffu, w[i].z & 0x7fffffffu)), w[i].w & 0x7fffffffu);
+            else
+                m = __vimax3_u16x2(__vimax3_u16x2(m, w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu);
         }
         return m;
     }
@@ -74,10 +75,14 @@ struct Vec8 {
         return __uint_as_float(i % 2 ? x & 0xffff0000u : x << 16);
     }
     __device__ __forceinline__ uint2 codes(float inv) const {
-        uint32_t c[4];
+        const F2 k = f2(inv, inv);
+        uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = e4m3x2(get(2 * i) * inv, get(2 * i + 1) * inv);
-        return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+        for (int i = 0; i < 2; ++i) {
+            const float2 x = f2_get(f2(get(4 * i), get(4 * i + 1)) * k), y = f2_get(f2(get(4 * i + 2), get(4 * i + 3)) * k);
+            c[i] = e4m3x4(x.x, x.y, y.x, y.y);
+        }
+        return make_uint2(c[0], c[1]);
     }
     // the same where an infinity may be among them: it becomes NaN
     __device__ __forceinline__ uint2 codes_any(float inv) const {
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
 // grid (runs of blocks x item groups, 1, L * B).  A CTA takes a few blocks of one request and layer, one after
 // another; wpi of its warps an item.  Up to kChunk vectors a lane stay in registers between the maximum and the
 // codes; items of more (blocks of 128 rows of 256 channels) are read twice.
-template <typename T>
+template <typename T, int D, bool NODE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_quant(const AppendArgs a) {
     __shared__ float s_max[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,11 +155,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
     const bool real = item < 2 * a.Hkv;
     const int isv = item & 1, g = min(item >> 1, a.Hkv - 1);
     // vector e of the item: 8 channels of its row e / (d / 8); a lane's are the same ones of every row
-    const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5), step = a.wpi * 32, e0 = part * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
-    const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * a.d + (long long)g * a.d + ch;
-    const int pitch = a.Hkv * a.d;  // (below 2^23)
+    constexpr int shift = D == 64 ? 3 : (D == 128 ? 4 : 5);
+    const int step = a.wpi * 32, e0 = part * 32 + lane, ch = (e0 & ((1 << shift) - 1)) * 8;
+    const T* src = static_cast<const T*>(isv ? a.v : a.k) + ((long long)l * a.B + b) * a.N * a.Hkv * D + (long long)g * D + ch;
+    const int pitch = a.Hkv * D;  // (below 2^23)
+    const long long hop = (long long)(step >> shift) * pitch;
+    // the blocks' page and the row in it
+    int lp = first * a.S / a.page_rows, in = first * a.S - lp * a.page_rows;
 
-    for (int turn = 0; turn < a.run && (long long)first * a.S < (long long)P + n; ++turn, ++first) {
+    for (int turn = 0; turn < a.run && first * a.S < P + n; ++turn, ++first, in += a.S) {
+        if (in >= a.page_rows) {
+            in = 0;
+            ++lp;
+        }
         const int r0 = first * a.S, lo = max(P - r0, 0), hi = min(P + n - r0, a.S);  // new rows [lo, hi) of the block
         const int count = real ? (hi - lo) << shift : 0;  // the item's vectors
         Vec8<T> x[kChunk];
@@ -165,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) {
                 x[i].zero();
-                if (e + i * step < count) x[i].load(a.node ? src + (long long)node[i * (step >> shift)] * pitch : at + (long long)(i * (step >> shift)) * pitch);
+                if (e + i * step < count) x[i].load(NODE ? src + (long long)node[i * (step >> shift)] * pitch : at);
+                at += hop;
             }
         };
         uint32_t most = 0;
@@ -178,9 +192,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
             asm volatile("griddepcontrol.wait;" ::: "memory");
             if (*static_cast<volatile int32_t*>(a.status + b) != DDT_OK) return;
         }
-        const int lp = r0 / a.page_rows, in = r0 - lp * a.page_rows;
         const long long plane = ((long long)l * a.num_pages + table[lp]) * a.Hkv + g;
-        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * a.d;
+        unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * D;
         unsigned char* byte = (isv ? a.vs : a.ks) + plane * (a.page_rows / a.S) + in / a.S;
         const int old = real && lo > 0 ? *byte : 0;
         if (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
@@ -210,11 +223,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
         const float inv = now ? scale_of(254 - now) : 0.f;
         for (int e = e0; e < count; e += kChunk * step) {
             if (count > kChunk * step) load(e);
-            unsigned char* to = page + (lo * a.d + (e >> shift) * a.d + ch);
-            const int rows = (step >> shift) * a.d;
+            unsigned char* to = page + (lo * D + (e >> shift) * D + ch);
+            const int rows = (step >> shift) * D;
+            if (finite) {
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i)
-                if (e + i * step < count) *reinterpret_cast<uint2*>(to + i * rows) = finite ? x[i].codes(inv) : x[i].codes_any(inv);
+                for (int i = 0; i < kChunk; ++i)
+                    if (e + i * step < count) *reinterpret_cast<uint2*>(to + i * rows) = x[i].codes(inv);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i)
+                    if (e + i * step < count) *reinterpret_cast<uint2*>(to + i * rows) = x[i].codes_any(inv);
+            }
         }
         if (old && now > old) {  // the rows that the block had, under its new scale
             const float f = scale_of(max(127 + old - now, 0));
@@ -236,6 +255,15 @@ __global__ void k_append_advance(int B, const int32_t* __restrict__ count, const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
     if (b < B && status[b] == DDT_OK) prefix_len[b] += count[b];
+}
+
+template <typename T, int D>
+static cudaError_t append_d_go(const cudaLaunchConfig_t& cfg, const AppendArgs& a) {
+    return a.node ? cudaLaunchKernelEx(&cfg, k_append_quant<T, D, true>, a) : cudaLaunchKernelEx(&cfg, k_append_quant<T, D, false>, a);
+}
+template <typename T>
+static cudaError_t append_go(const cudaLaunchConfig_t& cfg, const AppendArgs& a) {
+    return a.d == 64 ? append_d_go<T, 64>(cfg, a) : (a.d == 128 ? append_d_go<T, 128>(cfg, a) : append_d_go<T, 256>(cfg, a));
 }
 
 cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int S, const AttnPaging& pg, ddt_dtype in,
@@ -291,7 +319,7 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = a.checked ? 1 : 0;
-    cudaError_t e = in == DDT_BF16 ? cudaLaunchKernelEx(&cfg, k_append_quant<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, k_append_quant<float>, a);
+    cudaError_t e = in == DDT_BF16 ? append_go<__nv_bfloat16>(cfg, a) : append_go<float>(cfg, a);
     if (e != cudaSuccess || !advance || a.solo) return e;
     cfg.gridDim = dim3(counted((unsigned)(B + 127) / 128));
     cfg.blockDim = dim3(128);
@@ -313,7 +341,8 @@ struct ReadArgs {
     void* ko;
     void* vo;
     int32_t* status;
-    int turns;
+    int turns, block_shift;
+    int hop_pages, hop_rows;  // a thread's next vector, in pages and rows
 };
 constexpr int kReadVecs = 4;   // 16 codes each, in flight a thread
 }  // namespace
@@ -321,7 +350,7 @@ constexpr int kReadVecs = 4;   // 16 codes each, in flight a thread
 // grid (row chunks, 2 * Hkv, L * B): `turns` steps of kReadVecs * kThreads * 16 codes of one head's K or V a CTA.
 // (The grid goes by the table's rows; CTAs behind a request's own take a few hundred cycles each, which larger ones
 // make rarer.)
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
     const int tid = threadIdx.x, b = blockIdx.z % a.B, l = blockIdx.z / a.B, g = blockIdx.y >> 1, isv = blockIdx.y & 1;
     const int P = a.prefix_len[b];
@@ -334,28 +363,35 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
         bad = __syncthreads_or(bad);
         if (tid == 0) a.status[b] = !fits ? DDT_ERR_CAPACITY : (bad ? DDT_ERR_INVALID_ARG : DDT_OK);
     }
-    if (!fits) return;
-    const int vpr = a.d / 16, rows = kReadVecs * kThreads / vpr;
-    const unsigned char* pages = isv ? a.vp : a.kp;
-    const unsigned char* scales = isv ? a.vs : a.ks;
-    T* out = static_cast<T*>(isv ? a.vo : a.ko) + (((long long)l * a.B + b) * a.Hkv + g) * (long long)a.Pcap * a.d;
-    for (int y0 = blockIdx.x * a.turns * rows, turn = 0; turn < a.turns && y0 < P; ++turn, y0 += rows) {
+    constexpr int vpr = D / 16, hop = kThreads / vpr, rows = kReadVecs * hop;  // vectors a row; rows apart are a thread's vectors
+    int y = blockIdx.x * a.turns * rows + tid / vpr;
+    if (!fits || y - tid / vpr >= P) return;
+    const int ch = tid % vpr * 16;
+    const unsigned char* pages = (isv ? a.vp : a.kp) + ((long long)l * a.num_pages * a.Hkv + g) * a.page_rows * D + ch;
+    const unsigned char* scales = (isv ? a.vs : a.ks) + ((long long)l * a.num_pages * a.Hkv + g) * (a.page_rows >> a.block_shift);
+    const int page_pitch = a.Hkv * a.page_rows, scale_pitch = a.Hkv * (a.page_rows >> a.block_shift);
+    T* out = static_cast<T*>(isv ? a.vo : a.ko) + ((((long long)l * a.B + b) * a.Hkv + g) * a.Pcap + y) * D + ch;
+    int lp = y / a.page_rows, r = y - lp * a.page_rows;
+    for (int turn = 0; turn < a.turns && y - tid / vpr < P; ++turn) {
         uint4 c[kReadVecs];
         float f[kReadVecs];
         bool there[kReadVecs];
 #pragma unroll
-        for (int i = 0; i < kReadVecs; ++i) {
-            const int e = tid + i * kThreads, y = y0 + e / vpr;
-            there[i] = y < P;
+        for (int i = 0; i < kReadVecs; ++i, y += hop) {
+            const int phys = y < P ? table[lp] : -1;
+            there[i] = phys >= 0 && phys < a.num_pages;
             c[i] = make_uint4(0, 0, 0, 0);
             f[i] = 0.f;
-            if (!there[i]) continue;
-            const int lp = y / a.page_rows, phys = table[lp], r = y - lp * a.page_rows;
-            there[i] = phys >= 0 && phys < a.num_pages;
-            if (!there[i]) continue;
-            const long long plane = ((long long)l * a.num_pages + phys) * a.Hkv + g;
-            c[i] = ld_stream_u4(pages + (plane * a.page_rows + r) * a.d + e % vpr * 16);
-            f[i] = scale_of(scales[plane * (a.page_rows / a.S) + r / a.S]);
+            if (there[i]) {
+                c[i] = ld_stream_u4(pages + ((long long)phys * page_pitch + r) * D);
+                f[i] = scale_of(scales[(long long)phys * scale_pitch + (r >> a.block_shift)]);
+            }
+            lp += a.hop_pages;
+            r += a.hop_rows;
+            if (r >= a.page_rows) {
+                r -= a.page_rows;
+                ++lp;
+            }
         }
 #pragma unroll
         for (int i = 0; i < kReadVecs; ++i) {
@@ -383,9 +419,8 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
                     else w[k + 2] = r;
                 }
             }
+            T* to = out + i * hop * D - me * 16 + me * (16 / (int)sizeof(T));
             if (!there[i]) continue;
-            const int e = tid + i * kThreads;
-            T* to = out + (long long)(y0 + e / vpr) * a.d + e % vpr * 16 - me * 16 + me * (16 / (int)sizeof(T));
 #pragma unroll
             for (int x = 0; x < 2 * X; ++x) {
                 uint32_t z[4];
@@ -393,8 +428,9 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 v = e4m3_values(w[2 * x + k / 2] >> (k % 2 * 16) & 0xffffu);
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(v.x * f[i], v.y * f[i]);
-                        z[k] = *reinterpret_cast<const uint32_t*>(&y);
+                        const float2 p = f2_get(f2(v.x, v.y) * f2(f[i], f[i]));
+                        const __nv_bfloat162 q = __floats2bfloat162_rn(p.x, p.y);
+                        z[k] = *reinterpret_cast<const uint32_t*>(&q);
                     }
                 } else {
 #pragma unroll
@@ -407,7 +443,15 @@ __global__ void __launch_bounds__(kThreads) k_read_quant(const ReadArgs a) {
                 *reinterpret_cast<uint4*>(to + x * 16) = make_uint4(z[0], z[1], z[2], z[3]);
             }
         }
+        out += (long long)kReadVecs * hop * D;
     }
+}
+
+template <typename T>
+static void read_go(int d, dim3 grid, const ReadArgs& a, cudaStream_t st) {
+    if (d == 64) k_read_quant<T, 64><<<grid, kThreads, 0, st>>>(a);
+    else if (d == 128) k_read_quant<T, 128><<<grid, kThreads, 0, st>>>(a);
+    else k_read_quant<T, 256><<<grid, kThreads, 0, st>>>(a);
 }
 
 cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int S, int Pcap, const AttnPaging& pg, ddt_dtype out,
@@ -419,8 +463,11 @@ cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int S, int Pcap, con
     const long long steps = (most + rows - 1) / rows;
     a.turns = steps * 2 * Hkv * L * B > 16384 ? 4 : 1;  // 20 or more an SM's resident CTA
     const dim3 grid((unsigned)((steps + a.turns - 1) / a.turns), 2 * Hkv, L * B);
-    if (out == DDT_BF16) k_read_quant<__nv_bfloat16><<<counted(grid), kThreads, 0, st>>>(a);
-    else k_read_quant<float><<<counted(grid), kThreads, 0, st>>>(a);
+    while ((1 << a.block_shift) < S) ++a.block_shift;
+    a.hop_pages = kThreads / (d / 16) / pg.page_rows;
+    a.hop_rows = kThreads / (d / 16) % pg.page_rows;
+    if (out == DDT_BF16) read_go<__nv_bfloat16>(d, counted(grid), a, st);
+    else read_go<float>(d, counted(grid), a, st);
     return cudaGetLastError();
 }
 
