@@ -34,7 +34,8 @@ struct NormArgs {
     int B, N, Hq, Hkv, rot, tokens;  // tokens a CTA
     int dt, dh;                      // the rows that a CTA takes at a time, as tokens and heads
     float eps, offset;
-    long long qs[4], ks[4];  // strides of the inputs in elements: layer, request, row, head
+    long long qs[3], ks[3];  // strides of the inputs in elements: layer, request, row
+    int q_head, k_head;      // and in bytes: head
     const void* q;
     const void* k;
     const void* qw;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     // four float4 a lane, lane after lane: a quarter warp reads 128 consecutive bytes
     __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16]: two cosines, their sines
     __shared__ float4 s_w[2][4 * LPR];           // offset + weight: of q, of k
-    __shared__ long long s_at[kMaxTokens][2];    // a token's place in q and in k, or -1
+    __shared__ const char* s_at[kMaxTokens][2];  // where a token's head 0 is in q, and would be in k; or null
     const int tid = threadIdx.x, half = a.rot / 2, lanes = a.rot / 16, heads = a.Hq + a.Hkv;
     const unsigned rows = (unsigned)a.B * (unsigned)a.N, first = blockIdx.x * (unsigned)a.tokens;  // (fewer than 2^31)
     const int l = blockIdx.y, nt = (int)min((unsigned)a.tokens, rows - first);
@@ -125,10 +126,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
         const unsigned tok = first + tid, b = tok / (unsigned)a.N, n = tok - b * (unsigned)a.N;
         const int nn = a.n_nodes ? a.n_nodes[b] : a.N;
         const bool live = (int)n < nn && nn <= a.N;
-        s_at[tid][0] = live ? l * a.qs[0] + b * a.qs[1] + n * a.qs[2] : -1;
-        s_at[tid][1] = l * a.ks[0] + b * a.ks[1] + n * a.ks[2];
+        s_at[tid][0] = live ? reinterpret_cast<const char*>(static_cast<const T*>(a.q) + l * a.qs[0] + b * a.qs[1] + n * a.qs[2]) : nullptr;
+        s_at[tid][1] = live ? reinterpret_cast<const char*>(static_cast<const T*>(a.k) + l * a.ks[0] + b * a.ks[1] + n * a.ks[2]) -
+                                  (long long)a.Hq * a.k_head
+                            : nullptr;
     }
     __syncthreads();
+    // (a CTA's rows span less than 2^31 elements)
+    T* const yq = static_cast<T*>(a.qo) + ((long long)l * rows + first) * a.Hq * D + lo;
+    T* const yk = static_cast<T*>(a.ko) + (((long long)l * rows + first) * a.Hkv - a.Hq) * D + lo;
     // a lane group's rows, kThreads / LPR apart: head h of token t
     struct Item {
         int t, h;
@@ -148,13 +154,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     auto fetch = [&](int s) {
         live[s] = false;
         if (ahead.t < nt) {
-            const long long at = s_at[ahead.t][0];
-            if (at >= 0) {
+            const bool isk = ahead.h >= a.Hq;
+            const char* x = s_at[ahead.t][isk];
+            if (x) {
                 live[s] = true;
-                const T* x = ahead.h < a.Hq ? static_cast<const T*>(a.q) + at + ahead.h * a.qs[3]
-                                            : static_cast<const T*>(a.k) + s_at[ahead.t][1] + (ahead.h - a.Hq) * a.ks[3];
-                u[s].load(x + lo);
-                v[s].load(x + hi);
+                x += (long long)ahead.h * (isk ? a.k_head : a.q_head);
+                u[s].load(reinterpret_cast<const T*>(x + lo * (int)sizeof(T)));
+                v[s].load(reinterpret_cast<const T*>(x + hi * (int)sizeof(T)));
             }
         }
         ahead = next(ahead);
@@ -220,11 +226,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
                     q[i] = fma2(q[i], co, p0 * si);
                 }
             }
-            // (a CTA's rows span less than 2^31 elements)
-            T* y = isq ? static_cast<T*>(a.qo) + ((long long)l * rows + first) * a.Hq * D + (at.t * a.Hq + at.h) * D
-                       : static_cast<T*>(a.ko) + ((long long)l * rows + first) * a.Hkv * D + (at.t * a.Hkv + at.h - a.Hq) * D;
-            store_run<T, VEC>(y + lo, p);
-            store_run<T, VEC>(y + hi, q);
+            T* y = (isq ? yq : yk) + (at.t * (isq ? a.Hq : a.Hkv) + at.h) * D;
+            store_run<T, VEC>(y, p);
+            store_run<T, VEC>(y + (hi - lo), q);
         }
     }
 }
@@ -266,9 +270,15 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
     uintptr_t bits = (uintptr_t)q | (uintptr_t)k | (uintptr_t)qw | (uintptr_t)kw | (uintptr_t)qo | (uintptr_t)ko;
     const int qn[4] = {L, B, N, Hq}, kn[4] = {L, B, N, Hkv};
     for (int i = 0; i < 4; ++i) {  // (the stride of a single entry says nothing)
-        a.qs[i] = qn[i] > 1 ? q_stride[i] : 0;
-        a.ks[i] = kn[i] > 1 ? k_stride[i] : 0;
-        bits |= (uintptr_t)(a.qs[i] * esz) | (uintptr_t)(a.ks[i] * esz);
+        const int64_t x = qn[i] > 1 ? q_stride[i] * esz : 0, y = kn[i] > 1 ? k_stride[i] * esz : 0;
+        bits |= (uintptr_t)x | (uintptr_t)y;
+        if (i == 3) {
+            a.q_head = (int)x;
+            a.k_head = (int)y;
+        } else {
+            a.qs[i] = x / esz;
+            a.ks[i] = y / esz;
+        }
     }
     // frequency i as a product of two powers, 16 + 8 of them at most: a power takes the host some 50 ns
     NormFreq fr{};
