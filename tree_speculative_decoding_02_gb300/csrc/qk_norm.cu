@@ -117,9 +117,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     const unsigned rows = (unsigned)a.B * (unsigned)a.N, first = blockIdx.x * (unsigned)a.tokens;  // (fewer than 2^31)
     const int l = blockIdx.y, nt = (int)min((unsigned)a.tokens, rows - first);
     const int c = tid % LPR;
-    // this lane's two runs: of the rotated channels the halves of its pairs, of the others neighbours
+    // this lane's two runs: of the rotated channels the halves of its pairs, of the others too one in each half, so that
+    // neighbouring lanes' runs lie together
     const bool turned = c < lanes;
-    const int lo = turned ? 8 * c : 16 * c, hi = turned ? half + 8 * c : 16 * c + 8;
+    const int rest = (D - a.rot) / 2, lo = turned ? 8 * c : half + 8 * c, hi = lo + (turned ? half : rest);
     const unsigned mask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);  // the lanes of a row, which agree throughout
 
     if (tid < nt) {
@@ -178,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     }
     for (int e = tid; e < 2 * D; e += kThreads) {
         // channel ch is the j-th of its lane: of the low run 0..7, of the high one 8..15
-        const int x = e / D, ch = e % D, k = ch < half ? ch / 8 : (ch < a.rot ? (ch - half) / 8 : ch / 16);
-        const int j = ch < half ? ch % 8 : (ch < a.rot ? 8 + (ch - half) % 8 : ch % 16);
+        const int x = e / D, ch = e % D, of = ch < a.rot ? ch : ch - a.rot, size = ch < a.rot ? half : rest;
+        const int k = (ch < a.rot ? 0 : lanes) + of % size / 8, j = of / size * 8 + ch % 8;
         reinterpret_cast<float*>(s_w[x])[(j / 4 * LPR + k) * 4 + j % 4] =
             a.offset + to_f32(static_cast<const T*>(x ? a.kw : a.qw)[(long long)l * D + ch]);
     }
