@@ -26,6 +26,13 @@
 //   warps 4-7, 8-11 ..  softmax, eight heads a warpgroup, a thread a cached row
 // The split of the rows over the CTAs, the partials and the join are those of decode.cuh.
 // Every wait is bounded, as there.
+//
+// Bound by HBM for groups of up to 8 heads (heads of 128 and 256: 16): 32 requests of 1K to 32K rows, 24 heads over 4 of 256
+// (901 MB), 138 us, 6.5 TB/s; one of 131071 rows, 32 over 8 of 128 (269 MB), 46 us; 2 x 96 of up to 2500 rows, 16 over 16 of
+// 64 (453 MB), 83 us.  A tile is half as many bytes as in bf16 and its softmax as long, so two to four CTAs share an SM (heads
+// of 64, one head a kv head: 98 us with three, 93 with four), and instances for groups of up to 2 and 4 heads leave out what
+// the others would compute for nobody (139 -> 98).  Larger groups are bound by the softmax's instructions, 332 a warp for a
+// tile and eight heads: 16 heads of 64 read 4.1 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
 #include <cuda.h>
 #include <math.h>
 

