@@ -625,8 +625,8 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
 /* ddt_decode_attn_paged_quant -- ddt_decode_attn_paged over that cache, without the sums of the
  * weights: q, k_new, v_new, o, prefix_len, scale, status and workspace (of
  * ddt_decode_attn_paged_quant_workspace bytes) have the same meaning; the new token's own row enters
- * as it is given, unquantised.  A NaN or infinite channel of q makes its head's o NaN, and a NaN of
- * a cached row every o that the row enters.
+ * as it is given, unquantised.  A NaN or infinite channel of q makes its head's o NaN where the prefix
+ * has rows, and a NaN of a cached row every o that the row enters.
  * Precision: scores, exponentials (the hardware's base 2, relative error about 2^-22), sums and o in
  * fp32, rounded once to out_dtype.  The products run on e4m3 operands with fp32 accumulators: the
  * codes as they are, q and the weights as sums of e4m3 parts, each 16 times finer than the
@@ -667,7 +667,7 @@ ddt_status ddt_decode_attn_paged_quant(int n_layers, int B, int Hq, int Hkv, int
  *   q_out [L][B][N][Hq][d], k_out [L][B][N][Hkv][d] (dtype), contiguous.  q_out may be q itself where
  *     q is contiguous, and k_out k; otherwise outputs are apart from one another and from the
  *     inputs (the call is refused otherwise).
- * Precision: fp32 throughout, rounded once; an angle is off by at most 2^-23 for any position.
+ * Precision: fp32 throughout, rounded once; an angle is off by at most 2^-23 + 2^-51 |position|.
  * rot_dim: 0 (no rotation) or a multiple of 16 up to d; theta > 1; eps >= 0; weight_offset 0, or 1
  * for weights stored about zero.  d in {64, 128, 256}; buffers aligned to their elements (faster at
  * 16 bytes, strides included).

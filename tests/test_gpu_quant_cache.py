@@ -137,6 +137,49 @@ def test_bad_requests_are_left_alone():
     assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, gpu[:4]))
 
 
+@pytest.mark.parametrize("L,A", [(1, 1), (2, 1), (1, 20), (1, 3000)])
+def test_no_rows_no_page(L, A):
+    """Requests that append nothing: no page of theirs is looked at, whatever the table says behind the prefix (or in it),
+    in one CTA a request, in several, and where a kernel of its own checks the pages."""
+    c = Q.cache(31, L, 3, 2, 64, [5, 13, 8], 8, 8, cap_rows=A + 24)
+    gpu = Q.to_gpu(c)
+    gpu[4][:2] = torch.tensor([1 << 30, -7], dtype=torch.int32, device="cuda")[:, None]
+    k, v = _rows(31, L, 3, A, 2, 64, BF)
+    count = [0, 0, min(A, 2)]
+    r = ddt.ddt_append_paged_quant(k.cuda(), v.cuda(), *gpu, torch.tensor(count, dtype=torch.int32).cuda())
+    assert r["status"].tolist() == [0, 0, 0] and gpu[5].tolist() == [5, 13, 8 + count[2]]
+    for x, codes, scale in ((k, "k", "ks"), (v, "v", "vs")):
+        Q.append_ref(Q.f64(x), c[codes], c[scale], c["table"], c["lens"], count, None)
+    for have, want in zip(gpu[:4], (c["k"], c["v"], c["ks"], c["vs"])):
+        assert Q.same_codes(have.view(torch.uint8).cpu().numpy(), want).all()
+    # and nothing at all
+    before = [t.view(torch.uint8).clone() for t in gpu[:4]]
+    r = ddt.ddt_append_paged_quant(k.cuda(), v.cuda(), *gpu, torch.zeros(3, dtype=torch.int32).cuda())
+    assert r["status"].tolist() == [0, 0, 0] and all(torch.equal(x.view(torch.uint8), y) for x, y in zip(gpu[:4], before))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_prompts(dtype):
+    """Rows over hundreds of pages, where the pages are checked by a kernel of its own: beside requests that are refused (a
+    page that does not exist at the far end, lengths and counts that are wrong) and ones that append nothing."""
+    lens, count = [3, 40, 0, -1, 0, 9, 2200], [2300, 2100, 0, 100, 2301, 2300, 300]
+    c = Q.cache(32, 1, 7, 2, 64, [max(0, p) for p in lens], 8, 8, cap_rows=2400)
+    c["lens"] = lens
+    k, v = _rows(32, 1, 7, 2300, 2, 64, dtype)
+    k[:, 0, 1000, 0, 3] = float("inf")
+    gpu = Q.to_gpu(c)
+    gpu[4][5, 2300 // 8] = 1 << 29
+    r = ddt.ddt_append_paged_quant(k.cuda(), v.cuda(), *gpu, torch.tensor(count, dtype=torch.int32).cuda())
+    assert r["status"].tolist() == [0, 0, 0, 3, 1, 1, 3]
+    good = [n if s == 0 else 0 for n, s in zip(count, r["status"].tolist())]
+    assert gpu[5].tolist() == [p + n for p, n in zip(lens, good)]
+    c["lens"] = [max(0, p) for p in lens]
+    for x, codes, scale in ((k, "k", "ks"), (v, "v", "vs")):
+        Q.append_ref(Q.f64(x), c[codes], c[scale], c["table"], c["lens"], good, None)
+    for have, want in zip(gpu[:4], (c["k"], c["v"], c["ks"], c["vs"])):
+        assert Q.same_codes(have.view(torch.uint8).cpu().numpy(), want).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("d,page,block,Hkv", [(64, 8, 8, 3), (128, 16, 16, 2), (256, 64, 16, 4), (64, 192, 64, 1), (128, 128, 128, 1)])
 def test_read_back(dtype, d, page, block, Hkv):
@@ -192,3 +235,10 @@ def test_large_offsets():
         assert (np.abs(got[1, :, :70] - x[1]) <= np.abs(x[1]) * 2.0 ** -4 + 6 * 2.0 ** -17).all()
         assert (np.abs(got[0, :, 60:68] - x[0, :, :8]) <= np.abs(x[0, :, :8]) * 2.0 ** -4 + 6 * 2.0 ** -17).all()
         assert (got[0, :, :60] == 0).all()
+    # and attention over them
+    q = synth.normal((1, 2, 8, d), g=synth.gen(30, 84), dtype=BF).cuda()
+    o = ddt.ddt_decode_attn_paged_quant(q, None, None, *pools, table, plen, scale=d ** -0.5, out_dtype=F32)["o"]
+    for b, n in enumerate((68, 70)):
+        s = torch.einsum("ghd,gnd->ghn", q[0, b].double().reshape(Hkv, 2, d), out[0][0, b, :, :n].double()) * d ** -0.5
+        want = (torch.softmax(s, -1) @ out[1][0, b, :, :n].double()).reshape(8, d)
+        assert (o[0, b].double() - want).abs().max() <= 1e-3     # (weights to 2^-16, values up to 6, outputs in fp32)

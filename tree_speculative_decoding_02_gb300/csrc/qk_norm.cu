@@ -11,8 +11,8 @@
 // one layer; their cosines are formed once in shared memory for all heads, while the first rows are
 // on their way.
 // An angle is a fraction of a turn in 64-bit fixed point: frequency / 2 pi as a fraction of 2^64
-// (from the host) times the position, modulo 2^64, is the reduced angle with no rounding but the
-// table's, for any position; its upper half goes to sincospi.  No fp64, which is slow here.
+// (from the host, in fp64) times the position, modulo 2^64, is the reduced angle with no rounding but
+// the table's; its upper half goes to sincospi.  No fp64 on the device, where it is slow.
 //
 // Bound by HBM: 16 layers of 32 x 65 tree rows (three quarters of them nodes), 24 + 4 heads of 256, bf16 (716 MB), 129 us,
 // 5.5 TB/s; 169 with 64-bit divisions and half the instructions unpaired.  A row is a chain of a few hundred cycles (sum, four

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
         a.status[b] = err;
         if (a.solo && a.advance && !err) a.prefix_len[b] = P + n;
     }
-    if (err) return;
+    if (err || n == 0) return;  // (without rows no page has been looked at)
     const int32_t* table = a.table + (long long)b * a.max_pages;
     const int item = group * (kWarps / a.wpi) + warp / a.wpi, part = warp % a.wpi;
     const bool real = item < 2 * a.Hkv;
