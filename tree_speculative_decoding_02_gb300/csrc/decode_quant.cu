@@ -59,7 +59,7 @@ struct QuantCfg {
     static constexpr int kStageBytes = kDecTile * D;      // a K or V tile
     static constexpr int NQ = QP * HP;                    // N of Q K^T
     static constexpr int NP = pow2_at_least(PP * HP, 32); // N of P V, and the bytes of a row of P
-    static constexpr int kCtas = QP == 6 ? (D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? (GH < 8 ? 4 : 3) : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
+    static constexpr int kCtas = QP == 6 ? (HP == 8 && D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? (GH < 8 ? 4 : 3) : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
     static constexpr int kQBufs = kCtas == 2 && D == 256 ? 1 : 2;
     static constexpr int kQBytes = NQ * D;
     static constexpr int kPBytes = NP * kDecTile;
@@ -598,7 +598,7 @@ cudaError_t quant_go(DecodeParams& p, const DecQuantArgs& a, const CUtensorMap* 
 
 template <int D>
 cudaError_t quant_d_go(DecodeParams& p, ddt_dtype in, const DecQuantArgs& a, const CUtensorMap* maps, cudaStream_t st) {
-    if (in == DDT_F32) return quant_go<float, D, 8, 8, 6, 6>(p, a, maps, st);
+    if (in == DDT_F32) return p.hbs == 8 ? quant_go<float, D, 8, 8, 6, 6>(p, a, maps, st) : quant_go<float, D, 16, 8, 6, 6>(p, a, maps, st);
     return p.G <= 2      ? quant_go<__nv_bfloat16, D, 8, 2, 2, 4>(p, a, maps, st)
            : p.G <= 4    ? quant_go<__nv_bfloat16, D, 8, 4, 2, 4>(p, a, maps, st)
            : p.hbs == 8  ? quant_go<__nv_bfloat16, D, 8, 8, 2, 4>(p, a, maps, st)
@@ -608,8 +608,8 @@ cudaError_t quant_d_go(DecodeParams& p, ddt_dtype in, const DecQuantArgs& a, con
 
 }  // namespace
 
-// heads a block: the smallest of 8, 16 and 32 that holds the group; 8 where the parts are six
-int decode_quant_heads(int G, ddt_dtype in) { return G <= 8 || in == DDT_F32 ? 8 : (G <= 16 ? 16 : 32); }
+// heads a block: the smallest of 8, 16 and 32 that holds the group (16 at most where the parts are six: N of P V)
+int decode_quant_heads(int G, ddt_dtype in) { return G <= 8 ? 8 : (G <= 16 || in == DDT_F32 ? 16 : 32); }
 
 // p.C: SMs on entry, CTAs on return
 cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, int block, const uint8_t* ks, const uint8_t* vs, cudaStream_t st) {
