@@ -660,8 +660,8 @@ ddt_status ddt_decode_attn_paged_quant(int n_layers, int B, int Hq, int Hkv, int
  *   first rot_dim channels turned by position[b][n] * theta^(-2i/rot_dim) as in ddt_rope_tree.
  *   q [L][B][N][Hq][d], k [L][B][N][Hkv][d] (dtype) with consecutive channels and any strides, in
  *     elements, of their first four dimensions: q_stride, k_stride, HOST arrays of 4 (slices of one
- *     projection, for instance; the last, a head's, below 2^31 bytes); q_weight, k_weight [L][d]
- *     (dtype).
+ *     projection, for instance; the last, a head's, times Hq + Hkv below 2^31 bytes); q_weight,
+ *     k_weight [L][d] (dtype).
  *   position [B][N] int32; n_nodes [B] int32 or NULL.  Rows past n_nodes[b] are left as they are, and
  *     all of a request's whose n_nodes[b] is above N.
  *   q_out [L][B][N][Hq][d], k_out [L][B][N][Hkv][d] (dtype), contiguous.  q_out may be q itself where

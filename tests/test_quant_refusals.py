@@ -99,7 +99,7 @@ def test_norm(lib):  # noqa: F811
                *(dict([(x, at(257))]) for x in ("q", "k", "qw", "kw", "qo", "ko")), dict(qs=_strides(5120, 2560, -512, 64))):
         assert _norm(lib, **kw) == INVALID, kw
     for kw in (dict(d=80), dict(rot=8), dict(rot=24), dict(L=70000), dict(B=1 << 16, N=1 << 16), dict(qs=_strides(5120, 1 << 60, 512, 64)),
-               dict(ks=_strides(1280, 640, 128, 1 << 30))):
+               dict(ks=_strides(1280, 640, 128, 1 << 30)), dict(qs=_strides(5120, 2560, 512, 107374177))):
         assert _norm(lib, **kw) == UNSUPPORTED, kw
     # in place over rows that lie otherwise than the output's
     q = at(1 << 36)

@@ -573,7 +573,7 @@ ddt_status ddt_qk_norm_rope(int n_layers, int B, int N, int Hq, int Hkv, int d, 
         same[x] = in[x] == out[x];
         for (int i = 3; i >= 0; --i) {
             if (n[x][i] > 1 && stride[x][i] < 0) return DDT_ERR_INVALID_ARG;
-            if (n[x][i] > 1 && stride[x][i] > (i == 3 ? 0x7fffffff / esz : (INT64_C(1) << 56) / n[x][i])) return DDT_ERR_UNSUPPORTED;
+            if (n[x][i] > 1 && stride[x][i] > (i == 3 ? (0x7fffffff / esz - d) / (Hq + Hkv) : (INT64_C(1) << 56) / n[x][i])) return DDT_ERR_UNSUPPORTED;
             if (n[x][i] > 1) last += (n[x][i] - 1) * stride[x][i];
             same[x] = same[x] && (n[x][i] == 1 || stride[x][i] == dense);
             dense *= n[x][i];

@@ -117,7 +117,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     // four float4 a lane, lane after lane: a quarter warp reads 128 consecutive bytes
     __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16]: two cosines, their sines
     __shared__ float4 s_w[2][4 * LPR];           // offset + weight: of q, of k
-    __shared__ const char* s_at[kMaxTokens][2];  // where a token's head 0 is in q, and would be in k; or null
+    // where a token's head 0 is in q, and would be in k, or null; the same of the outputs
+    __shared__ const char* s_at[kMaxTokens][2];
+    __shared__ char* s_to[kMaxTokens][2];
     const int tid = threadIdx.x, half = a.rot / 2, lanes = a.rot / 16, heads = a.Hq + a.Hkv;
     const unsigned rows = (unsigned)a.B * (unsigned)a.N, first = blockIdx.x * (unsigned)a.tokens;  // (fewer than 2^31)
     const int l = blockIdx.y, nt = (int)min((unsigned)a.tokens, rows - first);
@@ -136,40 +138,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
         s_at[tid][1] = live ? reinterpret_cast<const char*>(static_cast<const T*>(a.k) + l * a.ks[0] + b * a.ks[1] + n * a.ks[2]) -
                                   (long long)a.Hq * a.k_head
                             : nullptr;
+        const long long row = (long long)l * rows + tok;
+        s_to[tid][0] = reinterpret_cast<char*>(static_cast<T*>(a.qo) + row * a.Hq * D);
+        s_to[tid][1] = reinterpret_cast<char*>(static_cast<T*>(a.ko) + (row * a.Hkv - a.Hq) * D);
     }
     __syncthreads();
-    // (a CTA's rows span less than 2^31 elements)
-    T* const yq = static_cast<T*>(a.qo) + ((long long)l * rows + first) * a.Hq * D + lo;
-    T* const yk = static_cast<T*>(a.ko) + (((long long)l * rows + first) * a.Hkv - a.Hq) * D + lo;
-    // a lane group's rows, kThreads / LPR apart: head h of token t
-    struct Item {
-        int t, h;
-    };
-    auto next = [&](Item x) {
-        x.t += a.dt;
-        x.h += a.dh;
-        if (x.h >= heads) {
-            x.h -= heads;
-            ++x.t;
-        }
-        return x;
-    };
-    Item now{tid / LPR / heads, tid / LPR % heads}, ahead = now;
+    // a lane group's rows, kThreads / LPR apart: head h of token t is the next to be fetched
+    int t = tid / LPR / heads, h = tid / LPR % heads;
+    const int at_lo = lo * (int)sizeof(T), gap = (hi - lo) * (int)sizeof(T);
     Run<T, VEC> u[2], v[2];  // two rows are on their way while one is worked on
-    bool live[2];
+    char* to[2];             // or null: no such row
+    int of[2];               // its place among the cosines; and k's sign bit
     auto fetch = [&](int s) {
-        live[s] = false;
-        if (ahead.t < nt) {
-            const bool isk = ahead.h >= a.Hq;
-            const char* x = s_at[ahead.t][isk];
+        to[s] = nullptr;
+        if (t < nt) {
+            const bool isk = h >= a.Hq;
+            const char* x = s_at[t][isk];
             if (x) {
-                live[s] = true;
-                x += (long long)ahead.h * (isk ? a.k_head : a.q_head);
-                u[s].load(reinterpret_cast<const T*>(x + lo * (int)sizeof(T)));
-                v[s].load(reinterpret_cast<const T*>(x + hi * (int)sizeof(T)));
+                x += h * (isk ? a.k_head : a.q_head) + at_lo;  // (a token's heads span less than 2^31 bytes)
+                to[s] = s_to[t][isk] + (h * D * (int)sizeof(T) + at_lo);
+                of[s] = (t * 4 * lanes + c) | (isk ? 1 << 31 : 0);
+                u[s].load(reinterpret_cast<const T*>(x));
+                v[s].load(reinterpret_cast<const T*>(x + gap));
             }
         }
-        ahead = next(ahead);
+        t += a.dt;
+        h += a.dh;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
+        }
     };
     fetch(0);
     fetch(1);
@@ -190,15 +188,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
             a.offset + to_f32(static_cast<const T*>(x ? a.kw : a.qw)[(long long)l * D + ch]);
     }
     __syncthreads();
-    while (now.t < nt) {
+    const int steps = (nt * heads + kThreads / LPR - 1) / (kThreads / LPR);
+    for (int step = 0; step < steps; step += 2) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const Item at = now;
-            now = next(now);
-            if (!live[s]) {
+            if (!to[s]) {
                 fetch(s);
                 continue;
             }
+            T* const y = reinterpret_cast<T*>(to[s]);
+            const bool isk = of[s] < 0;
+            const float4* cs = s_cs + (of[s] & 0x7fffffff);
             F2 p[4], q[4], sum = f2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
             const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
             const F2 rr = f2(r, r);
-            const bool isq = at.h < a.Hq;
-            const float4* w = s_w[!isq] + c;
+            const float4* w = s_w[isk] + c;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float4 x = w[i * LPR], z = w[(2 + i) * LPR];
@@ -223,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
                 q[2 * i + 1] = q[2 * i + 1] * (rr * f2(z.z, z.w));
             }
             if (turned) {
-                const float4* cs = s_cs + at.t * 4 * lanes + c;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 k = cs[i * lanes];
@@ -232,9 +230,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
                     q[i] = fma2(q[i], co, p0 * si);
                 }
             }
-            T* y = (isq ? yq : yk) + (at.t * (isq ? a.Hq : a.Hkv) + at.h) * D;
             store_run<T, VEC>(y, p);
-            store_run<T, VEC>(y + (hi - lo), q);
+            store_run<T, VEC>(reinterpret_cast<T*>(reinterpret_cast<char*>(y) + gap), q);
         }
     }
 }
