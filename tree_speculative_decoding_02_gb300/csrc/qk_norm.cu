@@ -14,10 +14,10 @@
 // (from the host, in fp64) times the position, modulo 2^64, is the reduced angle with no rounding but
 // the table's; its upper half goes to sincospi.  No fp64 on the device, where it is slow.
 //
-// Bound by HBM: 16 layers of 32 x 65 tree rows (three quarters of them nodes), 24 + 4 heads of 256, bf16 (716 MB), 129 us,
-// 5.5 TB/s; 169 with 64-bit divisions and half the instructions unpaired.  A row is a chain of a few hundred cycles (sum, four
-// exchanges, root, products), and two rows a lane group are on their way meanwhile; more, or two chains side by side, do not
-// fit in the registers of four CTAs an SM.
+// Bound by HBM: 16 layers of 32 x 65 tree rows (three quarters of them nodes), 24 + 4 heads of 256, bf16 (716 MB), 121 us,
+// 5.9 TB/s; 169 with 64-bit divisions and half the instructions unpaired.  A row is a chain of a few hundred cycles (sum, four
+// exchanges, root, products), and two rows a lane group are on their way meanwhile; three or four are no faster, and two
+// chains side by side do not fit in the registers of four CTAs an SM.
 #include <math.h>
 
 #include "common.cuh"
@@ -51,25 +51,27 @@ struct NormArgs {
     void* ko;
 };
 
-// 8 channels as they lie in memory (which may be what is written later: not the read-only path)
-template <typename T, bool VEC>
+// 8 channels as they lie in memory
+template <typename T>
 struct Run {
     static constexpr int W = 8 * (int)sizeof(T) / 4;
     uint32_t w[W];
-    __device__ __forceinline__ void load(const T* p) {
+    // VEC: from 16-byte words, else aligned to the elements (not by the read-only path: it may be written later)
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void* p) {
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
-                const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                const uint4 u = static_cast<const uint4*>(p)[i / 4];
                 w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (sizeof(T) == 4) {
-                    w[i % W] = reinterpret_cast<const uint32_t*>(p)[i];
+                    w[i % W] = static_cast<const uint32_t*>(p)[i];
                 } else {
-                    const uint32_t h = reinterpret_cast<const uint16_t*>(p)[i];
+                    const uint32_t h = static_cast<const uint16_t*>(p)[i];
                     w[i / 2] = i % 2 ? w[i / 2] | h << 16 : h;
                 }
             }
@@ -80,6 +82,9 @@ struct Run {
         return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
 };
+__device__ __forceinline__ void copy16(uint4* to, const char* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+}
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_run(T* p, const F2 (&x)[4]) {
@@ -146,9 +151,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     // a lane group's rows, kThreads / LPR apart: head h of token t is the next to be fetched
     int t = tid / LPR / heads, h = tid / LPR % heads;
     const int at_lo = lo * (int)sizeof(T), gap = (hi - lo) * (int)sizeof(T);
-    Run<T, VEC> u[2], v[2];  // two rows are on their way while one is worked on
-    char* to[2];             // or null: no such row
-    int of[2];               // its place among the cosines; and k's sign bit
+    // Two rows a lane group are on their way while one is worked on: bf16 words by asynchronous copies, every lane its own
+    // (in registers 128 us, so 121; fp32, whose runs are two words each, 21 and 25 us for the 4413 tokens)
+    constexpr bool kAsync = VEC && sizeof(T) == 2;
+    __shared__ uint4 s_rows[kAsync ? 4 * kThreads : 1];
+    uint4* const mine = s_rows + (kAsync ? tid : 0);
+    Run<T> u[2], v[2];
+    char* to[2];  // or null: no such row
+    int of[2];    // its place among the cosines; and k's sign bit
     auto fetch = [&](int s) {
         to[s] = nullptr;
         if (t < nt) {
@@ -158,10 +168,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
                 x += h * (isk ? a.k_head : a.q_head) + at_lo;  // (a token's heads span less than 2^31 bytes)
                 to[s] = s_to[t][isk] + (h * D * (int)sizeof(T) + at_lo);
                 of[s] = (t * 4 * lanes + c) | (isk ? 1 << 31 : 0);
-                u[s].load(reinterpret_cast<const T*>(x));
-                v[s].load(reinterpret_cast<const T*>(x + gap));
+                if (kAsync) {
+                    copy16(mine + 2 * s * kThreads, x);
+                    copy16(mine + (2 * s + 1) * kThreads, x + gap);
+                } else {
+                    u[s].template load<VEC>(x);
+                    v[s].template load<VEC>(x + gap);
+                }
             }
         }
+        if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
         t += a.dt;
         h += a.dh;
         if (h >= heads) {
@@ -192,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     for (int step = 0; step < steps; step += 2) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+            if (kAsync) asm volatile("cp.async.wait_group 1;" ::: "memory");
             if (!to[s]) {
                 fetch(s);
                 continue;
@@ -199,6 +216,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
             T* const y = reinterpret_cast<T*>(to[s]);
             const bool isk = of[s] < 0;
             const float4* cs = s_cs + (of[s] & 0x7fffffff);
+            if (kAsync) {
+                u[s].template load<true>(mine + 2 * s * kThreads);
+                v[s].template load<true>(mine + (2 * s + 1) * kThreads);
+            }
             F2 p[4], q[4], sum = f2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
