@@ -473,7 +473,11 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
 // eighth of the table's rows to all of them, 16 requests of up to 1000 rows, 32 heads over 8 of 128,
 // take 12.5 and 15.1 us; one of 160 shapes is slower as clusters (fp32, 16 units of 256, 1000 rows:
 // 26.7 and 22.2 us).
-cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
+// A tile of an 8-bit cache is half of bf16's bytes, and the second kernel as long: 1024 and 896.  24 heads over 4 of 256, 4
+// requests of 4000 rows 13.0 and 15.9 us, 16 of 2000 14.8 and 19.5; 32 over 8 of 128, one request of 8000 rows (6.3 tiles of
+// excess) 11.5 and 13.0, four 13.2 and 17.9, 16 of 2000 14.1 and 17.2; with lengths from an eighth of those on the gains are
+// larger; 24 over 4 of 256, one request of 8000 rows (7 tiles of excess) 17.0 and 14.4.
+cudaLaunchConfig_t decode_config(DecodeParams& p, DecodeSmall small, int ctas, int threads, int smem, cudaLaunchAttribute& at,
                                  cudaStream_t st) {
     p.C *= ctas;
     const long units = (long)p.L * p.B * p.Hkv;
@@ -481,7 +485,7 @@ cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threa
     int cl = 1;
     while (cl < 8 && units * 2 * cl <= (cl < 4 ? p.C : p.C - p.C / (ctas == 1 ? 4 : 8)) && cl < nt) cl *= 2;
     const double tiles = (nt + cl - 1) / cl, even = (double)units * nt / p.C;
-    p.cl = p.HB == 1 && units * cl <= p.C && tiles * p.d <= (fp32 ? 256. : 512.) && (tiles - (even > 1. ? even : 1.)) * p.d <= (fp32 ? 96. : 384.) ? cl : 0;
+    p.cl = p.HB == 1 && units * cl <= p.C && tiles * p.d <= small.most && (tiles - (even > 1. ? even : 1.)) * p.d <= small.excess ? cl : 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(counted(p.cl ? (unsigned)(units * cl) : (unsigned)p.C));
     cfg.blockDim = dim3(threads);
@@ -502,7 +506,7 @@ static cudaError_t simt_go(DecodeParams& p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k_decode_simt<D, HBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    cudaLaunchConfig_t cfg = decode_config(p, true, 2, kSimtThreads, smem, at, st);
+    cudaLaunchConfig_t cfg = decode_config(p, DecodeSmall{256., 96.}, 2, kSimtThreads, smem, at, st);
     return cudaLaunchKernelEx(&cfg, k_decode_simt<D, HBS>, p);
 }
 template <int D>

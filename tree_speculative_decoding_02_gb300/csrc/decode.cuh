@@ -398,7 +398,10 @@ cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
 int decode_quant_heads(int G, ddt_dtype in);
 cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, int block, const uint8_t* ks, const uint8_t* vs,
                                       cudaStream_t st);
-cudaLaunchConfig_t decode_config(DecodeParams& p, bool fp32, int ctas, int threads, int smem, cudaLaunchAttribute& at,
+struct DecodeSmall {
+    double most, excess;  // channels of a CTA's rows, in tiles, and of those above an even split's, up to which a call is small
+};
+cudaLaunchConfig_t decode_config(DecodeParams& p, DecodeSmall small, int ctas, int threads, int smem, cudaLaunchAttribute& at,
                                  cudaStream_t st);
 
 }  // namespace ddt

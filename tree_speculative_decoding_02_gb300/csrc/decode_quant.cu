@@ -592,7 +592,7 @@ cudaError_t quant_go(DecodeParams& p, const DecQuantArgs& a, const CUtensorMap* 
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    cudaLaunchConfig_t cfg = decode_config(p, false, Cfg::kCtas, Cfg::kThreads, Cfg::kSmem, at, st);
+    cudaLaunchConfig_t cfg = decode_config(p, DecodeSmall{1024., 896.}, Cfg::kCtas, Cfg::kThreads, Cfg::kSmem, at, st);
     return cudaLaunchKernelEx(&cfg, kernel, p, a, maps[0], maps[1]);
 }
 
