@@ -66,13 +66,13 @@ struct QuantCfg {
     static constexpr int kMB = D > 128 ? D / 128 : 1;     // M blocks of P V
     static constexpr int kOCol = 2 * NQ;                  // tensor memory: S x 2, O
     static constexpr int kTmemCols = pow2_at_least(2 * NQ + kMB * NP, 32);
-    static constexpr int kFixed = 1024 + kQBufs * kQBytes + 2 * kPBytes + 640 + (8 + 4 * 2 + 4) * HP * 4;
+    static constexpr int kFixed = 1024 + kQBufs * kQBytes + 2 * kPBytes + 1408 + (8 + 4 * 2 + 4) * HP * 4;
     static constexpr int kRing = (228 * 1024 / kCtas - 1024 - 256 - kFixed) / kStageBytes;
     static constexpr int kStages = kRing > 12 ? 12 : kRing;
     static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory");
     static_assert(kCtas * kTmemCols <= 512, "tensor memory");
-    static_assert((2 * kStages + 15) * 8 + 40 + 4 * 64 <= 640, "barriers and scales");
+    static_assert((2 * kStages + 15) * 8 + 40 + 15 + 4 * 256 <= 1408, "barriers and scales");
     // bad_tile and q_unit are kept for 8 tiles (segments): the producer is up to 6 tiles ahead of the products, they two of
     // the softmax
     static_assert(kStages <= 12, "rings of 8");
@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     int* bad_tile = abort_flag + 1;                            // [8] a page of the tile does not exist
-    int* scales = bad_tile + 8;                                // [4][16] a tile's scales by block: K's byte, V's << 8
+    // [4][16] a tile's scales by block: 2^a, v, 2^-v, and V's byte of the segment's first row
+    float4* scales = reinterpret_cast<float4*>(smem_raw + (reinterpret_cast<unsigned char*>(bad_tile + 8) - smem_raw + 15) / 16 * 16);
     float* q_unit = reinterpret_cast<float*>(scales + 4 * 16);  // [8][HP] log2 scores of a unit of Q K^T, by segment
     float* xm = q_unit + 8 * HP;                               // [2][4][HP] warps' tile maxima
     float* sm_l = xm + 2 * 4 * HP;                             // [4][HP] warps' sums of a segment
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 const int pos = t * kDecTile + lane * a.block;
                 return lane < n_blk && pos < w.P ? table[pos / p.page_rows] : -1;
             };
-            int phys = entry(w.t);
+            int phys = entry(w.t), base = 127;
             for (int t = w.t; t < w.t + n_seg; ++t, ++j) {
                 const bool good = phys >= 0 && phys < p.num_pages;
                 const int in = (t * kDecTile + lane * a.block) % p.page_rows / a.block;
@@ -365,7 +366,13 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 // at most two tiles ahead of the softmax, so no slot of four is written that it still reads
                 if (j >= 2) ok = __all_sync(kFull, tc::mbar_wait(p_full + (j & 1), ((j - 2) >> 1) & 1, abort));
                 if (!ok) break;
-                if (lane < n_blk) scales[(j & 3) * 16 + lane] = (int)(kb | vb << 8);
+                if (t == w.t) {
+                    const int first = __shfl_sync(kFull, (int)vb, 0);
+                    base = first ? first : 127;
+                }
+                const int dv = vb ? max(-126, min(126, (int)vb - base)) : 0;  // (a block of zeros: any scale)
+                if (lane < n_blk)
+                    scales[(j & 3) * 16 + lane] = make_float4(scale_of(kb), (float)dv, __int_as_float((127 - dv) << 23), __int_as_float(base));
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x_full + (j & 3));
             }
@@ -398,13 +405,12 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 bool above = false;  // a score is far above its head's reference
                 if (ok) {
                     tc::tc_fence_after();
-                    const int x = scales[(j & 3) * 16 + my_block], vb = x >> 8;
-                    if (i == 0 && scales[(j & 3) * 16] >> 8) base = scales[(j & 3) * 16] >> 8;
-                    const int dv = vb ? max(-126, min(126, vb - base)) : 0;  // (a block of zeros: any scale)
-                    const F2 k_unit = f2(scale_of(x & 255), scale_of(x & 255));
-                    const float add = r < n ? (float)dv : -INFINITY;  // a row past the prefix: weight 0
+                    const float4 x = scales[(j & 3) * 16 + my_block];
+                    const F2 k_unit = f2(x.x, x.x);
+                    const float add = r < n ? x.y : -INFINITY;  // a row past the prefix: weight 0
                     const F2 v_add = f2(add, add);
-                    v_back = __int_as_float((127 - dv) << 23);
+                    v_back = x.z;
+                    base = __float_as_int(x.w);
                     uint32_t sr[QP][8];
 #pragma unroll
                     for (int y = 0; y < QP; ++y) tmem_ld8(tmem + lane_base + (j & 1) * NQ + y * HP + hg, sr[y]);
