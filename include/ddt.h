@@ -566,7 +566,7 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
  *     ddt_tree_attn_paged;
  *   k_scale, v_scale [L][num_pages][Hkv][page_size / block] bytes: `block` consecutive rows of
  *     a head share the scale 2^(byte - 127) (an E8M0 byte); a row's value is code * scale.
- *     Byte 0 marks a block whose rows so far are all zero.
+ *     Byte 0 marks a block whose rows so far have no finite channels but zeros.
  *   block: 8, 16, 32, 64 or 128, and a divisor of page_size.  Hkv * page_size * d < 2^31.
  * The byte of a block is that of the smallest e in [-100, 120] with max|x| <= 448 * 2^e over the
  * finite channels of its rows so far: nothing saturates.  A channel above 2^-13 of its block's

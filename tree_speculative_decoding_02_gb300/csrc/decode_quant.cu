@@ -32,7 +32,7 @@
 // 64 (453 MB), 83 us.  A tile is half as many bytes as in bf16 and its softmax as long, so two to four CTAs share an SM (heads
 // of 64, one head a kv head: 98 us with three, 93 with four), and instances for groups of up to 2 and 4 heads leave out what
 // the others would compute for nobody (139 -> 98).  Larger groups are bound by the softmax's instructions, 332 a warp for a
-// tile and eight heads: 16 heads of 64 read 4.1 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
+// tile and eight heads: 16 heads of 64 read 4.2 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
 #include <cuda.h>
 #include <math.h>
 

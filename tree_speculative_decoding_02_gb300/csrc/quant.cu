@@ -2,7 +2,7 @@
 // as they are written, and ddt_read_paged_quant, which reads them back.
 //
 // A row's channels are e4m3 codes; a block of S tokens of one head shares a power of two as its
-// scale, one byte: value = code * 2^(byte - 127), and byte 0 marks a block whose rows are all zero.
+// scale, one byte: value = code * 2^(byte - 127), and byte 0 marks a block without finite channels but zeros.
 // A power of two because e4m3 is a floating-point format: a finer scale would move the rounding
 // steps, not narrow them (a value keeps 4 significant bits wherever it lies between 2^-6 and 448 of
 // its block's unit), and rescaling a block that a later, larger row joins is exact but for codes
@@ -35,7 +35,7 @@ struct AppendArgs {
     int wpi;          // warps an item (a block's K or V rows of one head)
     int run, groups;  // blocks a CTA; CTAs that share a block's items
     int advance, solo;  // solo: one CTA has all of a request
-    int checked;      // the status is there already
+    int checked;      // a kernel of its own looks at the pages
     const void* k;
     const void* v;
     const int32_t* node;   // or null
@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
 }
 
 // grid (runs of blocks x item groups, 1, L * B).  A CTA takes a few blocks of one request and layer, one after
-// another; wpi of its warps an item.  Up to kChunk vectors a lane stay in registers between the maximum and the
-// codes; items of more (blocks of 128 rows of 256 channels) are read twice.
+// another; wpi of its warps an item (a block's K or V rows of one head).  Up to kChunk vectors a lane stay in registers
+// between the maximum and the codes; items of more (blocks of 128 rows of 256 channels, a few rows of many requests) are
+// read twice.
 template <typename T, int D, bool NODE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_quant(const AppendArgs a) {
     __shared__ float s_max[2][kWarps];
