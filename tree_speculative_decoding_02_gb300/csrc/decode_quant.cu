@@ -21,7 +21,7 @@
 //
 //   warp 0      producer: block-table entries, TMA of K and V tiles into one ring
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
-//   warp 2      queries: the parts of a segment's heads
+//   warp 2      queries: the parts of a segment's heads (for 16 heads or more and one CTA an SM three more warps, the last)
 //   warp 3      scales: the bytes of a tile's blocks, two tiles ahead of the softmax
 //   warps 4-7, 8-11 ..  softmax, eight heads a warpgroup, a thread a cached row
 // The split of the rows over the CTAs, the partials and the join are those of decode.cuh.
@@ -32,7 +32,7 @@
 // 64 (453 MB), 83 us.  A tile is half as many bytes as in bf16 and its softmax as long, so two to four CTAs share an SM (heads
 // of 64, one head a kv head: 98 us with three, 93 with four), and instances for groups of up to 2 and 4 heads leave out what
 // the others would compute for nobody (139 -> 98).  Larger groups are bound by the softmax's instructions, 332 a warp for a
-// tile and eight heads: 16 heads of 64 read 4.2 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
+// tile and eight heads: 16 heads of 64 read 4.3 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
 #include <cuda.h>
 #include <math.h>
 
@@ -53,13 +53,17 @@ constexpr int pow2_at_least(int x, int y) { return x <= y ? y : pow2_at_least(x,
 template <int D, int HP, int GH, int QP, int PP>
 struct QuantCfg {
     static constexpr int kGroups = HP / 8;                // softmax warpgroups
-    static constexpr int kThreads = 128 + 128 * kGroups;
     static constexpr int kRow = D < 128 ? D : 128;        // bytes of a swizzled row
     static constexpr int kBlocks = D / kRow;              // of a cached row
     static constexpr int kStageBytes = kDecTile * D;      // a K or V tile
     static constexpr int NQ = QP * HP;                    // N of Q K^T
     static constexpr int NP = pow2_at_least(PP * HP, 32); // N of P V, and the bytes of a row of P
     static constexpr int kCtas = QP == 6 ? (HP == 8 && D < 256 ? 2 : 1) : HP == 8 ? (D == 64 ? (GH < 8 ? 4 : 3) : 2) : (HP == 16 && D < 256 ? 2 : 1);  // an SM
+    // warps of queries, those but the first behind the softmax.  One takes 4 us for 16 heads of 256, and longer than the tiles
+    // of a short segment (96 requests of up to 493 rows, 64 heads over 4: 40 us with one, 29 with four; 64 over 2: 38 and 26).
+    // Where a second CTA shares the SM, more of them would take registers from the softmax (16 heads of 64: 141 us, 151).
+    static constexpr int kQWarps = kCtas == 1 && HP > 8 ? 4 : 1;
+    static constexpr int kThreads = 128 + 128 * kGroups + 32 * (kQWarps - 1);
     static constexpr int kQBufs = kCtas == 2 && D == 256 ? 1 : 2;
     static constexpr int kQBytes = NQ * D;
     static constexpr int kPBytes = NP * kDecTile;
@@ -88,7 +92,58 @@ struct DecQuantArgs {
     const uint8_t* vs;
 };
 
-__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+// E channels of a query as they lie in memory (2, 4 or 8; aligned to their bytes)
+template <typename T, int E>
+struct QueryRun {
+    static constexpr int W = E * (int)sizeof(T) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (W == 1) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x; w[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    // bits of the largest |x| (integers order as the values do)
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = sizeof(T) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return sizeof(T) == 4 ? m : max(m & 0xffffu, m >> 16) << 16;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(w[i % W]);
+        return __uint_as_float(i % 2 ? w[i / 2 % W] & 0xffff0000u : w[i / 2 % W] << 16);
+    }
+    __device__ __forceinline__ uint32_t top_finite() const {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) m = fabsf(get(i)) < INFINITY ? fmaxf(m, fabsf(get(i))) : m;
+        return __float_as_uint(m);
+    }
+    __device__ __forceinline__ void without_infinities() {  // what has all bits of the exponent set becomes NaN
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (sizeof(T) == 4) {
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0x7fffffffu;
+            } else {
+                if ((w[i] & 0x7f80u) == 0x7f80u) w[i] |= 0x7fffu;
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] |= 0x7fff0000u;
+            }
+        }
+    }
+};
 
 // x[0..3] as PARTS codes each, a word a part.  Up to four parts: what the first one leaves is rounded to fp16, 11 bits
 // of at most 2^-4 x (2^-16 of x), which three more parts hold; more: fp32 throughout.
@@ -160,7 +215,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
     if (tid == 0) {
         for (int i = 0; i < 2 * kStages; ++i) tc::mbar_init(full + i, 1);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(q_full + i, 1);
+            tc::mbar_init(q_full + i, Cfg::kQWarps);
             tc::mbar_init(q_free + i, 1);
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 4 * Cfg::kGroups);
@@ -288,54 +343,70 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
             tc::mma_commit(drain);
             drain_wait(drain, 0);
         }
-    } else if (warp == 2) {
+    } else if (warp == 2 || warp >= 4 + 4 * Cfg::kGroups) {
         // -------------------------------------------------------------------- queries
-        constexpr int E = D / 32;  // consecutive channels a lane
+        constexpr int E = D / 32;                                     // consecutive channels a lane
+        constexpr int HW = HP / Cfg::kQWarps, N = GH < HW ? GH : HW;  // heads a warp, and of them at a time
+        const int hw = warp == 2 ? 0 : HW * (warp - 3 - 4 * Cfg::kGroups);
         int seg = 0;
         for (; w.left > 0; dec_next(p, w), ++seg) {
             const int g = w.g / p.HB, h0 = (w.g % p.HB) * HP, nh = min(HP, p.G - h0), qb = seg % kQBufs;
             const Tin* q = static_cast<const Tin*>(p.q) + (((long long)w.l * p.B + w.b) * p.Hq + g * p.G + h0) * D + lane * E;
             bool ok = true;
-            for (int hb = 0; hb < HP; hb += 8) {
-                float x[GH][E];
+            QueryRun<Tin, E> x[2][N];  // up to eight heads, and the next eight on their way
+            auto load = [&](int hb) {
 #pragma unroll
-                for (int h = 0; h < GH; ++h)
+                for (int h = 0; h < N; ++h) {
+                    x[hb / 8 & 1][h].zero();
+                    if (hw + hb + h < nh) x[hb / 8 & 1][h].load(q + (hw + hb + h) * D);
+                }
+            };
+            load(0);
+            unsigned char* const to = sQ + qb * Cfg::kQBytes + lane * E / kRow * (NQ * kRow);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[h][e] = hb + h < nh ? to_f32(q[(hb + h) * D + e]) : 0.f;
+            for (int hb = 0; hb < HW; hb += 8) {
+                if (hb + 8 < HW) load(hb + 8);
+                QueryRun<Tin, E>* v = x[hb / 8 & 1];
+                // (of heads that are not there: zeros.  Steps over all heads, no branch between them: a head's own chain is long)
+                uint32_t most[N], all = 0;
+#pragma unroll
+                for (int h = 0; h < N; ++h) most[h] = v[h].top();
+#pragma unroll
+                for (int h = 0; h < N; ++h) most[h] = __reduce_max_sync(kFull, most[h]);
+#pragma unroll
+                for (int h = 0; h < N; ++h) all = max(all, most[h]);
+                if (all >= 0x7f800000u) {  // infinities or NaN: the largest of the others; they become NaN
+#pragma unroll
+                    for (int h = 0; h < N; ++h) {
+                        v[h].without_infinities();
+                        most[h] = __reduce_max_sync(kFull, v[h].top_finite());
+                    }
+                }
                 if (hb == 0) ok = __all_sync(kFull, tc::mbar_wait(q_free + qb, ((seg / kQBufs) & 1) ^ 1, abort));
                 if (!ok) break;
 #pragma unroll
-                for (int h = 0; h < GH; ++h) {  // (of heads that are not there: zeros)
-                    float m = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float y = fabsf(x[h][e]);
-                        m = fmaxf(m, y < INFINITY ? y : 0.f);
-                    }
-                    m = redux_max(m);
+                for (int h = 0; h < N; ++h) {
                     // the power of two that takes the largest channel to [128, 256)
-                    const int up = m > 0.f ? min(134 - (__float_as_int(m) >> 23), 100) : 0;
+                    const int up = most[h] ? min(134 - (int)(most[h] >> 23), 100) : 0;
                     const float f = __int_as_float((127 + up) << 23);
-                    if (lane == 0) q_unit[(seg & 7) * HP + hb + h] = p.scale_log2 * __int_as_float((127 - up) << 23);
+                    if (lane == 0) q_unit[(seg & 7) * HP + hw + hb + h] = p.scale_log2 * __int_as_float((127 - up) << 23);
                     uint32_t c[(E + 3) / 4][QP];
 #pragma unroll
                     for (int e = 0; e < E; e += 4) {
                         float y[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) y[z] = e + z < E ? finite_or_nan(x[h][(e + z) % E]) * f : 0.f;
+                        for (int z = 0; z < 4; ++z) y[z] = e + z < E ? v[h].get((e + z) % E) * f : 0.f;
                         split4<QP>(y, c[e / 4]);
                     }
 #pragma unroll
                     for (int i = 0; i < QP; ++i) {
-                        const int ch = lane * E;
-                        unsigned char* to = sQ + qb * Cfg::kQBytes + ch / kRow * (NQ * kRow) +
-                                            tc::swizzled<kRow>((i * HP + hb + h) * kRow + ch % kRow);
+                        unsigned char* at = to + tc::swizzled<kRow>((i * HP + hw + hb + h) * kRow + lane * E % kRow);
                         if constexpr (E == 8)
-                            *reinterpret_cast<uint2*>(to) = make_uint2(c[0][i], c[E / 4 - 1][i]);
+                            *reinterpret_cast<uint2*>(at) = make_uint2(c[0][i], c[E / 4 - 1][i]);
                         else if constexpr (E == 4)
-                            *reinterpret_cast<uint32_t*>(to) = c[0][i];
+                            *reinterpret_cast<uint32_t*>(at) = c[0][i];
                         else
-                            *reinterpret_cast<uint16_t*>(to) = (uint16_t)c[0][i];
+                            *reinterpret_cast<uint16_t*>(at) = (uint16_t)c[0][i];
                     }
                 }
             }
