@@ -577,8 +577,8 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
  * In a round over such a cache: ddt_read_paged_quant, a layer at a time, into a contiguous
  * cache of 16 bits that ddt_tree_attn reads; after the walk ddt_append_paged_quant in the place of
  * the commit's attention part (node = acc_nodes, count = n_emitted, advance 0), then ddt_commit
- * without attention layers for the rest and prefix_len (or advance 1 and no ddt_commit where there
- * are no GDN layers).  ddt_evict_paged does not take these caches.
+ * without attention layers for the rest and prefix_len, with acc_len -1 for requests that the append
+ * refused (or advance 1 and no ddt_commit where there are no GDN layers).  ddt_evict_paged does not take these caches.
  * ------------------------------------------------------------------------------- */
 
 /* ddt_append_paged_quant -- rows quantised as they are written: entry j < count[b] of request b,

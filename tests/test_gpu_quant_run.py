@@ -138,6 +138,31 @@ def test_rounds_over_8_bit_prefixes(Lg, rope, qk_norm, dtype):
         assert torch.equal(r.attn_o[:, b, :nn[b]], want[-1][:, b, :nn[b]])
 
 
+@pytest.mark.parametrize("Lg", [0, 1])
+def test_a_full_request_is_left_as_it_is(Lg):
+    """A request whose rows do not fit is committed nowhere: neither its length nor its recurrent state moves."""
+    cfg = dict(synth.WORKLOADS[1], B=3, V=2000, budget=24, Lf=2, Hq=8, Hkv=2, d=128, dtype=BF, page=32, kv_quant=16,
+               P_lo=40, P_hi=300, Lg=Lg, Pcap=416)
+    cfg.pop("P", None)
+    if not Lg:
+        cfg.pop("Lg")
+    r = Round(cfg, device="cuda", workload=1, poison=True, attn_out_dtype=F32, gdn_out_dtype=F32)
+    full = r.block_table.shape[1] * 32
+    r.prefix_len[1] = full
+    before = r.prefix_len.tolist()
+    state = [x.clone() for x in ((r.gdn.S, r.gdn.conv_state) if Lg else ())]
+    r.step()
+    torch.cuda.synchronize()
+    n, acc = r.walk["n_emitted"].tolist(), r.walk["acc_nodes"].tolist()
+    assert r.append_status.tolist() == r.commit["status"].tolist() == [0, 3, 0]
+    assert r.prefix_len.tolist() == [before[0] + n[0], full, before[2] + n[2]]
+    for b in (0, 2):
+        assert r.commit["src_row"][b, :n[b]].tolist() == acc[b][:n[b]]
+        assert r.commit["dst_pos"][b, :n[b]].tolist() == list(range(before[b], before[b] + n[b]))
+    for x, y in zip((r.gdn.S, r.gdn.conv_state) if Lg else (), state):
+        assert torch.equal(x[:, 1], y[:, 1]) and not torch.equal(x[:, 0], y[:, 0])
+
+
 def test_kv_quant_needs_pages():
     with pytest.raises(ValueError):
         Round(dict(synth.WORKLOADS[1], kv_quant=16), device="cuda", workload=1)

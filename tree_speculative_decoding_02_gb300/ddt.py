@@ -477,15 +477,15 @@ def ddt_walk_accept_sample(token, parent, n_nodes, max_accept: int, *, target_lo
 
 # -------------------------------------------------------------------------- commit
 def ddt_commit(acc_nodes, acc_len, prefix_len, *, k_tree=None, v_tree=None, k_cache=None, v_cache=None, x=None,
-               conv_w=None, beta=None, decay=None, S=None, conv_state=None, Hk: int = 1, out=None):
-    """In-place commit of the accepted path into the caches / GDN state / conv state."""
+               conv_w=None, beta=None, decay=None, S=None, conv_state=None, Hk: int = 1, N: int = None, out=None):
+    """In-place commit of the accepted path into the caches / GDN state / conv state.  N, the tree's rows, is for a call
+    without either part: prefix_len, src_row and dst_pos alone (its rows are in an 8-bit cache)."""
     lib = _gpu()
     B, A = acc_nodes.shape
     dev = acc_nodes.device
     _need(acc_nodes, (B, A), torch.int32, "acc_nodes")
     _need(acc_len, (B,), torch.int32, "acc_len")
     _need(prefix_len, (B,), torch.int32, "prefix_len")
-    N = None
     if k_cache is not None:
         La, _, N, Hkv, d = k_tree.shape
         Pcap = k_cache.shape[3]
@@ -514,7 +514,7 @@ def ddt_commit(acc_nodes, acc_len, prefix_len, *, k_tree=None, v_tree=None, k_ca
     else:
         Lg, Hv, dk, dv, K, xd = 0, 1, 1, 1, 1, F32
     if N is None:
-        raise DDTError("ddt_commit needs the attention part, the GDN part, or both")
+        raise DDTError("ddt_commit needs the attention part, the GDN part, or both (or N)")
     o = out or {}
     i32 = dict(dtype=torch.int32, device=dev)
     res = {"src_row": o.get("src_row", torch.empty((B, A), **i32)),

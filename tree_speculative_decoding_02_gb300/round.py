@@ -147,7 +147,9 @@ class Round:
             ddt.ddt_append_paged_quant(k, v, *self._layer(l), self.block_table, none, self.prefix0, advance=False)
         self.k_scratch, self.v_scratch = a.k_cache[:1].clone(), a.v_cache[:1].clone()
         self.layer_status = torch.zeros((L, B), dtype=torch.int32, device=self.device)
-        self.read_status, self.append_status = (torch.zeros((B,), dtype=torch.int32, device=self.device) for _ in range(2))
+        self.read_status, self.append_status, self.commit_len = (torch.zeros((B,), dtype=torch.int32, device=self.device)
+                                                                 for _ in range(3))
+        self.refused = torch.full_like(self.commit_len, -1)   # as an accepted length: no commit
         a.k_cache = a.v_cache = None
 
     def _layer(self, l):
@@ -178,12 +180,13 @@ class Round:
         self.walk_step()
         kw = {}
         quant = bool(self.Lf and self.quant)
-        if quant:   # its rows first: the commit below moves prefix_len (where nothing else does, the append)
+        acc_len = self.walk["acc_len"]
+        if quant:   # its rows first: the commit below moves prefix_len, of the requests whose rows were written
             ddt.ddt_append_paged_quant(self.k_rows(), self.attn.v_tree, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
                                        self.block_table, self.prefix_len, self.walk["n_emitted"],
-                                       node=self.walk["acc_nodes"], advance=not self.Lg, status=self.append_status)
-            if not self.Lg:
-                return
+                                       node=self.walk["acc_nodes"], advance=False, status=self.append_status)
+            acc_len = torch.where(self.append_status == 0, acc_len, self.refused, out=self.commit_len)
+            kw.update(N=self.attn.k_tree.shape[2])
         if self.Lf and not self.page:
             kw.update(k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_cache=self.attn.k_cache,
                       v_cache=self.attn.v_cache)
@@ -198,7 +201,9 @@ class Round:
                                  k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_pages=self.k_pages,
                                  v_pages=self.v_pages, out=self.commit, **kw)
         else:
-            ddt.ddt_commit(self.walk["acc_nodes"], self.walk["acc_len"], self.prefix_len, out=self.commit, **kw)
+            ddt.ddt_commit(self.walk["acc_nodes"], acc_len, self.prefix_len, out=self.commit, **kw)
+            if quant:
+                torch.maximum(self.commit["status"], self.append_status, out=self.commit["status"])
 
     def walk_step(self):
         """The round's walk: greedy (or its flat safe mode), or rejection sampling at
