@@ -609,7 +609,7 @@ ddt_status ddt_append_paged_quant(int n_layers, int B, int N, int A, int Hkv, in
 
 /* ddt_read_paged_quant -- the rows read back: k_out, v_out [L][B][Hkv][Pcap][d] (out_dtype), the
  * layout of ddt_tree_attn's caches, get the values of rows 0..prefix_len[b]-1 (exact in fp32 and
- * in bf16, up to the largest finite value); rows behind are left as they are.
+ * in bf16; a value rounded up past the largest finite one is infinite); rows behind are left as they are.
  *   status [B]: DDT_ERR_CAPACITY if prefix_len[b] is outside [0, min(Pcap, max_pages * page_size)]
  *     (nothing of the request is written), DDT_ERR_INVALID_ARG if a block-table entry of the prefix is
  *     outside [0, num_pages) (the rows of such pages are left as they are).
