@@ -633,6 +633,9 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
  * one before.  bf16: q in two parts (a channel exact, or off by at most 2^-21 of its head's largest),
  * the weights in four (2^-16 of a weight, or 2^-26 of the largest where that is more); fp32: six parts
  * of each (2^-24 of a value, or 2^-34 of the largest).
+ * Blocks of V whose scales are more than 2^80 apart make o NaN where a CTA has rows of both (128 rows of
+ * zeros or more at its start count as 1).  The weighted sums are divided last: infinite where a request's
+ * rows times 2^8 times its largest |V| pass 2^127.
  * The same inputs give the same bits.  o, status and the workspace are apart from one another and
  * from the inputs (the call is refused otherwise).  d in {64, 128, 256}; Hq / Hkv <= 1024; q, k_new,
  * v_new, the pages and o 16-byte aligned. */

@@ -133,6 +133,42 @@ def test_value_scales_that_climb(dtype):
     _check(c, _run(c, out_dtype=F32))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("first,rest", [(60, 140), (180, 100), (0, 47), (0, 207)])
+def test_value_scales_far_apart(dtype, first, rest):
+    """2^80 between blocks in one tile: sums keep every weight that counts (2^17 rows below 2^-38 are 2^-21 at most)."""
+    c = _case(39, 1, 2, 8, 2, 64, [300, 40], 16, 16, dtype, new=False)
+    c["vs"][:] = rest
+    c["vs"][:, c["table"][:, 0]] = first
+    if not first:
+        c["v"][:, c["table"][:, 0]] = 0
+    _check(c, _run(c, out_dtype=F32))
+
+
+@pytest.mark.parametrize("first,rest", [(27, 247), (247, 27), (60, 141), (180, 99), (0, 208)])
+def test_value_scales_too_far_apart(first, rest):
+    """Farther apart than the sums reach: NaN, not a wrong value; a head without such blocks is as it was."""
+    c = _case(40, 1, 2, 8, 2, 64, [300, 40], 16, 16, BF, new=False)
+    want = _run(c, out_dtype=F32)["o"]
+    c["vs"][:, :, 0] = rest
+    head = slice(0, 1 if first else 8)  # a tile of zeros counts as 1
+    c["vs"][:, c["table"][0, head], 0] = first
+    if not first:
+        c["v"][:, c["table"][0, head], 0] = 0
+    r = _run(c, out_dtype=F32)
+    assert r["status"].tolist() == [0, 0]
+    assert torch.equal(r["o"][:, :, 4:], want[:, :, 4:])
+    far = r["o"][:, 0, :4]
+    if first:  # both in one tile
+        assert torch.isnan(far).all()
+    else:      # in two, which may be two CTAs': right there
+        exact, bound = Q.decode_ref(Q.f64(c["q"]), None, None, c, c["scale"], BF)
+        assert (torch.isnan(far).cpu().numpy() | (np.abs(Q.f64(far) - exact[:, 0, :4]) <= bound[:, 0, :4] + 1e-30)).all()
+    # the other request has no such blocks; (with byte 247 it has values up to 448 * 2^120 = 2^128.8, past fp32: infinities)
+    assert not torch.isnan(r["o"][:, 1]).any()
+    assert rest == 247 or torch.isfinite(r["o"][:, 1]).all()
+
+
 def test_non_finite():
     """A NaN code of a cached row, and a NaN or infinity of q, show in the heads that they enter and nowhere else."""
     c = _case(39, 1, 3, 8, 2, 64, [200, 200, 200], 16, 16, BF)

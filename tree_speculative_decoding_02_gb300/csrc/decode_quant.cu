@@ -17,7 +17,8 @@
 // The scales.  A block's power of two 2^a of K multiplies its rows' scores.  That of V, 2^v, goes
 // into the weights: t' = t + v (base 2), P = 2^(t' - m) with one reference m a head for all t', so
 // that P is at most 2^8 and loses nothing whatever the blocks' scales are; the softmax sum gets
-// 2^-v P = 2^(t - m).  (v counts from the scale of the segment's first row.)
+// 2^-v P = 2^(t - m).  (v counts from the scale of the segment's first block that is not of zeros, or from 2^0 if its first tile
+// has none.)
 //
 //   warp 0      producer: block-table entries, TMA of K and V tiles into one ring
 //   warp 1      MMA issuer: Q K^T of tile j + 1 ahead of P V of tile j
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     int* bad_tile = abort_flag + 1;                            // [8] a page of the tile does not exist
-    // [4][16] a tile's scales by block: 2^a, v, 2^-v, and V's byte of the segment's first row
+    // [4][16] a tile's scales by block: 2^a, v, 2^-v, and V's byte of the segment's first block
     float4* scales = reinterpret_cast<float4*>(smem_raw + (reinterpret_cast<unsigned char*>(bad_tile + 8) - smem_raw + 15) / 16 * 16);
     float* q_unit = reinterpret_cast<float*>(scales + 4 * 16);  // [8][HP] log2 scores of a unit of Q K^T, by segment
     float* xm = q_unit + 8 * HP;                               // [2][4][HP] warps' tile maxima
@@ -438,12 +439,16 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 if (j >= 2) ok = __all_sync(kFull, tc::mbar_wait(p_full + (j & 1), ((j - 2) >> 1) & 1, abort));
                 if (!ok) break;
                 if (t == w.t) {
-                    const int first = __shfl_sync(kFull, (int)vb, 0);
-                    base = first ? first : 127;
+                    const unsigned some = __ballot_sync(kFull, good && vb);
+                    const int first = __shfl_sync(kFull, (int)vb, max(__ffs(some) - 1, 0));
+                    base = some ? first : 127;
                 }
-                const int dv = vb ? max(-126, min(126, (int)vb - base)) : 0;  // (a block of zeros: any scale)
+                // A block of zeros takes any scale: a small one, so that the weights which do count keep their bits.
+                // Others up to 2^80 apart: sums hold weights down to 2^-38 of the largest.  Farther: NaN.
+                const int dv = vb ? max(-126, min(126, (int)vb - base)) : -60;
+                const int back = good && abs(dv) > 80 ? 0x7fffffff : (127 - dv) << 23;  // 2^-v
                 if (lane < n_blk)
-                    scales[(j & 3) * 16 + lane] = make_float4(scale_of(kb), (float)dv, __int_as_float((127 - dv) << 23), __int_as_float(base));
+                    scales[(j & 3) * 16 + lane] = make_float4(scale_of(kb), (float)dv, __int_as_float(back), __int_as_float(base));
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x_full + (j & 3));
             }
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
         bool ok = true;
         for (; w.left > 0; dec_next(p, w), ++seg) {
             const int h0 = (w.g % p.HB) * HP + hg, nh = min(8, p.G - h0), n_seg = dec_seg_tiles(w);
-            int base = 127;  // V's scale of the segment's first row
+            int base = 127;  // V's scale of the segment's first block
             F2 m[GH / 2], l[GH / 2];  // two heads each; m holds minus the reference
 #pragma unroll
             for (int h = 0; h < GH / 2; ++h) {
