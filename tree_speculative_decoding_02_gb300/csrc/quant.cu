@@ -35,7 +35,7 @@ struct AppendArgs {
     int wpi;          // warps an item (a block's K or V rows of one head)
     int run, groups;  // blocks a CTA; CTAs that share a block's items
     int advance, solo;  // solo: one CTA has all of a request
-    int checked;      // a kernel of its own looks at the pages
+    int checked;      // a kernel of its own looks at the pages (and advances prefix_len)
     const void* k;
     const void* v;
     const int32_t* node;   // or null
@@ -123,11 +123,14 @@ __device__ __forceinline__ int append_check(const AppendArgs& a, int b, int P, i
     return __syncthreads_or(bad) ? DDT_ERR_INVALID_ARG : err;
 }
 
-// grid B: the check by itself, where every CTA of the next kernel would look at many pages
+// grid B: the check by itself, where every CTA of the next kernel would look at many pages; and prefix_len
 __global__ void __launch_bounds__(kThreads) k_append_check(const AppendArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x, err = append_check(a, b, a.prefix_len[b], a.count[b]);
-    if (threadIdx.x == 0) a.status[b] = err;
+    const int b = blockIdx.x, P = a.prefix_len[b], n = a.count[b], err = append_check(a, b, P, n);
+    if (threadIdx.x == 0) {
+        a.status[b] = err;
+        if (a.advance && !err) a.prefix_len[b] = P + n;
+    }
 }
 
 // grid (runs of blocks x item groups, 1, L * B).  A CTA takes a few blocks of one request and layer, one after
@@ -140,17 +143,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.z % a.B, l = blockIdx.z / a.B, group = blockIdx.x % a.groups;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // k_append_advance may be set up
-    const int P = a.prefix_len[b], n = a.count[b];
+    if (a.checked) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (a.status[b] != DDT_OK) return;
+    }
+    const int n = a.count[b], P = a.prefix_len[b] - (a.checked && a.advance ? n : 0);
     int first = P / a.S + blockIdx.x / a.groups * a.run;  // block
     // a CTA without rows: none, or none so far behind the prefix (which is for others to judge)
     if ((blockIdx.x > 0 || l > 0) && (n <= 0 || (long long)first * a.S >= (long long)P + n)) return;
-    // (checked: the rows are read beside that kernel, and its verdict awaited before anything is written; the first CTA
-    // of a request awaits it in any case, so that this kernel does not end before it)
-    const bool sound = P >= 0 && P <= a.cap && n > 0 && n <= a.A && n <= a.cap - P;
-    if (a.checked && !sound) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
     const int err = a.checked ? DDT_OK : append_check(a, b, P, n);
     if (!a.checked && l == 0 && blockIdx.x == 0 && tid == 0) {
         a.status[b] = err;
@@ -194,10 +194,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_append_qua
             load(e);
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) most = x[i].top(most);
-        }
-        if (a.checked && turn == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            if (*static_cast<volatile int32_t*>(a.status + b) != DDT_OK) return;
         }
         const long long plane = ((long long)l * a.num_pages + table[lp]) * a.Hkv + g;
         unsigned char* page = (isv ? a.vp : a.kp) + (plane * a.page_rows + in) * D;
@@ -327,7 +323,7 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     cfg.attrs = &at;
     cfg.numAttrs = a.checked ? 1 : 0;
     cudaError_t e = in == DDT_BF16 ? append_go<__nv_bfloat16>(cfg, a) : append_go<float>(cfg, a);
-    if (e != cudaSuccess || !advance || a.solo) return e;
+    if (e != cudaSuccess || !advance || a.solo || a.checked) return e;
     cfg.gridDim = dim3(counted((unsigned)(B + 127) / 128));
     cfg.blockDim = dim3(128);
     cfg.numAttrs = 1;
