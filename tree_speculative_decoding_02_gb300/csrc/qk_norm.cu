@@ -29,7 +29,8 @@ namespace ddt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // a CTA
+// tokens a CTA at most: 4413 of 18 fp32 heads of 128 take 20.6 us with 8, 18.8 with 12; the batched rounds' bf16 rows 120.6 and 123.4
+constexpr int max_tokens(int esz) { return esz == 2 ? 8 : 12; }
 
 struct NormFreq {
     unsigned long long f[128];  // theta^(-2i/rot) / (2 pi), in units of 2^-64
@@ -118,7 +119,7 @@ __device__ __forceinline__ void store_run(T* p, const F2 (&x)[4]) {
 
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_rope(const NormArgs a, const __grid_constant__ NormFreq fr) {
-    constexpr int LPR = D / 16;  // lanes a row
+    constexpr int LPR = D / 16, kMaxTokens = max_tokens(sizeof(T));  // lanes a row
     // four float4 a lane, lane after lane: a quarter warp reads 128 consecutive bytes
     __shared__ float4 s_cs[kMaxTokens * D / 4];  // [token][4][rot / 16]: two cosines, their sines
     __shared__ float4 s_w[2][4 * LPR];           // offset + weight: of q, of k
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     int t = tid / LPR / heads, h = tid / LPR % heads;
     const int at_lo = lo * (int)sizeof(T), gap = (hi - lo) * (int)sizeof(T);
     // Two rows a lane group are on their way while one is worked on: bf16 words by asynchronous copies, every lane its own
-    // (in registers 128 us, so 121; fp32, whose runs are two words each, 21 and 25 us for the 4413 tokens)
+    // (in registers 128 us, so 121; fp32, whose runs are two words each, 21 and 25 us for 4413 tokens of 18 heads of 128)
     constexpr bool kAsync = VEC && sizeof(T) == 2;
     __shared__ uint4 s_rows[kAsync ? 4 * kThreads : 1];
     uint4* const mine = s_rows + (kAsync ? tid : 0);
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_qk_norm_ro
     for (int e = tid; e < 2 * D; e += kThreads) {
         // channel ch is the j-th of its lane: of the low run 0..7, of the high one 8..15
         const int x = e / D, ch = e % D, of = ch < a.rot ? ch : ch - a.rot, size = ch < a.rot ? half : rest;
-        const int k = (ch < a.rot ? 0 : lanes) + of % size / 8, j = of / size * 8 + ch % 8;
+        const int high = of >= size ? 8 : 0, k = (ch < a.rot ? 0 : lanes) + (high ? of - size : of) / 8, j = high + ch % 8;
         reinterpret_cast<float*>(s_w[x])[(j / 4 * LPR + k) * 4 + j % 4] =
             a.offset + to_f32(static_cast<const T*>(x ? a.kw : a.qw)[(long long)l * D + ch]);
     }
@@ -316,7 +317,7 @@ cudaError_t launch_qk_norm_rope(int L, int B, int N, int Hq, int Hkv, int d, int
     // full a CTA's last step is)
     const int at_once = kThreads / (d / 16), resident = (dtype == DDT_BF16 ? 4 : 3) * sms;
     long long best = 0;
-    for (int t = 1; t <= kMaxTokens; ++t) {
+    for (int t = 1; t <= max_tokens(esz); ++t) {
         const long long ctas = ((long long)B * N + t - 1) / t * L;
         const long long steps = (ctas + resident - 1) / resident * (2 + ((long long)t * (Hq + Hkv) + at_once - 1) / at_once);
         if (t == 1 || steps < best) {
