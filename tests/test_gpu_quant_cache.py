@@ -180,6 +180,38 @@ def test_long_prompts(dtype):
         assert Q.same_codes(have.view(torch.uint8).cpu().numpy(), want).all()
 
 
+def test_long_prompts_a_call_a_layer():
+    """The same a layer at a time (prefix_len moves with the last one), and replayed from a graph behind what it wrote."""
+    L, count = 2, [2300, 2101]
+    c = Q.cache(33, L, 2, 2, 64, [3, 16], 8, 8, cap_rows=4700)
+    k, v = (x.cuda() for x in _rows(33, L, 2, 2300, 2, 64, BF))
+    gpu = Q.to_gpu(c)
+    n = torch.tensor(count, dtype=torch.int32).cuda()
+    st = torch.zeros((L, 2), dtype=torch.int32).cuda()
+
+    def run():
+        for l in range(L):
+            at = slice(l, l + 1)
+            ddt.ddt_append_paged_quant(k[at], v[at], *(x[at] for x in gpu[:4]), *gpu[4:], n, advance=l == L - 1, status=st[l])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    graph.replay()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for x, codes, scale in ((k, "k", "ks"), (v, "v", "vs")):
+            Q.append_ref(Q.f64(x), c[codes], c[scale], c["table"], c["lens"], count, None)
+        c["lens"] = [p + m for p, m in zip(c["lens"], count)]
+    assert st.tolist() == [[0, 0]] * L and gpu[5].tolist() == c["lens"]
+    for have, want in zip(gpu[:4], (c["k"], c["v"], c["ks"], c["vs"])):
+        assert Q.same_codes(have.view(torch.uint8).cpu().numpy(), want).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("d,page,block,Hkv", [(64, 8, 8, 3), (128, 16, 16, 2), (256, 64, 16, 4), (64, 192, 64, 1), (128, 128, 128, 1)])
 def test_read_back(dtype, d, page, block, Hkv):
