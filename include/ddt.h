@@ -632,10 +632,13 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
  * codes as they are, q and the weights as sums of e4m3 parts, each 16 times finer than the
  * one before.  bf16: q in two parts (a channel exact, or off by at most 2^-21 of its head's largest),
  * the weights in four (2^-16 of a weight, or 2^-26 of the largest where that is more); fp32: six parts
- * of each (2^-24 of a value, or 2^-34 of the largest).
- * Blocks of V whose scales are more than 2^80 apart make o NaN where a CTA has rows of both (128 rows of
- * zeros or more at its start count as 1).  The weighted sums are divided last: infinite where a request's
- * rows times 2^8 times its largest |V| pass 2^127.
+ * of each (2^-24 of a value, or 2^-34 of the largest).  The largest weight counts times the ratio of its
+ * block's V scale to the row's, up to 2^8; the rows of blocks that are further from the others (2^4 from the
+ * first block, or the median, of a CTA's rows) are taken in fp32 throughout, one by one, which a call of few
+ * such blocks hardly feels.
+ * Blocks of V whose scales are more than 2^80 apart make o NaN where a CTA has rows of both (blocks of zeros
+ * have none).  The weighted sums are divided last: infinite where a request's rows times 2^8 times its largest
+ * |V| pass 2^127.
  * The same inputs give the same bits.  o, status and the workspace are apart from one another and
  * from the inputs (the call is refused otherwise).  d in {64, 128, 256}; Hq / Hkv <= 1024; q, k_new,
  * v_new, the pages and o 16-byte aligned. */

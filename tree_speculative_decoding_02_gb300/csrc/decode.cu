@@ -15,7 +15,7 @@
 //                   added to the running sum of row p's attention weights.
 #include <math.h>
 
-#include "decode.cuh"
+#include "decode_far.cuh"
 #include "tc.cuh"
 
 namespace ddt {
@@ -304,13 +304,85 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_decode_simt(const DecodePar
     }
 }
 
+// A head's output from its joined softmax, by WPH warps (8: all of a block; s_x [8][D]).
+template <typename Tin, typename Tout, int D, int WPH>
+__device__ __forceinline__ void write_head(const DecodeParams& p, int lb, int hq, const DecNew<Tin, D>& x, const HeadJoin& j, float* s_x) {
+    constexpr int E = D / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Tout* out = static_cast<Tout*>(p.o) + ((long long)lb * p.Hq + hq) * D;
+    if (j.err) {
+        if (WPH == 1 || warp == 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(0.f);
+            if (lane == 0) p.status[lb % p.B] = j.err;
+        }
+        return;  // (WPH 8: all warps)
+    }
+    const int h = (hq % p.G) % p.hbs;
+    const float w = WPH == 1 || warp == 0 ? tc::ex2(x.tn - j.ref) : 0.f;
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = w * x.v[e];
+    const float2* ml = p.part_ml + j.first * p.HT + h;
+    const float* po = p.part_o + (j.first * p.HT + h) * D;
+#pragma unroll 4
+    for (int s = WPH == 1 ? 0 : warp; s < j.ns; s += WPH) {
+        const float f = tc::ex2(ml[(long long)s * p.HT].x - j.ref);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, po[(long long)s * p.HT * D + e * 32 + lane], acc[e]);
+    }
+    const float inv = j.z > 0.f ? 1.f / j.z : j.z;  // no rows at all: 0; NaN stays
+    if (WPH == 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(acc[e] * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_x[warp * D + e * 32 + lane] = acc[e];
+        __syncthreads();
+        if (tid < D) {
+            float o = s_x[tid];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) o += s_x[w * D + tid];
+            out[tid] = from_f32<Tout>(o * inv);
+        }
+    }
+}
+
+// The same of a head whose segments have far blocks, which join their partials first.  (A function of its own, called last: the
+// kernel's ordinary way has no registers to spare.)
+template <typename Tin, typename Tout, int D, int WPH>
+__device__ __noinline__ void far_join(const DecodeParams& p, int lb, int hq, float* s_x) {
+    const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = hq % p.G / p.hbs, nt = dec_tiles(p.prefix_len[b], p.cap), HH = p.Hkv * p.HB;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const HeadJoin j = head_join(p, lb, hq, 0.f, lane);  // (for its segments)
+    // the head's tiles on the line
+    const long long all = p.pre[p.B], T = all * HH * p.L, from = l * all * HH + p.pre[b] * HH + (long long)(g * p.HB + hb) * nt;
+    const int C = (int)min((long long)p.C, T);
+    for (int s = WPH == 1 ? 0 : warp; s < j.ns; s += WPH) {
+        const int c = j.c0 + s, n = p.far[c];
+        const bool many = n > kFarTiles;  // more than are on the list: all of the segment's tiles are looked at
+        for (int i = 0; i < (many ? 1 : n); ++i) {
+            const int2 x = p.far_tile[c * kFarTiles + i];
+            if (!many && x.x != lb * HH + g * p.HB + hb) continue;
+            const int t0 = many ? (int)(max(dec_first(T, C, c), from) - from) : x.y >> 8;
+            const int t1 = many ? (int)(min(dec_first(T, C, c + 1), from + nt) - from) : t0 + 1;
+            far_rows<Tin, D>(p, lb, g, hq % p.G, t0, t1, many ? 0 : x.y & 255, j.first + s, hq % p.G % p.hbs, lane);
+        }
+    }
+    DecNew<Tin, D> mine;
+    mine.load(p, lb, g, hq % p.G, lane);
+    if (WPH == 1) __syncwarp();
+    else __syncthreads();  // (all warps are of this head)
+    write_head<Tin, Tout, D, WPH>(p, lb, hq, mine, head_join(p, lb, hq, mine.tn, lane), s_x);
+}
+
 // Blocks below n_join: WPH warps a head, O of the head.  The others: the weight sums of some rows
 // of one (layer, request, kv head); with them the kernel is bound by HBM (4 bytes a head and row,
 // written by the split and read here: about 20 us of 415 for 500000 rows of 24 heads), else by
 // the latency of the join.
-template <typename Tin, typename Tout, int D, int WPH>
-__global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, unsigned n_join, int chunks) {
-    constexpr int E = D / 32;
+// QUANT: of a cache in 8 bits, without weight sums; the far blocks' rows join their segments' partials first, where there are any.
+template <typename Tin, typename Tout, int D, int WPH, bool QUANT>
+__global__ void __launch_bounds__(256, QUANT ? 3 : 4) k_decode_finish(const __grid_constant__ DecodeParams p, unsigned n_join, int chunks) {
     extern __shared__ float s_x[];  // [8][D] sums of the warps of a head, or 3 floats a head of a group
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     DecNew<Tin, D> mine;
@@ -322,46 +394,12 @@ __global__ void __launch_bounds__(256, 4) k_decode_finish(const DecodeParams p, 
         if (lb < p.L * p.B) mine.load(p, lb, hq / p.G, hq % p.G, lane);
         partials();
         if (lb >= p.L * p.B) return;  // (WPH 1: whole warps, no barrier follows)
-        const HeadJoin j = head_join(p, lb, hq, mine.tn, lane);
-        Tout* out = static_cast<Tout*>(p.o) + (long long)x * D;
-        if (j.err) {
-            if (WPH == 1 || warp == 0) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(0.f);
-                if (lane == 0) p.status[lb % p.B] = j.err;
-            }
-            return;  // (WPH 8: all warps)
-        }
-        const int h = (hq % p.G) % p.hbs;
-        const float w = WPH == 1 || warp == 0 ? tc::ex2(mine.tn - j.ref) : 0.f;
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = w * mine.v[e];
-        const float2* ml = p.part_ml + j.first * p.HT + h;
-        const float* po = p.part_o + (j.first * p.HT + h) * D;
-#pragma unroll 4
-        for (int s = WPH == 1 ? 0 : warp; s < j.ns; s += WPH) {
-            const float f = tc::ex2(ml[(long long)s * p.HT].x - j.ref);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, po[(long long)s * p.HT * D + e * 32 + lane], acc[e]);
-        }
-        const float inv = j.z > 0.f ? 1.f / j.z : j.z;  // no rows at all: 0; NaN stays
-        if (WPH == 1) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) out[e * 32 + lane] = from_f32<Tout>(acc[e] * inv);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) s_x[warp * D + e * 32 + lane] = acc[e];
-            __syncthreads();
-            if (tid < D) {
-                float o = s_x[tid];
-#pragma unroll
-                for (int w = 1; w < 8; ++w) o += s_x[w * D + tid];
-                out[tid] = from_f32<Tout>(o * inv);
-            }
-        }
+        const HeadJoin j = head_join<QUANT>(p, lb, hq, mine.tn, lane);
+        if (QUANT && j.far) return far_join<Tin, Tout, D, WPH>(p, lb, hq, s_x);
+        write_head<Tin, Tout, D, WPH>(p, lb, hq, mine, j, s_x);
         return;
     }
+    if (QUANT) return;
     const unsigned y = blockIdx.x - n_join;
     const int lbg = (int)(y / chunks), part = (int)(y - (unsigned)lbg * chunks), lb = lbg / p.Hkv, g = lbg - lb * p.Hkv;
     float* s_ref = s_x;
@@ -427,7 +465,7 @@ static int simt_heads(int G) { return G <= 4 ? 4 : (G <= 8 ? 8 : 16); }
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // fills the workspace pointers; returns the bytes
-static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, unsigned char* ws) {
+static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, unsigned char* ws, bool far = false) {
     p.hbs = hbs;
     p.HB = (p.G + hbs - 1) / hbs;
     p.HT = p.G < hbs ? p.G : hbs;
@@ -442,6 +480,10 @@ static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, uns
     p.part_ml = reinterpret_cast<float2*>(take(slots * p.HT * sizeof(float2)));
     p.part_o = reinterpret_cast<float*>(take(slots * p.HT * p.d * sizeof(float)));
     p.score = weight ? reinterpret_cast<float*>(take(units * p.cap * p.G * sizeof(float))) : nullptr;
+    if (far) {
+        p.far = reinterpret_cast<int*>(take(ctas * sizeof(int)));
+        p.far_tile = reinterpret_cast<int2*>(take((size_t)ctas * kFarTiles * sizeof(int2)));
+    }
     return at;
 }
 
@@ -458,7 +500,7 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
                                       : decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight, nullptr);
 }
 
-// The grid of a split kernel with `ctas` CTAs an SM.  A cluster a unit saves the second kernel (2.7
+// p.C (SMs on entry) and p.cl of a split kernel with `ctas` CTAs an SM.  A cluster a unit saves the second kernel (2.7
 // us), but a CTA of it takes nt / cl tiles of a full table where an even split over all CTAs takes
 // units nt / C (one at least), and a tile takes about 1.2 us at head size 128 and 1.6 at 256 (fp32
 // 4.7 and 12): a call is small if the excess, times the head size, is within 384 (fp32 96).
@@ -477,8 +519,7 @@ size_t decode_ws_bytes(int L, int B, int Hq, int Hkv, int d, int cap, ddt_dtype 
 // requests of 4000 rows 13.0 and 15.9 us, 16 of 2000 14.8 and 19.5; 32 over 8 of 128, one request of 8000 rows (6.3 tiles of
 // excess) 11.5 and 13.0, four 13.2 and 17.9, 16 of 2000 14.1 and 17.2; with lengths from an eighth of those on the gains are
 // larger; 24 over 4 of 256, one request of 8000 rows (7 tiles of excess) 17.0 and 14.4.
-cudaLaunchConfig_t decode_config(DecodeParams& p, DecodeSmall small, int ctas, int threads, int smem, cudaLaunchAttribute& at,
-                                 cudaStream_t st) {
+void decode_clusters(DecodeParams& p, DecodeSmall small, int ctas) {
     p.C *= ctas;
     const long units = (long)p.L * p.B * p.Hkv;
     const int nt = (p.cap + kDecTile - 1) / kDecTile;
@@ -486,8 +527,11 @@ cudaLaunchConfig_t decode_config(DecodeParams& p, DecodeSmall small, int ctas, i
     while (cl < 8 && units * 2 * cl <= (cl < 4 ? p.C : p.C - p.C / (ctas == 1 ? 4 : 8)) && cl < nt) cl *= 2;
     const double tiles = (nt + cl - 1) / cl, even = (double)units * nt / p.C;
     p.cl = p.HB == 1 && units * cl <= p.C && tiles * p.d <= small.most && (tiles - (even > 1. ? even : 1.)) * p.d <= small.excess ? cl : 0;
+}
+
+cudaLaunchConfig_t decode_grid(const DecodeParams& p, int threads, int smem, cudaLaunchAttribute& at, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(counted(p.cl ? (unsigned)(units * cl) : (unsigned)p.C));
+    cfg.gridDim = dim3(counted(p.cl ? (unsigned)(p.L * p.B * p.Hkv * p.cl) : (unsigned)p.C));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -506,7 +550,8 @@ static cudaError_t simt_go(DecodeParams& p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k_decode_simt<D, HBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    cudaLaunchConfig_t cfg = decode_config(p, DecodeSmall{256., 96.}, 2, kSimtThreads, smem, at, st);
+    decode_clusters(p, DecodeSmall{256., 96.}, 2);
+    cudaLaunchConfig_t cfg = decode_grid(p, kSimtThreads, smem, at, st);
     return cudaLaunchKernelEx(&cfg, k_decode_simt<D, HBS>, p);
 }
 template <int D>
@@ -517,7 +562,7 @@ static cudaError_t simt_d_go(DecodeParams& p, cudaStream_t st) {
     return p.d == 64 ? simt_heads_go<64>(p, st) : (p.d == 128 ? simt_heads_go<128>(p, st) : simt_heads_go<256>(p, st));
 }
 
-template <typename Tin, typename Tout, int D, int WPH>
+template <typename Tin, typename Tout, int D, int WPH, bool QUANT>
 static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st) {
     const size_t heads = (size_t)p.L * p.B * p.Hq;
     const unsigned n_join = (unsigned)(WPH == 1 ? (heads + 7) / 8 : heads), units = (unsigned)p.L * p.B * p.Hkv;
@@ -536,26 +581,27 @@ static cudaError_t finish_launch(const DecodeParams& p, int sms, cudaStream_t st
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_decode_finish<Tin, Tout, D, WPH>, p, n_join, chunks);
+    return cudaLaunchKernelEx(&cfg, k_decode_finish<Tin, Tout, D, WPH, QUANT>, p, n_join, chunks);
 }
-template <typename Tin, typename Tout>
+template <typename Tin, typename Tout, bool QUANT>
 static cudaError_t finish_go(const DecodeParams& p, int sms, cudaStream_t st) {
     // Eight warps a head where it has a dozen segments (C / units) or more: whole calls with 8 and
     // with 1, one request of 131071 rows, 8 heads over one of 128 (304 segments) 21.2 and 44.1 us, 32
     // over 8 (39) 85.0 and 88.6; but 2 x 96 short requests of 16 heads (1 or 2) 182 and 166.
     const bool many = p.C >= 12L * p.L * p.B * p.Hkv * p.HB;
     switch (p.d) {
-        case 64: return many ? finish_launch<Tin, Tout, 64, 8>(p, sms, st) : finish_launch<Tin, Tout, 64, 1>(p, sms, st);
-        case 128: return many ? finish_launch<Tin, Tout, 128, 8>(p, sms, st) : finish_launch<Tin, Tout, 128, 1>(p, sms, st);
+        case 64: return many ? finish_launch<Tin, Tout, 64, 8, QUANT>(p, sms, st) : finish_launch<Tin, Tout, 64, 1, QUANT>(p, sms, st);
+        case 128: return many ? finish_launch<Tin, Tout, 128, 8, QUANT>(p, sms, st) : finish_launch<Tin, Tout, 128, 1, QUANT>(p, sms, st);
     }
-    return many ? finish_launch<Tin, Tout, 256, 8>(p, sms, st) : finish_launch<Tin, Tout, 256, 1>(p, sms, st);
+    return many ? finish_launch<Tin, Tout, 256, 8, QUANT>(p, sms, st) : finish_launch<Tin, Tout, 256, 1, QUANT>(p, sms, st);
 }
 
+template <bool QUANT>
 static cudaError_t finish_any(const DecodeParams& p, ddt_dtype in, int sms, cudaStream_t st) {
     if (in == DDT_BF16)
-        return p.out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16>(p, sms, st)
-                                 : finish_go<__nv_bfloat16, float>(p, sms, st);
-    return p.out == DDT_BF16 ? finish_go<float, __nv_bfloat16>(p, sms, st) : finish_go<float, float>(p, sms, st);
+        return p.out == DDT_BF16 ? finish_go<__nv_bfloat16, __nv_bfloat16, QUANT>(p, sms, st)
+                                 : finish_go<__nv_bfloat16, float, QUANT>(p, sms, st);
+    return p.out == DDT_BF16 ? finish_go<float, __nv_bfloat16, QUANT>(p, sms, st) : finish_go<float, float, QUANT>(p, sms, st);
 }
 
 static DecodeParams decode_params(int L, int B, int Hq, int Hkv, int d, const AttnPaging& pg, ddt_dtype out, const void* q,
@@ -610,7 +656,7 @@ cudaError_t launch_decode(int L, int B, int Hq, int Hkv, int d, const AttnPaging
         decode_layout(p, simt_heads(p.G), kSimtMaxCtas, weight != nullptr, w);
         e = simt_d_go(p, st);
     }
-    return e != cudaSuccess || p.cl ? e : finish_any(p, in, sms, st);
+    return e != cudaSuccess || p.cl ? e : finish_any<false>(p, in, sms, st);
 }
 
 // ---- the same over a cache held in 8 bits: the split kernel is another, the join the same
@@ -621,7 +667,7 @@ size_t decode_quant_ws_bytes(int L, int B, int Hq, int Hkv, int d, ddt_dtype in)
     p.Hkv = Hkv;
     p.G = Hq / Hkv;
     p.d = d;
-    return decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, nullptr);
+    return decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, nullptr, true);
 }
 
 cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block, const AttnPaging& pg, ddt_dtype in,
@@ -631,9 +677,12 @@ cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block,
     DecodeParams p = decode_params(L, B, Hq, Hkv, d, pg, out, q, k_new, v_new, k_pages, v_pages, prefix_len, scale, o, nullptr, status);
     const int sms = sm_count();
     p.C = sms < kQuantMaxCtas / 4 ? sms : kQuantMaxCtas / 4;
-    decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, static_cast<unsigned char*>(ws));
-    const cudaError_t e = launch_decode_quant_tiles(p, in, block, k_scale, v_scale, st);
-    return e != cudaSuccess || p.cl ? e : finish_any(p, in, sms, st);
+    decode_layout(p, decode_quant_heads(p.G, in), kQuantMaxCtas, false, static_cast<unsigned char*>(ws), true);
+    p.ks = k_scale;
+    p.vs = v_scale;
+    p.block = block;
+    const cudaError_t e = launch_decode_quant_tiles(p, in, st);
+    return e != cudaSuccess || p.cl ? e : finish_any<true>(p, in, sms, st);
 }
 
 }  // namespace ddt

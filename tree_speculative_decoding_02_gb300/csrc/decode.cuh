@@ -47,7 +47,14 @@ struct DecodeParams {
     float2* part_ml;  // [U + C][HT] (reference in log2 units, sum); sum < 0: see kSeg*
     float* part_o;    // [U + C][HT][d]
     float* score;     // [L][B][Hq][cap] scores in log2 units (weight only)
+    // caches in 8 bits
+    const uint8_t* ks;  // [L][num_pages][Hkv][page_rows / block]
+    const uint8_t* vs;
+    int block;          // rows a scale
+    int* far;           // (workspace) [C] tiles with far blocks of a CTA's segments
+    int2* far_tile;     // [C][kFarTiles] the first of them: the segment's unit (of layer, request, kv head, block of heads); tile << 8 | its scale
 };
+constexpr int kFarTiles = 64;
 
 // values of a partial's sum that say why there is none
 constexpr float kSegBadPage = -1.f;  // a block-table entry outside [0, num_pages)
@@ -214,8 +221,11 @@ struct HeadJoin {
     int err;           // a status for the request, or DDT_OK
     int ns;            // segments, from slot `first` on
     long long first;
+    int c0;            // the first one's CTA
+    bool far;          // FAR: one of their CTAs has far blocks
 };
 
+template <bool FAR = false>
 __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int hq, float tn, int lane) {
     const int l = lb / p.B, b = lb - l * p.B, g = hq / p.G, hb = (hq % p.G) / p.hbs, h = (hq % p.G) % p.hbs;
     // loads that do not wait for one another first
@@ -223,8 +233,9 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int
     const long long pre = p.cl ? 0 : p.pre[b], all = p.cl ? 0 : p.pre[p.B];
     HeadJoin j;
     j.ref = j.z = 0.f;
-    j.ns = 0;
+    j.ns = j.c0 = 0;
     j.first = 0;
+    j.far = false;
     j.err = (P < 0 || P > p.cap) ? DDT_ERR_CAPACITY : DDT_OK;
     if (j.err) return j;
     const int nt = dec_tiles(P, p.cap);
@@ -235,17 +246,20 @@ __device__ __forceinline__ HeadJoin head_join(const DecodeParams& p, int lb, int
         const int HH = p.Hkv * p.HB;
         const long long T = all * HH * p.L;
         const long long first = l * all * HH + pre * HH + (long long)(g * p.HB + hb) * nt;
-        const int C = (int)min((long long)p.C, T), c0 = dec_owner(T, C, first);
-        j.ns = dec_owner(T, C, first + nt - 1) - c0 + 1;
-        j.first = (long long)lb * HH + g * p.HB + hb + c0;
+        const int C = (int)min((long long)p.C, T);
+        j.c0 = dec_owner(T, C, first);
+        j.ns = dec_owner(T, C, first + nt - 1) - j.c0 + 1;
+        j.first = (long long)lb * HH + g * p.HB + hb + j.c0;
     }
     const float2* ml = p.part_ml + j.first * p.HT + h;
     float m = tn, low = 0.f;
     for (int s = lane; s < j.ns; s += 32) {
         const float2 v = ml[(long long)s * p.HT];
+        if (FAR) j.far |= p.far[j.c0 + s] != 0;
         m = fmaxf(m, v.x);
         low = fminf(low, v.y);
     }
+    if (FAR) j.far = __any_sync(kFull, j.far);
     m = warp_max(m);
     low = -warp_max(-low);
     if (low < 0.f) j.err = low == kSegTimeout ? DDT_ERR_TIMEOUT : DDT_ERR_INVALID_ARG;
@@ -396,12 +410,11 @@ bool decode_tc_supported(int d, ddt_dtype in);
 int decode_tc_heads(int G, int d);
 cudaError_t launch_decode_tc(DecodeParams& p, cudaStream_t st);
 int decode_quant_heads(int G, ddt_dtype in);
-cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, int block, const uint8_t* ks, const uint8_t* vs,
-                                      cudaStream_t st);
+cudaError_t launch_decode_quant_tiles(DecodeParams& p, ddt_dtype in, cudaStream_t st);
 struct DecodeSmall {
     double most, excess;  // channels of a CTA's rows, in tiles, and of those above an even split's, up to which a call is small
 };
-cudaLaunchConfig_t decode_config(DecodeParams& p, DecodeSmall small, int ctas, int threads, int smem, cudaLaunchAttribute& at,
-                                 cudaStream_t st);
+void decode_clusters(DecodeParams& p, DecodeSmall small, int ctas);
+cudaLaunchConfig_t decode_grid(const DecodeParams& p, int threads, int smem, cudaLaunchAttribute& at, cudaStream_t st);
 
 }  // namespace ddt

@@ -439,7 +439,8 @@ cudaError_t tc_go(DecodeParams& p, const DecTcArgs& a, const CUtensorMap* maps, 
     cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
-    cudaLaunchConfig_t cfg = decode_config(p, DecodeSmall{512., 384.}, DecCfg<D, HP>::kCtas, DecCfg<D, HP>::kThreads, smem, at, st);
+    decode_clusters(p, DecodeSmall{512., 384.}, DecCfg<D, HP>::kCtas);
+    cudaLaunchConfig_t cfg = decode_grid(p, DecCfg<D, HP>::kThreads, smem, at, st);
     return cudaLaunchKernelEx(&cfg, k_decode_tc<D, HP>, p, a, maps[0], maps[1], maps[2]);
 }
 
