@@ -575,7 +575,8 @@ ddt_status ddt_token_logprobs(int B, int N, int V, int A, int top_n, float tempe
  * finer scale would move the rounding steps, not narrow them.
  *
  * In a round over such a cache: ddt_read_paged_quant, a layer at a time, into a contiguous
- * cache of 16 bits that ddt_tree_attn reads; after the walk ddt_append_paged_quant in the place of
+ * cache of 16 bits that ddt_tree_attn reads, with prefix_len -1 for requests whose prefix could not be read
+ * (ddt_chain_status): their rows of the contiguous cache hold whatever was there before; after the walk ddt_append_paged_quant in the place of
  * the commit's attention part (node = acc_nodes, count = n_emitted, advance 0), then ddt_commit
  * without attention layers for the rest and prefix_len, with acc_len -1 for requests that the append
  * refused (or advance 1 and no ddt_commit where there are no GDN layers).  ddt_evict_paged does not take these caches.
@@ -621,6 +622,16 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
                                 const uint8_t* v_scale, const int32_t* block_table,
                                 const int32_t* prefix_len, void* k_out, void* v_out,
                                 int32_t* status, ddt_stream_t stream);
+
+/* ddt_chain_status -- requests that one call of a chain refused are refused by the next: s[b] is the first
+ * of status[0..n-1][b] that is not DDT_OK, or DDT_OK.
+ *   length_out[b] = length[b] where s[b] is DDT_OK, else -1, which every call refuses as a prefix_len
+ *     (its output rows are zeros then) or an accepted length (nothing of the request is committed).
+ *   status_out[b] = s[b].
+ *   status [n][B]; length and length_out [B], or both NULL; status_out [B] or NULL, one output at least.
+ * Outputs are apart from one another and from the inputs. */
+ddt_status ddt_chain_status(int n, int B, const int32_t* status, const int32_t* length, int32_t* length_out,
+                            int32_t* status_out, ddt_stream_t stream);
 
 /* ddt_decode_attn_paged_quant -- ddt_decode_attn_paged over that cache, without the sums of the
  * weights: q, k_new, v_new, o, prefix_len, scale, status and workspace (of

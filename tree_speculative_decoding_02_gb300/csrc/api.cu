@@ -642,6 +642,15 @@ ddt_status ddt_read_paged_quant(int n_layers, int B, int Hkv, int d, int Pcap, i
                                        prefix_len, k_out, v_out, status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+ddt_status ddt_chain_status(int n, int B, const int32_t* status, const int32_t* length, int32_t* length_out,
+                            int32_t* status_out, ddt_stream_t stream) {
+    if (n < 1 || B < 1 || !status || !length != !length_out || (!length_out && !status_out)) return DDT_ERR_INVALID_ARG;
+    const size_t n_b = (size_t)B * 4;
+    const Span spans[] = {{length_out, n_b}, {status_out, n_b}, {status, n_b * n}, {length, n_b}};
+    if (any_overlap(spans, 4, 2)) return DDT_ERR_INVALID_ARG;
+    return from_cuda(launch_chain_status(n, B, status, length, length_out, status_out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t ddt_decode_attn_paged_quant_workspace(int n_layers, int B, int Hq, int Hkv, int d, ddt_dtype in_dtype) {
     if (n_layers < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || !dtype_ok(in_dtype)) return 0;
     return decode_quant_ws_bytes(n_layers, B, Hq, Hkv, d, in_dtype);

@@ -87,6 +87,8 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
 cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int block, int Pcap, const AttnPaging& pg, ddt_dtype out,
                               const void* k_pages, const void* v_pages, const uint8_t* k_scale, const uint8_t* v_scale,
                               const int32_t* prefix_len, void* k_out, void* v_out, int32_t* status, cudaStream_t st);
+cudaError_t launch_chain_status(int n, int B, const int32_t* status, const int32_t* length, int32_t* length_out,
+                                int32_t* status_out, cudaStream_t st);
 size_t decode_quant_ws_bytes(int L, int B, int Hq, int Hkv, int d, ddt_dtype in);
 cudaError_t launch_decode_quant(int L, int B, int Hq, int Hkv, int d, int block, const AttnPaging& pg, ddt_dtype in,
                                 ddt_dtype out, const void* q, const void* k_new, const void* v_new, const void* k_pages,

@@ -330,6 +330,26 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     return cudaLaunchKernelEx(&cfg, k_append_advance, B, count, (const int32_t*)status, prefix_len);
 }
 
+// a thread a request
+__global__ void k_chain_status(int n, int B, const int32_t* __restrict__ status, const int32_t* __restrict__ length, int32_t* length_out,
+                               int32_t* status_out) {
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b >= B) return;
+    int s = DDT_OK;
+    for (int i = n - 1; i >= 0; --i) {
+        const int x = status[(long long)i * B + b];
+        s = x != DDT_OK ? x : s;
+    }
+    if (length) length_out[b] = s == DDT_OK ? length[b] : -1;
+    if (status_out) status_out[b] = s;
+}
+
+cudaError_t launch_chain_status(int n, int B, const int32_t* status, const int32_t* length, int32_t* length_out,
+                                int32_t* status_out, cudaStream_t st) {
+    k_chain_status<<<counted(dim3((unsigned)(((long long)B + 127) / 128))), 128, 0, st>>>(n, B, status, length, length_out, status_out);
+    return cudaGetLastError();
+}
+
 // ------------------------------------------------------------------------------ read back
 namespace {
 struct ReadArgs {

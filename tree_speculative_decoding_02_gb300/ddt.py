@@ -62,6 +62,7 @@ _SIGS = {
     "ddt_token_logprobs": ([_c_int] * 5 + [_c_float, _c_int] + [_c_p] * 9 + [_c_size, _c_p], _c_int),
     "ddt_append_paged_quant": ([_c_int] * 11 + [_c_p] * 6 + [_c_int] + [_c_p] * 6, _c_int),
     "ddt_read_paged_quant": ([_c_int] * 10 + [_c_p] * 10, _c_int),
+    "ddt_chain_status": ([_c_int] * 2 + [_c_p] * 5, _c_int),
     "ddt_decode_attn_paged_quant_workspace": ([_c_int] * 6, _c_size),
     "ddt_decode_attn_paged_quant": ([_c_int] * 11 + [_c_p] * 9 + [_c_float] + [_c_p] * 3 + [_c_size, _c_p], _c_int),
     "ddt_qk_norm_rope": ([_c_int] * 7 + [ctypes.c_double, _c_float, _c_float, _c_int] + [_c_p] * 11, _c_int),
@@ -839,6 +840,20 @@ def ddt_read_paged_quant(k_pages, v_pages, k_scale, v_scale, block_table, prefix
     if rc:
         _check(rc, "ddt_read_paged_quant")
     return {"status": status}
+
+
+def ddt_chain_status(status, *, length=None, length_out=None, status_out=None):
+    """The first of status [n][B] that is not OK, for every request, to status_out [B]; length [B] to length_out where there
+    is none, -1 (a length that the next call refuses) where there is."""
+    lib = _lib or _gpu()
+    n, B = status.shape
+    dev = _here(status, "status")
+    each = (B,)
+    at = [None if t is None else _at(t, dev, each, _I32, name)
+          for t, name in ((length, "length"), (length_out, "length_out"), (status_out, "status_out"))]
+    rc = lib.ddt_chain_status(n, B, _at(status, dev, (n, B), _I32, "status"), *at, _raw_stream(dev))
+    if rc:
+        _check(rc, "ddt_chain_status")
 
 
 def decode_attn_paged_quant_workspace(q, k_pages, block_table):

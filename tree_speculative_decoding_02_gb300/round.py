@@ -146,9 +146,12 @@ class Round:
             k, v = (x[l:l + 1, :, :, :rows].transpose(2, 3).contiguous() for x in (a.k_cache, a.v_cache))
             ddt.ddt_append_paged_quant(k, v, *self._layer(l), self.block_table, none, self.prefix0, advance=False)
         self.k_scratch, self.v_scratch = a.k_cache[:1].clone(), a.v_cache[:1].clone()
-        self.layer_status = torch.zeros((L, B), dtype=torch.int32, device=self.device)
-        self.read_status, self.append_status, self.commit_len = (torch.zeros((B,), dtype=torch.int32, device=self.device)
-                                                                 for _ in range(3))
+        # a round's statuses: of the read back (the same for every layer), then of each layer's attention
+        self.layer_status = torch.zeros((1 + L, B), dtype=torch.int32, device=self.device)
+        self.read_status = self.layer_status[0]
+        self.attn_len = torch.zeros((B,), dtype=torch.int32, device=self.device)
+        self.append_status, self.commit_len = (torch.zeros((B,), dtype=torch.int32, device=self.device)
+                                              for _ in range(2))
         self.refused = torch.full_like(self.commit_len, -1)   # as an accepted length: no commit
         a.k_cache = a.v_cache = None
 
@@ -263,17 +266,19 @@ class Round:
         """The tree attention of an 8-bit cache: layer by layer, over the layer's rows read back."""
         t, v_tree = self.tree, self.attn.v_tree
         for l in range(self.Lf):
-            at, st = slice(l, l + 1), self.layer_status[l]
+            at = slice(l, l + 1)
             ddt.ddt_read_paged_quant(*self._layer(l), self.block_table, self.prefix_len, self.k_scratch, self.v_scratch,
                                      status=self.read_status)
-            common = dict(scale=scale, out_dtype=self.attn_o.dtype, out=self.attn_o[at], status=st, workspace=self.attn_ws)
-            args = (q[at], k_tree[at], v_tree[at], self.k_scratch, self.v_scratch, self.prefix_len, t["n_nodes"], t["anc"])
+            if l == 0:   # what was not read is not attended over: the scratch holds another layer's rows there
+                ddt.ddt_chain_status(self.layer_status[:1], length=self.prefix_len, length_out=self.attn_len)
+            common = dict(scale=scale, out_dtype=self.attn_o.dtype, out=self.attn_o[at], status=self.layer_status[1 + l],
+                          workspace=self.attn_ws)
+            args = (q[at], k_tree[at], v_tree[at], self.k_scratch, self.v_scratch, self.attn_len, t["n_nodes"], t["anc"])
             if rot:
                 ddt.ddt_tree_attn_rope(*args, t["position"], rot_dim=rot, **common)
             else:
                 ddt.ddt_tree_attn(*args, **common)
-            torch.maximum(st, self.read_status, out=st)
-        torch.amax(self.layer_status, 0, out=self.attn_status)
+        ddt.ddt_chain_status(self.layer_status, status_out=self.attn_status)
 
     def k_rows(self):
         """The tree keys as the attention takes them and the commit copies them."""
