@@ -2,6 +2,7 @@
 why, and the other requests' rounds are as they are without it."""
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from tree_speculative_decoding_02_gb300 import ddt, synth
 from tree_speculative_decoding_02_gb300.round import Round
@@ -87,3 +88,26 @@ def test_chain_status(n, B):
     alone = torch.empty(B, dtype=torch.int32, device="cuda")
     ddt.ddt_chain_status(st.to(torch.int32).cuda(), status_out=alone)
     assert alone.tolist() == first
+
+
+class _Ops(TorchDispatchMode):
+    def __init__(self):
+        super().__init__()
+        self.names = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        if not func.is_view and "empty" not in str(func):
+            self.names.append(str(func))
+        return func(*args, **(kwargs or {}))
+
+
+@pytest.mark.parametrize("rope", [0, 64])
+def test_a_round_is_the_librarys_calls_alone(rope):
+    """No arithmetic of torch's between the calls, which the launch counter would not see."""
+    r = _round(rope)
+    r.step()
+    with _Ops() as ops:
+        r.step()
+    assert ops.names == []
+    torch.cuda.synchronize()
+    assert (r.commit["status"] == 0).all()

@@ -150,9 +150,10 @@ class Round:
         self.layer_status = torch.zeros((1 + L, B), dtype=torch.int32, device=self.device)
         self.read_status = self.layer_status[0]
         self.attn_len = torch.zeros((B,), dtype=torch.int32, device=self.device)
-        self.append_status, self.commit_len = (torch.zeros((B,), dtype=torch.int32, device=self.device)
-                                              for _ in range(2))
-        self.refused = torch.full_like(self.commit_len, -1)   # as an accepted length: no commit
+        # of the append and of the commit, and the accepted lengths of requests whose rows were appended
+        self.commit_status = torch.zeros((2, B), dtype=torch.int32, device=self.device)
+        self.append_status = self.commit_status[0]
+        self.commit_len = torch.zeros((B,), dtype=torch.int32, device=self.device)
         a.k_cache = a.v_cache = None
 
     def _layer(self, l):
@@ -183,12 +184,13 @@ class Round:
         self.walk_step()
         kw = {}
         quant = bool(self.Lf and self.quant)
-        acc_len = self.walk["acc_len"]
+        acc_len, out = self.walk["acc_len"], self.commit
         if quant:   # its rows first: the commit below moves prefix_len, of the requests whose rows were written
             ddt.ddt_append_paged_quant(self.k_rows(), self.attn.v_tree, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
                                        self.block_table, self.prefix_len, self.walk["n_emitted"],
                                        node=self.walk["acc_nodes"], advance=False, status=self.append_status)
-            acc_len = torch.where(self.append_status == 0, acc_len, self.refused, out=self.commit_len)
+            ddt.ddt_chain_status(self.commit_status[:1], length=acc_len, length_out=self.commit_len)
+            acc_len, out = self.commit_len, dict(out, status=self.commit_status[1])
             kw.update(N=self.attn.k_tree.shape[2])
         if self.Lf and not self.page:
             kw.update(k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_cache=self.attn.k_cache,
@@ -204,9 +206,9 @@ class Round:
                                  k_tree=self.k_rows(), v_tree=self.attn.v_tree, k_pages=self.k_pages,
                                  v_pages=self.v_pages, out=self.commit, **kw)
         else:
-            ddt.ddt_commit(self.walk["acc_nodes"], acc_len, self.prefix_len, out=self.commit, **kw)
+            ddt.ddt_commit(self.walk["acc_nodes"], acc_len, self.prefix_len, out=out, **kw)
             if quant:
-                torch.maximum(self.commit["status"], self.append_status, out=self.commit["status"])
+                ddt.ddt_chain_status(self.commit_status, status_out=self.commit["status"])
 
     def walk_step(self):
         """The round's walk: greedy (or its flat safe mode), or rejection sampling at
