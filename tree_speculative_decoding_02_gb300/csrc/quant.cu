@@ -30,7 +30,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 8;  // vectors of 8 channels a lane has in flight
 
 struct AppendArgs {
-    int L, B, N, A, Hkv, d, S;
+    int B, N, A, Hkv, S;
     int page_rows, num_pages, max_pages, cap;
     int wpi;          // warps an item (a block's K or V rows of one head)
     int run, groups;  // blocks a CTA; CTAs that share a block's items
@@ -265,8 +265,8 @@ static cudaError_t append_d_go(const cudaLaunchConfig_t& cfg, const AppendArgs& 
     return a.node ? cudaLaunchKernelEx(&cfg, k_append_quant<T, D, true>, a) : cudaLaunchKernelEx(&cfg, k_append_quant<T, D, false>, a);
 }
 template <typename T>
-static cudaError_t append_go(const cudaLaunchConfig_t& cfg, const AppendArgs& a) {
-    return a.d == 64 ? append_d_go<T, 64>(cfg, a) : (a.d == 128 ? append_d_go<T, 128>(cfg, a) : append_d_go<T, 256>(cfg, a));
+static cudaError_t append_go(int d, const cudaLaunchConfig_t& cfg, const AppendArgs& a) {
+    return d == 64 ? append_d_go<T, 64>(cfg, a) : (d == 128 ? append_d_go<T, 128>(cfg, a) : append_d_go<T, 256>(cfg, a));
 }
 
 cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int S, const AttnPaging& pg, ddt_dtype in,
@@ -274,12 +274,10 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
                                 int32_t* prefix_len, int advance, void* kp, void* vp, uint8_t* ks, uint8_t* vs,
                                 int32_t* status, cudaStream_t st) {
     AppendArgs a{};
-    a.L = L;
     a.B = B;
     a.N = N;
     a.A = A;
     a.Hkv = Hkv;
-    a.d = d;
     a.S = S;
     a.page_rows = pg.page_rows;
     a.num_pages = pg.num_pages;
@@ -299,7 +297,9 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     a.status = status;
     const int vectors = (S < A ? S : A) * d / 256;  // a lane of one warp has this many of an item at most
     a.wpi = 1;
-    // (a few rows of many requests: one warp, which reads up to 16 vectors twice, from L1 the second time)
+    // A few rows of many requests: one warp an item, which reads up to 16 vectors twice, from L1 the second time (blocks of 16 rows of
+    // 256, bf16, by two warps and by one: 1 to 16 rows, 128 units 4.2 and 6.0 us, 512 6.9 and 7.8, 1024 10.0 and 9.4, 8192 51 and
+    // 35; 1 to 32 rows, 1024 units 12.8 and 11.7, 8192 75 and 56; with 1 to 5 rows one is never slower)
     const bool few = A <= 32 && (long)L * B * Hkv >= 1024;
     while (a.wpi < kWarps && vectors > (few ? 2 : 1) * kChunk * a.wpi) a.wpi *= 2;
     const int blocks = (int)(((long long)A + S - 2) / S + 1);  // that a request's rows may fall into
@@ -322,7 +322,7 @@ cudaError_t launch_append_quant(int L, int B, int N, int A, int Hkv, int d, int 
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = a.checked ? 1 : 0;
-    cudaError_t e = in == DDT_BF16 ? append_go<__nv_bfloat16>(cfg, a) : append_go<float>(cfg, a);
+    cudaError_t e = in == DDT_BF16 ? append_go<__nv_bfloat16>(d, cfg, a) : append_go<float>(d, cfg, a);
     if (e != cudaSuccess || !advance || a.solo || a.checked) return e;
     cfg.gridDim = dim3(counted((unsigned)(B + 127) / 128));
     cfg.blockDim = dim3(128);
@@ -353,7 +353,7 @@ cudaError_t launch_chain_status(int n, int B, const int32_t* status, const int32
 // ------------------------------------------------------------------------------ read back
 namespace {
 struct ReadArgs {
-    int L, B, Hkv, d, S, Pcap;
+    int B, Hkv, Pcap;
     int page_rows, num_pages, max_pages, cap;
     const int32_t* table;
     const int32_t* prefix_len;
@@ -480,7 +480,7 @@ static void read_go(int d, dim3 grid, const ReadArgs& a, cudaStream_t st) {
 cudaError_t launch_read_quant(int L, int B, int Hkv, int d, int S, int Pcap, const AttnPaging& pg, ddt_dtype out,
                               const void* kp, const void* vp, const uint8_t* ks, const uint8_t* vs,
                               const int32_t* prefix_len, void* ko, void* vo, int32_t* status, cudaStream_t st) {
-    ReadArgs a{L, B, Hkv, d, S, Pcap, pg.page_rows, pg.num_pages, pg.max_pages, pg.page_rows * pg.max_pages, pg.block_table, prefix_len,
+    ReadArgs a{B, Hkv, Pcap, pg.page_rows, pg.num_pages, pg.max_pages, pg.page_rows * pg.max_pages, pg.block_table, prefix_len,
                static_cast<const unsigned char*>(kp), static_cast<const unsigned char*>(vp), ks, vs, ko, vo, status};
     const int rows = kReadVecs * kThreads / (d / 16), most = Pcap < a.cap ? Pcap : a.cap;
     const long long steps = (most + rows - 1) / rows;

@@ -857,7 +857,8 @@ def ddt_chain_status(status, *, length=None, length_out=None, status_out=None):
 
 
 def decode_attn_paged_quant_workspace(q, k_pages, block_table):
-    """A workspace for ddt_decode_attn_paged_quant calls of these shapes (one call at a time may use it)."""
+    """A workspace for ddt_decode_attn_paged_quant calls of these shapes (one call at a time may use it).  Any block_table:
+    it is an argument as decode_attn_paged_workspace has it, whose size goes by the table's."""
     lib = _gpu()
     L, B, Hq, d = q.shape
     return _ws(lib.ddt_decode_attn_paged_quant_workspace(L, B, Hq, k_pages.shape[2], d, _code(q.dtype, "q")), q.device)
