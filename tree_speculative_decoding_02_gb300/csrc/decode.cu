@@ -359,15 +359,10 @@ __device__ __noinline__ void far_join(const DecodeParams& p, int lb, int hq, flo
     const long long all = p.pre[p.B], T = all * HH * p.L, from = l * all * HH + p.pre[b] * HH + (long long)(g * p.HB + hb) * nt;
     const int C = (int)min((long long)p.C, T);
     for (int s = WPH == 1 ? 0 : warp; s < j.ns; s += WPH) {
-        const int c = j.c0 + s, n = p.far[c];
-        const bool many = n > kFarTiles;  // more than are on the list: all of the segment's tiles are looked at
-        for (int i = 0; i < (many ? 1 : n); ++i) {
-            const int2 x = p.far_tile[c * kFarTiles + i];
-            if (!many && x.x != lb * HH + g * p.HB + hb) continue;
-            const int t0 = many ? (int)(max(dec_first(T, C, c), from) - from) : x.y >> 8;
-            const int t1 = many ? (int)(min(dec_first(T, C, c + 1), from + nt) - from) : t0 + 1;
-            far_rows<Tin, D>(p, lb, g, hq % p.G, t0, t1, many ? 0 : x.y & 255, j.first + s, hq % p.G % p.hbs, lane);
-        }
+        const int c = j.c0 + s;
+        if (p.far[c])
+            far_rows<Tin, D>(p, lb, g, hq % p.G, (int)(max(dec_first(T, C, c), from) - from), (int)(min(dec_first(T, C, c + 1), from + nt) - from),
+                             j.first + s, hq % p.G % p.hbs, lane);
     }
     DecNew<Tin, D> mine;
     mine.load(p, lb, g, hq % p.G, lane);
@@ -480,10 +475,7 @@ static size_t decode_layout(DecodeParams& p, int hbs, int ctas, bool weight, uns
     p.part_ml = reinterpret_cast<float2*>(take(slots * p.HT * sizeof(float2)));
     p.part_o = reinterpret_cast<float*>(take(slots * p.HT * p.d * sizeof(float)));
     p.score = weight ? reinterpret_cast<float*>(take(units * p.cap * p.G * sizeof(float))) : nullptr;
-    if (far) {
-        p.far = reinterpret_cast<int*>(take(ctas * sizeof(int)));
-        p.far_tile = reinterpret_cast<int2*>(take((size_t)ctas * kFarTiles * sizeof(int2)));
-    }
+    p.far = far ? reinterpret_cast<int*>(take(ctas * sizeof(int))) : nullptr;
     return at;
 }
 

@@ -51,10 +51,8 @@ struct DecodeParams {
     const uint8_t* ks;  // [L][num_pages][Hkv][page_rows / block]
     const uint8_t* vs;
     int block;          // rows a scale
-    int* far;           // (workspace) [C] tiles with far blocks of a CTA's segments
-    int2* far_tile;     // [C][kFarTiles] the first of them: the segment's unit (of layer, request, kv head, block of heads); tile << 8 | its scale
+    int* far;           // [C] (workspace) whether a CTA's segments have far blocks
 };
-constexpr int kFarTiles = 64;
 
 // values of a partial's sum that say why there is none
 constexpr float kSegBadPage = -1.f;  // a block-table entry outside [0, num_pages)

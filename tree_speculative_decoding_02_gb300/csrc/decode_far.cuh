@@ -102,11 +102,9 @@ struct CodeRun {
 };
 
 // One warp: the far rows of tiles [t0, t1) of (layer, request) lb and kv head g join the partial of query head hq of g's, in
-// `slot` at place h.  unit: the segment's, or 0: t0 is its first tile.  Scores, weights and products in fp32 from the codes in
-// HBM, a few rows at once.
+// `slot` at place h: a segment's tiles.  Scores, weights and products in fp32 from the codes in HBM, a few rows at once.
 template <typename Tin, int D>
-__device__ __forceinline__ void far_rows(const DecodeParams& p, int lb, int g, int hq, int t0, int t1, int unit, long long slot, int h,
-                                         int lane) {
+__device__ __forceinline__ void far_rows(const DecodeParams& p, int lb, int g, int hq, int t0, int t1, long long slot, int h, int lane) {
     constexpr int E = D / 32, R = E == 8 ? 4 : 8;  // consecutive channels a lane; rows at once, the next ones on their way
     float2* const ml = p.part_ml + slot * p.HT + h;
     float2 part = *ml;
@@ -119,15 +117,17 @@ __device__ __forceinline__ void far_rows(const DecodeParams& p, int lb, int g, i
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = out[e];
-    int low = 255, high = 0;  // of the far blocks' scales
-    for (int r0 = t0 * kDecTile; r0 < end; r0 += kDecTile) {  // a block a lane, as k_decode_quant looks at them
+    int unit = 0, low = 255, high = 0;  // of the far blocks' scales
+    // 32 blocks at a time, one a lane; tile after tile while all are of zeros, as k_decode_quant looks for the unit
+    for (int r0 = t0 * kDecTile, step; r0 < end; r0 += step) {
+        step = unit || r0 == t0 * kDecTile ? 32 * p.block : kDecTile;
         const int pos = r0 + lane * p.block;
-        const bool there = pos < (unit || r0 > t0 * kDecTile ? min(end, r0 + kDecTile) : end);
+        const bool there = pos < min(end, r0 + step);
         const long long plane = there ? ((long long)l * p.num_pages + table[pos / p.page_rows]) * p.Hkv + g : 0;
         const long long at = plane * per_page + pos % p.page_rows / p.block;
         const int vb = there ? p.vs[at] : 0, kb = there ? p.ks[at] : 0;
         if (!unit) unit = v_unit_of(vb);
-        const bool mine = is_far(vb, unit) && lane < kDecTile / p.block;
+        const bool mine = is_far(vb, unit);
         if (mine) low = min(low, vb), high = max(high, vb);
         for (unsigned far = __ballot_sync(kFull, mine); far; far &= far - 1) {
             const int of = __ffs(far) - 1, first = r0 + of * p.block, n = min(p.block, end - first);

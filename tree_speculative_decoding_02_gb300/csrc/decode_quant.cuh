@@ -131,7 +131,7 @@ __device__ __forceinline__ void split4(const float (&x)[4], uint32_t (&c)[PARTS]
 template <typename Tin, int D, int THREADS>
 __device__ __forceinline__ void far_tail(const DecodeParams& p, const DecodeWalk& w, float* s_x) {
     const int lb = w.l * p.B + w.b, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int h = warp; h < p.G; h += THREADS / 32) far_rows<Tin, D>(p, lb, w.g, h, w.t, w.t + (int)w.left, 0, blockIdx.x, h, lane);
+    for (int h = warp; h < p.G; h += THREADS / 32) far_rows<Tin, D>(p, lb, w.g, h, w.t, w.t + (int)w.left, blockIdx.x, h, lane);
     DecNew<Tin, D> mine_new;
     mine_new.load(p, lb, w.g, dec_first_head(p), lane);
     __syncthreads();
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
     } else if (warp == 3) {
         // --------------------------------------------------------------------- scales
         const int n_blk = kDecTile / p.block, per_page = p.page_rows / p.block;
-        int j = 0, n_far = 0;  // tiles; those with far blocks
-        bool ok = true;
+        int j = 0;
+        bool ok = true, any_far = false;
         for (; w.left > 0 && ok; dec_next(p, w)) {
             const int g = w.g / p.HB, n_seg = dec_seg_tiles(w);
             const int32_t* table = p.block_table + (long long)w.b * p.max_pages;
@@ -403,19 +403,16 @@ __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCf
                 // A block of zeros takes any scale: a small one, so that the weights which do count keep their bits.
                 const int dv = vb ? vb - base : -60;
                 const bool far = is_far(vb, base) && lane < n_blk;
+                any_far |= far;
                 if (lane < n_blk)
                     scales[(j & 3) * 16 + lane] = make_float4(scale_of(kb), far ? -INFINITY : (float)dv, far ? 0.f : scale_of(127 - dv), __int_as_float(base));
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x_full + (j & 3));
-                if (__any_sync(kFull, far)) {
-                    if (!CLUSTER && lane == 0 && n_far < kFarTiles)
-                        p.far_tile[blockIdx.x * kFarTiles + n_far] = make_int2((w.l * p.B + w.b) * p.Hkv * p.HB + w.g, t << 8 | base);
-                    ++n_far;
-                }
             }
         }
-        if (CLUSTER) s_any_far = n_far > 0;
-        else if (lane == 0) p.far[blockIdx.x] = n_far;
+        any_far = __any_sync(kFull, any_far);
+        if (CLUSTER) s_any_far = any_far;
+        else if (lane == 0) p.far[blockIdx.x] = any_far;
     } else {
         // -------------------------------------------------- softmax, and the segments' partials
         const int ws = warp & 3, r = 32 * ws + lane;  // a warp reads its quarter of the lanes
