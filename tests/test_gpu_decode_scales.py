@@ -218,3 +218,21 @@ def test_many_far_blocks_a_cta(Hq, block, every, dtype):
     tol = torch.from_numpy(bound + Q.U * np.abs(want)).cuda()
     err = (r["o"].double() - torch.from_numpy(want).cuda()).abs()
     assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("zeros", [31, 32, 33, 49])
+def test_far_blocks_behind_many_blocks_of_zeros(zeros, dtype):
+    """Zeros over the 32 blocks that the scale the others are near is looked for in, then ordinary and far blocks: several
+    requests a CTA, cut anywhere."""
+    B = 100
+    lens = [520 + b % 9 for b in range(B)]
+    c = _case(60, 1, B, 8, 4, 64, lens, 16, 8, dtype, new=False, q_std=0.1)
+    c["vs"][:] = 120
+    for b in range(B):
+        for i, at in enumerate(_blocks(c, b)):
+            if i < zeros:
+                _set(c, at, 0, zero=True)
+            elif i % 7 == b % 7:
+                _set(c, at, 131 if i % 2 else 95, channel=b % 64 if i % 2 else None)
+    _check(c, _run(c, out_dtype=F32))

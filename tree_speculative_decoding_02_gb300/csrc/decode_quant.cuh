@@ -33,7 +33,7 @@
 // (901 MB), 138 us, 6.5 TB/s; one of 131071 rows, 32 over 8 of 128 (269 MB), 46 us; 2 x 96 of up to 2500 rows, 16 over 16 of
 // 64 (453 MB), 83 us.  A tile is half as many bytes as in bf16 and its softmax as long, so two to four CTAs share an SM (heads
 // of 64, one head a kv head: 98 us with three, 93 with four), and instances for groups of up to 2 and 4 heads leave out what
-// the others would compute for nobody (139 -> 98).  Larger groups are bound by the softmax's instructions, 332 a warp for a
+// the others would compute for nobody (139 -> 98).  Larger groups are bound by the softmax's instructions, 323 a warp for a
 // tile and eight heads: 16 heads of 64 read 4.3 TB/s.  Pairs of heads go through packed fp32 instructions, weights four a word.
 #pragma once
 
@@ -140,7 +140,7 @@ __device__ __forceinline__ void far_tail(const DecodeParams& p, const DecodeWalk
 }
 
 // CLUSTER: a unit a cluster, which joins its partials itself; else k_decode_finish does.  (Two instances: registers are short,
-// and what the one does behind its roles costs the other's roles up to 10 % of a call.)
+// and what the one does behind its roles costs the other's roles up to 15 % of a call.)
 template <typename Tin, int D, int HP, int GH, int QP, int PP, bool CLUSTER>
 __global__ void __launch_bounds__(QuantCfg<D, HP, GH, QP, PP>::kThreads, QuantCfg<D, HP, GH, QP, PP>::kCtas)
     k_decode_quant(const DecodeParams p, const DecQuantArgs a, const __grid_constant__ CUtensorMap tm_k,
